@@ -66,16 +66,18 @@ typedef enum pa_status {
     PA_ERR_SEQ_SWAPPED = 11        /* the sequence's blocks are swapped out (pa_seq_swap_out) */
 } pa_status;
 
-/* Element types.  PA_FP8_E4M3 (OCP FP8 E4M3 codes, one byte) is a pool type
- * only: pools of that type pair with bf16 queries and outputs through the
- * *_fp8 entry points. */
-typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+/* Element types.  PA_FP8_E4M3 (OCP FP8 E4M3 codes, one byte) and PA_FP4_E2M1
+ * (4-bit E2M1 codes with a scale per 16 elements, see "4-bit KV pools") are
+ * pool types only: pools of those types pair with bf16 queries and outputs
+ * through the *_fp8 and *_fp4 entry points. */
+typedef enum pa_dtype { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_FP4_E2M1 = 3 } pa_dtype;
 
 /* Bits of the device status word. */
 #define PA_DEV_BAD_BLOCK_ID 0x1 /* a block id outside [0, num_blocks) was read or given */
 #define PA_DEV_BAD_SLOT 0x2     /* a slot outside the pool was given */
 #define PA_DEV_BAD_SEQ_LEN 0x4  /* seq_lens[b] < 0, or beyond its block table or max_seq_len */
 #define PA_DEV_WAIT_TIMEOUT 0x8 /* an on-chip pipeline wait gave up (the output is not valid) */
+#define PA_DEV_BAD_POSITION 0x10 /* a position outside the cos / sin table was given */
 
 /* ------------------------------------------------------------------------ */
 /* Device kernels                                                            */
@@ -192,7 +194,7 @@ pa_status pa_decode_attention(void* out, const void* q, const void* k_pool, cons
  * aligned, plan_bytes long) from HOST copies of block_tables
  * ([num_seqs][max_blocks_per_seq]) and seq_lens, equal to the device copies
  * the call will read.  max_seq_len, partition_tokens and dtype (the pool's:
- * PA_F32, PA_BF16 or PA_FP8_E4M3) must be the call's.  Returns
+ * PA_F32, PA_BF16, PA_FP8_E4M3 or PA_FP4_E2M1) must be the call's.  Returns
  * PA_ERR_WORKSPACE_TOO_SMALL if plan_bytes is short; out-of-range lengths are
  * clamped as the decode clamps them (the decode still flags them).
  *
@@ -396,13 +398,118 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
                                   size_t workspace_bytes, void* stream);
 
 /*
+ * 4-bit KV pools (an extrapolation like the FP8 pools: the pages list
+ * quantised KV formats only by name).  A quarter of the bytes of bf16, with a
+ * scale for every 16 elements.
+ *
+ * Format (PA_FP4_E2M1).  An element is an E2M1 code (sign, 0, 0.5, 1, 1.5, 2,
+ * 3, 4 or 6); 16 consecutive elements of a row share one E4M3 scale; a pool
+ * has one fp32 scale.  Value = code * group scale * pool scale.  A pool is
+ * bytes [num_blocks][num_kv_heads][block_size * (head_dim / 2 + head_dim / 16)]:
+ * the record of one block and head holds the codes of its block_size token
+ * rows (head_dim / 2 bytes each, element 2 j in the low half of byte j), then
+ * their scale bytes (head_dim / 16 each).  head_dim 64 or 128, block_size 16 or
+ * 32.  pa_copy_blocks, pa_swap_out and pa_swap_in take pools of this type.
+ *
+ * Quantisation of a group x[0..15], in fp32: y = x / pool scale; the scale is
+ * E4M3(max|y| / 6), nearest even, saturated at 448; the codes are
+ * E2M1(y / scale), nearest even, saturated at 6, the sign y's.  A scale that
+ * rounds to zero makes every code zero.  A group with a NaN gets the NaN scale
+ * and reads as NaN (an infinity saturates).  The stored bytes are bit-exact
+ * against that definition.  k_scale and v_scale must be finite and > 0.
+ *
+ * pa_reshape_and_cache_fp4: the slot-mapped append of pa_reshape_and_cache
+ * (same slots, padding and errors) with that quantisation; k_new / v_new are
+ * in_dtype (bf16 or fp32) [num_tokens][num_kv_heads][head_dim].
+ *
+ * pa_unpack_blocks_fp4: for i < num, out[i] = the values of block blocks[i]
+ * (int32, device), every KV head, slot and element, in out_dtype (bf16 or
+ * fp32): fp32(code * scale) times the pool scale, rounded once more to bf16.
+ * k_out / v_out are [num][num_kv_heads][block_size][head_dim], so they are pools
+ * themselves: unpack a sequence's blocks and pa_prefill_attention reads them
+ * with the block table 0, 1, .., num - 1.  Slots that hold no token unpack to
+ * whatever their bytes stand for (NaN included).  A block id outside
+ * [0, num_blocks) sets PA_DEV_BAD_BLOCK_ID and its rows are left as they were.
+ *
+ * pa_decode_attention_fp4, pa_decode_attention_fp4_planned: pa_decode_attention
+ * and its planned form over 4-bit pools with bf16 q and out, as
+ * pa_decode_attention_fp8 does for FP8 pools (same layouts, workspace, split
+ * modes, plan and error reporting; plans are built with dtype PA_FP4_E2M1).
+ * code * scale is exact in f16, in which the MMAs run with fp32 sums; a query
+ * row is first scaled by a power of two so that its largest element lies in
+ * [1, 2), so any bf16 magnitudes are in range.
+ */
+pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                                   const int64_t* slot_mapping, int32_t num_tokens, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks, pa_dtype in_dtype,
+                                   float k_scale, float v_scale, int32_t* dev_status, void* stream);
+pa_status pa_unpack_blocks_fp4(const void* k_pool, const void* v_pool, const int32_t* blocks, int32_t num, void* k_out,
+                               void* v_out, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                               int32_t num_blocks, pa_dtype out_dtype, float k_scale, float v_scale,
+                               int32_t* dev_status, void* stream);
+pa_status pa_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool, float k_scale,
+                                  float v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* seq_lens, int32_t max_seq_len, int32_t num_seqs,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                  int32_t num_blocks, float scale, int32_t partition_tokens, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+pa_status pa_decode_attention_fp4_planned(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                          float k_scale, float v_scale, const int32_t* block_tables,
+                                          int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                          int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                                          int32_t partition_tokens, void* workspace, size_t workspace_bytes,
+                                          const void* plan, size_t plan_bytes, void* stream);
+
+/*
+ * Rotating append (rotary position embedding on the way into the cache; the
+ * pages do not name it: it joins the append to the step before it).  For
+ * every token i with slot s = slot_mapping[i] >= 0 and position p =
+ * positions[i]: each query and key head's first rot_dim elements are turned, pair
+ * j = 0 .. rot_dim / 2 - 1 by
+ *     a' = a cos_sin[p][j] - b cos_sin[p][rot_dim / 2 + j]
+ *     b' = b cos_sin[p][j] + a cos_sin[p][rot_dim / 2 + j]
+ * (a, b) = elements (j, j + rot_dim / 2), or (2 j, 2 j + 1) when interleaved;
+ * the other elements stay.  In fp32, every product and sum rounded.  Then
+ *     q_out[i] = turned q[i],  K pool at s = turned k[i],  V pool at s = v[i],
+ * rounded once: to in_dtype for q_out, to the pool's type for the pools, as
+ * pa_reshape_and_cache (pool_dtype == in_dtype), pa_reshape_and_cache_fp8 or
+ * pa_reshape_and_cache_fp4 store them.
+ *
+ * in_dtype is PA_F32 or PA_BF16; pool_dtype is in_dtype, PA_FP8_E4M3 (head_dim
+ * 128) or PA_FP4_E2M1; k_scale and v_scale (finite, > 0) are read for the
+ * quantised pools.  q, k, v: [num_tokens][heads][head_dim] with q_stride,
+ * k_stride, v_stride elements from one token to the next (multiples of 16
+ * bytes, at least heads * head_dim), so they may be parts of one fused
+ * projection.  q_out: [num_tokens][num_q_heads][head_dim], contiguous; it may be
+ * q itself when q is contiguous, and overlaps nothing else.  num_q_heads may be
+ * 0 (keys and values only; q and q_out are not read).  cos_sin: fp32
+ * [max_position][rot_dim].  rot_dim: a multiple of 16, of 32 for 4-bit pools,
+ * at most head_dim.  head_dim 64 or 128, block_size 16 or 32.
+ *
+ * A token with a negative slot is padding: its position is not looked at and
+ * nothing of it is written, q_out included.  A slot past the pool sets
+ * PA_DEV_BAD_SLOT, a position outside [0, max_position) PA_DEV_BAD_POSITION, and
+ * the token is skipped.  Slots of one call must be distinct.  Asynchronous on
+ * `stream`.  Allocates nothing.  A decode call that follows on the stream may
+ * start its prologue early, as after pa_reshape_and_cache.
+ */
+pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                            int32_t max_position, int32_t rot_dim, int32_t interleaved, void* k_pool, void* v_pool,
+                            const int64_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                            pa_dtype in_dtype, pa_dtype pool_dtype, float k_scale, float v_scale,
+                            int32_t* dev_status, void* stream);
+
+/*
  * Swap a preempted sequence's blocks out to a block store and back
  * (data.6616ai.com "PagedAttention 之外": KV swapped to CPU memory under
  * memory pressure and restored to resume).
  *
  * pa_swap_out: for i < num, store[i] = pool[blocks[i]] over the whole block
  * (every KV head, all block_size slots, all of head_dim), K and V.  Any pool
- * dtype, FP8 included (pa_copy_blocks likewise).
+ * dtype, FP8 and 4-bit included (pa_copy_blocks likewise).
  * pa_swap_in:  for i < num, pool[blocks[i]] = store[i].  Bit-exact.
  * The stores are [num][num_kv_heads][block_size][head_dim] in the pools'
  * dtype and may be pinned host memory (cudaHostAlloc / pinned tensors): the

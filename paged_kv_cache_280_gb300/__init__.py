@@ -22,8 +22,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
-PA_DEV_BAD_BLOCK_ID, PA_DEV_BAD_SLOT, PA_DEV_BAD_SEQ_LEN, PA_DEV_WAIT_TIMEOUT = 1, 2, 4, 8
+PA_F32, PA_BF16, PA_FP8_E4M3, PA_FP4_E2M1 = 0, 1, 2, 3
+PA_DEV_BAD_BLOCK_ID, PA_DEV_BAD_SLOT, PA_DEV_BAD_SEQ_LEN, PA_DEV_WAIT_TIMEOUT, PA_DEV_BAD_POSITION = 1, 2, 4, 8, 16
 STATUS_NAMES = {
     0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_OUT_OF_BLOCKS",
     4: "PA_ERR_NO_SUCH_SEQ", 5: "PA_ERR_SEQ_EXISTS", 6: "PA_ERR_REFCOUNT_LIMIT",
@@ -78,6 +78,18 @@ _SIGS = {
                                         ctypes.c_float, _vp, _vp]),
     "pa_decode_attention_fp8": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _i32, _vp, _i32,
                                        _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _i32, _vp, _sz, _vp]),
+    "pa_reshape_and_cache_fp4": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                        ctypes.c_float, _vp, _vp]),
+    "pa_unpack_blocks_fp4": (_i32, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                    ctypes.c_float, _vp, _vp]),
+    "pa_decode_attention_fp4": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _i32, _vp, _i32, _i32,
+                                       _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _i32, _vp, _sz, _vp]),
+    "pa_decode_attention_fp4_planned": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _i32, _vp,
+                                               _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _i32, _vp,
+                                               _sz, _vp, _sz, _vp]),
+    "pa_rope_and_cache": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                 _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float, _vp,
+                                 _vp]),
     "pa_prefill_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                     _i32, _i32, ctypes.c_float, _i32, _vp, _vp]),
     "pa_decode_set_ctas_per_sm": (_i32, [_i32]),
@@ -167,6 +179,56 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def fp4_block_bytes(head_dim: int, block_size: int) -> int:
+    """Bytes of one (block, KV head) record of a 4-bit pool: codes, then a scale byte per 16 elements."""
+    return block_size * (head_dim // 2 + head_dim // 16)
+
+
+def _pool_shape(pool):
+    """(num_blocks, Hkv, block_size, head_dim, dtype code) of a pool; a 4-bit pool is uint8
+    [num_blocks][Hkv][fp4_block_bytes], whose byte count is all that whole-block copies need."""
+    if pool.dim() == 4:
+        return (*pool.shape, _dtype_code(pool))
+    torch = _torch()
+    if pool.dim() == 3 and pool.dtype == torch.uint8:
+        for d in (128, 64):
+            for bs in (16, 32):
+                if pool.shape[2] == fp4_block_bytes(d, bs):
+                    return pool.shape[0], pool.shape[1], bs, d, PA_FP4_E2M1
+    raise PAError(2, f"pool of shape {tuple(pool.shape)} and dtype {pool.dtype}")
+
+
+def _fp4_block_size(pool, head_dim: int, name: str) -> int:
+    """The block size of a 4-bit pool whose rows hold head_dim elements."""
+    torch = _torch()
+    if pool.dtype != torch.uint8 or pool.dim() != 3:
+        raise PAError(1, f"{name}: a 4-bit pool is uint8 [num_blocks][Hkv][bytes]")
+    row = fp4_block_bytes(head_dim, 1)
+    if row <= 0 or pool.shape[2] % row:
+        raise PAError(1, f"{name}: {pool.shape[2]} bytes are no whole rows of {head_dim} elements")
+    return pool.shape[2] // row
+
+
+def _same_device(*tensors) -> None:
+    """The library launches on the current device: refuse tensors that live on another one."""
+    torch = _torch()
+    here = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.get_device() != here:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{here}")
+
+
+def _want(t, dtype, shape, name: str) -> None:
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise PAError(1, f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+
+
 def pa_reshape_and_cache(k_new, v_new, k_pool, v_pool, slot_mapping, status=None, stream=None):
     """k_new/v_new [N][Hkv][D]; pools [num_blocks][Hkv][bs][D]; slot_mapping int64 [N]."""
     nb, hkv, bs, d = k_pool.shape
@@ -179,10 +241,10 @@ def pa_reshape_and_cache(k_new, v_new, k_pool, v_pool, slot_mapping, status=None
 
 def pa_copy_blocks(k_pool, v_pool, src_dst_pairs, status=None, stream=None):
     """src_dst_pairs int32 [n][2] on the device."""
-    nb, hkv, bs, d = k_pool.shape
+    nb, hkv, bs, d, dt = _pool_shape(k_pool)
     n = src_dst_pairs.shape[0]
     _ok(_lib.pa_copy_blocks(_dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"),
-                            _dev_ptr(src_dst_pairs, "src_dst_pairs"), n, hkv, d, bs, nb, _dtype_code(k_pool),
+                            _dev_ptr(src_dst_pairs, "src_dst_pairs"), n, hkv, d, bs, nb, dt,
                             _dev_ptr(status, "status"), _stream(stream)),
         "pa_copy_blocks")
 
@@ -311,22 +373,128 @@ def pa_decode_attention_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tabl
                                                  _stream(stream)), "pa_decode_attention_fp8_planned")
 
 
+def pa_reshape_and_cache_fp4(k_new, v_new, k_pool, v_pool, slot_mapping, k_scale, v_scale, status=None, stream=None):
+    """Slot-mapped append into 4-bit pools (uint8 [num_blocks][Hkv][fp4_block_bytes(D, bs)]) of bf16/fp32 K/V
+    [N][Hkv][D]; slot_mapping int64 [N]."""
+    torch = _torch()
+    n, hkv, d = k_new.shape
+    bs = _fp4_block_size(k_pool, d, "pa_reshape_and_cache_fp4")
+    nb = k_pool.shape[0]
+    _same_device(k_new, v_new, k_pool, v_pool, slot_mapping, status)
+    _want(v_new, k_new.dtype, (n, hkv, d), "v_new")
+    _want(k_pool, torch.uint8, (nb, hkv, k_pool.shape[2]), "k_pool")
+    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
+    _want(slot_mapping, torch.int64, (n,), "slot_mapping")
+    _ok(_lib.pa_reshape_and_cache_fp4(_dev_ptr(k_new, "k_new"), _dev_ptr(v_new, "v_new"), _dev_ptr(k_pool, "k_pool"),
+                                      _dev_ptr(v_pool, "v_pool"), _dev_ptr(slot_mapping, "slot_mapping"), n, hkv, d, bs,
+                                      nb, _dtype_code(k_new), float(k_scale), float(v_scale), _dev_ptr(status, "status"),
+                                      _stream(stream)),
+        "pa_reshape_and_cache_fp4")
+
+
+def pa_unpack_blocks_fp4(k_pool, v_pool, blocks, k_out, v_out, k_scale, v_scale, status=None, stream=None):
+    """out[i] = the values of block blocks[i] (int32 [n]) of 4-bit pools; k_out/v_out [n][Hkv][bs][D] bf16 or fp32,
+    which pa_prefill_attention takes as pools (block table 0 .. n - 1)."""
+    torch = _torch()
+    n, hkv, bs, d = k_out.shape
+    nb = k_pool.shape[0]
+    _same_device(k_pool, v_pool, blocks, k_out, v_out, status)
+    _want(v_out, k_out.dtype, k_out.shape, "v_out")
+    _want(k_pool, torch.uint8, (nb, hkv, fp4_block_bytes(d, bs)), "k_pool")
+    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
+    _want(blocks, torch.int32, (n,), "blocks")
+    _ok(_lib.pa_unpack_blocks_fp4(_dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"), _dev_ptr(blocks, "blocks"), n,
+                                  _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"), hkv, d, bs, nb,
+                                  _dtype_code(k_out), float(k_scale), float(v_scale), _dev_ptr(status, "status"),
+                                  _stream(stream)),
+        "pa_unpack_blocks_fp4")
+
+
+def pa_decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, max_seq_len, scale,
+                            workspace, partition_tokens=0, stream=None, plan=None):
+    """Decode over 4-bit pools with bf16 q/out [B][Hq][D].  plan: as for pa_decode_attention (built with dtype
+    PA_FP4_E2M1)."""
+    torch = _torch()
+    b, hq, d = q.shape
+    bs = _fp4_block_size(k_pool, d, "pa_decode_attention_fp4")
+    nb, hkv = k_pool.shape[:2]
+    _same_device(out, q, k_pool, v_pool, block_tables, seq_lens, workspace, plan)
+    _want(q, torch.bfloat16, (b, hq, d), "q")
+    _want(out, torch.bfloat16, (b, hq, d), "out")
+    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
+    _want(block_tables, torch.int32, (b, block_tables.shape[1]), "block_tables")
+    _want(seq_lens, torch.int32, (b,), "seq_lens")
+    args = [_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"),
+            float(k_scale), float(v_scale), _dev_ptr(block_tables, "block_tables"), block_tables.shape[1],
+            _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), b, hq, hkv, d, bs, nb, float(scale),
+            int(partition_tokens), _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()]
+    if plan is None:
+        _ok(_lib.pa_decode_attention_fp4(*args, _stream(stream)), "pa_decode_attention_fp4")
+    else:
+        _ok(_lib.pa_decode_attention_fp4_planned(*args, _dev_ptr(plan, "plan"), plan.numel() * plan.element_size(),
+                                                 _stream(stream)), "pa_decode_attention_fp4_planned")
+
+
+def _token_rows(t, name: str) -> int:
+    """Elements from one token to the next of a [N][H][D] tensor whose heads are contiguous within a token."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_mapping, interleaved=False, k_scale=1.0,
+                      v_scale=1.0, status=None, stream=None):
+    """Turn q and k by their positions (rotary embedding), write q to q_out and append k and v at their slots.
+
+    q/k/v [N][H][D] bf16 or fp32, each token's heads contiguous (they may be parts of one fused projection); q_out
+    [N][Hq][D] (may be q itself; None with q None: keys and values only); positions int32 [N]; cos_sin fp32
+    [max_position][rot_dim] (cos, then sin); pools of k's dtype or FP8 codes [num_blocks][Hkv][bs][D], or 4-bit
+    [num_blocks][Hkv][fp4_block_bytes(D, bs)]; slot_mapping int64 [N], negative = padding."""
+    torch = _torch()
+    n, hkv, d = k.shape
+    hq = 0 if q is None else q.shape[1]
+    if k_pool.dim() == 3:
+        bs, pool_dtype = _fp4_block_size(k_pool, d, "pa_rope_and_cache"), PA_FP4_E2M1
+        _want(k_pool, torch.uint8, (k_pool.shape[0], hkv, k_pool.shape[2]), "k_pool")
+    else:
+        bs, pool_dtype = k_pool.shape[2], _dtype_code(k_pool)
+        _want(k_pool, k_pool.dtype, (k_pool.shape[0], hkv, bs, d), "k_pool")
+    _same_device(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_mapping, status)
+    _want(v, k.dtype, (n, hkv, d), "v")
+    _want(q, k.dtype, (n, hq, d), "q")
+    if (q is None) != (q_out is None):
+        raise PAError(1, "pa_rope_and_cache: q and q_out go together")
+    _want(q_out, k.dtype, (n, hq, d), "q_out")
+    _want(v_pool, k_pool.dtype, k_pool.shape, "v_pool")
+    _want(positions, torch.int32, (n,), "positions")
+    _want(slot_mapping, torch.int64, (n,), "slot_mapping")
+    _want(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
+    _ok(_lib.pa_rope_and_cache(_dev_ptr(q_out, "q_out"), None if q is None else q.data_ptr(),
+                               0 if q is None else _token_rows(q, "q"), k.data_ptr(), _token_rows(k, "k"), v.data_ptr(),
+                               _token_rows(v, "v"), _dev_ptr(positions, "positions"), _dev_ptr(cos_sin, "cos_sin"),
+                               cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), _dev_ptr(k_pool, "k_pool"),
+                               _dev_ptr(v_pool, "v_pool"), _dev_ptr(slot_mapping, "slot_mapping"), n, hq, hkv, d, bs,
+                               k_pool.shape[0], _dtype_code(k), pool_dtype, float(k_scale), float(v_scale),
+                               _dev_ptr(status, "status"), _stream(stream)),
+        "pa_rope_and_cache")
+
+
 def pa_swap_out(k_pool, v_pool, blocks, k_store, v_store, status=None, stream=None):
     """store[i] = pool[blocks[i]] (whole blocks, K and V).  Stores [n][Hkv][bs][D] and blocks int32 [n] may be
     CUDA tensors or pinned host tensors."""
-    nb, hkv, bs, d = k_pool.shape
+    nb, hkv, bs, d, dt = _pool_shape(k_pool)
     _ok(_lib.pa_swap_out(_dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"), _acc_ptr(blocks, "blocks"),
                          blocks.shape[0], _acc_ptr(k_store, "k_store"), _acc_ptr(v_store, "v_store"), hkv, d, bs, nb,
-                         _dtype_code(k_pool), _dev_ptr(status, "status"), _stream(stream)),
+                         dt, _dev_ptr(status, "status"), _stream(stream)),
         "pa_swap_out")
 
 
 def pa_swap_in(k_store, v_store, blocks, k_pool, v_pool, status=None, stream=None):
     """pool[blocks[i]] = store[i] (whole blocks, K and V); the inverse of pa_swap_out."""
-    nb, hkv, bs, d = k_pool.shape
+    nb, hkv, bs, d, dt = _pool_shape(k_pool)
     _ok(_lib.pa_swap_in(_acc_ptr(k_store, "k_store"), _acc_ptr(v_store, "v_store"), _acc_ptr(blocks, "blocks"),
                         blocks.shape[0], _dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"), hkv, d, bs, nb,
-                        _dtype_code(k_pool), _dev_ptr(status, "status"), _stream(stream)),
+                        dt, _dev_ptr(status, "status"), _stream(stream)),
         "pa_swap_in")
 
 

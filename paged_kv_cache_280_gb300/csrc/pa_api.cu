@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstring>
 #include <mutex>
 #include <vector>
 
@@ -237,6 +238,10 @@ pa_status check_shapes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_hea
     return PA_OK;
 }
 
+bool pool_dtype_ok(pa_dtype dtype) {
+    return dtype == PA_F32 || dtype == PA_BF16 || dtype == PA_FP8_E4M3 || dtype == PA_FP4_E2M1;
+}
+
 // Picks the compiled variant, the build and the grid for these shapes on the current device.
 struct LaunchPlan {
     DecodeVariant v;
@@ -258,11 +263,13 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
     int dev = 0;
     if (!current_device(&dev, &lp->sms)) return PA_ERR_CUDA;
     const int G = num_q_heads / num_kv_heads;
-    // dtype is the pool's: PA_FP8_E4M3 pools pair with bf16 queries and always take the
+    // dtype is the pool's: FP8 and 4-bit pools pair with bf16 queries and always take the
     // tensor cores (their codes are widened in registers); bf16 does for 4+ query heads
-    lp->mma = (dtype == PA_BF16 && G >= 4) || dtype == PA_FP8_E4M3;
+    const bool quantised = dtype == PA_FP8_E4M3 || dtype == PA_FP4_E2M1;
+    lp->mma = (dtype == PA_BF16 && G >= 4) || quantised;
     bool found = dtype == PA_F32         ? decode_variant_f32(head_dim, block_size, G, &lp->v)
                  : dtype == PA_FP8_E4M3 ? decode_variant_fp8(head_dim, block_size, G, &lp->v)
+                 : dtype == PA_FP4_E2M1 ? decode_variant_fp4(head_dim, block_size, G, &lp->v)
                  : lp->mma              ? decode_variant_bf16_mma(head_dim, block_size, &lp->v)
                                         : decode_variant_bf16_fma(head_dim, block_size, G, &lp->v);
     if (!found) return PA_ERR_UNSUPPORTED;
@@ -328,17 +335,18 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
                             (int64_t)mk.per_sm * (mk.smem + 1024) + lp->merge_smem + 1024 <= 228 * 1024;
     const int64_t segments = (int64_t)num_seqs * num_kv_heads;
     const int mode = g_merge_mode.load();
-    const bool auto_in_kernel = dtype != PA_FP8_E4M3 && (2 * segments >= 3 * in.grid || !merge_fits);
+    const bool auto_in_kernel = !quantised && (2 * segments >= 3 * in.grid || !merge_fits);
     lp->merge_in_kernel = lp->v.merge_in_kernel_ok && (mode == 1 || (mode == 0 && !fixed && auto_in_kernel));
     const DecodeBuild& b = lp->merge_in_kernel ? lp->v.in : lp->v.mk;
     const Shape& sh = lp->merge_in_kernel ? in : mk;
     const int su = g_seg_units.load();
     lp->seg_units = su > 0                     ? su
                     : dtype == PA_FP8_E4M3     ? PA_SEG_UNITS_FP8
+                    : dtype == PA_FP4_E2M1     ? PA_SEG_UNITS_FP4
                     : lp->mma                  ? PA_SEG_UNITS_MMA
                                                : PA_SEG_UNITS_FMA;
     const int ws = g_wave_skew.load();
-    lp->wave_skew = ws >= 0 ? ws : dtype == PA_FP8_E4M3 ? PA_WAVE_SKEW_FP8 : 0;
+    lp->wave_skew = ws >= 0 ? ws : dtype == PA_FP8_E4M3 ? PA_WAVE_SKEW_FP8 : dtype == PA_FP4_E2M1 ? PA_WAVE_SKEW_FP4 : 0;
     lp->smem = sh.smem;
     lp->grid = sh.grid;
     lp->stages = b.stages;
@@ -431,7 +439,7 @@ extern "C" pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads
                                            int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
                                            int32_t partition_tokens, pa_dtype dtype, int32_t* ctas,
                                            int32_t* stages, int32_t* smem_bytes, int32_t* uses_mma) {
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
     if (max_blocks_per_seq <= 0 || partition_tokens < 0 || partition_tokens % block_size) return PA_ERR_INVALID_ARG;
@@ -449,7 +457,7 @@ extern "C" pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads
 extern "C" pa_status pa_decode_kernels_per_call(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                                 int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
                                                 int32_t partition_tokens, pa_dtype dtype, int32_t* kernels) {
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     if (!kernels) return PA_ERR_INVALID_ARG;
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
@@ -474,7 +482,7 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
                         int32_t num_blocks, float scale, int32_t partition_tokens, void* workspace,
                         size_t workspace_bytes, pa_dtype dtype, float k_scale, float v_scale, void* stream,
                         bool clear_status, const void* plan, size_t plan_bytes) {
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
     if (dtype == PA_FP8_E4M3 && head_dim != 128) return PA_ERR_UNSUPPORTED;  // a pool row fills one 128-byte panel
@@ -509,9 +517,13 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     CUtensorMap tk, tv;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-    if (!pool_map(&tk, dev, k_pool, rows, head_dim, block_size, dtype) ||
-        !pool_map(&tv, dev, v_pool, rows, head_dim, block_size, dtype))
+    if (dtype == PA_FP4_E2M1) {
+        memset(&tk, 0, sizeof tk);  // not read: its tiles are contiguous records
+        memset(&tv, 0, sizeof tv);
+    } else if (!pool_map(&tk, dev, k_pool, rows, head_dim, block_size, dtype) ||
+               !pool_map(&tv, dev, v_pool, rows, head_dim, block_size, dtype)) {
         return PA_ERR_CUDA;
+    }
 
     DecodeParams p;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -540,6 +552,8 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     p.wait_limit_ns = lim ? lim : kWaitLimitNs;
     p.merge_in_kernel = lp.merge_in_kernel ? 1 : 0;
     p.plan = static_cast<const int32_t*>(plan);
+    p.k_pool = static_cast<const uint8_t*>(k_pool);
+    p.v_pool = static_cast<const uint8_t*>(v_pool);
     if (clear_status && cudaMemsetAsync(workspace, 0, wl.partials_off, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PA_ERR_CUDA;
     lp.v.launch(p, tk, tv, lp.grid, lp.smem, lp.merge_grid, lp.merge_smem, static_cast<cudaStream_t>(stream));
@@ -572,13 +586,25 @@ extern "C" pa_status pa_decode_attention_fp8(void* out, const void* q, const voi
                              workspace, workspace_bytes, PA_FP8_E4M3, k_scale, v_scale, stream, false);
 }
 
+extern "C" pa_status pa_decode_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                             float k_scale, float v_scale, const int32_t* block_tables,
+                                             int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                             int32_t max_seq_len, int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                             int32_t num_blocks, float scale, int32_t partition_tokens,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    return pa::decode_common(out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
+                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, partition_tokens,
+                             workspace, workspace_bytes, PA_FP4_E2M1, k_scale, v_scale, stream, false);
+}
+
 namespace {
 
 // The launch a decode call with these arguments makes: its length bound, plan and grid.
 pa_status decode_shape(int32_t max_blocks_per_seq, int32_t max_seq_len, int32_t num_seqs, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t partition_tokens,
                        pa_dtype dtype, int32_t* max_len_out, LaunchPlan* lp) {
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
     if (dtype == PA_FP8_E4M3 && head_dim != 128) return PA_ERR_UNSUPPORTED;
@@ -711,5 +737,21 @@ extern "C" pa_status pa_decode_attention_fp8_planned(void* out, const void* q, c
     return pa::decode_common(out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
                              num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, partition_tokens,
                              workspace, workspace_bytes, PA_FP8_E4M3, k_scale, v_scale, stream, false, plan,
+                             plan_bytes);
+}
+
+extern "C" pa_status pa_decode_attention_fp4_planned(void* out, const void* q, const void* k_pool,
+                                                     const void* v_pool, float k_scale, float v_scale,
+                                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                     const int32_t* seq_lens, int32_t max_seq_len, int32_t num_seqs,
+                                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                     int32_t block_size, int32_t num_blocks, float scale,
+                                                     int32_t partition_tokens, void* workspace,
+                                                     size_t workspace_bytes, const void* plan, size_t plan_bytes,
+                                                     void* stream) {
+    if (!plan) return PA_ERR_INVALID_ARG;
+    return pa::decode_common(out, q, k_pool, v_pool, block_tables, max_blocks_per_seq, seq_lens, max_seq_len, num_seqs,
+                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, partition_tokens,
+                             workspace, workspace_bytes, PA_FP4_E2M1, k_scale, v_scale, stream, false, plan,
                              plan_bytes);
 }

@@ -155,6 +155,20 @@ static bool shape_ok(int32_t head_dim, int32_t block_size) {
     return (head_dim == 64 || head_dim == 128) && (block_size == 16 || block_size == 32);
 }
 
+static bool pool_dtype_ok(pa_dtype dtype) {
+    return dtype == PA_F32 || dtype == PA_BF16 || dtype == PA_FP8_E4M3 || dtype == PA_FP4_E2M1;
+}
+
+// 16-byte chunks of one whole block (every KV head) of a pool.
+static int64_t block_chunks_of(pa_dtype dtype, int32_t num_kv_heads, int32_t block_size, int32_t head_dim) {
+    const int64_t rows = (int64_t)num_kv_heads * block_size;
+    const int64_t row_bytes = dtype == PA_F32    ? head_dim * 4
+                              : dtype == PA_BF16 ? head_dim * 2
+                              : dtype == PA_FP8_E4M3 ? head_dim
+                                                     : head_dim / 2 + head_dim / 16;  // a block and head is a multiple of 64 bytes
+    return rows * row_bytes / 16;
+}
+
 }  // namespace pa
 
 extern "C" pa_status pa_reshape_and_cache(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
@@ -189,7 +203,7 @@ extern "C" pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* s
                                     pa_dtype dtype, int32_t* dev_status, void* stream) {
     using namespace pa;
     if (num_pairs < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     if (!shape_ok(head_dim, block_size) || (dtype == PA_FP8_E4M3 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PA_OK;
     if (num_pairs > 65535) return PA_ERR_UNSUPPORTED;  // one grid row per pair
@@ -197,8 +211,7 @@ extern "C" pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* s
     if (!aligned16(k_pool) || !aligned16(v_pool) || (reinterpret_cast<uintptr_t>(src_dst_pairs) & 3u) ||
         (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
-    const int elem = dtype == PA_F32 ? 4 : (dtype == PA_BF16 ? 2 : 1);
-    const int64_t block_chunks = (int64_t)num_kv_heads * block_size * head_dim * elem / 16;
+    const int64_t block_chunks = block_chunks_of(dtype, num_kv_heads, block_size, head_dim);
     int64_t slices = (block_chunks + 256 * 4 - 1) / (256 * 4);  // ~4 chunks per thread
     if (slices < 1) slices = 1;
     if (slices > 1024) slices = 1024;
@@ -215,7 +228,7 @@ static pa_status swap_blocks(bool out, void* k_pool, void* v_pool, const int32_t
                              void* v_store, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                              int32_t num_blocks, pa_dtype dtype, int32_t* dev_status, void* stream) {
     if (n < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
-    if (dtype != PA_F32 && dtype != PA_BF16 && dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+    if (!pool_dtype_ok(dtype)) return PA_ERR_UNSUPPORTED;
     if (!shape_ok(head_dim, block_size) || (dtype == PA_FP8_E4M3 && head_dim != 128)) return PA_ERR_UNSUPPORTED;
     if (n == 0) return PA_OK;
     if (n > 65535) return PA_ERR_UNSUPPORTED;  // one grid row per block
@@ -223,8 +236,7 @@ static pa_status swap_blocks(bool out, void* k_pool, void* v_pool, const int32_t
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_store) || !aligned16(v_store) ||
         (reinterpret_cast<uintptr_t>(blocks) & 3u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
-    const int elem = dtype == PA_F32 ? 4 : (dtype == PA_BF16 ? 2 : 1);
-    const int64_t block_chunks = (int64_t)num_kv_heads * block_size * head_dim * elem / 16;
+    const int64_t block_chunks = block_chunks_of(dtype, num_kv_heads, block_size, head_dim);
     int64_t slices = (block_chunks + 256 * 4 - 1) / (256 * 4);  // ~4 chunks per thread
     if (slices < 1) slices = 1;
     if (slices > 1024) slices = 1024;

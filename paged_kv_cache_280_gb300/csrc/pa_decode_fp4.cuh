@@ -1,0 +1,336 @@
+// Softmax state of a decode consumer warp over a 4-bit pool (format: pa_fp4.cuh), on the tensor cores
+// (mma.sync m16n8k16, f16 operands, fp32 sums).
+//
+// The bound.  A token row of one KV head is 9/16 D bytes of K and the same of V (144 bytes at D = 128),
+// and every code has to become an f16 in registers: at the measured HBM rate an SM receives a token
+// row pair every 6 cycles, so the consumer has about 25 issue slots for its 2 D elements, 8 per lane.
+// The fragments are laid out so that an element costs one half of a conversion and one half of a
+// multiplication by its group's scale, which is exact in f16, and nothing is moved between lanes:
+//  - S^T = K q^T, 16 tokens x 8 heads.  Lane (g, c) = (lane / 4, lane % 4) reads D / 4 consecutive
+//    dims of its two token rows at once (16 bytes at D = 128: two scale groups).  The order of a dot
+//    product's terms is free, so k-step j takes each lane's dims 4 j .. 4 j + 3 and q's fragments
+//    hold the same dims.
+//  - O^T = V^T P^T, 16 dims x 8 heads.  Lane (g, c) reads the D / 8 dims from D / 8 g of its four
+//    tokens (at D = 128 one scale group).  A nibble merge of two tokens' words pairs the tokens of
+//    each dim, which a conversion turns into the f16 pair of an A operand; m16 block i holds dims
+//    2 i (row g) and 2 i + 1 (row g + 8) of each lane's run, which the stores undo.
+//  - Tokens: the 16 slots of a step are permuted so that the row reads of S spread over the
+//    shared-memory banks and those of V over half of them (slot_token below).
+//  - The row sums l come from one more MMA, whose A operand is all ones: they are sums of the rounded
+//    weights that P V uses, and need no reduction over lanes.
+// Slots past the sequence's end may hold any bits: their scores become -inf, and their V rows get
+// scale 0 (codes are always finite), so neither reaches the output.
+#pragma once
+
+#include "pa_fp4.cuh"
+
+namespace pa {
+
+struct Fp4 {};  // the pool type tag of the decode templates
+
+__device__ __forceinline__ float ex2_approx(float x) {  // 2^x, 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Two E4M3 bytes (low byte first) to an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(b));
+    return d;
+}
+// The eight codes of w to four f16 pairs: byte i to r[i], the byte's low code in the low half.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t f16x2_low_twice(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
+__device__ __forceinline__ uint32_t f16x2_high_twice(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
+
+// N consecutive 32-bit words of shared memory (N = 1, 2 or 4, naturally aligned).
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+template <int D, int BS>
+struct Fp4State {
+    static constexpr int MT = D / 16;       // m16 blocks of O^T, and 16-dim k-steps of S
+    static constexpr int KW = D / 32;       // words of a lane's part of a K row (D / 4 dims)
+    static constexpr int VW = D / 64;       // words of a lane's part of a V row (D / 8 dims)
+    static constexpr int kScalesOff = BS * (D / 2);  // the tile's scale bytes
+    static constexpr int kSteps = 4;        // 16-token steps of a full stage
+    uint32_t qb[MT][2];  // B fragments of q^T per k-step, rows scaled by a power of two
+    float sc[2];         // score scale (base 2) of heads 2c and 2c + 1, the power of two undone
+    float m[2];          // running max of heads 2c, 2c + 1
+    float l[4];          // running sums: [0], [1] of heads 2c, 2c + 1 (the same in every g; [2], [3] repeat them)
+    float o[MT][4];
+
+    // token of slot r (0..7) of a step; slot r + 8 holds token + 8
+    __device__ static __forceinline__ int slot_token(int r) { return 4 * (r & 1) + ((r >> 1) ^ (r & 1)); }
+    // token of the i-th (0..3) of the slots 2c, 2c + 1, 2c + 8, 2c + 9 of lane c: slot_token in c's terms
+    __device__ static __forceinline__ int lane_token(int c, int i) { return 4 * i + (c ^ (i & 1)); }
+
+    __device__ __forceinline__ void reset() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = l[2] = l[3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+
+    // f16 holds a bf16 value exactly while it is neither above 65504 nor far below 2^-14, so each row is
+    // scaled by the power of two that brings its largest element to [1, 2): a smaller element loses
+    // less than 2^-25 of that one, and any bf16 magnitudes are in range.
+    __device__ __forceinline__ void load_q(const uint8_t* qslot, int G, int lane, float scale_log2) {
+        const int g = lane >> 2, c = lane & 3;
+        float x[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            if (g < G) {
+                load8(reinterpret_cast<const __nv_bfloat16*>(qslot) + g * D + c * (D / 4) + 8 * i, x + 8 * i);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[8 * i + e] = 0.f;
+            }
+        }
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) a = fmaxf(a, fabsf(x[i]));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const int e = min(max((int)(__float_as_uint(a) >> 23), 1), 253);
+        const float f = __uint_as_float((uint32_t)(254 - e) << 23), inv = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            qb[j][0] = pack_f16x2(x[4 * j] * f, x[4 * j + 1] * f);
+            qb[j][1] = pack_f16x2(x[4 * j + 2] * f, x[4 * j + 3] * f);
+        }
+        sc[0] = scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c);
+        sc[1] = scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
+    }
+
+    // S^T of the 16 tokens from row row0 of the tile at kbase: (slot g, head 2c), (g, 2c + 1),
+    // (g + 8, 2c), (g + 8, 2c + 1).
+    __device__ __forceinline__ void scores(uint32_t kbase, int row0, int lane, float (&acc)[4]) const {
+        const int g = lane >> 2, c = lane & 3;
+        const int row = row0 + slot_token(g);
+        uint32_t w0[KW], w1[KW];
+        lds_words<KW>(kbase + row * (D / 2) + c * (D / 8), w0);
+        lds_words<KW>(kbase + (row + 8) * (D / 2) + c * (D / 8), w1);
+        const uint32_t sa = kbase + kScalesOff + row * (D / 16) + c * (D / 64);
+        uint32_t s0[2], s1[2];  // the lane's scale groups of each row, twice in a pair
+        if constexpr (D == 128) {
+            const uint32_t p0 = e4m3x2_to_f16x2(lds_u16(sa)), p1 = e4m3x2_to_f16x2(lds_u16(sa + 8 * (D / 16)));
+            s0[0] = f16x2_low_twice(p0), s0[1] = f16x2_high_twice(p0);
+            s1[0] = f16x2_low_twice(p1), s1[1] = f16x2_high_twice(p1);
+        } else {
+            s0[0] = s0[1] = f16x2_low_twice(e4m3x2_to_f16x2(lds_u8(sa)));
+            s1[0] = s1[1] = f16x2_low_twice(e4m3x2_to_f16x2(lds_u8(sa + 8 * (D / 16))));
+        }
+        float acc2[4] = {0.f, 0.f, 0.f, 0.f};  // two independent chains over the k-steps
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            uint32_t x0[4], x1[4];
+            e2m1x8_to_f16x2(w0[w], x0);
+            e2m1x8_to_f16x2(w1[w], x1);
+            const uint32_t k0 = s0[w / 2], k1 = s1[w / 2];  // 16 dims: two words to a group
+            mma_f16_16816(acc, mul_f16x2(x0[0], k0), mul_f16x2(x1[0], k1), mul_f16x2(x0[1], k0), mul_f16x2(x1[1], k1),
+                          qb[2 * w][0], qb[2 * w][1]);
+            mma_f16_16816(acc2, mul_f16x2(x0[2], k0), mul_f16x2(x1[2], k1), mul_f16x2(x0[3], k0), mul_f16x2(x1[3], k1),
+                          qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += acc2[i];
+    }
+
+    // O^T += V^T P^T and l += sum P of the 16 tokens from row row0 of the tile at vbase; MASK: only the
+    // first `valid` of them exist.
+    template <bool MASK>
+    __device__ __forceinline__ void accumulate_pv(uint32_t vbase, int row0, int valid, uint32_t b0, uint32_t b1, int lane) {
+        const int g = lane >> 2, c = lane & 3;
+        uint32_t v[4][VW], sb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = lane_token(c, i);
+            lds_words<VW>(vbase + (row0 + t) * (D / 2) + g * (D / 16), v[i]);
+            sb[i] = lds_u8(vbase + kScalesOff + (row0 + t) * (D / 16) + (D == 128 ? g : g >> 1));
+            if (MASK && t >= valid) sb[i] = 0;
+        }
+        const uint32_t s01 = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8)), s23 = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+        constexpr uint32_t kOnes = 0x3c003c00u, kLow = 0x0f0f0f0fu;
+        mma_f16_16816(l, kOnes, kOnes, kOnes, kOnes, b0, b1);
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            uint32_t even01[4], odd01[4], even23[4], odd23[4];
+            e2m1x8_to_f16x2((v[0][w] & kLow) | ((v[1][w] & kLow) << 4), even01);
+            e2m1x8_to_f16x2(((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow), odd01);
+            e2m1x8_to_f16x2((v[2][w] & kLow) | ((v[3][w] & kLow) << 4), even23);
+            e2m1x8_to_f16x2(((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow), odd23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_f16_16816(o[4 * w + i], mul_f16x2(even01[i], s01), mul_f16x2(odd01[i], s01), mul_f16x2(even23[i], s23),
+                              mul_f16x2(odd23[i], s23), b0, b1);
+        }
+    }
+
+    // N 16-token steps (step s: K rows kt[s], V rows vt[s], both from row r[s]) with one softmax update.
+    // MASK (N = 1): only the first `valid` tokens exist (at least one).
+    template <int N, bool MASK>
+    __device__ __forceinline__ void steps(const uint32_t (&kt)[N], const uint32_t (&vt)[N], const int (&r)[N], int valid,
+                                          int lane) {
+        const int g = lane >> 2;
+        float x[N][4];
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+            scores(kt[s], r[s], lane, x[s]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[s][i] *= sc[i & 1];
+                if (MASK && slot_token(g) + 8 * (i >> 1) >= valid) x[s][i] = -INFINITY;
+            }
+        }
+        float n0 = m[0], n1 = m[1];
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+            n0 = fmaxf(n0, fmaxf(x[s][0], x[s][2]));
+            n1 = fmaxf(n1, fmaxf(x[s][1], x[s][3]));
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+        }
+        if (__any_sync(0xffffffffu, n0 != m[0] || n1 != m[1])) {  // some row max grew (or is not a number)
+            const float a0 = ex2_approx(m[0] - n0), a1 = ex2_approx(m[1] - n1);
+            l[0] *= a0, l[1] *= a1, l[2] *= a0, l[3] *= a1;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i][0] *= a0, o[i][1] *= a1, o[i][2] *= a0, o[i][3] *= a1;
+            m[0] = n0, m[1] = n1;
+        }
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+            const uint32_t p0 = pack_f16x2(ex2_approx(x[s][0] - n0), ex2_approx(x[s][1] - n1));
+            const uint32_t p1 = pack_f16x2(ex2_approx(x[s][2] - n0), ex2_approx(x[s][3] - n1));
+            accumulate_pv<MASK>(vt[s], r[s], valid, movmatrix_trans(p0), movmatrix_trans(p1), lane);
+        }
+    }
+
+    // The first `valid` tokens (1 .. 64) of a stage: tile t's K at kb + t * tile bytes, V at vb + t * tile bytes.
+    __device__ __forceinline__ void stage(uint32_t kb, uint32_t vb, int valid, int lane) {
+        constexpr int kTile = BS * fp4_row_bytes(D), kPer = BS / 16;  // 16-token steps per tile
+        if (valid == 16 * kSteps) {
+            uint32_t kt[kSteps], vt[kSteps];
+            int r[kSteps];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                kt[s] = kb + (s / kPer) * kTile;
+                vt[s] = vb + (s / kPer) * kTile;
+                r[s] = 16 * (s % kPer);
+            }
+            steps<kSteps, false>(kt, vt, r, 16, lane);
+        } else {
+            for (int s = 0; 16 * s < valid; ++s) {
+                const uint32_t kt[1] = {kb + (uint32_t)((s / kPer) * kTile)}, vt[1] = {vb + (uint32_t)((s / kPer) * kTile)};
+                const int r[1] = {16 * (s % kPer)};
+                steps<1, true>(kt, vt, r, min(16, valid - 16 * s), lane);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish() {}  // l is whole already
+
+    // This lane's state as 4 + 4 MT floats at scr[f * 32 + lane], and the merge of a saved state (other
+    // tokens of the same heads).  A side that saw no token has m = -inf and weighs 0.
+    __device__ __forceinline__ void save(float* scr, int lane) const {
+        scr[lane] = m[0];
+        scr[32 + lane] = m[1];
+        scr[64 + lane] = l[0];
+        scr[96 + lane] = l[1];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) scr[(4 + 4 * i + j) * 32 + lane] = o[i][j];
+    }
+    __device__ __forceinline__ void combine(const float* scr, int lane) {
+        const float om0 = scr[lane], om1 = scr[32 + lane];
+        const float n0 = fmaxf(m[0], om0), n1 = fmaxf(m[1], om1);
+        const float a0 = n0 == -INFINITY ? 0.f : ex2_approx(m[0] - n0), b0 = n0 == -INFINITY ? 0.f : ex2_approx(om0 - n0);
+        const float a1 = n1 == -INFINITY ? 0.f : ex2_approx(m[1] - n1), b1 = n1 == -INFINITY ? 0.f : ex2_approx(om1 - n1);
+        l[0] = l[0] * a0 + scr[64 + lane] * b0;
+        l[1] = l[1] * a1 + scr[96 + lane] * b1;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            o[i][0] = o[i][0] * a0 + scr[(4 + 4 * i) * 32 + lane] * b0;
+            o[i][1] = o[i][1] * a1 + scr[(5 + 4 * i) * 32 + lane] * b1;
+            o[i][2] = o[i][2] * a0 + scr[(6 + 4 * i) * 32 + lane] * b0;
+            o[i][3] = o[i][3] * a1 + scr[(7 + 4 * i) * 32 + lane] * b1;
+        }
+        m[0] = n0;
+        m[1] = n1;
+    }
+
+    // Normalised output rows (o_rows = out[b][h * G]): a lane holds D / 8 consecutive dims of its two heads.
+    __device__ __forceinline__ void store_out(__nv_bfloat16* o_rows, int G, int lane, float oscale) const {
+        const int g = lane >> 2, h0 = 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (h0 + j < G) {
+                const float r = oscale / l[j];
+                __nv_bfloat16* dst = o_rows + (h0 + j) * D + g * (D / 8);
+#pragma unroll
+                for (int i = 0; i < MT; i += 4)
+                    *reinterpret_cast<uint4*>(dst + 2 * i) =
+                        make_uint4(pack_bf16x2(o[i][j] * r, o[i][2 + j] * r), pack_bf16x2(o[i + 1][j] * r, o[i + 1][2 + j] * r),
+                                   pack_bf16x2(o[i + 2][j] * r, o[i + 2][2 + j] * r),
+                                   pack_bf16x2(o[i + 3][j] * r, o[i + 3][2 + j] * r));
+            }
+        }
+    }
+
+    // Unnormalised partial: slot = [G][D] o, then [G] (m, l).
+    __device__ __forceinline__ void store_partial(float* slot, int G, int lane) const {
+        const int g = lane >> 2, h0 = 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (h0 + j < G) {
+                float* dst = slot + (h0 + j) * D + g * (D / 8);
+#pragma unroll
+                for (int i = 0; i < MT; i += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[i][j], o[i][2 + j], o[i + 1][j], o[i + 1][2 + j]);
+                if (g == 0) {
+                    slot[G * D + 2 * (h0 + j)] = m[j];
+                    slot[G * D + 2 * (h0 + j) + 1] = l[j];
+                }
+            }
+        }
+    }
+};
+
+}  // namespace pa

@@ -45,6 +45,9 @@ constexpr int kTileUnits = 4;
 #ifndef PA_SEG_UNITS_FP8
 #define PA_SEG_UNITS_FP8 24
 #endif
+#ifndef PA_SEG_UNITS_FP4
+#define PA_SEG_UNITS_FP4 24
+#endif
 constexpr int kMaxSegUnits = 4096;  // bound of pa_debug_set_seg_units
 // Shares of the decode's CTAs by dispatch wave (the CTAs of a launch take the SMs in waves of one
 // per SM): wave v of NWV takes kWaveWeight + skew (NWV - 1 - 2 v) parts.  An SM's warp scheduler
@@ -54,6 +57,9 @@ constexpr int kMaxSegUnits = 4096;  // bound of pa_debug_set_seg_units
 constexpr int kWaveWeight = 64;
 #ifndef PA_WAVE_SKEW_FP8
 #define PA_WAVE_SKEW_FP8 2
+#endif
+#ifndef PA_WAVE_SKEW_FP4
+#define PA_WAVE_SKEW_FP4 2
 #endif
 
 struct DecodeParams {
@@ -93,6 +99,9 @@ struct DecodeParams {
     // a host-built plan of this launch in device memory (pa_plan.h), or null: the kernels then
     // scan the lengths and search the CTA ranges themselves
     const int32_t* plan;
+    // 4-bit pools are copied record by record instead of through tensor maps
+    const uint8_t* k_pool;
+    const uint8_t* v_pool;
 };
 
 // One compiled decode kernel (dtype, head_dim, block_size, compute path).
@@ -128,6 +137,8 @@ bool decode_variant_bf16_mma(int head_dim, int block_size, DecodeVariant* out);
 bool decode_variant_bf16_fma(int head_dim, int block_size, int group, DecodeVariant* out);
 // bf16 queries and outputs over FP8 (E4M3) pools, CUDA-core path.
 bool decode_variant_fp8(int head_dim, int block_size, int group, DecodeVariant* out);
+// bf16 queries and outputs over 4-bit pools, tensor-core path.
+bool decode_variant_fp4(int head_dim, int block_size, int group, DecodeVariant* out);
 
 // The decode of pa_decode_attention / _fp8 (pa_api.cu): checks, plan and launch.
 // Refuses a workspace smaller than the bytes its own grid touches (the status
