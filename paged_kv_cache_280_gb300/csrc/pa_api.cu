@@ -247,7 +247,7 @@ struct LaunchPlan {
     DecodeVariant v;
     bool mma;
     int smem;
-    int grid;
+    int grid;  // ranges of the work list: CTAs, except where a CTA takes several
     int sms;
     int stages;
     int threads;
@@ -256,6 +256,7 @@ struct LaunchPlan {
     bool merge_in_kernel;
     int seg_units;  // the range balance's weight of a segment (DecodeParams::seg_units)
     int wave_skew;  // the CTA shares' skew by dispatch wave (DecodeParams::wave_skew)
+    int wave_ctas;  // ranges of one dispatch wave (DecodeParams::wave_ctas)
 };
 
 pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -290,7 +291,9 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
         if (!kernel_occupancy(dev, b.kernel, b.threads, sh->smem, &occ)) return PA_ERR_CUDA;
         if (occ <= 0) return PA_ERR_UNSUPPORTED;
         sh->per_sm = occ < want ? occ : want;
-        int64_t grid = (int64_t)lp->sms * sh->per_sm;
+        // over 4-bit pools a range's two partial slots cost G (D + 2) floats each: with large groups fewer ranges
+        if (dtype == PA_FP4_E2M1 && G * head_dim > 512 && sh->per_sm > kFp4WideGroupCtas) sh->per_sm = kFp4WideGroupCtas;
+        int64_t grid = (int64_t)lp->sms * sh->per_sm * lp->v.ranges_per_cta;
         if (grid > tiles_bound) grid = tiles_bound;
         sh->grid = (int)(grid < 1 ? 1 : grid);
         return PA_OK;
@@ -347,6 +350,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
                                                : PA_SEG_UNITS_FMA;
     const int ws = g_wave_skew.load();
     lp->wave_skew = ws >= 0 ? ws : dtype == PA_FP8_E4M3 ? PA_WAVE_SKEW_FP8 : dtype == PA_FP4_E2M1 ? PA_WAVE_SKEW_FP4 : 0;
+    lp->wave_ctas = lp->sms * lp->v.ranges_per_cta;
     lp->smem = sh.smem;
     lp->grid = sh.grid;
     lp->stages = b.stages;
@@ -367,7 +371,7 @@ extern "C" pa_status pa_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_h
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
     // enough for the largest grid any launch on this device can take
-    *bytes_out = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)sms * kMaxCtasPerSm).total;
+    *bytes_out = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)sms * kMaxRangesPerSm).total;
     return PA_OK;
 }
 
@@ -447,7 +451,7 @@ extern "C" pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                     partition_tokens > 0, dtype, &lp);
     if (s != PA_OK) return s;
-    if (ctas) *ctas = lp.grid;
+    if (ctas) *ctas = (lp.grid + lp.v.ranges_per_cta - 1) / lp.v.ranges_per_cta;
     if (stages) *stages = lp.stages;
     if (smem_bytes) *smem_bytes = lp.smem;
     if (uses_mma) *uses_mma = lp.mma ? 1 : 0;
@@ -544,7 +548,7 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     p.partition_tiles = partition_tokens / block_size;
     p.num_ctas = lp.grid;
     p.seg_units = lp.seg_units;
-    p.wave_ctas = lp.sms;
+    p.wave_ctas = lp.wave_ctas;
     p.wave_skew = lp.wave_skew;
     p.scale_log2 = scale * 1.4426950408889634f * k_scale;
     p.out_scale = v_scale;
@@ -653,7 +657,7 @@ extern "C" pa_status pa_decode_build_plan(const int32_t* block_tables, int32_t m
     const int PT = partition_tokens / block_size;
     const int A = lp.seg_units;
     for (int w = 0; w < kPlanHeaderWords; ++w) pl[w] = 0;
-    pl[kPlanWMagic] = kPlanMagic;
+    pl[kPlanWMagic] = dtype == PA_FP4_E2M1 ? kPlanMagicFp4 : kPlanMagic;
     pl[kPlanWNumSeqs] = B;
     pl[kPlanWGrid] = C;
     pl[kPlanWKvHeads] = Hkv;
@@ -663,7 +667,7 @@ extern "C" pa_status pa_decode_build_plan(const int32_t* block_tables, int32_t m
     pl[kPlanWMaxLen] = max_len;
     pl[kPlanWMergeInKernel] = lp.merge_in_kernel ? 1 : 0;
     pl[kPlanWMaxBlocks] = max_blocks_per_seq;
-    pl[kPlanWWaveCtas] = lp.sms;
+    pl[kPlanWWaveCtas] = lp.wave_ctas;
     pl[kPlanWWaveSkew] = lp.wave_skew;
     // the lengths scan of the kernels: clamped lengths, block and partition prefix sums
     int32_t* pref = pl + kPlanHeaderWords;
@@ -681,7 +685,8 @@ extern "C" pa_status pa_decode_build_plan(const int32_t* block_tables, int32_t m
     }
     pref[B] = nb_sum;
     upref[B] = PT > 0 ? np_sum : 0;
-    const Plan P = plan_from_prefix(pref, upref, B, Hkv, PT, A, C, lp.sms, lp.wave_skew);
+    const int ranges = dtype == PA_FP4_E2M1 ? fp4_ranges((int64_t)Hkv * nb_sum, C, PT, block_size) : C;
+    const Plan P = plan_from_prefix(pref, upref, B, Hkv, PT, A, ranges, lp.wave_ctas, lp.wave_skew);
     for (int c = 0; c < C; ++c) {
         int32_t* rec = pl + plan_rec_off(B, c);
         for (int w = 0; w < kPlanRecWords; ++w) rec[w] = 0;

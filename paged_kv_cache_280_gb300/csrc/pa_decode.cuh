@@ -30,13 +30,11 @@
 // is no merge between warps and no CTA-wide barrier in the loop.
 //
 // Two compute paths:
-//   MMA (bf16 with G >= 4, and every FP8 and 4-bit pool): tensor-core mma.sync m16n8k16.
+//   MMA (bf16 with G >= 4, and every FP8 pool): tensor-core mma.sync m16n8k16.
 //     S^T = K q^T with the 16 tokens of a half-block as M and the (padded) 8
 //     query heads as N; P^T is moved into B-fragment layout with movmatrix;
 //     O^T = V^T P^T with the head dimension as M.  FP8 codes are widened to f16
-//     in registers (see MmaState).  4-bit pools have a state of their own
-//     (Fp4State, pa_decode_fp4.cuh), take 64 tokens per stage and softmax update,
-//     and their tiles arrive by plain bulk copies (a tile is one contiguous record).
+//     in registers (see MmaState).
 //   FMA (fp32, or bf16 with G < 4): CUDA cores; lane (t, half) forms the dot
 //     products of token t over half the head dimension, lanes own D/32
 //     output dimensions for P V.
@@ -46,7 +44,6 @@
 
 #include <type_traits>
 
-#include "pa_decode_fp4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_plan.h"
@@ -71,10 +68,6 @@ template <>
 struct ElemBytes<__nv_fp8_e4m3> {  // FP8 pools (OCP E4M3 codes)
     static constexpr int value = 1;
 };
-template <>
-struct ElemBytes<Fp4> {  // 4-bit pools: no whole bytes; Layout takes their tile size from the format
-    static constexpr int value = 0;
-};
 
 // Pipeline depth: about PA_STAGE_BYTES (32 KB) of tiles in flight per CTA on
 // the tensor-core path and PA_STAGE_BYTES_FMA (16 KB) on the CUDA-core path,
@@ -93,9 +86,6 @@ struct ElemBytes<Fp4> {  // 4-bit pools: no whole bytes; Layout takes their tile
 #ifndef PA_STAGE_BYTES_FP8_ONE  // the same with one consumer warp (8 CTAs per SM): 2 stages
 #define PA_STAGE_BYTES_FP8_ONE 16384
 #endif
-#ifndef PA_STAGES_FP4  // 4-bit pools: stages of 64 tokens
-#define PA_STAGES_FP4 4
-#endif
 constexpr int stages_for(int ring_bytes, int bs, int d, int e) {
     int n = ring_bytes / (2 * bs * d * e);
     return n < 2 ? 2 : (n > 16 ? 16 : n);
@@ -108,10 +98,9 @@ struct Layout {
     static constexpr int E = ElemBytes<KV>::value;  // pool element bytes
     static constexpr int EQ = ElemBytes<T>::value;  // query / output element bytes
     // tiles per stage: two 16-token tiles on the tensor-core path (one handshake and one softmax
-    // update per 32 tokens), 64 tokens over 4-bit pools, one tile otherwise
-    static constexpr bool kF4 = std::is_same<KV, Fp4>::value;
-    static constexpr int TPS = kF4 ? 64 / BS : MMA && BS == 16 ? 2 : 1;
-    static constexpr int S = kF4 ? PA_STAGES_FP4 : stages_for(
+    // update per 32 tokens), one tile otherwise
+    static constexpr int TPS = MMA && BS == 16 ? 2 : 1;
+    static constexpr int S = stages_for(
         MMA ? (E == 1 ? (NC_ > 1 ? PA_STAGE_BYTES_FP8 : PA_STAGE_BYTES_FP8_ONE) : PA_STAGE_BYTES) : PA_STAGE_BYTES_FMA,
         BS * TPS, D, E);
     // tensor-core path over an FP8 pool: K and V codes are widened in registers
@@ -125,7 +114,7 @@ struct Layout {
     // CTAs per SM that the register budget is planned for: that of 8 two-warp CTAs
     static constexpr int kMinCtas = kMaxCtasPerSm * 64 / kThreadsCta;
     static constexpr int GN = GF > 0 ? GF : kMaxGroup;  // query rows a q slot holds
-    static constexpr int kTileBytes = kF4 ? BS * fp4_row_bytes(D) : BS * D * E;  // K (or V) of one tile
+    static constexpr int kTileBytes = BS * D * E;  // K (or V) of one tile
     static constexpr int kPanels = D * E / 128;    // 128-byte column panels per row
     static constexpr int kStageBytes = 2 * TPS * kTileBytes;  // K of its tiles, then their V
     static constexpr int kQSlotBytes = GN * D * EQ;
@@ -150,7 +139,7 @@ struct Layout {
     static constexpr int kWsumOff = kPendOff + 32;
     static constexpr int kMiscBytes = (kWsumOff + 2 * 4 * (NC + 1) + 15) / 16 * 16;
     static constexpr int kPrefixOff = kMiscOff + kMiscBytes;
-    static_assert(kF4 ? kTileBytes % 16 == 0 && kQOff % 16 == 0 : kTileBytes % 1024 == 0, "tiles must keep 1024-byte alignment for the 128B swizzle");
+    static_assert(kTileBytes % 1024 == 0, "tiles must keep 1024-byte alignment for the 128B swizzle");
     static_assert(kQSlotBytes % 16 == 0, "bulk-copy destination alignment");
     static_assert(kBarOff % 8 == 0, "mbarrier alignment");
     // dynamic shared memory for num_seqs sequences: prefix sums (two with a
@@ -950,7 +939,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
     // the producer's tensor maps and cache policy, requested before the plan is known
     uint64_t policy = 0;
     if (warp == L::kProducer) {
-        if (!L::kF4 && lane == 0) {
+        if (lane == 0) {
             prefetch_tensormap(&tmap_k);
             prefetch_tensormap(&tmap_v);
         }
@@ -1070,22 +1059,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
                 }
                 const int st = k % S;
                 if (role_wait(empty_bar(st), ((k / S) & 1) ^ 1, misc, p.status)) {
-                    if constexpr (L::kF4) {
-                        // one contiguous record per tile and pool; lanes t and TPS + t copy tile t's K and V
-                        if (lane == 0) mbar_arrive_expect_tx(full_bar(st), (uint32_t)(nt * 2 * L::kTileBytes));
-                        __syncwarp();
-                        const int t = lane % L::TPS;
-                        int32_t bid = bids[0];
-#pragma unroll
-                        for (int i2 = 1; i2 < L::TPS; ++i2)
-                            if (t == i2) bid = bids[i2];
-                        if (lane < 2 * L::TPS && t < nt) {
-                            const uint8_t* pool = lane < L::TPS ? p.k_pool : p.v_pool;
-                            bulk_load_hint(base_s + L::kStagesOff + st * L::kStageBytes + lane * L::kTileBytes,
-                                           pool + ((int64_t)bid * Hkv + h) * L::kTileBytes, L::kTileBytes, full_bar(st),
-                                           policy);
-                        }
-                    } else if (lane == 0) {
+                    if (lane == 0) {
                         mbar_arrive_expect_tx(full_bar(st), (uint32_t)(nt * 2 * L::kTileBytes));
                         const uint32_t ks = base_s + L::kStagesOff + st * L::kStageBytes;
 #pragma unroll
@@ -1140,8 +1114,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
         }
         float* qf = reinterpret_cast<float*>(base + L::kQfOff);
         float* ptile = reinterpret_cast<float*>(base + L::kPTileOff);
-        using MmaSt = typename std::conditional<L::kF4, Fp4State<D, BS>, MmaState<D, BS, L::kF8>>::type;
-        typename std::conditional<MMA, MmaSt, FmaState<KV, D, BS, GF>>::type st;
+        typename std::conditional<MMA, MmaState<D, BS, L::kF8>, FmaState<KV, D, BS, GF>>::type st;
         uint32_t k = 0, pi = 0;
         // In-kernel merges this CTA completes wait for the end of its range when they would
         // otherwise come last (its last piece) or take many round trips (more than
@@ -1157,9 +1130,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
             const int qs = pi % kQSlots;
             const uint8_t* qslot = base + L::kQOff + qs * L::kQSlotBytes;
             const bool qok = role_wait(qfull_bar(qs), (pi / kQSlots) & 1, misc, p.status, p.wait_limit_ns);
-            if constexpr (L::kF4) {
-                if (qok) st.load_q(qslot, G, lane, p.scale_log2);
-            } else if constexpr (MMA) {
+            if constexpr (MMA) {
                 if (qok) st.load_q(qslot, G, lane);
             } else {
                 const T* qsrc = reinterpret_cast<const T*>(qslot);
@@ -1187,9 +1158,6 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
                         const uint32_t kb = base_s + L::kStagesOff + sidx * L::kStageBytes;
                         const uint32_t vb = kb + L::TPS * L::kTileBytes;
                         const int tok0 = (j0 + i) * BS;
-                        if constexpr (L::kF4) {
-                            st.stage(kb, vb, min(min(L::TPS, ntile - i) * BS, len - tok0), lane);
-                        } else {
                         // a second 16-token step: the tile's second half (32-token tiles), or the
                         // stage's second tile, which exists only if the piece holds one more tile
                         // (a piece may end before its sequence does)
@@ -1201,7 +1169,6 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p, const CUtenso
                                 st.step2(kb, vb, 0, v0, kb + L::kTileBytes, vb + L::kTileBytes, 0, v1, p.scale_log2, lane);
                         } else {
                             st.step(kb, vb, 0, v0, p.scale_log2, lane);
-                        }
                         }
                     }
                     __syncwarp();

@@ -1,4 +1,4 @@
-// Softmax state of a decode consumer warp over a 4-bit pool (format: pa_fp4.cuh), on the tensor cores
+// Softmax state of a decode warp over a 4-bit pool (format: pa_fp4.cuh), on the tensor cores
 // (mma.sync m16n8k16, f16 operands, fp32 sums).
 //
 // The bound.  A token row of one KV head is 9/16 D bytes of K and the same of V (144 bytes at D = 128),
@@ -25,8 +25,6 @@
 #include "pa_fp4.cuh"
 
 namespace pa {
-
-struct Fp4 {};  // the pool type tag of the decode templates
 
 __device__ __forceinline__ float ex2_approx(float x) {  // 2^x, 2^-inf = 0
     float y;
@@ -85,10 +83,9 @@ struct Fp4State {
     static constexpr int KW = D / 32;       // words of a lane's part of a K row (D / 4 dims)
     static constexpr int VW = D / 64;       // words of a lane's part of a V row (D / 8 dims)
     static constexpr int kScalesOff = BS * (D / 2);  // the tile's scale bytes
-    static constexpr int kSteps = 4;        // 16-token steps of a full stage
     uint32_t qb[MT][2];  // B fragments of q^T per k-step, rows scaled by a power of two
     float sc[2];         // score scale (base 2) of heads 2c and 2c + 1, the power of two undone
-    float m[2];          // running max of heads 2c, 2c + 1
+    float m[2];          // reference of the weights of heads 2c, 2c + 1 (base 2), the same in every g
     float l[4];          // running sums: [0], [1] of heads 2c, 2c + 1 (the same in every g; [2], [3] repeat them)
     float o[MT][4];
 
@@ -107,13 +104,14 @@ struct Fp4State {
     // f16 holds a bf16 value exactly while it is neither above 65504 nor far below 2^-14, so each row is
     // scaled by the power of two that brings its largest element to [1, 2): a smaller element loses
     // less than 2^-25 of that one, and any bf16 magnitudes are in range.
-    __device__ __forceinline__ void load_q(const uint8_t* qslot, int G, int lane, float scale_log2) {
+    // rows: q[b][h * G] in global memory.
+    __device__ __forceinline__ void load_q(const __nv_bfloat16* rows, int G, int lane, float scale_log2) {
         const int g = lane >> 2, c = lane & 3;
         float x[D / 4];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
             if (g < G) {
-                load8(reinterpret_cast<const __nv_bfloat16*>(qslot) + g * D + c * (D / 4) + 8 * i, x + 8 * i);
+                load8(rows + g * D + c * (D / 4) + 8 * i, x + 8 * i);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[8 * i + e] = 0.f;
@@ -202,6 +200,10 @@ struct Fp4State {
 
     // N 16-token steps (step s: K rows kt[s], V rows vt[s], both from row r[s]) with one softmax update.
     // MASK (N = 1): only the first `valid` tokens exist (at least one).
+    // m is a reference, not the exact maximum: it moves (and O and l are rescaled) only when a score
+    // passes it by more than kRaise, so that most steps need no reduction over lanes.  The weights then
+    // stay at most 2^kRaise, within f16, and the final ratio does not depend on the reference.
+    static constexpr float kRaise = 8.f;
     template <int N, bool MASK>
     __device__ __forceinline__ void steps(const uint32_t (&kt)[N], const uint32_t (&vt)[N], const int (&r)[N], int valid,
                                           int lane) {
@@ -216,19 +218,21 @@ struct Fp4State {
                 if (MASK && slot_token(g) + 8 * (i >> 1) >= valid) x[s][i] = -INFINITY;
             }
         }
-        float n0 = m[0], n1 = m[1];
+        float n0 = fmaxf(x[0][0], x[0][2]), n1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
-        for (int s = 0; s < N; ++s) {
+        for (int s = 1; s < N; ++s) {
             n0 = fmaxf(n0, fmaxf(x[s][0], x[s][2]));
             n1 = fmaxf(n1, fmaxf(x[s][1], x[s][3]));
         }
+        if (__any_sync(0xffffffffu, n0 > m[0] + kRaise || n1 > m[1] + kRaise)) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-        }
-        if (__any_sync(0xffffffffu, n0 != m[0] || n1 != m[1])) {  // some row max grew (or is not a number)
-            const float a0 = ex2_approx(m[0] - n0), a1 = ex2_approx(m[1] - n1);
+            for (int off = 4; off < 32; off <<= 1) {
+                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+            }
+            n0 = fmaxf(n0, m[0]), n1 = fmaxf(n1, m[1]);
+            // a head whose scores are all -inf so far keeps its state (nothing is weighed yet)
+            const float a0 = n0 == m[0] ? 1.f : ex2_approx(m[0] - n0), a1 = n1 == m[1] ? 1.f : ex2_approx(m[1] - n1);
             l[0] *= a0, l[1] *= a1, l[2] *= a0, l[3] *= a1;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][0] *= a0, o[i][1] *= a1, o[i][2] *= a0, o[i][3] *= a1;
@@ -236,25 +240,19 @@ struct Fp4State {
         }
 #pragma unroll
         for (int s = 0; s < N; ++s) {
-            const uint32_t p0 = pack_f16x2(ex2_approx(x[s][0] - n0), ex2_approx(x[s][1] - n1));
-            const uint32_t p1 = pack_f16x2(ex2_approx(x[s][2] - n0), ex2_approx(x[s][3] - n1));
+            const uint32_t p0 = pack_f16x2(ex2_approx(x[s][0] - m[0]), ex2_approx(x[s][1] - m[1]));
+            const uint32_t p1 = pack_f16x2(ex2_approx(x[s][2] - m[0]), ex2_approx(x[s][3] - m[1]));
             accumulate_pv<MASK>(vt[s], r[s], valid, movmatrix_trans(p0), movmatrix_trans(p1), lane);
         }
     }
 
-    // The first `valid` tokens (1 .. 64) of a stage: tile t's K at kb + t * tile bytes, V at vb + t * tile bytes.
+    // The first `valid` tokens (1 .. 32) of a stage: tile t's K at kb + t * tile bytes, V at vb + t * tile bytes.
     __device__ __forceinline__ void stage(uint32_t kb, uint32_t vb, int valid, int lane) {
         constexpr int kTile = BS * fp4_row_bytes(D), kPer = BS / 16;  // 16-token steps per tile
-        if (valid == 16 * kSteps) {
-            uint32_t kt[kSteps], vt[kSteps];
-            int r[kSteps];
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                kt[s] = kb + (s / kPer) * kTile;
-                vt[s] = vb + (s / kPer) * kTile;
-                r[s] = 16 * (s % kPer);
-            }
-            steps<kSteps, false>(kt, vt, r, 16, lane);
+        if (valid == 32) {
+            const uint32_t kt[2] = {kb, kb + (1 / kPer) * kTile}, vt[2] = {vb, vb + (1 / kPer) * kTile};
+            const int r[2] = {0, 16 * (1 % kPer)};
+            steps<2, false>(kt, vt, r, 16, lane);
         } else {
             for (int s = 0; 16 * s < valid; ++s) {
                 const uint32_t kt[1] = {kb + (uint32_t)((s / kPer) * kTile)}, vt[1] = {vb + (uint32_t)((s / kPer) * kTile)};
@@ -262,38 +260,6 @@ struct Fp4State {
                 steps<1, true>(kt, vt, r, min(16, valid - 16 * s), lane);
             }
         }
-    }
-
-    __device__ __forceinline__ void finish() {}  // l is whole already
-
-    // This lane's state as 4 + 4 MT floats at scr[f * 32 + lane], and the merge of a saved state (other
-    // tokens of the same heads).  A side that saw no token has m = -inf and weighs 0.
-    __device__ __forceinline__ void save(float* scr, int lane) const {
-        scr[lane] = m[0];
-        scr[32 + lane] = m[1];
-        scr[64 + lane] = l[0];
-        scr[96 + lane] = l[1];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) scr[(4 + 4 * i + j) * 32 + lane] = o[i][j];
-    }
-    __device__ __forceinline__ void combine(const float* scr, int lane) {
-        const float om0 = scr[lane], om1 = scr[32 + lane];
-        const float n0 = fmaxf(m[0], om0), n1 = fmaxf(m[1], om1);
-        const float a0 = n0 == -INFINITY ? 0.f : ex2_approx(m[0] - n0), b0 = n0 == -INFINITY ? 0.f : ex2_approx(om0 - n0);
-        const float a1 = n1 == -INFINITY ? 0.f : ex2_approx(m[1] - n1), b1 = n1 == -INFINITY ? 0.f : ex2_approx(om1 - n1);
-        l[0] = l[0] * a0 + scr[64 + lane] * b0;
-        l[1] = l[1] * a1 + scr[96 + lane] * b1;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            o[i][0] = o[i][0] * a0 + scr[(4 + 4 * i) * 32 + lane] * b0;
-            o[i][1] = o[i][1] * a1 + scr[(5 + 4 * i) * 32 + lane] * b1;
-            o[i][2] = o[i][2] * a0 + scr[(6 + 4 * i) * 32 + lane] * b0;
-            o[i][3] = o[i][3] * a1 + scr[(7 + 4 * i) * 32 + lane] * b1;
-        }
-        m[0] = n0;
-        m[1] = n1;
     }
 
     // Normalised output rows (o_rows = out[b][h * G]): a lane holds D / 8 consecutive dims of its two heads.

@@ -14,10 +14,13 @@ namespace pa {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 constexpr int kMaxCtasPerSm = 8;
+constexpr int kMaxRangesPerSm = 16;  // ranges of the work list on an SM: 4-bit pools run several per CTA
+constexpr int kFp4WideGroupCtas = 3;
 constexpr int kDefaultCtasPerSmMma = 4;  // default CTAs per SM on the bf16 tensor-core path
 // Decode workspace: the status head, one merge counter per CTA, then two
-// partial slots per CTA of the launch's grid (pa_decode_workspace_bytes sizes
-// it for kMaxCtasPerSm CTAs on every SM, the largest grid); a slot is [G][D]
+// partial slots per CTA (over 4-bit pools: per range) of the launch's grid
+// (pa_decode_workspace_bytes sizes it for kMaxRangesPerSm on every SM, the most
+// any launch has); a slot is [G][D]
 // floats of o plus [G][2] floats of (m, l).
 constexpr int kSlotExtraFloatsPerHead = 2;
 // floats of one partial slot, a multiple of 4 so that every slot is 16-byte aligned
@@ -127,6 +130,7 @@ struct DecodeVariant {
     bool merge_in_kernel_ok;   // `in` has the in-kernel merge
     void (*launch)(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid, int smem,
                    int merge_grid, int merge_smem, cudaStream_t stream);
+    int ranges_per_cta = 1;  // ranges of the plan that one CTA takes (the grid passed to launch counts ranges)
 };
 
 // Compiled variants.  `group` is Hq / Hkv; the CUDA-core path has exact

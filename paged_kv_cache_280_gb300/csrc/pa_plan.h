@@ -240,12 +240,26 @@ PA_HD Plan plan_from_prefix(const int32_t* pref, const int32_t* upref, int B, in
     return P;
 }
 
+// Ranges that take work in a launch of num_ctas over a 4-bit pool: without partitions a range spans at
+// least kFp4MinRangeTokens tokens (of one KV head), so that a short batch is not cut into pieces whose merge
+// costs more than their computation.  (tiles: of the whole batch.)
+#ifndef PA_FP4_MIN_RANGE
+#define PA_FP4_MIN_RANGE 64
+#endif
+constexpr int kFp4MinRangeTokens = PA_FP4_MIN_RANGE;
+PA_HD int32_t fp4_ranges(int64_t tiles, int num_ctas, int partition_tiles, int block_size) {
+    if (partition_tiles > 0) return num_ctas;
+    const int64_t most = tiles * block_size / kFp4MinRangeTokens;
+    return (int32_t)(most < 1 ? 1 : most < num_ctas ? most : num_ctas);
+}
+
 // ---- host-built plans (pa_decode_build_plan) ----------------------------------
 // A plan buffer is int32 words: a header, then pref[B + 1], upref[B + 1] (zeros without
 // partitions) and the clamped lengths[B], then one record per CTA of the launch's grid.  A
 // record holds the CTA's range ends, the rotation point, the piece walk's sequence hints and
 // the block-table entries of the first 32 tiles of its first piece.
-constexpr int32_t kPlanMagic = 0x4c504150;  // "PAPL"
+constexpr int32_t kPlanMagic = 0x4c504150;     // "PAPL"
+constexpr int32_t kPlanMagicFp4 = 0x34504150;  // "PAP4": ranges of fp4_ranges()
 constexpr int kPlanHeaderWords = 16;
 constexpr int kPlanRecWords = 40;
 constexpr int kPlanChunk = 32;
