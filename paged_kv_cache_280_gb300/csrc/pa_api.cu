@@ -247,7 +247,7 @@ struct LaunchPlan {
     DecodeVariant v;
     bool mma;
     int smem;
-    int grid;  // ranges of the work list: CTAs, except where a CTA takes several
+    int grid;
     int sms;
     int stages;
     int threads;
@@ -256,7 +256,6 @@ struct LaunchPlan {
     bool merge_in_kernel;
     int seg_units;  // the range balance's weight of a segment (DecodeParams::seg_units)
     int wave_skew;  // the CTA shares' skew by dispatch wave (DecodeParams::wave_skew)
-    int wave_ctas;  // ranges of one dispatch wave (DecodeParams::wave_ctas)
 };
 
 pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -270,7 +269,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
     lp->mma = (dtype == PA_BF16 && G >= 4) || quantised;
     bool found = dtype == PA_F32         ? decode_variant_f32(head_dim, block_size, G, &lp->v)
                  : dtype == PA_FP8_E4M3 ? decode_variant_fp8(head_dim, block_size, G, &lp->v)
-                 : dtype == PA_FP4_E2M1 ? decode_variant_fp4(head_dim, block_size, G, &lp->v)
+                 : dtype == PA_FP4_E2M1 ? decode_variant_fp4(head_dim, block_size, G, num_seqs, fixed, &lp->v)
                  : lp->mma              ? decode_variant_bf16_mma(head_dim, block_size, &lp->v)
                                         : decode_variant_bf16_fma(head_dim, block_size, G, &lp->v);
     if (!found) return PA_ERR_UNSUPPORTED;
@@ -291,9 +290,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
         if (!kernel_occupancy(dev, b.kernel, b.threads, sh->smem, &occ)) return PA_ERR_CUDA;
         if (occ <= 0) return PA_ERR_UNSUPPORTED;
         sh->per_sm = occ < want ? occ : want;
-        // over 4-bit pools a range's two partial slots cost G (D + 2) floats each: with large groups fewer ranges
-        if (dtype == PA_FP4_E2M1 && G * head_dim > 512 && sh->per_sm > kFp4WideGroupCtas) sh->per_sm = kFp4WideGroupCtas;
-        int64_t grid = (int64_t)lp->sms * sh->per_sm * lp->v.ranges_per_cta;
+        int64_t grid = (int64_t)lp->sms * sh->per_sm;
         if (grid > tiles_bound) grid = tiles_bound;
         sh->grid = (int)(grid < 1 ? 1 : grid);
         return PA_OK;
@@ -349,8 +346,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
                     : lp->mma                  ? PA_SEG_UNITS_MMA
                                                : PA_SEG_UNITS_FMA;
     const int ws = g_wave_skew.load();
-    lp->wave_skew = ws >= 0 ? ws : dtype == PA_FP8_E4M3 ? PA_WAVE_SKEW_FP8 : dtype == PA_FP4_E2M1 ? PA_WAVE_SKEW_FP4 : 0;
-    lp->wave_ctas = lp->sms * lp->v.ranges_per_cta;
+    lp->wave_skew = ws >= 0 ? ws : dtype == PA_FP8_E4M3 ? PA_WAVE_SKEW_FP8 : 0;
     lp->smem = sh.smem;
     lp->grid = sh.grid;
     lp->stages = b.stages;
@@ -371,7 +367,7 @@ extern "C" pa_status pa_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_h
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
     // enough for the largest grid any launch on this device can take
-    *bytes_out = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)sms * kMaxRangesPerSm).total;
+    *bytes_out = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)sms * kMaxCtasPerSm).total;
     return PA_OK;
 }
 
@@ -451,7 +447,7 @@ extern "C" pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                     partition_tokens > 0, dtype, &lp);
     if (s != PA_OK) return s;
-    if (ctas) *ctas = (lp.grid + lp.v.ranges_per_cta - 1) / lp.v.ranges_per_cta;
+    if (ctas) *ctas = lp.grid;
     if (stages) *stages = lp.stages;
     if (smem_bytes) *smem_bytes = lp.smem;
     if (uses_mma) *uses_mma = lp.mma ? 1 : 0;
@@ -490,6 +486,7 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
     if (dtype == PA_FP8_E4M3 && head_dim != 128) return PA_ERR_UNSUPPORTED;  // a pool row fills one 128-byte panel
+    if (dtype == PA_FP4_E2M1 && num_kv_heads > 32767) return PA_ERR_UNSUPPORTED;  // 15 bits of a stage descriptor
     if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
         return PA_ERR_INVALID_ARG;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !workspace) return PA_ERR_INVALID_ARG;
@@ -548,7 +545,7 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     p.partition_tiles = partition_tokens / block_size;
     p.num_ctas = lp.grid;
     p.seg_units = lp.seg_units;
-    p.wave_ctas = lp.wave_ctas;
+    p.wave_ctas = lp.sms;
     p.wave_skew = lp.wave_skew;
     p.scale_log2 = scale * 1.4426950408889634f * k_scale;
     p.out_scale = v_scale;
@@ -612,6 +609,7 @@ pa_status decode_shape(int32_t max_blocks_per_seq, int32_t max_seq_len, int32_t 
     pa_status s = check_shapes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size);
     if (s != PA_OK) return s;
     if (dtype == PA_FP8_E4M3 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (dtype == PA_FP4_E2M1 && num_kv_heads > 32767) return PA_ERR_UNSUPPORTED;
     if (max_blocks_per_seq <= 0 || max_seq_len < 0) return PA_ERR_INVALID_ARG;
     if (partition_tokens < 0 || (partition_tokens % block_size) != 0) return PA_ERR_INVALID_ARG;
     if ((int64_t)num_seqs * num_kv_heads * max_blocks_per_seq >= INT32_MAX) return PA_ERR_UNSUPPORTED;
@@ -667,7 +665,7 @@ extern "C" pa_status pa_decode_build_plan(const int32_t* block_tables, int32_t m
     pl[kPlanWMaxLen] = max_len;
     pl[kPlanWMergeInKernel] = lp.merge_in_kernel ? 1 : 0;
     pl[kPlanWMaxBlocks] = max_blocks_per_seq;
-    pl[kPlanWWaveCtas] = lp.wave_ctas;
+    pl[kPlanWWaveCtas] = lp.sms;
     pl[kPlanWWaveSkew] = lp.wave_skew;
     // the lengths scan of the kernels: clamped lengths, block and partition prefix sums
     int32_t* pref = pl + kPlanHeaderWords;
@@ -686,7 +684,7 @@ extern "C" pa_status pa_decode_build_plan(const int32_t* block_tables, int32_t m
     pref[B] = nb_sum;
     upref[B] = PT > 0 ? np_sum : 0;
     const int ranges = dtype == PA_FP4_E2M1 ? fp4_ranges((int64_t)Hkv * nb_sum, C, PT, block_size) : C;
-    const Plan P = plan_from_prefix(pref, upref, B, Hkv, PT, A, ranges, lp.wave_ctas, lp.wave_skew);
+    const Plan P = plan_from_prefix(pref, upref, B, Hkv, PT, A, ranges, lp.sms, lp.wave_skew);
     for (int c = 0; c < C; ++c) {
         int32_t* rec = pl + plan_rec_off(B, c);
         for (int w = 0; w < kPlanRecWords; ++w) rec[w] = 0;

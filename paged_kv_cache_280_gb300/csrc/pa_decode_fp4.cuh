@@ -198,32 +198,30 @@ struct Fp4State {
         }
     }
 
-    // N 16-token steps (step s: K rows kt[s], V rows vt[s], both from row r[s]) with one softmax update.
-    // MASK (N = 1): only the first `valid` tokens exist (at least one).
+    // A stage holds 32 tokens, two 16-token steps, with one softmax update.  MASK: only the first `valid`
+    // (1 .. 32) of them exist.  Tile t's K is at kb + t * tile bytes, its V at vb + t * tile bytes.
+    static constexpr int kTile = BS * fp4_row_bytes(D), kStep1 = BS == 16 ? kTile : 0, kRow1 = BS == 16 ? 0 : 16;
+
+    // The weights of the stage's tokens as P^T B fragments (step 0: pb[0], pb[1]; step 1: pb[2], pb[3]).
     // m is a reference, not the exact maximum: it moves (and O and l are rescaled) only when a score
-    // passes it by more than kRaise, so that most steps need no reduction over lanes.  The weights then
-    // stay at most 2^kRaise, within f16, and the final ratio does not depend on the reference.
+    // passes it by more than kRaise, so that most stages need no reduction over lanes.  The weights
+    // then stay at most 2^kRaise, within f16, and the final ratio does not depend on the reference.
     static constexpr float kRaise = 8.f;
-    template <int N, bool MASK>
-    __device__ __forceinline__ void steps(const uint32_t (&kt)[N], const uint32_t (&vt)[N], const int (&r)[N], int valid,
-                                          int lane) {
+    template <bool MASK>
+    __device__ __forceinline__ void weights(uint32_t kb, int valid, int lane, uint32_t (&pb)[4]) {
         const int g = lane >> 2;
-        float x[N][4];
+        float x[2][4];
+        scores(kb, 0, lane, x[0]);
+        scores(kb + kStep1, kRow1, lane, x[1]);
 #pragma unroll
-        for (int s = 0; s < N; ++s) {
-            scores(kt[s], r[s], lane, x[s]);
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[s][i] *= sc[i & 1];
-                if (MASK && slot_token(g) + 8 * (i >> 1) >= valid) x[s][i] = -INFINITY;
+                if (MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid) x[s][i] = -INFINITY;
             }
-        }
-        float n0 = fmaxf(x[0][0], x[0][2]), n1 = fmaxf(x[0][1], x[0][3]);
-#pragma unroll
-        for (int s = 1; s < N; ++s) {
-            n0 = fmaxf(n0, fmaxf(x[s][0], x[s][2]));
-            n1 = fmaxf(n1, fmaxf(x[s][1], x[s][3]));
-        }
+        float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
         if (__any_sync(0xffffffffu, n0 > m[0] + kRaise || n1 > m[1] + kRaise)) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -239,27 +237,17 @@ struct Fp4State {
             m[0] = n0, m[1] = n1;
         }
 #pragma unroll
-        for (int s = 0; s < N; ++s) {
-            const uint32_t p0 = pack_f16x2(ex2_approx(x[s][0] - m[0]), ex2_approx(x[s][1] - m[1]));
-            const uint32_t p1 = pack_f16x2(ex2_approx(x[s][2] - m[0]), ex2_approx(x[s][3] - m[1]));
-            accumulate_pv<MASK>(vt[s], r[s], valid, movmatrix_trans(p0), movmatrix_trans(p1), lane);
+        for (int s = 0; s < 2; ++s) {
+            pb[2 * s] = movmatrix_trans(pack_f16x2(ex2_approx(x[s][0] - m[0]), ex2_approx(x[s][1] - m[1])));
+            pb[2 * s + 1] = movmatrix_trans(pack_f16x2(ex2_approx(x[s][2] - m[0]), ex2_approx(x[s][3] - m[1])));
         }
     }
 
-    // The first `valid` tokens (1 .. 32) of a stage: tile t's K at kb + t * tile bytes, V at vb + t * tile bytes.
-    __device__ __forceinline__ void stage(uint32_t kb, uint32_t vb, int valid, int lane) {
-        constexpr int kTile = BS * fp4_row_bytes(D), kPer = BS / 16;  // 16-token steps per tile
-        if (valid == 32) {
-            const uint32_t kt[2] = {kb, kb + (1 / kPer) * kTile}, vt[2] = {vb, vb + (1 / kPer) * kTile};
-            const int r[2] = {0, 16 * (1 % kPer)};
-            steps<2, false>(kt, vt, r, 16, lane);
-        } else {
-            for (int s = 0; 16 * s < valid; ++s) {
-                const uint32_t kt[1] = {kb + (uint32_t)((s / kPer) * kTile)}, vt[1] = {vb + (uint32_t)((s / kPer) * kTile)};
-                const int r[1] = {16 * (s % kPer)};
-                steps<1, true>(kt, vt, r, min(16, valid - 16 * s), lane);
-            }
-        }
+    // O and l with those weights.
+    template <bool MASK>
+    __device__ __forceinline__ void accumulate(uint32_t vb, int valid, int lane, const uint32_t (&pb)[4]) {
+        accumulate_pv<MASK>(vb, 0, valid, pb[0], pb[1], lane);
+        accumulate_pv<MASK>(vb + kStep1, kRow1, valid - 16, pb[2], pb[3], lane);
     }
 
     // Normalised output rows (o_rows = out[b][h * G]): a lane holds D / 8 consecutive dims of its two heads.

@@ -75,6 +75,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // suspend the thread for longer than the whole limit.
 constexpr uint64_t kShortWaitNs = 1000000;  // 1 ms
 
+// True in exactly one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Wait for the phase of `bar` with the given parity to complete.  Returns
 // false if it did not within limit_ns (the caller then flags and aborts), or,
 // when abort_flag is given, once another warp of the CTA has set it.

@@ -14,13 +14,10 @@ namespace pa {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 constexpr int kMaxCtasPerSm = 8;
-constexpr int kMaxRangesPerSm = 16;  // ranges of the work list on an SM: 4-bit pools run several per CTA
-constexpr int kFp4WideGroupCtas = 3;
 constexpr int kDefaultCtasPerSmMma = 4;  // default CTAs per SM on the bf16 tensor-core path
 // Decode workspace: the status head, one merge counter per CTA, then two
-// partial slots per CTA (over 4-bit pools: per range) of the launch's grid
-// (pa_decode_workspace_bytes sizes it for kMaxRangesPerSm on every SM, the most
-// any launch has); a slot is [G][D]
+// partial slots per CTA of the launch's grid (pa_decode_workspace_bytes sizes
+// it for kMaxCtasPerSm CTAs on every SM, the largest grid); a slot is [G][D]
 // floats of o plus [G][2] floats of (m, l).
 constexpr int kSlotExtraFloatsPerHead = 2;
 // floats of one partial slot, a multiple of 4 so that every slot is 16-byte aligned
@@ -49,7 +46,7 @@ constexpr int kTileUnits = 4;
 #define PA_SEG_UNITS_FP8 24
 #endif
 #ifndef PA_SEG_UNITS_FP4
-#define PA_SEG_UNITS_FP4 24
+#define PA_SEG_UNITS_FP4 8
 #endif
 constexpr int kMaxSegUnits = 4096;  // bound of pa_debug_set_seg_units
 // Shares of the decode's CTAs by dispatch wave (the CTAs of a launch take the SMs in waves of one
@@ -60,9 +57,6 @@ constexpr int kMaxSegUnits = 4096;  // bound of pa_debug_set_seg_units
 constexpr int kWaveWeight = 64;
 #ifndef PA_WAVE_SKEW_FP8
 #define PA_WAVE_SKEW_FP8 2
-#endif
-#ifndef PA_WAVE_SKEW_FP4
-#define PA_WAVE_SKEW_FP4 2
 #endif
 
 struct DecodeParams {
@@ -130,7 +124,6 @@ struct DecodeVariant {
     bool merge_in_kernel_ok;   // `in` has the in-kernel merge
     void (*launch)(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, int grid, int smem,
                    int merge_grid, int merge_smem, cudaStream_t stream);
-    int ranges_per_cta = 1;  // ranges of the plan that one CTA takes (the grid passed to launch counts ranges)
 };
 
 // Compiled variants.  `group` is Hq / Hkv; the CUDA-core path has exact
@@ -142,7 +135,7 @@ bool decode_variant_bf16_fma(int head_dim, int block_size, int group, DecodeVari
 // bf16 queries and outputs over FP8 (E4M3) pools, CUDA-core path.
 bool decode_variant_fp8(int head_dim, int block_size, int group, DecodeVariant* out);
 // bf16 queries and outputs over 4-bit pools, tensor-core path.
-bool decode_variant_fp4(int head_dim, int block_size, int group, DecodeVariant* out);
+bool decode_variant_fp4(int head_dim, int block_size, int group, int num_seqs, bool fixed, DecodeVariant* out);
 
 // The decode of pa_decode_attention / _fp8 (pa_api.cu): checks, plan and launch.
 // Refuses a workspace smaller than the bytes its own grid touches (the status

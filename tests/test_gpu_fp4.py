@@ -253,17 +253,21 @@ def test_decode_flags_bad_inputs():
 
 
 def test_decode_wait_timeout_is_reported():
-    """A wait limit far below a DRAM round trip: the kernel reports it and the context stays usable."""
+    """A wait limit far below a DRAM round trip: the kernel reports it and the context stays usable.  The queries are
+    in L2 and the pools, larger than it, are not, so that the first tiles are still on their way when they are wanted."""
     import paged_kv_cache_280_gb300 as pa
 
-    c = Case(14, 32, 8, 128, 16, [2000] * 16)
+    c = Case(14, 32, 8, 128, 16, [8000] * 32)
+    c.check(c.run(), seqs=[0])
+    q, kp, vp, tab, lens = c.dev
+    out = q.clone()
     try:
         pa.pa_debug_set_wait_limit_ns(1)
-        c.run()
+        pa.pa_decode_attention_fp4(out, q, kp, vp, *c.scales, tab, lens, 8000, c.scale, c.ws)
         assert status_word(c.ws) & pa.PA_DEV_WAIT_TIMEOUT
     finally:
         pa.pa_debug_set_wait_limit_ns(0)
-    c.check(c.run(), seqs=[0, 15])
+    c.check(c.run(), seqs=[0, 31])
 
 
 def test_decode_on_another_stream_and_captured():
