@@ -23,14 +23,13 @@ constexpr int kStages = 2;   // ring stages per warp
 constexpr int kStageTok = 32;
 constexpr size_t partial_slot_bytes_max(int d) { return (size_t)(kMaxGroup * (d + kSlotExtraFloatsPerHead) + 3) / 4 * 16; }
 
-// What a warp has left of a segment at the end of its part: slot 0 a piece that continues a segment, slot
-// 1 a segment's first piece, if the segment goes on.
-struct Fp4Left {
+// What a warp has left of a segment at the end of its part: slot 0 a piece that continues a segment, slot 1 a
+// segment's first piece, if the segment goes on.
+struct alignas(16) Fp4Left {
     int32_t b, h;
-    int32_t kind;  // 0 none; else bit 0: the segment starts in this piece, bit 1: it ends in it
+    int32_t kind;  // 0 none; else 4, and bit 0: the segment starts in this piece, bit 1: it ends in it
     int32_t pad;
 };
-
 // kWarps: 16, one CTA per SM (512 threads of 128 registers), or 8 where a batch's prefix arrays leave no
 // room for 16 rings.
 template <int D, int BS, int kWarps>
@@ -39,8 +38,8 @@ struct Fp4Layout {
     static constexpr int kTile = BS * fp4_row_bytes(D);
     static constexpr int kStageBytes = 2 * TPS * kTile;  // K of its tiles, then their V
     static constexpr int kRing = kStages * kStageBytes;  // per warp; slot 1's state goes here once the ring is idle
-    static constexpr int kDescOff = kWarps * kRing;                  // int2 per stage
-    static constexpr int kBarOff = kDescOff + kWarps * kStages * 8;  // full barrier per stage
+    static constexpr int kDescOff = kWarps * kRing;                  // int4 per stage
+    static constexpr int kBarOff = kDescOff + kWarps * kStages * 16;  // full barrier per stage
     static constexpr int kLeftOff = (kBarOff + kWarps * kStages * 8 + 15) / 16 * 16;  // Fp4Left [kWarps][2]
     static constexpr int kWsumOff = kLeftOff + kWarps * 2 * 16;
     static constexpr int kSlot0Off = (kWsumOff + 2 * kWarps * 4 + 15) / 16 * 16;  // [kWarps][partial_slot_floats]
@@ -60,6 +59,74 @@ __device__ __forceinline__ Plan fp4_plan(const DecodeParams& p, const int32_t* p
                             fp4_ranges(tiles, p.num_ctas, p.partition_tiles, BS), p.wave_ctas, p.wave_skew);
 }
 
+// The plan's ranges in 32 bits, where the batch allows (`small`): the same arithmetic as Plan's without
+// partitions and skew.  Both kernels do it before anything is requested from HBM (or with the merge at
+// the end of everything), so it is worth keeping short.
+struct Fp4Ranges {
+    const Plan& P;
+    bool small;
+    uint32_t U, C, q, r;
+    float c_per_unit;
+    __device__ __forceinline__ explicit Fp4Ranges(const Plan& plan) : P(plan) {
+        small = P.PT == 0 && P.KS == 0 && P.U < (int64_t)1 << 31;
+        U = (uint32_t)P.U, C = (uint32_t)P.C;
+        q = U / max(C, 1u), r = U - q * C;
+        c_per_unit = (float)C / (float)U;
+    }
+    // the first unit of CTA c's range, ceil(c U / C) = c (U / C) + ceil(c (U % C) / C)
+    __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c * r + C - 1) / C; }
+    // where unit x falls: its sequence, KV head, and the tile of the segment at or after it
+    __device__ __forceinline__ void locate(uint32_t x, int32_t& b, int32_t& h, int32_t& j) const {
+        const uint32_t K = Plan::K, A = P.A, H = P.Hkv;
+        int lo = 0, hi = P.B - 1;  // largest sequence whose units start at or before x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (H * (K * P.pref[mid] + A * mid) <= x)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const uint32_t span = K * P.nblocks(lo) + A, local = x - H * (K * P.pref[lo] + A * lo);
+        const uint32_t hh = local / span, rem = local - hh * span;
+        b = lo, h = (int32_t)hh, j = (int32_t)(rem <= A ? 0 : (rem - A + K - 1) / K);
+    }
+    // the CTA whose range holds tile t of segment (b, h): the largest c with start(c) <= its unit
+    __device__ __forceinline__ int cta_of(int64_t t, int b, int h) const {
+        if (!small) return P.cta_of_seg(t, b, h);
+        const uint32_t x = (uint32_t)(Plan::K * t + (int64_t)P.A * ((int64_t)P.Hkv * b + h + 1));
+        int c = min((int)(C - 1), (int)((float)x * c_per_unit));  // off by one at most: C <= 2^16, and 24 bits of x
+        while (c + 1 < (int)C && start(c + 1) <= x) ++c;
+        while (c > 0 && start(c) > x) --c;
+        return c;
+    }
+};
+
+// The first tile of part w (0 .. kWarps) of CTA c's range, and in seq a sequence at or before the one that
+// holds it.  Without partitions the parts are of equal cost in the plan's units, with partitions of equal
+// numbers of tiles.
+template <int kWarps>
+__device__ __forceinline__ int32_t fp4_part_start(const Fp4Ranges& R, int c, int w, int32_t& seq) {
+    const Plan& P = R.P;
+    int s0 = 0, s1 = 0;
+    int64_t split;
+    if (P.PT > 0) {
+        const int64_t r0 = P.cta_start(c, &split, &s0), r1 = P.cta_start(c + 1, &split, &s1);
+        seq = s0;
+        return (int32_t)(r0 + (r1 - r0) * w / kWarps);
+    }
+    if (c + 1 == P.C && w == kWarps) return (int32_t)P.T;
+    if (R.small) {
+        const uint32_t u0 = R.start(c), u1 = R.start(c + 1);
+        int32_t h, j;
+        R.locate(u0 + (uint32_t)((uint64_t)(u1 - u0) * w / kWarps), seq, h, j);
+        return P.Hkv * P.pref[seq] + h * P.nblocks(seq) + j;
+    }
+    const int64_t u0 = P.start_unit(c), u1 = P.start_unit(c + 1);
+    const int64_t t = P.first_tile_at_unit(u0 + (u1 - u0) * w / kWarps, &split, &s0);
+    seq = s0;
+    return (int32_t)t;
+}
+
 // As plan_matches, for a plan built for a 4-bit pool (its magic word differs, since its ranges do).
 __device__ __forceinline__ bool fp4_plan_matches(const DecodeParams& p, int bs) {
     const int32_t* pl = p.plan;
@@ -73,37 +140,83 @@ __device__ __forceinline__ bool fp4_plan_matches(const DecodeParams& p, int bs) 
            __ldg(pl + kPlanWWaveSkew) == p.wave_skew;
 }
 
-// How the merge enumerates its items (see merge_fp4_kernel).
-__host__ __device__ inline bool fp4_merge_wide(int num_seqs, int num_kv_heads, int ranges) {
-    return (int64_t)num_seqs * num_kv_heads <= ranges;
-}
-
-// A stage's descriptor: x = valid tokens (1 .. 32) | flags | KV head << 16, y = sequence.
+// A stage's descriptor: x = valid tokens (1 .. 32) | flags | KV head << 16, y = sequence, z = stages of its piece.
 enum StageFlag { kFirst = 64, kLast = 128, kStarts = 256, kEnds = 512 };
 
-// Sum of a run of pieces for one query head: lane `lane` holds D / 32 elements.
+// max over the warp (no operand is a NaN).
+__device__ __forceinline__ float warp_max(float x) {
+    const int32_t i = __float_as_int(x), o = i ^ ((i >> 31) & 0x7fffffff);  // integers in the floats' order
+    const int32_t r = __reduce_max_sync(0xffffffffu, o);
+    return __int_as_float(r ^ ((r >> 31) & 0x7fffffff));
+}
+
+// One query head's sum over pieces: E elements a lane.
 template <int E>
 struct Fp4Sum {
-    float m = -INFINITY, l = 0.f, a[E];
-    __device__ __forceinline__ Fp4Sum() {
+    float m, l, a[E];  // m and l the same in every lane
+    __device__ __forceinline__ void reset() {
+        m = -INFINITY, l = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) a[e] = 0.f;
     }
-    __device__ __forceinline__ void add(float om, float ol, const float* oa) {
-        const float mc = fmaxf(m, om);
-        const float f = m == mc ? 1.f : ex2_approx(m - mc), w = om == mc ? 1.f : ex2_approx(om - mc);
-        l = l * f + w * ol;
+    // Adds up to 32 pieces, one to each lane in `set`, in order of the lanes: ml(lane) loads a lane's piece's (m, l)
+    // for this head, at(k) is the address of lane k's piece's elements.  The loads of four pieces go together,
+    // the first four with the (m, l).
+    template <class Ml, class At>
+    __device__ __forceinline__ void add(uint32_t set, int lane, Ml ml_of, At at) {
+        const bool mine = set >> lane & 1;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (mine) ml = ml_of();
+        float w = 0.f;
+        bool first = true;
+        while (set != 0) {
+            int k[4];
+            float x[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = a[e] * f + w * oa[e];
-        m = mc;
+            for (int i = 0; i < 4; ++i) {
+                k[i] = __ffs(set) - 1;
+                set &= set - 1;  // stays 0
+                if (k[i] >= 0) {
+                    const float* src = at(k[i]);
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(src + e);
+                        x[i][e] = v.x, x[i][e + 1] = v.y;
+                    }
+                }
+            }
+            if (first) {
+                first = false;
+                const float to = fmaxf(m, warp_max(ml.x));
+                const float f = to == m ? 1.f : ex2_approx(m - to);
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) a[e] *= f;
+                m = to;
+                w = !mine ? 0.f : ml.x == m ? 1.f : ex2_approx(ml.x - m);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k[i] >= 0) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k[i]);
+                    l = fmaf(wk, __shfl_sync(0xffffffffu, ml.y, k[i]), l);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) a[e] = fmaf(wk, x[i][e], a[e]);
+                }
+        }
     }
-    __device__ __forceinline__ void store_out(__nv_bfloat16* row, int lane, float oscale) const {
+    __device__ __forceinline__ void store_out(__nv_bfloat16* dst, float oscale) const {
         const float r = oscale / l;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(row + E * lane + e) = pack_bf16x2(a[e] * r, a[e + 1] * r);
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(a[e] * r, a[e + 1] * r);
     }
 };
+
+// The lane that holds set bit number r of `set` (r < popc(set)).
+__device__ __forceinline__ int nth_set_lane(uint32_t set, int r, int lane) {
+    const bool is = (set >> lane & 1) && __popc(set & ((1u << lane) - 1)) == r;
+    return __ffs(__ballot_sync(0xffffffffu, is)) - 1;
+}
 
 template <int D, int BS, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(const DecodeParams p) {
@@ -122,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     Fp4Left* left = reinterpret_cast<Fp4Left*>(smem + L::kLeftOff);
     const uint32_t ring = smem_u32(smem) + warp * L::kRing;
     const uint32_t bar = smem_u32(smem) + L::kBarOff + warp * kStages * 8;
-    int2* desc = reinterpret_cast<int2*>(smem + L::kDescOff) + warp * kStages;
+    int4* desc = reinterpret_cast<int4*>(smem + L::kDescOff) + warp * kStages;
 
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
@@ -139,21 +252,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     const Plan P = fp4_plan<BS>(p, pref, upref);
     pdl_launch_dependents();
     // this warp's part of the CTA's range, and a sequence at or before its start: two searches, lanes 0 and 1
-    int64_t tb = 0, split = -1;
-    int seqh = 0;
-    if (P.T > 0 && c < P.C && lane < 2) {
-        const int w = warp + lane;
-        if (!fixed) {
-            const int64_t u0 = P.start_unit(c), u1 = P.start_unit(c + 1), x = u0 + (u1 - u0) * w / kWarps;
-            tb = c + 1 == P.C && w == kWarps ? P.T : P.first_tile_at_unit(x, &split, &seqh);
-        } else {
-            const int64_t r0 = P.cta_start(c, &split, &seqh);
-            int dummy;
-            const int64_t r1 = P.cta_start(c + 1, &split, &dummy);
-            tb = r0 + (r1 - r0) * w / kWarps;
-        }
-    }
-    const int32_t t0 = (int32_t)__shfl_sync(0xffffffffu, tb, 0), t1 = (int32_t)__shfl_sync(0xffffffffu, tb, 1);
+    int32_t tb = 0, seqh = 0;
+    if (P.T > 0 && c < P.C && lane < 2) tb = fp4_part_start<kWarps>(Fp4Ranges(P), c, warp + lane, seqh);
+    const int32_t t0 = __shfl_sync(0xffffffffu, tb, 0), t1 = __shfl_sync(0xffffffffu, tb, 1);
     const int seq0 = __shfl_sync(0xffffffffu, seqh, 0);
 
     // The walk of the copies, kStages stages ahead of the computation.  Whatever stays the same within a
@@ -163,6 +264,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     PieceIter<false> it;
     it.init(P, t0, t1, -1, seq0, seq0);
     int b = 0, j = 0, j1 = 0, rem = 0, pflags = 0;  // sequence; next tile, end tile; tokens from tile j on; flags
+    int pstages = 0;                                // stages of the piece
     const uint8_t *kp = nullptr, *vp = nullptr;     // the pools at the piece's head
     int32_t blk = 0;                                // lane i: the block of tile i of the chunk
     int ci = 0;                                     // next tile within the chunk
@@ -182,6 +284,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
         if (!it.next(P, b, h, j0, j1)) return false;
         j = j0;
         rem = lens_s[b] - j0 * BS;
+        pstages = (j1 - j0 + TPS - 1) / TPS;
         pflags = kFirst | (j0 == 0 ? kStarts : 0) | (j1 == P.nblocks(b) ? kEnds : 0) | h << 16;
         kp = p.k_pool + (size_t)h * L::kTile;
         vp = p.v_pool + (size_t)h * L::kTile;
@@ -197,14 +300,11 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
         }
     }
     const uint32_t block_bytes = (uint32_t)Hkv * L::kTile;  // < 2^31 (checked on the host)
-    // Copy the walk's next stage into ring slot s (whose previous contents this warp has read).
-    auto issue = [&](int s) {
-        const int nt = TPS == 1 ? 1 : min(TPS, j1 - j);
-        const bool last = j + nt == j1;
+    // Copy nt tiles of the walk into ring slot s (whose previous contents this warp has read).
+    auto copy = [&](int s, int nt) {
         const uint64_t o0 = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, blk, ci) * block_bytes;
         const uint64_t o1 = TPS == 1 ? 0 : (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, blk, (ci + 1) & 31) * block_bytes;
         if (elect_one()) {
-            desc[s] = make_int2(min(nt * BS, rem) | pflags | (last ? kLast : 0), b);
             const uint32_t full = bar + 8 * s, dst = ring + s * L::kStageBytes;
             mbar_arrive_expect_tx(full, (uint32_t)(nt * 2 * L::kTile));
             bulk_load_hint(dst, kp + o0, L::kTile, full, policy);
@@ -214,11 +314,18 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
                 bulk_load_hint(dst + (TPS + 1) * L::kTile, vp + o1, L::kTile, full, policy);
             }
         }
+        ci += nt;
+    };
+    // The walk's next stage, any: its descriptor and copies, then the walk moves on.
+    auto issue = [&](int s) {
+        const int nt = TPS == 1 ? 1 : min(TPS, j1 - j);
+        const bool last = j + nt == j1;
+        if (lane == 0) desc[s] = make_int4(min(nt * BS, rem) | pflags | (last ? kLast : 0), b, pstages, 0);
+        copy(s, nt);
         __syncwarp();
         pflags &= ~kFirst;
         j += nt;
         rem -= nt * BS;
-        ci += nt;
         if (last)
             have = next_piece();
         else if (ci == 32)
@@ -232,28 +339,54 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     bool ok = true;
     int s = 0;
     uint32_t parity = 0;
+    int c_left = 0;  // stages of the piece in hand that are still to be computed
+    auto wait = [&]() {
+        if (!__all_sync(0xffffffffu, mbar_test_wait(bar + 8 * s, parity)))
+            ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * s, parity, p.wait_limit_ns));
+        return ok;
+    };
     while (used < issued) {
-        const int2 d = desc[s];
+        // A run of stages inside pieces: full ones to compute, full ones to copy, no table chunk to fetch.
+        int n = min(c_left, (j1 - j + TPS - 1) / TPS) - 1;
+        n = have && !(pflags & kFirst) ? min(n, (32 - ci) / TPS) : 0;
+        if (n >= kStages) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                if (!wait()) break;
+                const uint32_t kb = ring + s * L::kStageBytes;
+                uint32_t pb[4];
+                st.template weights<false>(kb, kStageTok, lane, pb);
+                st.template accumulate<false>(kb + TPS * L::kTile, kStageTok, lane, pb);
+                __syncwarp();
+                ++used;
+                copy(s, TPS);
+                ++issued;
+                if (++s == kStages) s = 0, parity ^= 1;
+            }
+            if (!ok) break;
+            if (lane < kStages) desc[lane] = make_int4(kStageTok | pflags, b, pstages, 0);  // what every slot now holds
+            __syncwarp();
+            c_left -= n;
+            j += n * TPS;
+            rem -= n * kStageTok;
+            if (ci == 32) load_chunk();
+        }
+        // Any stage.
+        const int4 d = desc[s];
         const int sh = d.x >> 16, valid = d.x & 63;
         if (d.x & kFirst) {
             st.load_q(static_cast<const __nv_bfloat16*>(p.q) + ((size_t)d.y * Hq + (size_t)sh * G) * D, G, lane, p.scale_log2);
             st.reset();
+            c_left = d.z;
         }
-        if (!__all_sync(0xffffffffu, mbar_test_wait(bar + 8 * s, parity))) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar + 8 * s, parity, p.wait_limit_ns));
-            if (!ok) break;
-        }
+        if (!wait()) break;
         const uint32_t kb = ring + s * L::kStageBytes, vb = kb + TPS * L::kTile;
         uint32_t pb[4];
-        if (valid == kStageTok) {
-            st.template weights<false>(kb, valid, lane, pb);
-            st.template accumulate<false>(vb, valid, lane, pb);
-        } else {
-            st.template weights<true>(kb, valid, lane, pb);
-            st.template accumulate<true>(vb, valid, lane, pb);
-        }
+        st.template weights<true>(kb, valid, lane, pb);
+        st.template accumulate<true>(vb, valid, lane, pb);
         __syncwarp();
         ++used;
+        --c_left;
         if (have) {
             issue(s);
             ++issued;
@@ -280,63 +413,64 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
         }
     }
     __syncthreads();
-    // Runs of pieces of one segment, in warp order: a run opens with a piece in slot 1, or with the CTA's first
-    // piece, and goes on through the following warps' slot 0.  One warp per (run, head).
+    // Lane i looks at slot i (slot 0 of warp 0, its slot 1, slot 0 of warp 1, ...).  A run of pieces of one
+    // segment opens with a slot 1, or with the CTA's first piece, and goes on through the slots 0 after it.
+    // An item is one query head of one run; the warps take them in turn.
+    static_assert(2 * kWarps <= 32, "a lane per slot");
     constexpr int E = D / 32;
-    int item = 0;
-    for (int i = 0; i < 2 * kWarps; ++i) {  // slots in order: warp 0's slot 0, its slot 1, ...
-        const Fp4Left f = left[i];
-        if (f.kind == 0) continue;
-        // the run goes on through the slots 0 of the warps up to wl; a warp without a part has none
-        const int w0 = i >> 1;
-        int wl = w0, ends = f.kind & 2;
-        for (int w = w0 + 1; w < kWarps && !ends; ++w) {
-            const int kind = left[2 * w].kind;
-            if (kind == 0) continue;
-            ends = kind & 2;
-            wl = w;
-        }
-        for (int hq = 0; hq < G; ++hq, ++item) {
-            if (item % kWarps != warp) continue;
-            Fp4Sum<E> sum;
-            for (int w = w0; w <= wl; ++w) {
-                if (w > w0 && left[2 * w].kind == 0) continue;
-                const float* src = w == w0 && (i & 1) ? reinterpret_cast<const float*>(smem + w0 * L::kRing)
-                                                      : slot0 + w * slot_floats;
-                const float2 ml = *reinterpret_cast<const float2*>(src + G * D + 2 * hq);
-                float x[E];
+    const Fp4Left f = left[lane & (2 * kWarps - 1)];
+    const uint32_t filled = __ballot_sync(0xffffffffu, lane < 2 * kWarps && f.kind != 0);
+    const uint32_t ending = __ballot_sync(0xffffffffu, lane < 2 * kWarps && (f.kind & 2));
+    const uint32_t heads = filled & (0xaaaaaaaau | (filled & (0u - filled)));
+    const int items = __popc(heads) * G;
+    auto state = [&](int slot) {
+        return slot & 1 ? reinterpret_cast<const float*>(smem + (slot >> 1) * L::kRing) : slot0 + (slot >> 1) * slot_floats;
+    };
+    for (int item = warp; item < items; item += kWarps) {
+        const int r = item / G, hq = item - r * G;
+        const int head = nth_set_lane(heads, r, lane);
+        const uint32_t later = heads & ~((2u << head) - 1);  // the runs after it
+        const uint32_t run = filled & (0xffffffffu << head) & (later ? (later & (0u - later)) - 1 : 0xffffffffu);
+        const int fb = __shfl_sync(0xffffffffu, f.b, head), fh = __shfl_sync(0xffffffffu, f.h, head);
+        const int starts = __shfl_sync(0xffffffffu, f.kind, head) & 1, ends = (run & ending) ? 2 : 0;
+        Fp4Sum<E> sum;
+        sum.reset();
+        sum.add(run, lane, [&]() { return *reinterpret_cast<const float2*>(state(lane) + G * D + 2 * hq); },
+                [&](int k) { return state(k) + hq * D + E * lane; });
+        if (starts && ends) {
+            sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)fb * Hq + (size_t)fh * G + hq) * D + E * lane, p.out_scale);
+        } else {  // slot 1: a split segment's first piece; slot 0: one that continues it
+            float* dst = p.partials + (size_t)(2 * c + starts) * slot_floats;
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = src[hq * D + E * lane + e];
-                sum.add(ml.x, ml.y, x);
-            }
-            if ((f.kind & 1) && ends) {
-                sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)f.b * Hq + (size_t)f.h * G + hq) * D, lane,
-                              p.out_scale);
-            } else {  // slot 1: a split segment's first piece; slot 0: one that continues it
-                float* dst = p.partials + (size_t)(2 * c + (f.kind & 1)) * slot_floats;
-#pragma unroll
-                for (int e = 0; e < E; ++e) dst[hq * D + E * lane + e] = sum.a[e];
-                if (lane == 0) dst[G * D + 2 * hq] = sum.m, dst[G * D + 2 * hq + 1] = sum.l;
-            }
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<float2*>(dst + hq * D + E * lane + e) = make_float2(sum.a[e], sum.a[e + 1]);
+            if (lane == 0) *reinterpret_cast<float2*>(dst + G * D + 2 * hq) = make_float2(sum.m, sum.l);
         }
-        if (wl > w0) i = 2 * wl;  // the slots 0 up to wl are taken
     }
 }
 
-// The merge of split segments: M = max m_p, out = sum 2^(m_p - M) o_p / sum 2^(m_p - M) l_p over a
-// segment's pieces.  An item is one query head of one segment.  With no more segments than ranges
-// (long contexts: many pieces each) the items are enumerated by segment and the four warps of a CTA
-// share an item's pieces; with more (most segments whole, a split one in two or three pieces) they
-// are enumerated by range boundary, the first boundary inside a segment naming it, a warp to an item.
-// The loads of four pieces are in flight together.  Pieces are folded in a fixed order: a call's
-// result does not depend on timing.
+// How the merge goes about its items (see merge_fp4_kernel): by segment, and a CTA to an item.
+__host__ __device__ inline bool fp4_merge_by_segment(int num_seqs, int num_kv_heads, int ctas) {
+    return (int64_t)num_seqs * num_kv_heads <= ctas;
+}
+__host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads, int ctas) {
+    return (int64_t)num_seqs * num_kv_heads * 8 <= ctas;
+}
+
+// The merge of split segments: M = max m_p, out = sum 2^(m_p - M) o_p / sum 2^(m_p - M) l_p over the
+// CTAs that hold a piece of the segment, in their order.  An item is one query head of one segment.  With
+// no more segments than CTAs the items are enumerated by segment, else by the boundary between two
+// CTAs' ranges, the first boundary inside a segment naming it.  A warp takes an item, or, when segments
+// have eight pieces or more, the four warps of a CTA share its pieces.  The kernel works out its
+// first items while the decode kernel's last CTAs still run; then one round of loads brings the states.
+constexpr int kMergeWarps = kMergeThreads / 32;
 template <int D, int BS>
 __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const DecodeParams p) {
     extern __shared__ __align__(16) int32_t msm[];
-    constexpr int E = D / 32;  // output elements per lane
-    constexpr int kW = kMergeThreads / 32;
-    __shared__ float part[kW][D + 2];
+    constexpr int E = D / 32;
+    __shared__ float part[kMergeWarps][D + 2];
     const int B = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool fixed = p.partition_tiles > 0;
     int32_t* pref = msm;
     int32_t* upref = pref + (B + 1);
@@ -350,119 +484,75 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const DecodePa
         scan_lengths<BS, kMergeThreads>(p, false, pref, upref, lens_s, wsum);
     __syncthreads();
     const Plan P = fp4_plan<BS>(p, pref, upref);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Fp4Ranges R(P);
     const size_t slot_floats = partial_slot_floats(G, D);
-    const bool wide = fp4_merge_wide(B, Hkv, p.num_ctas);
-    const int step = wide ? kW : 1, first = wide ? warp : 0;  // this warp's pieces of an item
-    const int64_t items = wide ? (int64_t)B * Hkv * G : (int64_t)(P.C - 1) * G;
-    const int64_t stride = (int64_t)gridDim.x * (wide ? 1 : kW);
-    int64_t item = wide ? blockIdx.x : (int64_t)blockIdx.x * kW + warp;
-    // the item's sequence, KV head, first range and pieces; false if its segment is not split (or named elsewhere)
-    auto named = [&](int64_t i, int& b, int& h, int& ca, int& np) -> bool {
-        if (wide) {
-            const int seg = (int)(i / G);
-            b = seg / Hkv;
-            h = seg - b * Hkv;
-            const int nb = P.nblocks(b);
-            if (nb == 0) return false;
-            const int64_t s0 = P.seg_start(b, h);
-            ca = P.cta_of_seg(s0, b, h);
-            np = P.cta_of_seg(s0 + nb - 1, b, h) - ca + 1;
-            return np > 1;
+    const bool by_segment = fp4_merge_by_segment(B, Hkv, p.num_ctas), shared = fp4_merge_shared(B, Hkv, p.num_ctas);
+    const int64_t items = P.T == 0 ? 0 : (int64_t)G * (by_segment ? B * Hkv : P.C - 1);
+    // an item's sequence, KV head, first CTA and pieces; false if its segment is not split, or named elsewhere
+    auto named = [&](int64_t item, int& b, int& h, int& ca, int& np) -> bool {
+        const int i = (int)(item / G);
+        if (by_segment) {
+            b = i / Hkv;
+            h = i - b * Hkv;
+        } else {
+            int32_t j;
+            if (R.small) {
+                R.locate(R.start(i + 1), b, h, j);
+            } else {
+                int64_t split;
+                int seq;
+                const int64_t t = P.cta_start(i + 1, &split, &seq);
+                if (t >= P.T) return false;
+                b = P.find_seq(P.pref, t);
+                const int64_t local = t - (int64_t)Hkv * P.pref[b];
+                h = (int)(local / P.nblocks(b));
+                j = (int)(local - (int64_t)h * P.nblocks(b));
+            }
+            if (j == 0 || j >= P.nblocks(b)) return false;  // the boundary falls between segments
         }
-        int64_t split;
-        int seq;
-        const int c = 1 + (int)(i / G);
-        const int64_t t = P.cta_start(c, &split, &seq);
-        if (t >= P.T) return false;
-        b = P.find_seq(P.pref, t);
         const int nb = P.nblocks(b);
-        const int64_t local = t - (int64_t)Hkv * P.pref[b];
-        h = (int)(local / nb);
-        if (local == (int64_t)h * nb) return false;  // the boundary falls between segments
-        const int64_t s0 = (int64_t)Hkv * P.pref[b] + (int64_t)h * nb;
-        ca = P.cta_of_seg(s0, b, h);
-        if (ca != c - 1) return false;  // an earlier boundary of this segment names it
-        np = P.cta_of_seg(s0 + nb - 1, b, h) - ca + 1;
-        return true;
+        if (nb == 0) return false;
+        const int64_t s0 = P.seg_start(b, h);
+        ca = R.cta_of(s0, b, h);
+        if (!by_segment && ca != i) return false;  // an earlier boundary of this segment names it
+        np = R.cta_of(s0 + nb - 1, b, h) - ca + 1;
+        return np > 1;
     };
+    const int64_t step = shared ? gridDim.x : (int64_t)gridDim.x * kMergeWarps;
+    int64_t item = shared ? blockIdx.x : (int64_t)blockIdx.x * kMergeWarps + warp;
     int b = 0, h = 0, ca = 0, np = 0;
-    bool have = P.T > 0 && item < items && named(item, b, h, ca, np);  // found while the decode runs
+    bool have = item < items && named(item, b, h, ca, np);
     pdl_wait_prerequisites();  // the decode grid has finished; its partials are in memory
-    while (P.T > 0 && item < items) {
+    while (item < items) {
         if (have) {
             const int hq = (int)(item % G);
-            float m = -INFINITY, l = 0.f, a[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) a[e] = 0.f;
-            for (int i0 = first; i0 < np; i0 += 4 * step) {
-                float2 ml[4];
-                float x[4][E];
-                float mc = m;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int q = i0 + i * step;
-                    if (q < np) {
-                        const float* sp = piece_slot(p.partials, slot_floats, ca + q, ca);
-                        ml[i] = __ldcg(reinterpret_cast<const float2*>(sp + G * D) + hq);
-                        if constexpr (E == 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + hq * D) + lane);
-                            x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-                        } else {
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(sp + hq * D) + lane);
-                            x[i][0] = v.x, x[i][1] = v.y;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i0 + i * step < np) mc = fmaxf(mc, ml[i].x);
-                const float resc = m == mc ? 1.f : ex2_approx(m - mc);
-                l *= resc;
-#pragma unroll
-                for (int e = 0; e < E; ++e) a[e] *= resc;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i0 + i * step < np) {
-                        const float w = ex2_approx(ml[i].x - mc);
-                        l = fmaf(w, ml[i].y, l);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) a[e] = fmaf(w, x[i][e], a[e]);
-                    }
-                m = mc;
+            Fp4Sum<E> sum;
+            sum.reset();
+            for (int base = 0; base < np; base += 32) {  // lane k's piece is number base + k
+                const int n = min(32, np - base);
+                uint32_t set = n == 32 ? 0xffffffffu : (1u << n) - 1;
+                if (shared) set &= 0x11111111u << warp;
+                sum.add(set, lane,
+                        [&]() { return __ldcg(reinterpret_cast<const float2*>(piece_slot(p.partials, slot_floats, ca + base + lane, ca) + G * D) + hq); },
+                        [&](int k) { return piece_slot(p.partials, slot_floats, ca + base + k, ca) + hq * D + E * lane; });
             }
-            if (wide) {
-                // fold the warps' sums, in warp order
+            if (shared) {
                 __syncthreads();
-                if (lane == 0) part[warp][D] = m, part[warp][D + 1] = l;
 #pragma unroll
-                for (int e = 0; e < E; ++e) part[warp][E * lane + e] = a[e];
+                for (int e = 0; e < E; ++e) part[warp][E * lane + e] = sum.a[e];
+                if (lane == 0) part[warp][D] = sum.m, part[warp][D + 1] = sum.l;
                 __syncthreads();
                 if (warp == 0) {
-                    float mc = m;
-                    for (int w = 1; w < kW && w < np; ++w) mc = fmaxf(mc, part[w][D]);
-                    const float r0 = m == mc ? 1.f : ex2_approx(m - mc);
-                    l *= r0;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) a[e] *= r0;
-                    for (int w = 1; w < kW && w < np; ++w) {
-                        const float f = ex2_approx(part[w][D] - mc);
-                        l = fmaf(f, part[w][D + 1], l);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) a[e] = fmaf(f, part[w][E * lane + e], a[e]);
-                    }
+                    sum.reset();
+                    sum.add((1u << kMergeWarps) - 1, lane, [&]() { return make_float2(part[lane][D], part[lane][D + 1]); },
+                            [&](int k) { return part[k] + E * lane; });
                 }
             }
-            if (!wide || warp == 0) {
-                const float r = p.out_scale / l;
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) +
-                                   ((size_t)b * p.num_q_heads + (size_t)h * G + hq) * D + E * lane;
-#pragma unroll
-                for (int e = 0; e < E; e += 2)
-                    *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(a[e] * r, a[e + 1] * r);
-            }
+            if (!shared || warp == 0)
+                sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)h * G + hq) * D + E * lane,
+                              p.out_scale);
         }
-        item += stride;
+        item += step;
         have = item < items && named(item, b, h, ca, np);
     }
 }
@@ -472,7 +562,7 @@ struct Fp4Variant {
     using L = Fp4Layout<D, BS, kWarps>;
     template <int G>
     static int smem(int num_seqs, bool fixed) { return L::bytes(G, num_seqs, fixed); }
-    static void launch(const DecodeParams& p, const CUtensorMap&, const CUtensorMap&, int grid, int smem_bytes, int /*merge_grid*/,
+    static void launch(const DecodeParams& p, const CUtensorMap&, const CUtensorMap&, int grid, int smem_bytes, int,
                        int merge_smem, cudaStream_t stream) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -486,11 +576,13 @@ struct Fp4Variant {
         cfg.numAttrs = 1;
         if (cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, BS, kWarps>, p) != cudaSuccess) return;
         cudaLaunchConfig_t mcfg = cfg;
-        const int64_t items = fp4_merge_wide(p.num_seqs, p.num_kv_heads, grid)
-                                  ? (int64_t)p.num_seqs * p.num_kv_heads * p.group
-                                  : ((int64_t)(grid - 1) * p.group + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
-        const int64_t most = (int64_t)p.wave_ctas * 8;  // (wave_ctas: the SM count)
-        mcfg.gridDim = dim3((unsigned)(items < 1 ? 1 : items < most ? items : most));
+        if (grid == 1) return;  // one CTA: nothing is split
+        int64_t items = (int64_t)p.group * (fp4_merge_by_segment(p.num_seqs, p.num_kv_heads, grid)
+                                                ? p.num_seqs * p.num_kv_heads
+                                                : grid - 1);
+        if (!fp4_merge_shared(p.num_seqs, p.num_kv_heads, grid)) items = (items + kMergeWarps - 1) / kMergeWarps;
+        const int64_t most = (int64_t)p.wave_ctas * 2;  // (wave_ctas: the SM count)
+        mcfg.gridDim = dim3((unsigned)(items < most ? items : most));
         mcfg.blockDim = dim3(kMergeThreads);
         mcfg.dynamicSmemBytes = merge_smem;
         cudaLaunchKernelEx(&mcfg, merge_fp4_kernel<D, BS>, p);

@@ -31,6 +31,11 @@ __device__ __forceinline__ float ex2_approx(float x) {  // 2^x, 2^-inf = 0
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -210,36 +215,46 @@ struct Fp4State {
     template <bool MASK>
     __device__ __forceinline__ void weights(uint32_t kb, int valid, int lane, uint32_t (&pb)[4]) {
         const int g = lane >> 2;
-        float x[2][4];
+        float x[2][4], y[2][4];  // scores; base-2 exponents of the weights
         scores(kb, 0, lane, x[0]);
         scores(kb + kStep1, kRow1, lane, x[1]);
+        auto exponents = [&]() {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[s][i] *= sc[i & 1];
-                if (MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid) x[s][i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) {
+                    y[s][i] = fmaf(x[s][i], sc[i & 1], -m[i & 1]);
+                    if (MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid) y[s][i] = -INFINITY;
+                }
+        };
+        exponents();  // +inf while m = -inf: no score has been seen
+        const float top = max3(max3(y[0][0], y[0][1], y[0][2]), max3(y[0][3], y[1][0], y[1][1]), fmaxf(y[1][2], y[1][3]));
+        if (__any_sync(0xffffffffu, top > kRaise)) {
+            float n[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                n[i] = -INFINITY;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (!MASK || slot_token(g) + 8 * r + 16 * s < valid) n[i] = fmaxf(n[i], x[s][2 * r + i] * sc[i]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) n[i] = fmaxf(n[i], __shfl_xor_sync(0xffffffffu, n[i], off));
+                n[i] = fmaxf(n[i], m[i]);
             }
-        float n0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        float n1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-        if (__any_sync(0xffffffffu, n0 > m[0] + kRaise || n1 > m[1] + kRaise)) {
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
-                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-            }
-            n0 = fmaxf(n0, m[0]), n1 = fmaxf(n1, m[1]);
             // a head whose scores are all -inf so far keeps its state (nothing is weighed yet)
-            const float a0 = n0 == m[0] ? 1.f : ex2_approx(m[0] - n0), a1 = n1 == m[1] ? 1.f : ex2_approx(m[1] - n1);
+            const float a0 = n[0] == m[0] ? 1.f : ex2_approx(m[0] - n[0]), a1 = n[1] == m[1] ? 1.f : ex2_approx(m[1] - n[1]);
             l[0] *= a0, l[1] *= a1, l[2] *= a0, l[3] *= a1;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][0] *= a0, o[i][1] *= a1, o[i][2] *= a0, o[i][3] *= a1;
-            m[0] = n0, m[1] = n1;
+            m[0] = n[0], m[1] = n[1];
+            exponents();
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            pb[2 * s] = movmatrix_trans(pack_f16x2(ex2_approx(x[s][0] - m[0]), ex2_approx(x[s][1] - m[1])));
-            pb[2 * s + 1] = movmatrix_trans(pack_f16x2(ex2_approx(x[s][2] - m[0]), ex2_approx(x[s][3] - m[1])));
+            pb[2 * s] = movmatrix_trans(pack_f16x2(ex2_approx(y[s][0]), ex2_approx(y[s][1])));
+            pb[2 * s + 1] = movmatrix_trans(pack_f16x2(ex2_approx(y[s][2]), ex2_approx(y[s][3])));
         }
     }
 

@@ -46,7 +46,7 @@ constexpr int kTileUnits = 4;
 #define PA_SEG_UNITS_FP8 24
 #endif
 #ifndef PA_SEG_UNITS_FP4
-#define PA_SEG_UNITS_FP4 8
+#define PA_SEG_UNITS_FP4 18
 #endif
 constexpr int kMaxSegUnits = 4096;  // bound of pa_debug_set_seg_units
 // Shares of the decode's CTAs by dispatch wave (the CTAs of a launch take the SMs in waves of one
