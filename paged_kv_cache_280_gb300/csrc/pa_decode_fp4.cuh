@@ -36,31 +36,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-// Two E4M3 bytes (low byte first) to an f16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
-    uint32_t d;
-    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(b));
-    return d;
-}
-// The eight codes of w to four f16 pairs: byte i to r[i], the byte's low code in the low half.
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t f16x2_low_twice(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
-__device__ __forceinline__ uint32_t f16x2_high_twice(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
-
 // N consecutive 32-bit words of shared memory (N = 1, 2 or 4, naturally aligned).
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {

@@ -27,58 +27,159 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t b) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
-// The scale byte of a group whose largest |x / pool_scale| is amax, and the scale's value.  amax / 6
-// puts the largest element on the largest code; a group with a NaN gets the NaN scale.
-__device__ __forceinline__ uint8_t fp4_scale(float amax, bool has_nan, float& s) {
-    const uint8_t b = has_nan ? kFp4NanScale : (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.f), __NV_SATFINITE, __NV_E4M3);
-    s = e4m3_to_float(b);
-    return b;
+// ---- fp32 pairs (one instruction for two elements) -----------------------------------------------
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+    uint64_t x, y, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+    uint64_t x, y, z, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+    return r;
 }
 
-// Eight codes of y[0..7] = x / pool_scale under scale value s, element i in bits 4 i .. 4 i + 3:
-// E2M1 of fp32(y / s), nearest even, saturated at 6.  A group whose scale rounds to zero, or is NaN,
-// has all codes zero.
-__device__ __forceinline__ uint32_t fp4_codes8(const float* y, float s) {
-    uint32_t w = 0;
-    if (s > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 z = make_float2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
-            w |= (uint32_t)__nv_cvt_float2_to_fp4x2(z, __NV_E2M1, cudaRoundNearest) << (8 * i);
-        }
-    }
-    return w;
-}
+// ---- correctly rounded quotients of many elements by one divisor ----------------------------------
+// With r the correctly rounded reciprocal of b: q = x r is within an ulp of x / b, its remainder x - q b is
+// exact, and q + remainder * r, rounded, is x / b correctly rounded (Markstein 1990).  This needs no term to
+// leave the normal range: kQuotientMax bounds |x| and b's range (its reciprocal is in range with it).
+// Below, where a quotient or a remainder is tiny, the result may be off by a unit of the smallest number; the
+// callers round what is so small to zero.  A zero loses its sign.
+constexpr float kQuotientMax = 1.15292150e18f;  // 2^60
 
-// max |y[i]| of N values; has_nan when one is a NaN.
+struct Divisor {  // of a launch: b, its reciprocal, and whether both are in [2^-60, 2^60]
+    float b, r;
+    bool in_range;
+};
+inline Divisor divisor(float b) { return Divisor{b, 1.f / b, b <= kQuotientMax && b >= 1.f / kQuotientMax}; }
+
+__device__ __forceinline__ float quotient(float x, float b, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, b, x), r, q);
+}
 template <int N>
-__device__ __forceinline__ float fp4_amax(const float* y, bool& has_nan) {
-    float a = 0.f;
-    has_nan = false;
+__device__ __forceinline__ void quotients(const float* x, float b, float r, float* y) {
+    const float2 rr = make_float2(r, r), nb = make_float2(-b, -b);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        a = fmaxf(a, fabsf(y[i]));
-        has_nan |= y[i] != y[i];
+    for (int i = 0; i < N; i += 2) {
+        const float2 v = make_float2(x[i], x[i + 1]), q = mul_f32x2(v, rr);
+        const float2 d = fma_f32x2(fma_f32x2(q, nb, v), rr, q);
+        y[i] = d.x, y[i + 1] = d.y;
     }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // the larger, or NaN if either is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// max |x[i]| of N values, NaN if one is.
+template <int N>
+__device__ __forceinline__ float amax_nan(const float* x) {
+    float a = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) a = max_nan(a, fabsf(x[i]));
     return a;
 }
 
-// The values (without the pool scale) of the eight codes of w, as fp32.
-__device__ __forceinline__ void fp4_values8(uint32_t w, float s, float* x) {
+// ---- quantisation ---------------------------------------------------------------------------------
+// A group's scale from amax, its largest |x| (NaN if it holds one): the byte, and the value and its
+// reciprocal for fp4_codes8.  Division is monotonic, so max |x / b| is amax / b; a sixth of it puts the
+// largest element on the largest code.
+struct Fp4Scale {
+    float s, r;
+    uint8_t byte;
+    bool plain;  // fp4_codes8 may use quotients()
+};
+__device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Divisor& d) {
+    Fp4Scale f;
+    f.plain = d.in_range && amax <= kQuotientMax;
+    if (f.plain) {
+        f.byte = (uint8_t)__nv_cvt_float_to_fp8(quotient(quotient(amax, d.b, d.r), 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
+    } else if (amax != amax) {
+        f.byte = kFp4NanScale;
+    } else {
+        f.byte = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(__fdiv_rn(amax, d.b), 6.f), __NV_SATFINITE, __NV_E4M3);
+    }
+    f.s = e4m3_to_float(f.byte);
+    f.r = f.s > 0.f ? __frcp_rn(f.s) : 0.f;  // 0: every code zero
+    return f;
+}
+
+// Eight codes of x under a group's scale, element i in bits 4 i .. 4 i + 3: E2M1 of fp32(fp32(x / b) / s),
+// nearest even, saturated at 6, with x's sign.  All zero where the scale is zero or NaN.
+__device__ __forceinline__ uint32_t fp4_codes8(const float* x, const Divisor& d, const Fp4Scale& f) {
+    float y[8];
+    if (f.plain) {
+        quotients<8>(x, d.b, d.r, y);
+        quotients<8>(y, f.s, f.r, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = f.s > 0.f ? __fdiv_rn(__fdiv_rn(x[i], d.b), f.s) : 0.f;
+    }
+    uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * i)), __NV_E2M1));
-        x[2 * i] = __low2float(h) * s;
-        x[2 * i + 1] = __high2float(h) * s;
+        const float2 z = make_float2(copysignf(y[2 * i], x[2 * i]), copysignf(y[2 * i + 1], x[2 * i + 1]));
+        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(z, __NV_E2M1, cudaRoundNearest) << (8 * i);
+    }
+    return f.r > 0.f ? w : 0u;
+}
+
+// Two E4M3 bytes (low byte first) to an f16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(b));
+    return d;
+}
+// The eight codes of w to four f16 pairs: byte i to r[i], the byte's low code in the low half.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t f16x2_low_twice(uint32_t v) { return __byte_perm(v, 0, 0x1010); }
+__device__ __forceinline__ uint32_t f16x2_high_twice(uint32_t v) { return __byte_perm(v, 0, 0x3232); }
+
+// The values of the eight codes of w times the pool scale, as fp32: code * s in f16 (exact; s a pair of the
+// group's scale), then one fp32 rounding.
+__device__ __forceinline__ void fp4_values8(uint32_t w, uint32_t s, float pool_scale, float* x) {
+    uint32_t r[4];
+    e2m1x8_to_f16x2(w, r);
+    const float2 p = make_float2(pool_scale, pool_scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t v = mul_f16x2(r[i], s);
+        const float2 y = mul_f32x2(make_float2(f16_lo(v), f16_hi(v)), p);
+        x[2 * i] = y.x, x[2 * i + 1] = y.y;
     }
 }
 
 // Eight elements of a row as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void widen8(const uint4& r, float* x) {
     x[0] = bf16_lo(r.x), x[1] = bf16_hi(r.x), x[2] = bf16_lo(r.y), x[3] = bf16_hi(r.y);
     x[4] = bf16_lo(r.z), x[5] = bf16_hi(r.z), x[6] = bf16_lo(r.w), x[7] = bf16_hi(r.w);
 }
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) { widen8(*reinterpret_cast<const uint4*>(p), x); }
 __device__ __forceinline__ void load8(const float* p, float* x) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;

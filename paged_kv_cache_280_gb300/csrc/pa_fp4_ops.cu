@@ -10,91 +10,122 @@
 namespace pa {
 namespace {
 
-// Token i, slot s = slots[i]: block s / BS, row s % BS of every KV head's record.
+// Token i, slot s = slots[i]: block s / BS, row s % BS of every KV head's record.  A thread takes the same
+// group of K and of V: four 16-byte loads in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(const T* k_new, const T* v_new, uint8_t* k_pool,
                                                                     uint8_t* v_pool, const int64_t* __restrict__ slots,
                                                                     int32_t num_tokens, int32_t num_kv_heads,
-                                                                    int32_t block_size, int64_t pool_slots, float k_scale,
-                                                                    float v_scale, int32_t* status) {
+                                                                    int32_t bs_shift, int64_t pool_slots, const Divisor kd,
+                                                                    const Divisor vd, int32_t* status) {
     pdl_launch_dependents();
     constexpr int U = D / kFp4Group;
-    const int64_t total = (int64_t)num_tokens * num_kv_heads * U;
-    for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < total;
-         idx += (int64_t)gridDim.x * blockDim.x) {
-        const int u = (int)(idx & (U - 1));
-        const uint32_t row = (uint32_t)(idx / U);  // < 2^31 (checked on the host)
-        const int tok = (int)(row / (uint32_t)num_kv_heads), h = (int)(row - (uint32_t)tok * (uint32_t)num_kv_heads);
+    const uint32_t total = (uint32_t)num_tokens * num_kv_heads * U;  // < 2^31 (checked on the host)
+    for (uint32_t idx = blockIdx.x * blockDim.x + threadIdx.x; idx < total; idx += gridDim.x * blockDim.x) {
+        const uint32_t u = idx & (U - 1), row = idx / U;
+        const uint32_t tok = row / (uint32_t)num_kv_heads, h = row - tok * (uint32_t)num_kv_heads;
         const int64_t slot = __ldg(slots + tok);
+        float x[2][16];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const T* src = (kv ? v_new : k_new) + (size_t)row * D + kFp4Group * u;
+            load8(src, x[kv]);
+            load8(src + 8, x[kv] + 8);
+        }
         if (slot < 0) continue;
         if (slot >= pool_slots) {
             if (h == 0 && u == 0) flag_status(status, PA_DEV_BAD_SLOT);
             continue;
         }
-        const int64_t blk = slot / block_size, off = slot - blk * block_size;
-        const int64_t rec = (blk * num_kv_heads + h) * (int64_t)block_size * fp4_row_bytes(D);
+        const int64_t rec = ((slot >> bs_shift) * num_kv_heads + h) * (int64_t)(fp4_row_bytes(D) << bs_shift);
+        const uint32_t off = (uint32_t)slot & ((1u << bs_shift) - 1);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-            const T* src = (kv ? v_new : k_new) + (int64_t)row * D + kFp4Group * u;
-            const float scale = kv ? v_scale : k_scale;
-            float y[16];
-            load8(src, y);
-            load8(src + 8, y + 8);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], scale);
-            bool has_nan;
-            const float amax = fp4_amax<16>(y, has_nan);
-            float s;
-            const uint8_t sb = fp4_scale(amax, has_nan, s);
+            const Divisor& d = kv ? vd : kd;
+            const Fp4Scale f = fp4_scale(amax_nan<16>(x[kv]), d);
             uint8_t* dst = (kv ? v_pool : k_pool) + rec;
-            *reinterpret_cast<uint2*>(dst + off * (D / 2) + 8 * u) = make_uint2(fp4_codes8(y, s), fp4_codes8(y + 8, s));
-            dst[block_size * (D / 2) + off * U + u] = sb;
+            *reinterpret_cast<uint2*>(dst + off * (D / 2) + 8 * u) =
+                make_uint2(fp4_codes8(x[kv], d, f), fp4_codes8(x[kv] + 8, d, f));
+            dst[((D / 2) << bs_shift) + off * U + u] = f.byte;
         }
     }
 }
 
-// out[i] = the values of block blocks[i], every KV head, row and element, in T.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* k_pool, const uint8_t* v_pool,
-                                                                const int32_t* __restrict__ blocks, int64_t num, T* k_out,
-                                                                T* v_out, int32_t num_kv_heads, int32_t block_size,
-                                                                int32_t num_blocks, float k_scale, float v_scale,
-                                                                int32_t* status) {
+// 16 elements to 32-byte-aligned memory in one store (two for fp32): a warp's store covers whole lines.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* x) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void store16(float* p, const float* x) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 8 * i), "f"(x[8 * i]), "f"(x[8 * i + 1]),
+                     "f"(x[8 * i + 2]), "f"(x[8 * i + 3]), "f"(x[8 * i + 4]), "f"(x[8 * i + 5]), "f"(x[8 * i + 6]), "f"(x[8 * i + 7])
+                     : "memory");
+}
+
+// out[i] = the values of block blocks[i], every KV head, row and element, in T.  A thread takes the same group
+// of K and of V, kPer times; a CTA's groups are consecutive.  WIDE: the outputs are 32-byte aligned.
+constexpr int kUnpackPer = 2;
+template <typename T, int D, int BS, bool WIDE>
+__global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* __restrict__ k_pool,
+                                                                const uint8_t* __restrict__ v_pool,
+                                                                const int32_t* __restrict__ blocks, uint32_t cta_per_block,
+                                                                T* k_out, T* v_out, int32_t num_kv_heads, int32_t num_blocks,
+                                                                float k_scale, float v_scale, int32_t* status) {
     pdl_launch_dependents();
     constexpr int U = D / kFp4Group;
-    const int per_block = num_kv_heads * block_size * U;  // < 2^31 (checked on the host)
-    const int64_t total = num * per_block;
-    for (int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; idx < total;
-         idx += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t i = idx / per_block;
-        const int within = (int)(idx - i * per_block);
-        const int u = within & (U - 1), r = within / U;
-        const int h = r / block_size, off = r - h * block_size;
-        const int32_t blk = __ldg(blocks + i);
-        if (blk < 0 || blk >= num_blocks) {
-            if (within == 0) flag_status(status, PA_DEV_BAD_BLOCK_ID);
-            continue;
-        }
-        const int64_t rec = ((int64_t)blk * num_kv_heads + h) * block_size * fp4_row_bytes(D);
+    constexpr int kRec = BS * fp4_row_bytes(D);
+    const uint32_t i = blockIdx.x / cta_per_block, part = blockIdx.x - i * cta_per_block;
+    const int32_t blk = __ldg(blocks + i);
+    if (blk < 0 || blk >= num_blocks) {
+        if (part == 0 && threadIdx.x == 0) flag_status(status, PA_DEV_BAD_BLOCK_ID);
+        return;
+    }
+    const uint32_t per_block = (uint32_t)num_kv_heads * BS * U;  // groups of a block
+    uint2 w[kUnpackPer][2];
+    uint32_t sb[kUnpackPer][2];
+#pragma unroll
+    for (int t = 0; t < kUnpackPer; ++t) {
+        const uint32_t g = (part * kUnpackPer + t) * 256 + threadIdx.x;
+        if (g >= per_block) break;
+        const uint32_t h = g / (BS * U), r = g % (BS * U);  // r = row * U + group: the order of the codes and of the scales
+        const size_t rec = ((size_t)blk * num_kv_heads + h) * kRec;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             const uint8_t* src = (kv ? v_pool : k_pool) + rec;
-            const float scale = kv ? v_scale : k_scale;
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + off * (D / 2) + 8 * u));
-            const float s = e4m3_to_float(__ldg(src + block_size * (D / 2) + off * U + u));
-            float x[16];
-            fp4_values8(w.x, s, x);
-            fp4_values8(w.y, s, x + 8);
+            w[t][kv] = __ldg(reinterpret_cast<const uint2*>(src + 8 * r));
+            sb[t][kv] = __ldg(src + BS * (D / 2) + r);
+        }
+    }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(x[e], scale);
-            T* dst = (kv ? v_out : k_out) + idx * kFp4Group;
-            store8(dst, x);
-            store8(dst + 8, x + 8);
+    for (int t = 0; t < kUnpackPer; ++t) {
+        const uint32_t g = (part * kUnpackPer + t) * 256 + threadIdx.x;
+        if (g >= per_block) break;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t s = f16x2_low_twice(e4m3x2_to_f16x2(sb[t][kv]));
+            const float scale = kv ? v_scale : k_scale;
+            float x[16];
+            fp4_values8(w[t][kv].x, s, scale, x);
+            fp4_values8(w[t][kv].y, s, scale, x + 8);
+            T* dst = (kv ? v_out : k_out) + ((size_t)i * per_block + g) * kFp4Group;
+            if constexpr (WIDE) {
+                store16(dst, x);
+            } else {
+                store8(dst, x);
+                store8(dst + 8, x + 8);
+            }
         }
     }
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+bool aligned32(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 31u) == 0; }
 
 pa_status fp4_shape_check(int32_t n, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
                           pa_dtype dtype, float k_scale, float v_scale) {
@@ -105,12 +136,22 @@ pa_status fp4_shape_check(int32_t n, int32_t num_kv_heads, int32_t head_dim, int
     return PA_OK;
 }
 
-int grid_for(int64_t threads) {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    const int64_t want = (threads + 255) / 256;
-    return (int)(want < (int64_t)sms * 8 ? want : (int64_t)sms * 8);
+struct UnpackArgs {
+    const uint8_t *k_pool, *v_pool;
+    const int32_t* blocks;
+    void *k_out, *v_out;
+    int32_t num_kv_heads, num_blocks;
+    float k_scale, v_scale;
+    int32_t* status;
+    unsigned grid, cta_per_block;
+    bool wide;
+};
+
+template <typename T, int D, int BS>
+void launch_unpack(const UnpackArgs& a, cudaStream_t st) {
+    auto* kernel = a.wide ? &unpack_blocks_fp4_kernel<T, D, BS, true> : &unpack_blocks_fp4_kernel<T, D, BS, false>;
+    kernel<<<a.grid, 256, 0, st>>>(a.k_pool, a.v_pool, a.blocks, a.cta_per_block, static_cast<T*>(a.k_out),
+                                   static_cast<T*>(a.v_out), a.num_kv_heads, a.num_blocks, a.k_scale, a.v_scale, a.status);
 }
 
 }  // namespace
@@ -124,21 +165,21 @@ extern "C" pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_n
     using namespace pa;
     const pa_status st = fp4_shape_check(num_tokens, num_kv_heads, head_dim, block_size, num_blocks, in_dtype, k_scale, v_scale);
     if (st != PA_OK) return st;
-    if ((int64_t)num_tokens * num_kv_heads >= INT32_MAX) return PA_ERR_UNSUPPORTED;
+    const int64_t total = (int64_t)num_tokens * num_kv_heads * (head_dim / kFp4Group);
+    if (total >= INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if (!k_new || !v_new || !k_pool || !v_pool || !slot_mapping) return PA_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
-    const int grid = grid_for((int64_t)num_tokens * num_kv_heads * (head_dim / kFp4Group));
-    if (grid <= 0) return PA_ERR_CUDA;
+    const int grid = (int)((total + 255) / 256);
     const int64_t pool_slots = (int64_t)num_blocks * block_size;
     auto go = [&](auto kernel, auto elem) {
         using T = decltype(elem);
         kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
             static_cast<const T*>(k_new), static_cast<const T*>(v_new), static_cast<uint8_t*>(k_pool),
-            static_cast<uint8_t*>(v_pool), slot_mapping, num_tokens, num_kv_heads, block_size, pool_slots, k_scale, v_scale,
-            dev_status);
+            static_cast<uint8_t*>(v_pool), slot_mapping, num_tokens, num_kv_heads, block_size == 16 ? 4 : 5, pool_slots,
+            divisor(k_scale), divisor(v_scale), dev_status);
     };
     if (in_dtype == PA_BF16)
         head_dim == 128 ? go(&reshape_and_cache_fp4_kernel<__nv_bfloat16, 128>, __nv_bfloat16{})
@@ -157,25 +198,23 @@ extern "C" pa_status pa_unpack_blocks_fp4(const void* k_pool, const void* v_pool
     const pa_status st = fp4_shape_check(num, num_kv_heads, head_dim, block_size, num_blocks, out_dtype, k_scale, v_scale);
     if (st != PA_OK) return st;
     const int64_t per_block = (int64_t)num_kv_heads * block_size * (head_dim / kFp4Group);
-    if (per_block >= INT32_MAX) return PA_ERR_UNSUPPORTED;
+    const int64_t cta_per_block = (per_block + 256 * kUnpackPer - 1) / (256 * kUnpackPer);
+    if (per_block >= INT32_MAX || cta_per_block * num >= INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (num == 0) return PA_OK;
     if (!k_pool || !v_pool || !blocks || !k_out || !v_out) return PA_ERR_INVALID_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(k_out) || !aligned16(v_out) ||
         (reinterpret_cast<uintptr_t>(blocks) & 3u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
-    const int grid = grid_for(num * per_block);
-    if (grid <= 0) return PA_ERR_CUDA;
-    auto go = [&](auto kernel, auto elem) {
-        using T = decltype(elem);
-        kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), blocks, (int64_t)num,
-            static_cast<T*>(k_out), static_cast<T*>(v_out), num_kv_heads, block_size, num_blocks, k_scale, v_scale,
-            dev_status);
-    };
+    const UnpackArgs a{static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool), blocks, k_out, v_out,
+                       num_kv_heads, num_blocks, k_scale, v_scale, dev_status, (unsigned)(cta_per_block * num),
+                       (unsigned)cta_per_block, aligned32(k_out) && aligned32(v_out)};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool b16 = block_size == 16, d128 = head_dim == 128;
     if (out_dtype == PA_BF16)
-        head_dim == 128 ? go(&unpack_blocks_fp4_kernel<__nv_bfloat16, 128>, __nv_bfloat16{})
-                        : go(&unpack_blocks_fp4_kernel<__nv_bfloat16, 64>, __nv_bfloat16{});
+        d128 ? (b16 ? launch_unpack<__nv_bfloat16, 128, 16>(a, s) : launch_unpack<__nv_bfloat16, 128, 32>(a, s))
+             : (b16 ? launch_unpack<__nv_bfloat16, 64, 16>(a, s) : launch_unpack<__nv_bfloat16, 64, 32>(a, s));
     else
-        head_dim == 128 ? go(&unpack_blocks_fp4_kernel<float, 128>, 0.f) : go(&unpack_blocks_fp4_kernel<float, 64>, 0.f);
+        d128 ? (b16 ? launch_unpack<float, 128, 16>(a, s) : launch_unpack<float, 128, 32>(a, s))
+             : (b16 ? launch_unpack<float, 64, 16>(a, s) : launch_unpack<float, 64, 32>(a, s));
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -244,7 +244,7 @@ PA_HD Plan plan_from_prefix(const int32_t* pref, const int32_t* upref, int B, in
 // least kFp4MinRangeTokens tokens (of one KV head), so that a short batch is not cut into pieces whose merge
 // costs more than their computation.  (tiles: of the whole batch.)
 #ifndef PA_FP4_MIN_RANGE
-#define PA_FP4_MIN_RANGE 64
+#define PA_FP4_MIN_RANGE 96
 #endif
 constexpr int kFp4MinRangeTokens = PA_FP4_MIN_RANGE;
 PA_HD int32_t fp4_ranges(int64_t tiles, int num_ctas, int partition_tiles, int block_size) {
