@@ -14,6 +14,8 @@
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <cmath>
+
 #include "pa_device.cuh"
 
 namespace pa {
@@ -49,31 +51,47 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 }
 
 // ---- correctly rounded quotients of many elements by one divisor ----------------------------------
-// With r the correctly rounded reciprocal of b: q = x r is within an ulp of x / b, its remainder x - q b is
-// exact, and q + remainder * r, rounded, is x / b correctly rounded (Markstein 1990).  This needs no term to
+// With r the correctly rounded reciprocal of b: q = x r is within an ulp of x / b, its remainder q b - x is
+// exact, and q - remainder * r, rounded, is x / b correctly rounded (Markstein 1990).  This needs no term to
 // leave the normal range: kQuotientMax bounds |x| and b's range (its reciprocal is in range with it).
 // Below, where a quotient or a remainder is tiny, the result may be off by a unit of the smallest number; the
-// callers round what is so small to zero.  A zero loses its sign.
+// callers round what is so small to zero.  A zero keeps its sign.  For b a power of two q is x / b.
 constexpr float kQuotientMax = 1.15292150e18f;  // 2^60
 
-struct Divisor {  // of a launch: b, its reciprocal, and whether both are in [2^-60, 2^60]
+struct Divisor {  // of a launch: b, its reciprocal, whether both are in [2^-60, 2^60], and whether b = 2^n
     float b, r;
-    bool in_range;
+    bool in_range, pow2;
 };
-inline Divisor divisor(float b) { return Divisor{b, 1.f / b, b <= kQuotientMax && b >= 1.f / kQuotientMax}; }
+inline Divisor divisor(float b) {
+    int e;
+    return Divisor{b, 1.f / b, b <= kQuotientMax && b >= 1.f / kQuotientMax, std::frexp(b, &e) == 0.5f};
+}
 
 __device__ __forceinline__ float quotient(float x, float b, float r) {
     const float q = __fmul_rn(x, r);
-    return __fmaf_rn(__fmaf_rn(-q, b, x), r, q);
+    return __fmaf_rn(__fmaf_rn(q, b, -x), -r, q);
 }
 template <int N>
 __device__ __forceinline__ void quotients(const float* x, float b, float r, float* y) {
-    const float2 rr = make_float2(r, r), nb = make_float2(-b, -b);
+    const float2 rr = make_float2(r, r), nr = make_float2(-r, -r), bb = make_float2(b, b);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const float2 v = make_float2(x[i], x[i + 1]), q = mul_f32x2(v, rr);
-        const float2 d = fma_f32x2(fma_f32x2(q, nb, v), rr, q);
+        const float2 q = mul_f32x2(make_float2(x[i], x[i + 1]), rr);
+        const float2 d = fma_f32x2(fma_f32x2(q, bb, make_float2(-x[i], -x[i + 1])), nr, q);
         y[i] = d.x, y[i + 1] = d.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void quotients(const float* x, const Divisor& d, float* y) {
+    if (d.pow2) {
+        const float2 rr = make_float2(d.r, d.r);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 q = mul_f32x2(make_float2(x[i], x[i + 1]), rr);
+            y[i] = q.x, y[i + 1] = q.y;
+        }
+    } else {
+        quotients<N>(x, d.b, d.r, y);
     }
 }
 
@@ -91,12 +109,24 @@ __device__ __forceinline__ float amax_nan(const float* x) {
     return a;
 }
 
+// x / b for a b with the reciprocal r + t (r rounded, t = (1 - b r) r): within 2^-47 before its one rounding.  Enough
+// where no quotient lies that close to a value that matters (see fp4_codes8).
+template <int N>
+__device__ __forceinline__ void near_quotients(const float* x, float r, float t, float* y) {
+    const float2 rr = make_float2(r, r), tt = make_float2(t, t);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 v = make_float2(x[i], x[i + 1]), d = fma_f32x2(v, rr, mul_f32x2(v, tt));
+        y[i] = d.x, y[i + 1] = d.y;
+    }
+}
+
 // ---- quantisation ---------------------------------------------------------------------------------
 // A group's scale from amax, its largest |x| (NaN if it holds one): the byte, and the value and its
 // reciprocal for fp4_codes8.  Division is monotonic, so max |x / b| is amax / b; a sixth of it puts the
 // largest element on the largest code.
 struct Fp4Scale {
-    float s, r;
+    float s, r, t;  // s, and its reciprocal as r + t
     uint8_t byte;
     bool plain;  // fp4_codes8 may use quotients()
 };
@@ -112,16 +142,20 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Divisor& d) {
     }
     f.s = e4m3_to_float(f.byte);
     f.r = f.s > 0.f ? __frcp_rn(f.s) : 0.f;  // 0: every code zero
+    f.t = __fmaf_rn(-f.s, f.r, 1.f) * f.r;
     return f;
 }
 
 // Eight codes of x under a group's scale, element i in bits 4 i .. 4 i + 3: E2M1 of fp32(fp32(x / b) / s),
 // nearest even, saturated at 6, with x's sign.  All zero where the scale is zero or NaN.
+// The inner quotient y is exact to its rounding.  The outer one only has to fall on the right side of, or on, the
+// codes' midpoints m: m s is an fp32 number of at most 7 significant bits, so y is m s itself, and y / s comes
+// out as m, or differs from it by 2^-24 of it or more.
 __device__ __forceinline__ uint32_t fp4_codes8(const float* x, const Divisor& d, const Fp4Scale& f) {
     float y[8];
     if (f.plain) {
-        quotients<8>(x, d.b, d.r, y);
-        quotients<8>(y, f.s, f.r, y);
+        quotients<8>(x, d, y);
+        near_quotients<8>(y, f.r, f.t, y);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = f.s > 0.f ? __fdiv_rn(__fdiv_rn(x[i], d.b), f.s) : 0.f;
@@ -129,8 +163,7 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* x, const Divisor& d,
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 z = make_float2(copysignf(y[2 * i], x[2 * i]), copysignf(y[2 * i + 1], x[2 * i + 1]));
-        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(z, __NV_E2M1, cudaRoundNearest) << (8 * i);
+        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * i);
     }
     return f.r > 0.f ? w : 0u;
 }
@@ -171,6 +204,52 @@ __device__ __forceinline__ void fp4_values8(uint32_t w, uint32_t s, float pool_s
         const uint32_t v = mul_f16x2(r[i], s);
         const float2 y = mul_f32x2(make_float2(f16_lo(v), f16_hi(v)), p);
         x[2 * i] = y.x, x[2 * i + 1] = y.y;
+    }
+}
+
+// n / d for n < 2^31 and a launch's d >= 1, as a multiplication: q = (high word of n m, plus n) >> s with
+// s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1 (Granlund and Montgomery 1994).
+struct FastDiv {
+    uint32_t d, m, s;
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return FastDiv{d, (uint32_t)((((1ull << s) - d) << 32) / d + 1), s};
+}
+
+// ---- rows copied ahead -----------------------------------------------------------------------------
+// Copies from global to shared memory, 16 bytes a thread, some turns of a loop ahead: the bytes in flight then
+// need no registers.  CA: through L1, for copies of half a sector each, so that the other half is found there.
+template <bool CA = false>
+__device__ __forceinline__ void copy_ahead16(uint32_t dst, const void* src) {
+    if constexpr (CA)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups of this thread's copies have landed
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// Eight elements of T in shared memory as fp32: 16 bytes, or for fp32 two times 16, `step` bytes apart.
+template <typename T>
+__device__ __forceinline__ void take8(uint32_t src, uint32_t step, float* x) {
+    const uint4 a = lds16(src);
+    if constexpr (sizeof(T) == 2) {
+        x[0] = bf16_lo(a.x), x[1] = bf16_hi(a.x), x[2] = bf16_lo(a.y), x[3] = bf16_hi(a.y);
+        x[4] = bf16_lo(a.z), x[5] = bf16_hi(a.z), x[6] = bf16_lo(a.w), x[7] = bf16_hi(a.w);
+    } else {
+        const uint4 b = lds16(src + step);
+        x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+        x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y), x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
     }
 }
 

@@ -10,44 +10,64 @@
 namespace pa {
 namespace {
 
-// Token i, slot s = slots[i]: block s / BS, row s % BS of every KV head's record.  A thread takes the same
-// group of K and of V: four 16-byte loads in flight.
+// Token i, slot s = slots[i]: block s / BS, row s % BS of every KV head's record.  A thread takes one group of K
+// (blockIdx.y = 0) or of V per turn; a warp's 32 groups are consecutive in the input, and the warp has
+// copied those of its next turns ahead into shared memory: the arithmetic costs about as much as HBM takes,
+// so neither may wait for the other.
+constexpr int kAppendAhead = 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(const T* k_new, const T* v_new, uint8_t* k_pool,
                                                                     uint8_t* v_pool, const int64_t* __restrict__ slots,
-                                                                    int32_t num_tokens, int32_t num_kv_heads,
-                                                                    int32_t bs_shift, int64_t pool_slots, const Divisor kd,
-                                                                    const Divisor vd, int32_t* status) {
+                                                                    uint32_t total, const FastDiv heads, int32_t bs_shift,
+                                                                    int64_t pool_slots, const Divisor kd, const Divisor vd,
+                                                                    int32_t* status) {
     pdl_launch_dependents();
-    constexpr int U = D / kFp4Group;
-    const uint32_t total = (uint32_t)num_tokens * num_kv_heads * U;  // < 2^31 (checked on the host)
-    for (uint32_t idx = blockIdx.x * blockDim.x + threadIdx.x; idx < total; idx += gridDim.x * blockDim.x) {
-        const uint32_t u = idx & (U - 1), row = idx / U;
-        const uint32_t tok = row / (uint32_t)num_kv_heads, h = row - tok * (uint32_t)num_kv_heads;
-        const int64_t slot = __ldg(slots + tok);
-        float x[2][16];
+    constexpr int U = D / kFp4Group;                     // groups of a row
+    constexpr int kGroup = kFp4Group * (int)sizeof(T);   // bytes of a group
+    constexpr int kTurn = 32 * kGroup;                   // bytes of a warp's turn
+    __shared__ __align__(16) uint8_t ahead[8 * kAppendAhead * kTurn];
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t ring = smem_u32(ahead) + (threadIdx.x >> 5) * kAppendAhead * kTurn;
+    const bool is_v = blockIdx.y != 0;
+    const uint8_t* in = reinterpret_cast<const uint8_t*>(is_v ? v_new : k_new);
+    const uint32_t stride = gridDim.x * 256;
+    auto fetch = [&](uint32_t base, int turn) {  // groups base .. base + 31
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const T* src = (kv ? v_new : k_new) + (size_t)row * D + kFp4Group * u;
-            load8(src, x[kv]);
-            load8(src + 8, x[kv] + 8);
+        for (int i = 0; i < kGroup / 16; ++i) {
+            const uint32_t chunk = 32 * i + lane;  // 16 bytes each
+            if (base + chunk / (kGroup / 16) < total)
+                copy_ahead16(ring + turn * kTurn + chunk * 16, in + (size_t)base * kGroup + chunk * 16);
         }
+        copies_commit();
+    };
+    uint32_t base = blockIdx.x * 256 + (threadIdx.x & ~31u);
+#pragma unroll
+    for (int i = 0; i < kAppendAhead; ++i) fetch(base + i * stride, i);
+    const Divisor d = is_v ? vd : kd;
+    int turn = 0;
+    for (; base < total; base += stride) {
+        const uint32_t idx = base + lane, u = idx & (U - 1), row = idx / U;
+        const uint32_t tok = heads.div(row), h = row - tok * heads.d;
+        const int64_t slot = idx < total ? __ldg(slots + tok) : -1;
+        copies_wait<kAppendAhead - 1>();
+        __syncwarp();  // the other lanes' copies too
+        float x[16];
+        const uint32_t src = ring + turn * kTurn + lane * kGroup;
+        take8<T>(src, 16, x);
+        take8<T>(src + kGroup / 2, 16, x + 8);
+        __syncwarp();  // read by every lane: the space may be copied into
+        fetch(base + kAppendAhead * stride, turn);
+        if (++turn == kAppendAhead) turn = 0;
         if (slot < 0) continue;
         if (slot >= pool_slots) {
             if (h == 0 && u == 0) flag_status(status, PA_DEV_BAD_SLOT);
             continue;
         }
-        const int64_t rec = ((slot >> bs_shift) * num_kv_heads + h) * (int64_t)(fp4_row_bytes(D) << bs_shift);
+        const Fp4Scale f = fp4_scale(amax_nan<16>(x), d);
+        uint8_t* rec = (is_v ? v_pool : k_pool) + ((slot >> bs_shift) * heads.d + h) * (int64_t)(fp4_row_bytes(D) << bs_shift);
         const uint32_t off = (uint32_t)slot & ((1u << bs_shift) - 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const Divisor& d = kv ? vd : kd;
-            const Fp4Scale f = fp4_scale(amax_nan<16>(x[kv]), d);
-            uint8_t* dst = (kv ? v_pool : k_pool) + rec;
-            *reinterpret_cast<uint2*>(dst + off * (D / 2) + 8 * u) =
-                make_uint2(fp4_codes8(x[kv], d, f), fp4_codes8(x[kv] + 8, d, f));
-            dst[((D / 2) << bs_shift) + off * U + u] = f.byte;
-        }
+        *reinterpret_cast<uint2*>(rec + off * (D / 2) + 8 * u) = make_uint2(fp4_codes8(x, d, f), fp4_codes8(x + 8, d, f));
+        rec[((D / 2) << bs_shift) + off * U + u] = f.byte;
     }
 }
 
@@ -166,19 +186,25 @@ extern "C" pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_n
     const pa_status st = fp4_shape_check(num_tokens, num_kv_heads, head_dim, block_size, num_blocks, in_dtype, k_scale, v_scale);
     if (st != PA_OK) return st;
     const int64_t total = (int64_t)num_tokens * num_kv_heads * (head_dim / kFp4Group);
-    if (total >= INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (total >= INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if (!k_new || !v_new || !k_pool || !v_pool || !slot_mapping) return PA_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
-    const int grid = (int)((total + 255) / 256);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return PA_ERR_CUDA;
+    // K and V each: as many CTAs as half the SMs' room for them (four per SM in all), or as there is work for
+    const int64_t want = (total + 255) / 256, room = (int64_t)sms * 2;
+    const dim3 grid((unsigned)(want < room ? want : room), 2);
     const int64_t pool_slots = (int64_t)num_blocks * block_size;
     auto go = [&](auto kernel, auto elem) {
         using T = decltype(elem);
         kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
             static_cast<const T*>(k_new), static_cast<const T*>(v_new), static_cast<uint8_t*>(k_pool),
-            static_cast<uint8_t*>(v_pool), slot_mapping, num_tokens, num_kv_heads, block_size == 16 ? 4 : 5, pool_slots,
+            static_cast<uint8_t*>(v_pool), slot_mapping, (uint32_t)total, fast_div(num_kv_heads), block_size == 16 ? 4 : 5, pool_slots,
             divisor(k_scale), divisor(v_scale), dev_status);
     };
     if (in_dtype == PA_BF16)
