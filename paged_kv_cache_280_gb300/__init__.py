@@ -134,10 +134,16 @@ def abi_version() -> int:
 # device entry points (torch tensors on the current CUDA device)
 # ---------------------------------------------------------------------------
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -209,24 +215,48 @@ def _fp4_block_size(pool, head_dim: int, name: str) -> int:
     return pool.shape[2] // row
 
 
-def _same_device(*tensors) -> None:
-    """The library launches on the current device: refuse tensors that live on another one."""
-    torch = _torch()
-    here = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if here is None:
-            here = torch.cuda.current_device()
-        if t.get_device() != here:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{here}")
+# The entry points below are called once per layer and step, on calls of a few microseconds: they look at each
+# tensor once and keep nothing from one call to the next.
 
-
-def _want(t, dtype, shape, name: str) -> None:
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+def _refuse(t, dtype, shape, dev: int, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+    if t.dtype != dtype or t.shape != shape:
         raise PAError(1, f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _ptr(t, dtype, shape, dev: int, name: str) -> int:
+    """Pointer to a contiguous tensor of this type and shape on the current device."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _status_ptr(t, dev: int):
+    """Pointer to a status word: any int32 tensor on the current device with at least one element, or None."""
+    if t is None:
+        return None
+    torch = _torch()
+    if t.get_device() != dev or t.dtype != torch.int32 or t.numel() < 1:
+        _refuse(t, torch.int32, (1,), dev, "status")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    """The current device, on which the library launches; -2, no tensor's, where there is none."""
+    try:
+        return _torch().cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _stream_of(stream, dev: int) -> int:
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def pa_reshape_and_cache(k_new, v_new, k_pool, v_pool, slot_mapping, status=None, stream=None):
@@ -377,37 +407,36 @@ def pa_reshape_and_cache_fp4(k_new, v_new, k_pool, v_pool, slot_mapping, k_scale
     """Slot-mapped append into 4-bit pools (uint8 [num_blocks][Hkv][fp4_block_bytes(D, bs)]) of bf16/fp32 K/V
     [N][Hkv][D]; slot_mapping int64 [N]."""
     torch = _torch()
-    n, hkv, d = k_new.shape
+    shape = k_new.shape
+    n, hkv, d = shape
     bs = _fp4_block_size(k_pool, d, "pa_reshape_and_cache_fp4")
-    nb = k_pool.shape[0]
-    _same_device(k_new, v_new, k_pool, v_pool, slot_mapping, status)
-    _want(v_new, k_new.dtype, (n, hkv, d), "v_new")
-    _want(k_pool, torch.uint8, (nb, hkv, k_pool.shape[2]), "k_pool")
-    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
-    _want(slot_mapping, torch.int64, (n,), "slot_mapping")
-    _ok(_lib.pa_reshape_and_cache_fp4(_dev_ptr(k_new, "k_new"), _dev_ptr(v_new, "v_new"), _dev_ptr(k_pool, "k_pool"),
-                                      _dev_ptr(v_pool, "v_pool"), _dev_ptr(slot_mapping, "slot_mapping"), n, hkv, d, bs,
-                                      nb, _dtype_code(k_new), float(k_scale), float(v_scale), _dev_ptr(status, "status"),
-                                      _stream(stream)),
-        "pa_reshape_and_cache_fp4")
+    nb, _, rec = pshape = k_pool.shape
+    dev = _device()
+    status_code = _lib.pa_reshape_and_cache_fp4(
+        _ptr(k_new, k_new.dtype, shape, dev, "k_new"), _ptr(v_new, k_new.dtype, shape, dev, "v_new"),
+        _ptr(k_pool, torch.uint8, (nb, hkv, rec), dev, "k_pool"), _ptr(v_pool, torch.uint8, pshape, dev, "v_pool"),
+        _ptr(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, hkv, d, bs, nb, _dtype_code(k_new), k_scale, v_scale,
+        _status_ptr(status, dev), _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_reshape_and_cache_fp4")
 
 
 def pa_unpack_blocks_fp4(k_pool, v_pool, blocks, k_out, v_out, k_scale, v_scale, status=None, stream=None):
     """out[i] = the values of block blocks[i] (int32 [n]) of 4-bit pools; k_out/v_out [n][Hkv][bs][D] bf16 or fp32,
     which pa_prefill_attention takes as pools (block table 0 .. n - 1)."""
     torch = _torch()
-    n, hkv, bs, d = k_out.shape
+    shape = k_out.shape
+    n, hkv, bs, d = shape
     nb = k_pool.shape[0]
-    _same_device(k_pool, v_pool, blocks, k_out, v_out, status)
-    _want(v_out, k_out.dtype, k_out.shape, "v_out")
-    _want(k_pool, torch.uint8, (nb, hkv, fp4_block_bytes(d, bs)), "k_pool")
-    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
-    _want(blocks, torch.int32, (n,), "blocks")
-    _ok(_lib.pa_unpack_blocks_fp4(_dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"), _dev_ptr(blocks, "blocks"), n,
-                                  _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"), hkv, d, bs, nb,
-                                  _dtype_code(k_out), float(k_scale), float(v_scale), _dev_ptr(status, "status"),
-                                  _stream(stream)),
-        "pa_unpack_blocks_fp4")
+    pshape = (nb, hkv, fp4_block_bytes(d, bs))
+    dev = _device()
+    status_code = _lib.pa_unpack_blocks_fp4(
+        _ptr(k_pool, torch.uint8, pshape, dev, "k_pool"), _ptr(v_pool, torch.uint8, pshape, dev, "v_pool"),
+        _ptr(blocks, torch.int32, (n,), dev, "blocks"), n, _ptr(k_out, k_out.dtype, shape, dev, "k_out"),
+        _ptr(v_out, k_out.dtype, shape, dev, "v_out"), hkv, d, bs, nb, _dtype_code(k_out), k_scale, v_scale,
+        _status_ptr(status, dev), _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_unpack_blocks_fp4")
 
 
 def pa_decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, max_seq_len, scale,
@@ -415,31 +444,40 @@ def pa_decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tabl
     """Decode over 4-bit pools with bf16 q/out [B][Hq][D].  plan: as for pa_decode_attention (built with dtype
     PA_FP4_E2M1)."""
     torch = _torch()
-    b, hq, d = q.shape
+    shape = q.shape
+    b, hq, d = shape
     bs = _fp4_block_size(k_pool, d, "pa_decode_attention_fp4")
-    nb, hkv = k_pool.shape[:2]
-    _same_device(out, q, k_pool, v_pool, block_tables, seq_lens, workspace, plan)
-    _want(q, torch.bfloat16, (b, hq, d), "q")
-    _want(out, torch.bfloat16, (b, hq, d), "out")
-    _want(v_pool, torch.uint8, k_pool.shape, "v_pool")
-    _want(block_tables, torch.int32, (b, block_tables.shape[1]), "block_tables")
-    _want(seq_lens, torch.int32, (b,), "seq_lens")
-    args = [_dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool"),
-            float(k_scale), float(v_scale), _dev_ptr(block_tables, "block_tables"), block_tables.shape[1],
-            _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), b, hq, hkv, d, bs, nb, float(scale),
-            int(partition_tokens), _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()]
+    nb, hkv, _ = pshape = k_pool.shape
+    mb = block_tables.shape[1]
+    dev = _device()
+    args = (_ptr(out, torch.bfloat16, shape, dev, "out"), _ptr(q, torch.bfloat16, shape, dev, "q"),
+            _ptr(k_pool, torch.uint8, pshape, dev, "k_pool"), _ptr(v_pool, torch.uint8, pshape, dev, "v_pool"), k_scale,
+            v_scale, _ptr(block_tables, torch.int32, (b, mb), dev, "block_tables"), mb,
+            _ptr(seq_lens, torch.int32, (b,), dev, "seq_lens"), int(max_seq_len), b, hq, hkv, d, bs, nb, scale,
+            int(partition_tokens), _ptr(workspace, workspace.dtype, workspace.shape, dev, "workspace"), workspace.nbytes)
     if plan is None:
-        _ok(_lib.pa_decode_attention_fp4(*args, _stream(stream)), "pa_decode_attention_fp4")
+        status_code = _lib.pa_decode_attention_fp4(*args, _stream_of(stream, dev))
     else:
-        _ok(_lib.pa_decode_attention_fp4_planned(*args, _dev_ptr(plan, "plan"), plan.numel() * plan.element_size(),
-                                                 _stream(stream)), "pa_decode_attention_fp4_planned")
+        status_code = _lib.pa_decode_attention_fp4_planned(*args, _ptr(plan, plan.dtype, plan.shape, dev, "plan"), plan.nbytes,
+                                                           _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_decode_attention_fp4")
 
 
 def _token_rows(t, name: str) -> int:
     """Elements from one token to the next of a [N][H][D] tensor whose heads are contiguous within a token."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    n, h, d = t.shape
+    stride = t.stride()
+    if (d > 1 and stride[2] != 1) or (h > 1 and stride[1] != d):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if n > 1 else h * d
+
+
+def _rows_ptr(t, dtype, shape, dev: int, name: str) -> int:
+    """As _ptr, without the contiguity (see _token_rows)."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
 
 
 def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_mapping, interleaved=False, k_scale=1.0,
@@ -451,32 +489,33 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_m
     [max_position][rot_dim] (cos, then sin); pools of k's dtype or FP8 codes [num_blocks][Hkv][bs][D], or 4-bit
     [num_blocks][Hkv][fp4_block_bytes(D, bs)]; slot_mapping int64 [N], negative = padding."""
     torch = _torch()
-    n, hkv, d = k.shape
-    hq = 0 if q is None else q.shape[1]
-    if k_pool.dim() == 3:
+    shape, dtype, pdtype, pshape = k.shape, k.dtype, k_pool.dtype, k_pool.shape
+    n, hkv, d = shape
+    if len(pshape) == 3:
         bs, pool_dtype = _fp4_block_size(k_pool, d, "pa_rope_and_cache"), PA_FP4_E2M1
-        _want(k_pool, torch.uint8, (k_pool.shape[0], hkv, k_pool.shape[2]), "k_pool")
+        want = (pshape[0], hkv, pshape[2])
     else:
-        bs, pool_dtype = k_pool.shape[2], _dtype_code(k_pool)
-        _want(k_pool, k_pool.dtype, (k_pool.shape[0], hkv, bs, d), "k_pool")
-    _same_device(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_mapping, status)
-    _want(v, k.dtype, (n, hkv, d), "v")
-    _want(q, k.dtype, (n, hq, d), "q")
-    if (q is None) != (q_out is None):
-        raise PAError(1, "pa_rope_and_cache: q and q_out go together")
-    _want(q_out, k.dtype, (n, hq, d), "q_out")
-    _want(v_pool, k_pool.dtype, k_pool.shape, "v_pool")
-    _want(positions, torch.int32, (n,), "positions")
-    _want(slot_mapping, torch.int64, (n,), "slot_mapping")
-    _want(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
-    _ok(_lib.pa_rope_and_cache(_dev_ptr(q_out, "q_out"), None if q is None else q.data_ptr(),
-                               0 if q is None else _token_rows(q, "q"), k.data_ptr(), _token_rows(k, "k"), v.data_ptr(),
-                               _token_rows(v, "v"), _dev_ptr(positions, "positions"), _dev_ptr(cos_sin, "cos_sin"),
-                               cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), _dev_ptr(k_pool, "k_pool"),
-                               _dev_ptr(v_pool, "v_pool"), _dev_ptr(slot_mapping, "slot_mapping"), n, hq, hkv, d, bs,
-                               k_pool.shape[0], _dtype_code(k), pool_dtype, float(k_scale), float(v_scale),
-                               _dev_ptr(status, "status"), _stream(stream)),
-        "pa_rope_and_cache")
+        bs, pool_dtype = pshape[2], _dtype_code(k_pool)
+        want = (pshape[0], hkv, bs, d)
+    dev = _device()
+    if q is None or q_out is None:
+        if q is not None or q_out is not None:
+            raise PAError(1, "pa_rope_and_cache: q and q_out go together")
+        hq, qo_ptr, q_ptr, q_rows = 0, None, None, 0
+    else:
+        hq = q.shape[1]
+        qo_ptr, q_ptr = _ptr(q_out, dtype, (n, hq, d), dev, "q_out"), _rows_ptr(q, dtype, (n, hq, d), dev, "q")
+        q_rows = _token_rows(q, "q")
+    max_position, rot_dim = cos_sin.shape
+    status_code = _lib.pa_rope_and_cache(
+        qo_ptr, q_ptr, q_rows, _rows_ptr(k, dtype, shape, dev, "k"), _token_rows(k, "k"), _rows_ptr(v, dtype, shape, dev, "v"),
+        _token_rows(v, "v"), _ptr(positions, torch.int32, (n,), dev, "positions"),
+        _ptr(cos_sin, torch.float32, (max_position, rot_dim), dev, "cos_sin"), max_position, rot_dim, 1 if interleaved else 0,
+        _ptr(k_pool, pdtype, want, dev, "k_pool"), _ptr(v_pool, pdtype, want, dev, "v_pool"),
+        _ptr(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, hq, hkv, d, bs, pshape[0], _dtype_code(k), pool_dtype,
+        k_scale, v_scale, _status_ptr(status, dev), _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_rope_and_cache")
 
 
 def pa_swap_out(k_pool, v_pool, blocks, k_store, v_store, status=None, stream=None):

@@ -27,6 +27,8 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 
+}  // namespace
+
 bool current_device(int* dev, int* sms) {
     if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return false;
     std::lock_guard<std::mutex> lk(g_mu);
@@ -38,6 +40,8 @@ bool current_device(int* dev, int* sms) {
     *sms = g_dev[*dev].sms;
     return true;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

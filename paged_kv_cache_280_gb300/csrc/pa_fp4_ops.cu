@@ -193,9 +193,7 @@ extern "C" pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_n
         (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(dev_status) & 3u))
         return PA_ERR_INVALID_ARG;
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return PA_ERR_CUDA;
+    if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
     // K and V each: as many CTAs as half the SMs' room for them (four per SM in all), or as there is work for
     const int64_t want = (total + 255) / 256, room = (int64_t)sms * 2;
     const dim3 grid((unsigned)(want < room ? want : room), 2);

@@ -150,7 +150,9 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
                         size_t workspace_bytes, pa_dtype dtype, float k_scale, float v_scale, void* stream,
                         bool clear_status, const void* plan = nullptr, size_t plan_bytes = 0);
 
-// Host launch helpers shared by the attention entry points (pa_api.cu).
+// Host launch helpers shared by the entry points (pa_api.cu).
+// The current device and its SM count, which is asked for once.
+bool current_device(int* dev, int* sms);
 // The TMA map of a pool viewed as [num_blocks * Hkv * block_size][head_dim]
 // rows, one box = block_size rows x 128 bytes with the 128-byte swizzle;
 // cached per (device, pool, shape).

@@ -261,9 +261,7 @@ extern "C" pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_str
     // queries in place must be laid out as q_out is
     if (num_q_heads > 0 && q == q_out && q_stride != (int64_t)num_q_heads * head_dim) return PA_ERR_INVALID_ARG;
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return PA_ERR_CUDA;
+    if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
     RopeParams p;
     p.q_out = q_out, p.q = q, p.k = k, p.v = v;
     p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;

@@ -104,17 +104,21 @@ def test_binding_refusals():
     torch = pytest.importorskip("torch")
     k = torch.zeros(3, 2, 128)
     pool = torch.zeros(5, 2, pa.fp4_block_bytes(128, 16), dtype=torch.uint8)
-    slots = torch.zeros(3, dtype=torch.int64)
-    with pytest.raises(ValueError, match="CUDA"):
+    slots, ids = torch.zeros(3, dtype=torch.int64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="k_new must be a CUDA"):
         pa.pa_reshape_and_cache_fp4(k, k, pool, pool, slots, 1.0, 1.0)
     with pytest.raises(pa.PAError, match="whole rows"):
         pa.pa_reshape_and_cache_fp4(k, k, pool[..., :100], pool, slots, 1.0, 1.0)
     with pytest.raises(pa.PAError, match="uint8"):
         pa.pa_decode_attention_fp4(k, k, pool.float(), pool, 1.0, 1.0, slots, slots, 1, 1.0, pool)
-    with pytest.raises(ValueError, match="CUDA"):
-        pa.pa_unpack_blocks_fp4(pool, pool, slots, torch.zeros(1, 2, 16, 128), torch.zeros(1, 2, 16, 128), 1.0, 1.0)
-    with pytest.raises(ValueError, match="CUDA"):
-        pa.pa_rope_and_cache(None, None, k, k, slots, k, pool, pool, slots)
+    with pytest.raises(ValueError, match="out must be a CUDA"):
+        pa.pa_decode_attention_fp4(k, k, pool, pool, 1.0, 1.0, ids[None], ids, 1, 1.0, pool)
+    with pytest.raises(ValueError, match="k_pool must be a CUDA"):
+        pa.pa_unpack_blocks_fp4(pool, pool, ids, torch.zeros(3, 2, 16, 128), torch.zeros(3, 2, 16, 128), 1.0, 1.0)
+    with pytest.raises(ValueError, match="k must be a CUDA"):
+        pa.pa_rope_and_cache(None, None, k, k, ids, k[0], pool, pool, slots)
+    with pytest.raises(pa.PAError, match="go together"):
+        pa.pa_rope_and_cache(None, k, k, k, ids, k[0], pool, pool, slots)
     with pytest.raises(pa.PAError):
         pa.pa_copy_blocks(torch.zeros(5, 2, 100, dtype=torch.uint8), pool, torch.zeros(1, 2, dtype=torch.int32))
     assert pa._token_rows(torch.zeros(4, 12, 64)[:, 2:5], "k") == 12 * 64 and pa._token_rows(torch.zeros(1, 3, 64), "k") == 192
@@ -123,19 +127,37 @@ def test_binding_refusals():
             pa._token_rows(bad, "k")
 
 
-def test_device_check_refuses_another_device(monkeypatch):
+class _On:
+    """A tensor's face: what the binding asks of one."""
+
+    def __init__(self, device, dtype, shape, contiguous=True):
+        self.device_, self.dtype, self.shape, self.contiguous, self.is_cuda = device, dtype, shape, contiguous, device >= 0
+
+    def get_device(self):
+        return self.device_
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return 1
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_tensor_checks():
+    assert pa._ptr(_On(0, "f", (2, 3)), "f", (2, 3), 0, "x") == 1 << 20
+    for bad, error, text in ((_On(1, "f", (2, 3)), ValueError, "x is on cuda:1, but the current device is cuda:0"),
+                             (_On(-1, "f", (2, 3)), ValueError, "x must be a CUDA tensor"),
+                             (_On(0, "g", (2, 3)), pa.PAError, "expected f"), (_On(0, "f", (2, 4)), pa.PAError, "expected"),
+                             (_On(0, "f", (2, 3), False), ValueError, "contiguous")):
+        with pytest.raises(error, match=text):
+            pa._ptr(bad, "f", (2, 3), 0, "x")
+    assert pa._rows_ptr(_On(0, "f", (2, 3), False), "f", (2, 3), 0, "x") == 1 << 20
+    with pytest.raises(ValueError, match="current device"):
+        pa._rows_ptr(_On(1, "f", (2, 3)), "f", (2, 3), 0, "x")
     torch = pytest.importorskip("torch")
-
-    class Fake:
-        is_cuda = True
-
-        def __init__(self, d):
-            self.d = d
-
-        def get_device(self):
-            return self.d
-
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    pa._same_device(Fake(0), None, Fake(0))
-    with pytest.raises(ValueError, match="current device is cuda:0"):
-        pa._same_device(Fake(0), Fake(1))
+    assert pa._status_ptr(None, 0) is None and pa._status_ptr(_On(0, torch.int32, (1,)), 0) == 1 << 20
+    with pytest.raises(pa.PAError):
+        pa._status_ptr(_On(0, torch.int64, (1,)), 0)
