@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const DecodePa
     int64_t item = shared ? blockIdx.x : (int64_t)blockIdx.x * kMergeWarps + warp;
     int b = 0, h = 0, ca = 0, np = 0;
     bool have = item < items && named(item, b, h, ca, np);
+    pdl_launch_dependents();  // what follows may start its own prologue; it waits for this grid before it reads or writes
     pdl_wait_prerequisites();  // the decode grid has finished; its partials are in memory
     while (item < items) {
         if (have) {

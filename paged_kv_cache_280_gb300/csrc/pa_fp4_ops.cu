@@ -17,11 +17,11 @@ namespace {
 constexpr int kAppendAhead = 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(const T* k_new, const T* v_new, uint8_t* k_pool,
-                                                                    uint8_t* v_pool, const int64_t* __restrict__ slots,
-                                                                    uint32_t total, const FastDiv heads, int32_t bs_shift,
+                                                                    uint8_t* v_pool, const int64_t* slots, uint32_t total, const FastDiv heads, int32_t bs_shift,
                                                                     int64_t pool_slots, const Divisor kd, const Divisor vd,
                                                                     int32_t* status) {
     pdl_launch_dependents();
+    pdl_wait_prerequisites();
     constexpr int U = D / kFp4Group;                     // groups of a row
     constexpr int kGroup = kFp4Group * (int)sizeof(T);   // bytes of a group
     constexpr int kTurn = 32 * kGroup;                   // bytes of a warp's turn
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(const T* k_n
     for (; base < total; base += stride) {
         const uint32_t idx = base + lane, u = idx & (U - 1), row = idx / U;
         const uint32_t tok = heads.div(row), h = row - tok * heads.d;
-        const int64_t slot = idx < total ? __ldg(slots + tok) : -1;
+        const int64_t slot = idx < total ? slots[tok] : -1;
         copies_wait<kAppendAhead - 1>();
         __syncwarp();  // the other lanes' copies too
         float x[16];
@@ -92,16 +92,16 @@ __device__ __forceinline__ void store16(float* p, const float* x) {
 // of K and of V, kPer times; a CTA's groups are consecutive.  WIDE: the outputs are 32-byte aligned.
 constexpr int kUnpackPer = 2;
 template <typename T, int D, int BS, bool WIDE>
-__global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* __restrict__ k_pool,
-                                                                const uint8_t* __restrict__ v_pool,
-                                                                const int32_t* __restrict__ blocks, uint32_t cta_per_block,
+__global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* k_pool, const uint8_t* v_pool,
+                                                                const int32_t* blocks, uint32_t cta_per_block,
                                                                 T* k_out, T* v_out, int32_t num_kv_heads, int32_t num_blocks,
                                                                 float k_scale, float v_scale, int32_t* status) {
     pdl_launch_dependents();
+    pdl_wait_prerequisites();
     constexpr int U = D / kFp4Group;
     constexpr int kRec = BS * fp4_row_bytes(D);
     const uint32_t i = blockIdx.x / cta_per_block, part = blockIdx.x - i * cta_per_block;
-    const int32_t blk = __ldg(blocks + i);
+    const int32_t blk = blocks[i];
     if (blk < 0 || blk >= num_blocks) {
         if (part == 0 && threadIdx.x == 0) flag_status(status, PA_DEV_BAD_BLOCK_ID);
         return;
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* _
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             const uint8_t* src = (kv ? v_pool : k_pool) + rec;
-            w[t][kv] = __ldg(reinterpret_cast<const uint2*>(src + 8 * r));
-            sb[t][kv] = __ldg(src + BS * (D / 2) + r);
+            w[t][kv] = *reinterpret_cast<const uint2*>(src + 8 * r);
+            sb[t][kv] = src[BS * (D / 2) + r];
         }
     }
 #pragma unroll
@@ -170,8 +170,8 @@ struct UnpackArgs {
 template <typename T, int D, int BS>
 void launch_unpack(const UnpackArgs& a, cudaStream_t st) {
     auto* kernel = a.wide ? &unpack_blocks_fp4_kernel<T, D, BS, true> : &unpack_blocks_fp4_kernel<T, D, BS, false>;
-    kernel<<<a.grid, 256, 0, st>>>(a.k_pool, a.v_pool, a.blocks, a.cta_per_block, static_cast<T*>(a.k_out),
-                                   static_cast<T*>(a.v_out), a.num_kv_heads, a.num_blocks, a.k_scale, a.v_scale, a.status);
+    launch_dependent(kernel, dim3(a.grid), 256, 0, st, a.k_pool, a.v_pool, a.blocks, a.cta_per_block, static_cast<T*>(a.k_out),
+                     static_cast<T*>(a.v_out), a.num_kv_heads, a.num_blocks, a.k_scale, a.v_scale, a.status);
 }
 
 }  // namespace
@@ -200,10 +200,10 @@ extern "C" pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_n
     const int64_t pool_slots = (int64_t)num_blocks * block_size;
     auto go = [&](auto kernel, auto elem) {
         using T = decltype(elem);
-        kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const T*>(k_new), static_cast<const T*>(v_new), static_cast<uint8_t*>(k_pool),
-            static_cast<uint8_t*>(v_pool), slot_mapping, (uint32_t)total, fast_div(num_kv_heads), block_size == 16 ? 4 : 5, pool_slots,
-            divisor(k_scale), divisor(v_scale), dev_status);
+        launch_dependent(kernel, grid, 256, 0, static_cast<cudaStream_t>(stream), static_cast<const T*>(k_new),
+                         static_cast<const T*>(v_new), static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
+                         slot_mapping, (uint32_t)total, fast_div(num_kv_heads), block_size == 16 ? 4 : 5, pool_slots,
+                         divisor(k_scale), divisor(v_scale), dev_status);
     };
     if (in_dtype == PA_BF16)
         head_dim == 128 ? go(&reshape_and_cache_fp4_kernel<__nv_bfloat16, 128>, __nv_bfloat16{})

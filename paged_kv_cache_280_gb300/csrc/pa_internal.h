@@ -166,6 +166,26 @@ bool prefill_q_map(CUtensorMap* map, int dev, const void* q, int64_t tokens, int
 // CTAs per SM; cached per (device, kernel, smem).
 bool kernel_occupancy(int dev, const void* kernel, int threads, int smem, int* occ);
 
+#if defined(__CUDACC__)
+// Launches a kernel as a programmatic dependent of what precedes it on the stream: it may start while a kernel
+// that allows it still runs, and waits for that kernel (pdl_wait_prerequisites) before it touches memory.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, int smem, cudaStream_t stream,
+                             Args&&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+#endif
+
 // Paged prefill (chunked causal) attention, bf16.
 struct PrefillParams {
     void* out;

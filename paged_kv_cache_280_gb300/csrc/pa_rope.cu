@@ -62,6 +62,7 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* x, const Divisor& d) {
 template <typename T, int POOL, int D>
 __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams p) {
     pdl_launch_dependents();  // a decode that follows may start its prologue (it reads nothing written here)
+    pdl_wait_prerequisites();
     constexpr int U = D / 16;  // units per row
     constexpr int kParts = (int)sizeof(T) / 2;      // 16-byte parts of a run
     constexpr uint32_t kPart = 256 * 16;            // one part of every thread's run
@@ -208,8 +209,8 @@ bool launch_pool(const RopeParams& p, int dev, int sms, cudaStream_t st) {
     int occ = 0;
     if (!kernel_occupancy(dev, reinterpret_cast<const void*>(kernel), 256, 0, &occ) || occ <= 0) return false;
     const int64_t units = (int64_t)p.num_tokens * p.heads.d * (D / 16), want = (units + 255) / 256;
-    kernel<<<(unsigned)(want < (int64_t)sms * occ ? want : (int64_t)sms * occ), 256, 0, st>>>(p);
-    return true;
+    const unsigned grid = (unsigned)(want < (int64_t)sms * occ ? want : (int64_t)sms * occ);
+    return launch_dependent(kernel, dim3(grid), 256, 0, st, p) == cudaSuccess;
 }
 
 template <typename T, int D>
