@@ -103,28 +103,34 @@ struct Fp4Ranges {
 
 // The first tile of part w (0 .. kWarps) of CTA c's range, and in seq a sequence at or before the one that
 // holds it.  Without partitions the parts are of equal cost in the plan's units, with partitions of equal
-// numbers of tiles.
-template <int kWarps>
-__device__ __forceinline__ int32_t fp4_part_start(const Fp4Ranges& R, int c, int w, int32_t& seq) {
-    const Plan& P = R.P;
+// numbers of tiles.  The general form is kept out of line: the kernel's first instructions come from memory,
+// and these would lie between them.
+template <int BS, int kWarps>
+__device__ __noinline__ int32_t fp4_part_start_general(const DecodeParams& p, const int32_t* pref, const int32_t* upref, int c,
+                                                       int w, int32_t* seq) {
+    const Plan P = fp4_plan<BS>(p, pref, upref);
     int s0 = 0, s1 = 0;
     int64_t split;
     if (P.PT > 0) {
         const int64_t r0 = P.cta_start(c, &split, &s0), r1 = P.cta_start(c + 1, &split, &s1);
-        seq = s0;
+        *seq = s0;
         return (int32_t)(r0 + (r1 - r0) * w / kWarps);
-    }
-    if (c + 1 == P.C && w == kWarps) return (int32_t)P.T;
-    if (R.small) {
-        const uint32_t u0 = R.start(c), u1 = R.start(c + 1);
-        int32_t h, j;
-        R.locate(u0 + (uint32_t)((uint64_t)(u1 - u0) * w / kWarps), seq, h, j);
-        return P.Hkv * P.pref[seq] + h * P.nblocks(seq) + j;
     }
     const int64_t u0 = P.start_unit(c), u1 = P.start_unit(c + 1);
     const int64_t t = P.first_tile_at_unit(u0 + (u1 - u0) * w / kWarps, &split, &s0);
-    seq = s0;
+    *seq = s0;
     return (int32_t)t;
+}
+template <int BS, int kWarps>
+__device__ __forceinline__ int32_t fp4_part_start(const DecodeParams& p, const Fp4Ranges& R, const int32_t* pref,
+                                                  const int32_t* upref, int c, int w, int32_t& seq) {
+    const Plan& P = R.P;
+    if (c + 1 == P.C && w == kWarps) return (int32_t)P.T;
+    if (!R.small) return fp4_part_start_general<BS, kWarps>(p, pref, upref, c, w, &seq);
+    const uint32_t u0 = R.start(c), u1 = R.start(c + 1);
+    int32_t h, j;
+    R.locate(u0 + (uint32_t)((uint64_t)(u1 - u0) * w / kWarps), seq, h, j);
+    return P.Hkv * P.pref[seq] + h * P.nblocks(seq) + j;
 }
 
 // As plan_matches, for a plan built for a 4-bit pool (its magic word differs, since its ranges do).
@@ -219,7 +225,7 @@ __device__ __forceinline__ int nth_set_lane(uint32_t set, int r, int lane) {
 }
 
 template <int D, int BS, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
     using L = Fp4Layout<D, BS, kWarps>;
     constexpr int TPS = L::TPS, NT = 32 * kWarps;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     pdl_launch_dependents();
     // this warp's part of the CTA's range, and a sequence at or before its start: two searches, lanes 0 and 1
     int32_t tb = 0, seqh = 0;
-    if (P.T > 0 && c < P.C && lane < 2) tb = fp4_part_start<kWarps>(Fp4Ranges(P), c, warp + lane, seqh);
+    if (P.T > 0 && c < P.C && lane < 2) tb = fp4_part_start<BS, kWarps>(p, Fp4Ranges(P), pref, upref, c, warp + lane, seqh);
     const int32_t t0 = __shfl_sync(0xffffffffu, tb, 0), t1 = __shfl_sync(0xffffffffu, tb, 1);
     const int seq0 = __shfl_sync(0xffffffffu, seqh, 0);
 
