@@ -91,9 +91,8 @@ struct Fp4Ranges {
         b = lo, h = (int32_t)hh, j = (int32_t)(rem <= A ? 0 : (rem - A + K - 1) / K);
     }
     // the CTA whose range holds tile t of segment (b, h): the largest c with start(c) <= its unit
-    __device__ __forceinline__ int cta_of(int64_t t, int b, int h) const {
-        if (!small) return P.cta_of_seg(t, b, h);
-        const uint32_t x = (uint32_t)(Plan::K * t + (int64_t)P.A * ((int64_t)P.Hkv * b + h + 1));
+    __device__ __forceinline__ int cta_of(uint32_t t, int b, int h) const {
+        const uint32_t x = Plan::K * t + (uint32_t)P.A * ((uint32_t)P.Hkv * b + h + 1);
         int c = min((int)(C - 1), (int)((float)x * c_per_unit));  // off by one at most: C <= 2^16, and 24 bits of x
         while (c + 1 < (int)C && start(c + 1) <= x) ++c;
         while (c > 0 && start(c) > x) --c;
@@ -470,8 +469,33 @@ __host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads,
 // have eight pieces or more, the four warps of a CTA share its pieces.  The kernel works out its
 // first items while the decode kernel's last CTAs still run; then one round of loads brings the states.
 constexpr int kMergeWarps = kMergeThreads / 32;
+template <int BS>
+__device__ __noinline__ bool fp4_named_general(const DecodeParams& p, const int32_t* pref, const int32_t* upref,
+                                               bool by_segment, int i, int* b, int* h, int* ca, int* np) {
+    const Plan P = fp4_plan<BS>(p, pref, upref);
+    if (by_segment) {
+        *b = i / P.Hkv;
+        *h = i - *b * P.Hkv;
+    } else {
+        int64_t split;
+        int seq;
+        const int64_t t = P.cta_start(i + 1, &split, &seq);
+        if (t >= P.T) return false;
+        *b = P.find_seq(P.pref, t);
+        const int64_t local = t - (int64_t)P.Hkv * P.pref[*b];
+        *h = (int)(local / P.nblocks(*b));
+        if (local == (int64_t)*h * P.nblocks(*b)) return false;  // the boundary falls between segments
+    }
+    const int nb = P.nblocks(*b);
+    if (nb == 0) return false;
+    const int64_t s0 = P.seg_start(*b, *h);
+    *ca = P.cta_of_seg(s0, *b, *h);
+    if (!by_segment && *ca != i) return false;  // an earlier boundary of this segment names it
+    *np = P.cta_of_seg(s0 + nb - 1, *b, *h) - *ca + 1;
+    return *np > 1;
+}
 template <int D, int BS>
-__global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const __grid_constant__ DecodeParams p) {
     extern __shared__ __align__(16) int32_t msm[];
     constexpr int E = D / 32;
     __shared__ float part[kMergeWarps][D + 2];
@@ -497,28 +521,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const DecodePa
     // an item's sequence, KV head, first CTA and pieces; false if its segment is not split, or named elsewhere
     auto named = [&](int64_t item, int& b, int& h, int& ca, int& np) -> bool {
         const int i = (int)(item / G);
+        if (!R.small) return fp4_named_general<BS>(p, pref, upref, by_segment, i, &b, &h, &ca, &np);
         if (by_segment) {
             b = i / Hkv;
             h = i - b * Hkv;
         } else {
             int32_t j;
-            if (R.small) {
-                R.locate(R.start(i + 1), b, h, j);
-            } else {
-                int64_t split;
-                int seq;
-                const int64_t t = P.cta_start(i + 1, &split, &seq);
-                if (t >= P.T) return false;
-                b = P.find_seq(P.pref, t);
-                const int64_t local = t - (int64_t)Hkv * P.pref[b];
-                h = (int)(local / P.nblocks(b));
-                j = (int)(local - (int64_t)h * P.nblocks(b));
-            }
+            R.locate(R.start(i + 1), b, h, j);
             if (j == 0 || j >= P.nblocks(b)) return false;  // the boundary falls between segments
         }
         const int nb = P.nblocks(b);
         if (nb == 0) return false;
-        const int64_t s0 = P.seg_start(b, h);
+        const uint32_t s0 = (uint32_t)Hkv * P.pref[b] + (uint32_t)h * nb;
         ca = R.cta_of(s0, b, h);
         if (!by_segment && ca != i) return false;  // an earlier boundary of this segment names it
         np = R.cta_of(s0 + nb - 1, b, h) - ca + 1;
