@@ -382,7 +382,8 @@ double oracle_e4m3_value(uint8_t c) {
 uint8_t oracle_e4m3_encode(float y) {
     if (isnan(y)) return 0x7F;
     const uint8_t sign = signbit(y) ? 0x80 : 0x00;
-    const double a = fabs((double)y);
+    /* past the largest code every one is nearest to it; capped, so that the distances stay apart in double */
+    const double a = fmin(fabs((double)y), 1024.0);
     int best = 0;
     for (int c = 1; c <= 0x7E; ++c) {
         const double dc = fabs(oracle_e4m3_value((uint8_t)c) - a), db = fabs(oracle_e4m3_value((uint8_t)best) - a);

@@ -31,6 +31,11 @@ def test_encoder_matches_exact_search():
         assert got == want + (8 if np.signbit(x) else 0), x
 
 
+def test_e4m3_encoder_saturates_at_any_size():
+    x = np.array([448.0, 464.0, 1e4, 2.0 ** 62, 1e30, np.inf], np.float32)
+    assert oracle.e4m3_encode(np.concatenate([x, -x])).tolist() == [0x7E] * 6 + [0xFE] * 6
+
+
 @pytest.mark.parametrize("pool_scale", [1.0, 0.043, 3.7])
 def test_group_quantiser(pool_scale):
     rng = np.random.default_rng(1)
