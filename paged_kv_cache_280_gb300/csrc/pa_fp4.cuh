@@ -109,8 +109,9 @@ __device__ __forceinline__ float amax_nan(const float* x) {
     return a;
 }
 
-// x / b for a b with the reciprocal r + t (r rounded, t = (1 - b r) r): within 2^-47 before its one rounding.  Enough
-// where no quotient lies that close to a value that matters (see fp4_codes8).
+// x / b for a b > 0 with the reciprocal r + t (r rounded down, t = (1 - b r) r >= 0): within 2^-46 before its one
+// rounding.  Enough where no quotient lies that close to a value that matters (see fp4_codes8).  A zero keeps its
+// sign, since t has none.
 template <int N>
 __device__ __forceinline__ void near_quotients(const float* x, float r, float t, float* y) {
     const float2 rr = make_float2(r, r), tt = make_float2(t, t);
@@ -141,7 +142,7 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Divisor& d) {
         f.byte = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(__fdiv_rn(amax, d.b), 6.f), __NV_SATFINITE, __NV_E4M3);
     }
     f.s = e4m3_to_float(f.byte);
-    f.r = f.s > 0.f ? __frcp_rn(f.s) : 0.f;  // 0: every code zero
+    f.r = f.s > 0.f ? __frcp_rd(f.s) : 0.f;  // 0: every code zero
     f.t = __fmaf_rn(-f.s, f.r, 1.f) * f.r;
     return f;
 }

@@ -48,6 +48,32 @@ def test_append_bit_exact(n, hkv, d, bs, scales, dtype):
     assert np.array_equal(to_numpy(dk), kp) and np.array_equal(to_numpy(dv), vp)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.043, 3.0 * 2.0 ** 59, 1.1 * 2.0 ** -60, 1e30, 3e-33, 1e-40, 2.0 ** -30])
+def test_append_of_any_bits(scale):
+    """Quotients over the whole range of fp32: every exponent, subnormal numbers and results, zeros of both signs,
+    infinities and NaN, with pool scales in and out of the range where the quotients are formed by multiplication."""
+    import paged_kv_cache_280_gb300 as pa
+
+    n, hkv, d, bs, nb = 64, 4, 128, 16, 5
+    rng = np.random.default_rng(17)
+    bits = rng.integers(0, 1 << 32, (2, n, hkv, d), dtype=np.uint32)
+    # half of the groups: elements near each other in size, around the pool scale and over fp32's range of it
+    near = (rng.standard_normal((2, n, hkv, d)) * np.exp2(rng.integers(-14, 14, (2, n, hkv, d // 16))).repeat(16, -1)
+            * np.float64(np.float32(scale)))
+    with np.errstate(over="ignore"):
+        near = np.clip(near, -3e38, 3e38).astype(np.float32).view(np.uint32)
+    take = (rng.random((2, n, hkv, d // 16)) < 0.75).repeat(16, -1)
+    bits = np.where(take, near, bits)
+    bits[:, :, 0, ::7] = 0x80000000  # negative zeros
+    kn, vn = bits.view(np.float32)
+    slots = synth.permutation(3, nb * bs)[:n].astype(np.int64)
+    kp, vp = _random_pool(1, nb, hkv, bs, d), _random_pool(2, nb, hkv, bs, d)
+    dk, dv = to_torch(kp), to_torch(vp)
+    pa.pa_reshape_and_cache_fp4(to_torch(kn), to_torch(vn), dk, dv, to_torch(slots), scale, scale)
+    kv4.append_fp4(kn, vn, kp, vp, slots, bs, scale, scale)
+    assert np.array_equal(to_numpy(dk), kp) and np.array_equal(to_numpy(dv), vp)
+
+
 def test_append_flags_a_bad_slot_and_leaves_the_rest():
     import torch
     import paged_kv_cache_280_gb300 as pa
@@ -173,7 +199,8 @@ LENS = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 250]
 
 @pytest.mark.parametrize("hq,hkv,d,bs,part", [
     (8, 8, 128, 16, 0), (4, 2, 128, 32, 0), (32, 8, 128, 16, 0), (12, 4, 64, 16, 0), (8, 1, 64, 32, 0), (5, 1, 128, 16, 0),
-    (14, 2, 128, 32, 0), (32, 4, 128, 16, 32), (16, 8, 64, 16, 64), (8, 8, 64, 32, 32), (1, 1, 64, 16, 0)])
+    (14, 2, 128, 32, 0), (32, 4, 128, 16, 32), (16, 8, 64, 16, 64), (8, 8, 64, 32, 32), (1, 1, 64, 16, 0),
+    (16, 16, 128, 16, 0), (48, 16, 64, 32, 0), (16, 16, 128, 32, 64)])  # the last three: more segments than CTAs
 def test_decode_matches_oracle(hq, hkv, d, bs, part):
     c = Case(40 + hq + d + bs, hq, hkv, d, bs, LENS)
     got = c.run(part)
@@ -197,6 +224,22 @@ def test_decode_merge_modes_and_plan(hq, hkv, d, bs, mode):
         assert status_word(c.ws) == 0
     finally:
         pa.pa_debug_set_merge_mode(0)
+
+
+def test_decode_of_nothing():
+    c = Case(3, 8, 2, 128, 16, [0, 0, 0])
+    assert not c.run().any() and not c.run(part=64).any() and not c.run(max_seq_len=100).any()
+    assert status_word(c.ws) == 0
+
+
+@pytest.mark.parametrize("part", [0, 32])
+def test_decode_many_sequences(part):
+    """More sequences than the 16-warp kernel's shared memory holds the lengths of."""
+    lens = synth.uniform_ints(77, 2300, 0, 40).astype(np.int32)
+    lens[1111] = 900
+    c = Case(21, 8, 1, 128, 16, lens)
+    c.check(c.run(part), seqs=[0, 1, 2, 1110, 1111, 1112, 2298, 2299] + list(range(100, 2300, 100)))
+    assert status_word(c.ws) == 0
 
 
 def test_decode_one_long_sequence():

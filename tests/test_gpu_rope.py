@@ -174,6 +174,34 @@ def test_rope_special_values():
     assert np.isnan(got[0, 0, 0, :16]).all() and np.isfinite(got[0, 0, 0, 16:]).all() and np.isfinite(got[0, 0, 5]).all()
 
 
+@pytest.mark.parametrize("scale", [0.043, 2.0 ** -5, 1e30, 3e-33])
+def test_rope_fp8_codes_of_any_bits(scale):
+    """Values (not turned) quantised over the whole range of fp32."""
+    import paged_kv_cache_280_gb300 as pa
+
+    n, hkv, d, bs, nb = 40, 2, 128, 16, 4
+    rng = np.random.default_rng(5)
+    bits = rng.integers(0, 1 << 32, (n, hkv, d), dtype=np.uint32)
+    near = (rng.standard_normal((n, hkv, d)) * np.exp2(rng.integers(-12, 10, (n, hkv, d))) * np.float64(np.float32(scale)))
+    with np.errstate(over="ignore"):
+        near = np.clip(near, -3e38, 3e38).astype(np.float32).view(np.uint32)
+    v = np.where(rng.random((n, hkv, d)) < 0.8, near, bits).astype(np.uint32).view(np.float32)
+    v[np.isnan(v)] = np.nan  # one NaN pattern: the code is the NaN code either way
+    v[:, :, 5] = -0.0
+    k = np.ones((n, hkv, d), np.float32)
+    table = kv4.cos_sin_table(4, d)
+    slots, pos = np.arange(n, dtype=np.int64), np.zeros(n, np.int32)
+    kp, vp = np.zeros((nb, hkv, bs, d), np.uint8), np.zeros((nb, hkv, bs, d), np.uint8)
+    dkp, dvp = to_torch(kp), to_torch(vp)
+    pa.pa_rope_and_cache(None, None, to_torch(k), to_torch(v), to_torch(pos), to_torch(table), dkp, dvp, to_torch(slots),
+                         k_scale=1.0, v_scale=scale)
+    with np.errstate(all="ignore"):
+        want = oracle.e4m3_encode(v / np.float32(scale))
+    got = to_numpy(dvp).transpose(0, 2, 1, 3).reshape(nb * bs, hkv, d)[:n]
+    bad = np.isnan(v)
+    assert np.all((got[bad] & 0x7F) == 0x7F) and np.array_equal(got[~bad], want[~bad])
+
+
 def test_rope_on_another_stream_and_captured():
     import torch
     import paged_kv_cache_280_gb300 as pa
