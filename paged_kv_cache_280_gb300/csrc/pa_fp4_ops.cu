@@ -20,8 +20,8 @@ __global__ void __launch_bounds__(256) reshape_and_cache_fp4_kernel(const T* k_n
                                                                     uint8_t* v_pool, const int64_t* slots, uint32_t total, const FastDiv heads, int32_t bs_shift,
                                                                     int64_t pool_slots, const Divisor kd, const Divisor vd,
                                                                     int32_t* status) {
-    pdl_launch_dependents();
     pdl_wait_prerequisites();
+    pdl_launch_dependents();  // in this order: see rope_and_cache_kernel
     constexpr int U = D / kFp4Group;                     // groups of a row
     constexpr int kGroup = kFp4Group * (int)sizeof(T);   // bytes of a group
     constexpr int kTurn = 32 * kGroup;                   // bytes of a warp's turn
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* k
                                                                 const int32_t* blocks, uint32_t cta_per_block,
                                                                 T* k_out, T* v_out, int32_t num_kv_heads, int32_t num_blocks,
                                                                 float k_scale, float v_scale, int32_t* status) {
-    pdl_launch_dependents();
     pdl_wait_prerequisites();
+    pdl_launch_dependents();  // in this order: see rope_and_cache_kernel
     constexpr int U = D / kFp4Group;
     constexpr int kRec = BS * fp4_row_bytes(D);
     const uint32_t i = blockIdx.x / cta_per_block, part = blockIdx.x - i * cta_per_block;

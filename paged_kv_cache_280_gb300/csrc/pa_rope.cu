@@ -61,8 +61,10 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* x, const Divisor& d) {
 
 template <typename T, int POOL, int D>
 __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams p) {
-    pdl_launch_dependents();  // a decode that follows may start its prologue (it reads nothing written here)
+    // A decode that follows may start its prologue, which reads nothing written here, but only once what came
+    // before this kernel is complete: that may have written the lengths and tables it reads.
     pdl_wait_prerequisites();
+    pdl_launch_dependents();
     constexpr int U = D / 16;  // units per row
     constexpr int kParts = (int)sizeof(T) / 2;      // 16-byte parts of a run
     constexpr uint32_t kPart = 256 * 16;            // one part of every thread's run

@@ -474,3 +474,56 @@ def test_serving_steps_over_a_4_bit_cache(captured):
         ref, bound = kv4.decode_fp4(rq, kp, vp, ks, vs, tables, lens, scale, bs)
         assert np.all(np.abs(widen(to_numpy(o1)) - ref) <= 2.0 ** -8 * (np.abs(ref) + bound) + bound)
     assert status_word(ws) == 0
+
+
+def test_a_captured_step_whose_inputs_come_from_two_streams():
+    """The lengths and the rows are written in the graph, the rows on a second stream that joins before the append; the
+    decode follows the append.  Each replay takes what the buffers then hold."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    hq, hkv, d, bs, nb, B = 8, 2, 128, 16, 12, 3
+    gen = np.random.default_rng(5)
+    steps = [kv4.to_bf16(gen.standard_normal((B, hq + 2 * hkv, d)).astype(np.float32)) for _ in range(3)]
+    table = kv4.cos_sin_table(64, d)
+    dtable, dsteps = to_torch(table), [to_torch(x) for x in steps]
+    kp, vp = _random_pool(1, nb, hkv, bs, d), _random_pool(2, nb, hkv, bs, d)
+    dkp, dvp = to_torch(kp), to_torch(vp)
+    tables = np.arange(nb, dtype=np.int32).reshape(B, 4)[:, ::-1].copy()
+    start = np.array([0, 15, 40], np.int32)
+    dtables, lens = to_torch(tables), to_torch(start)
+    given, x = (torch.empty_like(dsteps[0]) for _ in range(2))
+    q_rot, out = (torch.empty(B, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.zeros(pa.pa_decode_workspace_bytes(B, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    rows = torch.arange(B, device="cuda")
+
+    def step():
+        main, side = torch.cuda.current_stream(), step.side
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.copy_(given)
+        pos = lens.clone()
+        at = pos.long()
+        slots = dtables[rows, at // bs].long() * bs + at % bs
+        lens.add_(1)
+        main.wait_stream(side)
+        pa.pa_rope_and_cache(q_rot, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, dtable, dkp, dvp, slots)
+        pa.pa_decode_attention_fp4(out, q_rot, dkp, dvp, 1.0, 1.0, dtables, lens, 64, d ** -0.5, ws)
+
+    step.side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i, s in enumerate(steps):
+        given.copy_(dsteps[i])
+        graph.replay()
+        pos = start + i
+        slots = tables[np.arange(B), pos // bs].astype(np.int64) * bs + pos % bs
+        k = kv4.rotate_f32(s[:, hq:hq + hkv], pos, table, False)
+        kv4.append_fp4(k, s[:, hq + hkv:], kp, vp, slots, bs, 1.0, 1.0)
+        rq = kv4.to_bf16(kv4.rotate_f32(s[:, :hq], pos, table, False))
+        assert np.array_equal(to_numpy(dkp), kp) and np.array_equal(to_numpy(dvp), vp)
+        assert np.array_equal(to_numpy(lens), pos + 1) and np.array_equal(to_numpy(q_rot), rq)
+        ref, bound = kv4.decode_fp4(rq, kp, vp, 1.0, 1.0, tables, pos + 1, d ** -0.5, bs)
+        assert np.all(np.abs(widen(to_numpy(out)) - ref) <= 2.0 ** -8 * (np.abs(ref) + bound) + bound)
+    assert status_word(ws) == 0
