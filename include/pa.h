@@ -270,7 +270,8 @@ pa_status pa_decode_attention_static(void* out, const void* q, const void* k_poo
 /*
  * Launch facts of pa_decode_attention for these shapes on the current device
  * (no launch): CTAs in the grid, pipeline stages per CTA (on the tensor-core
- * path at block size 16 a stage holds two blocks' tiles), dynamic shared
+ * path at block size 16 a stage holds two blocks' tiles; over 4-bit pools each
+ * warp of a CTA has that many stages of 32 tokens), dynamic shared
  * memory per CTA in bytes, and 1 if the tensor-core (mma) path is used, else
  * 0 (CUDA-core FMA path).  max_blocks_per_seq bounds the blocks of every
  * sequence; partition_tokens is as for pa_decode_attention (the build and the
@@ -282,7 +283,7 @@ pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads, int32_t n
                                 int32_t* uses_mma);
 
 /*
- * Kernels one pa_decode_attention (or _fp8, _static) call with these shapes
+ * Kernels one pa_decode_attention (or _fp8, _fp4, _static) call with these shapes
  * launches on the current device (no launch): 1 when it merges split
  * segments in the decode kernel, 2 when the merge kernel follows it.
  * max_blocks_per_seq bounds the blocks of every sequence, as for
@@ -294,9 +295,9 @@ pa_status pa_decode_kernels_per_call(int32_t num_seqs, int32_t num_q_heads, int3
 
 /*
  * Tuning: CTAs per SM of the decode grid (1..8; 0 restores the default: 4 on
- * the bf16 tensor-core path, otherwise, FP8 pools included, as many as fit,
- * at most 8).  Process-wide; affects later pa_decode_attention and
- * pa_decode_attention_fp8 calls.  More CTAs per SM keep more tiles in flight
+ * the bf16 tensor-core path, otherwise, FP8 and 4-bit pools included, as many
+ * as fit, at most 8).  Process-wide; affects later pa_decode_attention,
+ * pa_decode_attention_fp8 and pa_decode_attention_fp4 calls.  More CTAs per SM keep more tiles in flight
  * but add split points (partials) at CTA edges.
  */
 pa_status pa_decode_set_ctas_per_sm(int32_t ctas);
@@ -311,7 +312,7 @@ pa_status pa_decode_set_ctas_per_sm(int32_t ctas);
  * that call is not valid.  A limit far below a DRAM round trip makes the waits
  * run out on purpose.  0 restores the default (2 s); values above it return
  * PA_ERR_INVALID_ARG.  Process-wide; affects later pa_decode_attention,
- * pa_decode_attention_fp8 and pa_decode_attention_static calls.
+ * pa_decode_attention_fp8, _fp4 and pa_decode_attention_static calls.
  */
 pa_status pa_debug_set_wait_limit_ns(uint64_t ns);
 
@@ -437,7 +438,15 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
  * modes, plan and error reporting; plans are built with dtype PA_FP4_E2M1).
  * code * scale is exact in f16, in which the MMAs run with fp32 sums; a query
  * row is first scaled by a power of two so that its largest element lies in
- * [1, 2), so any bf16 magnitudes are in range.
+ * [1, 2), so any bf16 magnitudes are in range.  The call is two kernels, the
+ * second, which merges split segments, a programmatic dependent (with one
+ * CTA there is nothing to merge and one kernel); pa_debug_set_merge_mode does not
+ * change that.  num_kv_heads <= 32767; num_seqs is bounded by the lengths' room
+ * in shared memory (at least 10,000; PA_ERR_UNSUPPORTED past it).
+ *
+ * The append and the unpacking are launched as programmatic dependents too: they
+ * touch memory only after the preceding kernel has completed, and a decode call
+ * that follows may start its prologue once that is so.
  */
 pa_status pa_reshape_and_cache_fp4(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
                                    const int64_t* slot_mapping, int32_t num_tokens, int32_t num_kv_heads,
@@ -491,8 +500,10 @@ pa_status pa_decode_attention_fp4_planned(void* out, const void* q, const void* 
  * nothing of it is written, q_out included.  A slot past the pool sets
  * PA_DEV_BAD_SLOT, a position outside [0, max_position) PA_DEV_BAD_POSITION, and
  * the token is skipped.  Slots of one call must be distinct.  Asynchronous on
- * `stream`.  Allocates nothing.  A decode call that follows on the stream may
- * start its prologue early, as after pa_reshape_and_cache.
+ * `stream`.  Allocates nothing.  Launched as a programmatic dependent: the
+ * kernel touches memory only after the preceding kernel on the stream has
+ * completed, and a decode call that follows may start its prologue from then on,
+ * as after pa_reshape_and_cache.
  */
 pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,

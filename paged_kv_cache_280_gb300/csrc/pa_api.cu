@@ -280,7 +280,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
     // Default CTAs per SM: the bf16 tensor-core path, which spends little time per tile,
     // keeps four (about 128 KB of tiles in flight, enough to cover HBM latency with fewer
     // split points); the CUDA-core path and the FP8 tensor-core path (which widens every
-    // stage first) take as many as fit.
+    // stage first) take as many as fit, as do the large CTAs over 4-bit pools (one or two).
     int want = g_ctas_per_sm.load();
     if (want <= 0) want = lp->mma && dtype == PA_BF16 ? kDefaultCtasPerSmMma : kMaxCtasPerSm;
     const int64_t tiles_bound = (int64_t)num_seqs * num_kv_heads * max_tiles_per_head;
@@ -327,7 +327,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
     // its fence and count stall the only consumer warp); with segments weighted as FP8
     // ranges weigh them the second is faster on every workload measured, though its four
     // CTAs fill an SM's registers and merge_kernel starts only as they exit, so FP8 calls
-    // always take it.  With fixed partitions
+    // always take it.  The decode over 4-bit pools has no in-kernel merge (pa_decode_fp4.cu).  With fixed partitions
     // (long contexts) a segment spans many CTAs and is merged after the streaming either
     // way: merge_kernel.  (Measured on GB300 on the workloads of the pages: each rule
     // picked the faster choice or one within 0.5 % of it.)
@@ -470,7 +470,8 @@ extern "C" pa_status pa_decode_kernels_per_call(int32_t num_seqs, int32_t num_q_
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
                     partition_tokens > 0, dtype, &lp);
     if (s != PA_OK) return s;
-    *kernels = lp.merge_in_kernel ? 1 : 2;
+    // (over a 4-bit pool a grid of one CTA has nothing to merge and launches no second kernel)
+    *kernels = lp.merge_in_kernel || (dtype == PA_FP4_E2M1 && lp.grid == 1) ? 1 : 2;
     return PA_OK;
 }
 

@@ -13,12 +13,21 @@
 // that make up a segment are merged and written to out, a run that goes on in the next CTA or came from
 // the one before becomes the CTA's partial in the workspace, and a second kernel, launched as the
 // programmatic dependent of this one, merges those.
+//
+// Measured (both kernels, device time): 256 sequences of 32 .. 4095 tokens with 32 heads of their own 165 us, 6.0 TB/s
+// (0.89 of the measured copy rate); 4 sequences of 131072 tokens with 64 / 8 heads 100 us (0.89); 64 sequences with
+// 32 / 8 heads 22 us (0.42: 4.7 us pass before the first tile arrives, 4.5 after the last); one sequence of 1031
+// tokens 7.2 us.  With producer and consumer warps and four CTAs per SM, as over FP8 pools, the first three took
+// 299, 142 and 31 us: the hand-over cost a third of the issue slots.
 #include "pa_decode.cuh"
 #include "pa_decode_fp4.cuh"
 
 namespace pa {
 namespace {
 
+// Two stages of 32 tokens a warp (2 x 4.6 KB at D = 128, 147 KB per SM): what one warp lacks in depth the
+// other fifteen have.  Measured on the first two batches above (us), warps x stages: 16 x 2 186 / 114, 14 x 2
+// 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.
 constexpr int kStages = 2;   // ring stages per warp
 constexpr int kStageTok = 32;
 constexpr size_t partial_slot_bytes_max(int d) { return (size_t)(kMaxGroup * (d + kSlotExtraFloatsPerHead) + 3) / 4 * 16; }
@@ -31,7 +40,8 @@ struct alignas(16) Fp4Left {
     int32_t pad;
 };
 // kWarps: 16, one CTA per SM (512 threads of 128 registers), or 8 where a batch's prefix arrays leave no
-// room for 16 rings.
+// room for 16 rings (at D = 128 without partitions: past 2,125 sequences with 8 query
+// heads to a KV head, 9,389 with one; 8 warps take 15,589 and 19,221).
 template <int D, int BS, int kWarps>
 struct Fp4Layout {
     static constexpr int TPS = kStageTok / BS;  // tiles per stage
@@ -454,7 +464,9 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     }
 }
 
-// How the merge goes about its items (see merge_fp4_kernel): by segment, and a CTA to an item.
+// How the merge goes about its items (see merge_fp4_kernel): by segment, and a CTA to an item.  By boundary there is
+// an item for each CTA however many segments there are (256 sequences of 32 heads: 8,192 segments, 151 boundaries), by
+// segment an item for each segment however many CTAs hold it (one sequence of 8 heads: 8 against 151).
 __host__ __device__ inline bool fp4_merge_by_segment(int num_seqs, int num_kv_heads, int ctas) {
     return (int64_t)num_seqs * num_kv_heads <= ctas;
 }

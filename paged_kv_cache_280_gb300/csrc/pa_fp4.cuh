@@ -100,16 +100,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // the larger, or 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-// max |x[i]| of N values, NaN if one is.
+// max |x[i]| of N (even) values, NaN if one is.
 template <int N>
 __device__ __forceinline__ float amax_nan(const float* x) {
-    float a = fabsf(x[0]);
+    float a = max_nan(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-    for (int i = 1; i < N; ++i) a = max_nan(a, fabsf(x[i]));
+    for (int i = 2; i < N; i += 2)
+        asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(fabsf(x[i])), "f"(fabsf(x[i + 1])));
     return a;
 }
 
-// x / b for a b > 0 with the reciprocal r + t (r rounded down, t = (1 - b r) r >= 0): within 2^-46 before its one
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// x / b for a b > 0 with the reciprocal r + t (r at most 1 / b, t = (1 - b r) r >= 0): within 2^-41 before its one
 // rounding.  Enough where no quotient lies that close to a value that matters (see fp4_codes8).  A zero keeps its
 // sign, since t has none.
 template <int N>
@@ -142,7 +148,9 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Divisor& d) {
         f.byte = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(__fdiv_rn(amax, d.b), 6.f), __NV_SATFINITE, __NV_E4M3);
     }
     f.s = e4m3_to_float(f.byte);
-    f.r = f.s > 0.f ? __frcp_rd(f.s) : 0.f;  // 0: every code zero
+    // The hardware's reciprocal is within 2^-23 of 1 / s; 2^-22 less is below it, by less than 2^-21.  Then
+    // 1 - s r is exact (s has 4 significant bits), and r + t is within (2^-21)^2 and t's rounding of 1 / s.
+    f.r = f.s > 0.f ? rcp_approx(f.s) * (1.f - 0x1p-22f) : 0.f;  // 0: every code zero
     f.t = __fmaf_rn(-f.s, f.r, 1.f) * f.r;
     return f;
 }
@@ -161,11 +169,15 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* x, const Divisor& d,
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = f.s > 0.f ? __fdiv_rn(__fdiv_rn(x[i], d.b), f.s) : 0.f;
     }
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_E2M1, cudaRoundNearest) << (8 * i);
-    }
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
     return f.r > 0.f ? w : 0u;
 }
 

@@ -34,7 +34,9 @@ constexpr int kMaxSmem = 227 * 1024;
 // (its query rows, the softmax's end, the partial store and merge count) costs
 // about six FP8 tiles: a fit of loop ends against tiles and segments per CTA
 // gave 5.8, and a sweep of the weight was fastest at 24 units on all three
-// unpartitioned workloads.
+// unpartitioned workloads.  Over 4-bit pools a segment costs a warp its query fragments, one masked
+// stage and a join: a sweep of the weight at 4, 8, 12, 16, 24, 40 and 64 units took 204, 186, 177, 172,
+// 172, 180 and 193 us on 256 sequences of 32 heads of their own.
 constexpr int kTileUnits = 4;
 #ifndef PA_SEG_UNITS_MMA
 #define PA_SEG_UNITS_MMA 4
@@ -137,7 +139,7 @@ bool decode_variant_fp8(int head_dim, int block_size, int group, DecodeVariant* 
 // bf16 queries and outputs over 4-bit pools, tensor-core path.
 bool decode_variant_fp4(int head_dim, int block_size, int group, int num_seqs, bool fixed, DecodeVariant* out);
 
-// The decode of pa_decode_attention / _fp8 (pa_api.cu): checks, plan and launch.
+// The decode of pa_decode_attention / _fp8 / _fp4 (pa_api.cu): checks, plan and launch.
 // Refuses a workspace smaller than the bytes its own grid touches (the status
 // head, a merge counter and two partial slots per CTA).  clear_status zeroes
 // the status head and the merge counters on the stream after every check has

@@ -226,6 +226,17 @@ def test_decode_merge_modes_and_plan(hq, hkv, d, bs, mode):
         pa.pa_debug_set_merge_mode(0)
 
 
+def test_launch_facts():
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    ctas, stages, smem, mma = pa.pa_decode_launch_info(64, 32, 8, 128, 16, 256, pa.PA_FP4_E2M1)
+    assert (ctas, stages, mma) == (torch.cuda.get_device_properties(0).multi_processor_count, 2, 1) and smem <= 227 * 1024
+    assert pa.pa_decode_kernels_per_call(64, 32, 8, 128, 16, 256, 0, pa.PA_FP4_E2M1) == 2
+    assert pa.pa_decode_kernels_per_call(1, 8, 1, 128, 16, 1, 0, pa.PA_FP4_E2M1) == 1  # a grid of one CTA
+    assert pa.pa_decode_kernels_per_call(1, 8, 1, 128, 16, 1, 0, pa.PA_FP8_E4M3) == 2
+
+
 def test_decode_of_nothing():
     c = Case(3, 8, 2, 128, 16, [0, 0, 0])
     assert not c.run().any() and not c.run(part=64).any() and not c.run(max_seq_len=100).any()
