@@ -28,7 +28,6 @@ namespace {
 // Two stages of 32 tokens a warp (2 x 4.6 KB at D = 128, 147 KB per SM): what one warp lacks in depth the
 // other fifteen have.  Measured on the first two batches above (us), warps x stages: 16 x 2 186 / 114, 14 x 2
 // 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.
-constexpr int kStages = 2;   // ring stages per warp
 constexpr int kStageTok = 32;
 constexpr size_t partial_slot_bytes_max(int d) { return (size_t)(kMaxGroup * (d + kSlotExtraFloatsPerHead) + 3) / 4 * 16; }
 
@@ -44,6 +43,7 @@ struct alignas(16) Fp4Left {
 // heads to a KV head, 9,389 with one; 8 warps take 15,589 and 19,221).
 template <int D, int BS, int kWarps>
 struct Fp4Layout {
+    static constexpr int kStages = 2;           // ring stages per warp
     static constexpr int TPS = kStageTok / BS;  // tiles per stage
     static constexpr int kTile = BS * fp4_row_bytes(D);
     static constexpr int kStageBytes = 2 * TPS * kTile;  // K of its tiles, then their V
@@ -70,76 +70,118 @@ __device__ __forceinline__ Plan fp4_plan(const DecodeParams& p, const int32_t* p
 }
 
 // The plan's ranges in 32 bits, where the batch allows (`small`): the same arithmetic as Plan's without
-// partitions and skew.  Both kernels do it before anything is requested from HBM (or with the merge at
-// the end of everything), so it is worth keeping short.
+// skew.  Both kernels do it before anything is requested from HBM (or with the merge at the end of
+// everything), so it is worth keeping short.  Units are the plan's: weighted tiles, or partitions.
 struct Fp4Ranges {
     const Plan& P;
-    bool small;
+    bool fixed, small;
     uint32_t U, C, q, r;
     float c_per_unit;
-    __device__ __forceinline__ explicit Fp4Ranges(const Plan& plan) : P(plan) {
-        small = P.PT == 0 && P.KS == 0 && P.U < (int64_t)1 << 31;
+    // partitions: whether the plan has them; a constant where one is given
+    __device__ __forceinline__ Fp4Ranges(const Plan& plan, bool partitions) : P(plan), fixed(partitions) {
+        small = P.KS == 0 && P.U < (int64_t)1 << 31;
         U = (uint32_t)P.U, C = (uint32_t)P.C;
         q = U / max(C, 1u), r = U - q * C;
         c_per_unit = (float)C / (float)U;
     }
-    // the first unit of CTA c's range, ceil(c U / C) = c (U / C) + ceil(c (U % C) / C)
-    __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c * r + C - 1) / C; }
-    // where unit x falls: its sequence, KV head, and the tile of the segment at or after it
+    // the first unit of CTA c's range: c U / C = c (U / C) + c (U % C) / C, rounded up, with partitions down
+    __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c * r + (fixed ? 0 : C - 1)) / C; }
+    // where unit x < U falls: its sequence, KV head, and the tile of the segment at or after it
     __device__ __forceinline__ void locate(uint32_t x, int32_t& b, int32_t& h, int32_t& j) const {
         const uint32_t K = Plan::K, A = P.A, H = P.Hkv;
         int lo = 0, hi = P.B - 1;  // largest sequence whose units start at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (H * (K * P.pref[mid] + A * mid) <= x)
+            if ((fixed ? H * P.upref[mid] : H * (K * P.pref[mid] + A * mid)) <= x)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const uint32_t span = K * P.nblocks(lo) + A, local = x - H * (K * P.pref[lo] + A * lo);
+        const uint32_t span = fixed ? P.upref[lo + 1] - P.upref[lo] : K * P.nblocks(lo) + A;
+        const uint32_t local = x - (fixed ? H * P.upref[lo] : H * (K * P.pref[lo] + A * lo));
         const uint32_t hh = local / span, rem = local - hh * span;
-        b = lo, h = (int32_t)hh, j = (int32_t)(rem <= A ? 0 : (rem - A + K - 1) / K);
+        b = lo, h = (int32_t)hh, j = (int32_t)(fixed ? rem * P.PT : rem <= A ? 0 : (rem - A + K - 1) / K);
     }
-    // the CTA whose range holds tile t of segment (b, h): the largest c with start(c) <= its unit
-    __device__ __forceinline__ int cta_of(uint32_t t, int b, int h) const {
-        const uint32_t x = Plan::K * t + (uint32_t)P.A * ((uint32_t)P.Hkv * b + h + 1);
+    __device__ __forceinline__ int32_t tile(int32_t b, int32_t h, int32_t j) const { return P.Hkv * P.pref[b] + h * P.nblocks(b) + j; }
+    // the CTA whose range holds unit x: the largest c with start(c) <= x
+    __device__ __forceinline__ int cta_of(uint32_t x) const {
         int c = min((int)(C - 1), (int)((float)x * c_per_unit));  // off by one at most: C <= 2^16, and 24 bits of x
         while (c + 1 < (int)C && start(c + 1) <= x) ++c;
         while (c > 0 && start(c) > x) --c;
         return c;
     }
+    // the CTAs that hold the first and the last tile of segment (b, h) of nb > 0 tiles
+    __device__ __forceinline__ void segment_ctas(int32_t b, int32_t h, int32_t nb, int32_t& first, int32_t& last) const {
+        const uint32_t H = P.Hkv, K = Plan::K;
+        if (fixed) {
+            const uint32_t n = P.upref[b + 1] - P.upref[b], x = H * P.upref[b] + h * n;
+            first = cta_of(x), last = cta_of(x + n - 1);
+        } else {
+            const uint32_t x = K * (uint32_t)tile(b, h, 0) + (uint32_t)P.A * (H * b + h + 1);
+            first = cta_of(x), last = cta_of(x + K * (nb - 1));
+        }
+    }
 };
 
-// The first tile of part w (0 .. kWarps) of CTA c's range, and in seq a sequence at or before the one that
-// holds it.  Without partitions the parts are of equal cost in the plan's units, with partitions of equal
-// numbers of tiles.  The general form is kept out of line: the kernel's first instructions come from memory,
-// and these would lie between them.
+// The first tile of part e (0 .. kWarps) of CTA c's range, and in seq a sequence at or before the one that
+// holds it, for plans with partitions or past 32 bits.  Kept out of line: the kernel's first instructions come from
+// memory, and these would lie between them.
 template <int BS, int kWarps>
 __device__ __noinline__ int32_t fp4_part_start_general(const DecodeParams& p, const int32_t* pref, const int32_t* upref, int c,
-                                                       int w, int32_t* seq) {
+                                                       int e, int32_t* seq) {
     const Plan P = fp4_plan<BS>(p, pref, upref);
-    int s0 = 0, s1 = 0;
-    int64_t split;
     if (P.PT > 0) {
-        const int64_t r0 = P.cta_start(c, &split, &s0), r1 = P.cta_start(c + 1, &split, &s1);
+        const Fp4Ranges R(P, true);
+        c += e == kWarps;
+        if (c == P.C) return (int32_t)P.T;
+        int s0 = 0;
+        if (R.small) {
+            int32_t h, j;
+            R.locate(R.start(c), s0, h, j);
+            *seq = s0;
+            return R.tile(s0, h, j);
+        }
+        int64_t split;
+        const int64_t t = P.cta_start(c, &split, &s0);
         *seq = s0;
-        return (int32_t)(r0 + (r1 - r0) * w / kWarps);
+        return (int32_t)t;
     }
+    int s0 = 0;
+    int64_t split;
     const int64_t u0 = P.start_unit(c), u1 = P.start_unit(c + 1);
-    const int64_t t = P.first_tile_at_unit(u0 + (u1 - u0) * w / kWarps, &split, &s0);
+    const int64_t t = P.first_tile_at_unit(u0 + (u1 - u0) * e / kWarps, &split, &s0);
     *seq = s0;
     return (int32_t)t;
 }
+// The part (tiles t0 .. t1) of warp w of CTA c's range, and a sequence at or before the one that holds t0.
+// Without partitions the parts are of equal cost in the plan's units, with partitions of equal numbers of tiles.
+// The two ends are two searches, in lanes 0 and 1.
 template <int BS, int kWarps>
-__device__ __forceinline__ int32_t fp4_part_start(const DecodeParams& p, const Fp4Ranges& R, const int32_t* pref,
-                                                  const int32_t* upref, int c, int w, int32_t& seq) {
-    const Plan& P = R.P;
-    if (c + 1 == P.C && w == kWarps) return (int32_t)P.T;
-    if (!R.small) return fp4_part_start_general<BS, kWarps>(p, pref, upref, c, w, &seq);
-    const uint32_t u0 = R.start(c), u1 = R.start(c + 1);
-    int32_t h, j;
-    R.locate(u0 + (uint32_t)((uint64_t)(u1 - u0) * w / kWarps), seq, h, j);
-    return P.Hkv * P.pref[seq] + h * P.nblocks(seq) + j;
+__device__ __forceinline__ void fp4_part(const DecodeParams& p, const Plan& P, const int32_t* pref, const int32_t* upref, int c,
+                                         int w, int lane, int32_t& t0, int32_t& t1, int32_t& seq) {
+    const Fp4Ranges R(P, false);
+    const bool fixed = P.PT > 0;
+    int32_t t = 0, s = 0;
+    if (P.T > 0 && c < P.C && lane < 2) {
+        const int e = fixed ? kWarps * lane : w + lane;  // the end to search for; with partitions the range's own
+        if (c + 1 == P.C && e == kWarps) {
+            t = (int32_t)P.T;
+        } else if (fixed || !R.small) {
+            t = fp4_part_start_general<BS, kWarps>(p, pref, upref, c, e, &s);
+        } else {
+            const uint32_t u0 = R.start(c), u1 = R.start(c + 1);
+            int32_t h, j;
+            R.locate(u0 + (uint32_t)((uint64_t)(u1 - u0) * e / kWarps), s, h, j);
+            t = R.tile(s, h, j);
+        }
+    }
+    t0 = __shfl_sync(0xffffffffu, t, 0), t1 = __shfl_sync(0xffffffffu, t, 1);
+    seq = __shfl_sync(0xffffffffu, s, 0);
+    if (fixed) {
+        const int32_t r0 = t0;
+        const uint64_t n = (uint32_t)(t1 - t0);
+        t0 = r0 + (int32_t)(n * w / kWarps), t1 = r0 + (int32_t)(n * (w + 1) / kWarps);
+    }
 }
 
 // As plan_matches, for a plan built for a 4-bit pool (its magic word differs, since its ranges do).
@@ -236,7 +278,7 @@ __device__ __forceinline__ int nth_set_lane(uint32_t set, int r, int lane) {
 template <int D, int BS, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
     using L = Fp4Layout<D, BS, kWarps>;
-    constexpr int TPS = L::TPS, NT = 32 * kWarps;
+    constexpr int TPS = L::TPS, NT = 32 * kWarps, kStages = L::kStages;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = p.num_seqs, Hkv = p.num_kv_heads, Hq = p.num_q_heads, G = p.group, c = blockIdx.x;
@@ -266,11 +308,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     __syncthreads();
     const Plan P = fp4_plan<BS>(p, pref, upref);
     pdl_launch_dependents();
-    // this warp's part of the CTA's range, and a sequence at or before its start: two searches, lanes 0 and 1
-    int32_t tb = 0, seqh = 0;
-    if (P.T > 0 && c < P.C && lane < 2) tb = fp4_part_start<BS, kWarps>(p, Fp4Ranges(P), pref, upref, c, warp + lane, seqh);
-    const int32_t t0 = __shfl_sync(0xffffffffu, tb, 0), t1 = __shfl_sync(0xffffffffu, tb, 1);
-    const int seq0 = __shfl_sync(0xffffffffu, seqh, 0);
+    int32_t t0, t1, seq0;
+    fp4_part<BS, kWarps>(p, P, pref, upref, c, warp, lane, t0, t1, seq0);
 
     // The walk of the copies, kStages stages ahead of the computation.  Whatever stays the same within a
     // piece or a chunk of 32 table entries is worked out when they change: a stage then costs a few
@@ -526,7 +565,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const __grid_c
         scan_lengths<BS, kMergeThreads>(p, false, pref, upref, lens_s, wsum);
     __syncthreads();
     const Plan P = fp4_plan<BS>(p, pref, upref);
-    const Fp4Ranges R(P);
+    const Fp4Ranges R(P, fixed);
     const size_t slot_floats = partial_slot_floats(G, D);
     const bool by_segment = fp4_merge_by_segment(B, Hkv, p.num_ctas), shared = fp4_merge_shared(B, Hkv, p.num_ctas);
     const int64_t items = P.T == 0 ? 0 : (int64_t)G * (by_segment ? B * Hkv : P.C - 1);
@@ -544,10 +583,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const __grid_c
         }
         const int nb = P.nblocks(b);
         if (nb == 0) return false;
-        const uint32_t s0 = (uint32_t)Hkv * P.pref[b] + (uint32_t)h * nb;
-        ca = R.cta_of(s0, b, h);
+        int last;
+        R.segment_ctas(b, h, nb, ca, last);
         if (!by_segment && ca != i) return false;  // an earlier boundary of this segment names it
-        np = R.cta_of(s0 + nb - 1, b, h) - ca + 1;
+        np = last - ca + 1;
         return np > 1;
     };
     const int64_t step = shared ? gridDim.x : (int64_t)gridDim.x * kMergeWarps;
@@ -623,7 +662,7 @@ struct Fp4Variant {
     static DecodeVariant get(int group) {
         static constexpr int (*sizes[kMaxGroup])(int, bool) = {&smem<1>, &smem<2>, &smem<3>, &smem<4>,
                                                                &smem<5>, &smem<6>, &smem<7>, &smem<8>};
-        const DecodeBuild b{reinterpret_cast<const void*>(&decode_fp4_kernel<D, BS, kWarps>), kStages, 32 * kWarps, sizes[group - 1]};
+        const DecodeBuild b{reinterpret_cast<const void*>(&decode_fp4_kernel<D, BS, kWarps>), L::kStages, 32 * kWarps, sizes[group - 1]};
         return DecodeVariant{b, b, reinterpret_cast<const void*>(&merge_fp4_kernel<D, BS>), false, &launch};
     }
 };
