@@ -263,7 +263,8 @@ struct LaunchPlan {
 };
 
 pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                      int32_t block_size, int32_t max_tiles_per_head, bool fixed, pa_dtype dtype, LaunchPlan* lp) {
+                      int32_t block_size, int32_t max_tiles_per_head, int32_t partition_tiles, pa_dtype dtype, LaunchPlan* lp) {
+    const bool fixed = partition_tiles > 0;
     int dev = 0;
     if (!current_device(&dev, &lp->sms)) return PA_ERR_CUDA;
     const int G = num_q_heads / num_kv_heads;
@@ -296,6 +297,11 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
         sh->per_sm = occ < want ? occ : want;
         int64_t grid = (int64_t)lp->sms * sh->per_sm;
         if (grid > tiles_bound) grid = tiles_bound;
+        if (dtype == PA_FP4_E2M1) {  // no more CTAs than ranges can take work: its merge has some for every CTA
+            const int64_t parts = !fixed ? fp4_ranges(tiles_bound, (int)grid, 0, block_size)
+                                         : (int64_t)num_seqs * num_kv_heads * ((max_tiles_per_head + partition_tiles - 1) / partition_tiles);
+            if (grid > parts) grid = parts;
+        }
         sh->grid = (int)(grid < 1 ? 1 : grid);
         return PA_OK;
     };
@@ -449,7 +455,7 @@ extern "C" pa_status pa_decode_launch_info(int32_t num_seqs, int32_t num_q_heads
     if (max_blocks_per_seq <= 0 || partition_tokens < 0 || partition_tokens % block_size) return PA_ERR_INVALID_ARG;
     LaunchPlan lp;
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                    partition_tokens > 0, dtype, &lp);
+                    partition_tokens / block_size, dtype, &lp);
     if (s != PA_OK) return s;
     if (ctas) *ctas = lp.grid;
     if (stages) *stages = lp.stages;
@@ -468,7 +474,7 @@ extern "C" pa_status pa_decode_kernels_per_call(int32_t num_seqs, int32_t num_q_
     if (max_blocks_per_seq <= 0 || partition_tokens < 0 || partition_tokens % block_size) return PA_ERR_INVALID_ARG;
     LaunchPlan lp;
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                    partition_tokens > 0, dtype, &lp);
+                    partition_tokens / block_size, dtype, &lp);
     if (s != PA_OK) return s;
     // (over a 4-bit pool a grid of one CTA has nothing to merge and launches no second kernel)
     *kernels = lp.merge_in_kernel || (dtype == PA_FP4_E2M1 && lp.grid == 1) ? 1 : 2;
@@ -509,13 +515,18 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     const int64_t table_len = (int64_t)max_blocks_per_seq * block_size;
     const int32_t max_len = (int32_t)(max_seq_len < table_len ? max_seq_len : table_len);
     const int32_t max_tiles = (max_len + block_size - 1) / block_size;
-    const bool fixed = partition_tokens > 0;
     LaunchPlan lp;
-    s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_tiles > 0 ? max_tiles : 1, fixed,
-                    dtype, &lp);
+    s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_tiles > 0 ? max_tiles : 1,
+                    partition_tokens / block_size, dtype, &lp);
     if (s != PA_OK) return s;
-    // the bytes this launch touches: the status head, a merge counter and two partial slots per CTA of its grid
-    const WorkspaceLayout wl = workspace_layout(num_q_heads, num_kv_heads, head_dim, lp.grid);
+    // the bytes this launch touches: the status head, a merge counter and two partial slots per CTA of its grid; over
+    // a 4-bit pool no counters, but its partials keep clear of those of any grid, and a record per CTA follows them
+    WorkspaceLayout wl = workspace_layout(num_q_heads, num_kv_heads, head_dim, lp.grid);
+    if (dtype == PA_FP4_E2M1) {
+        const size_t counts_end = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)lp.sms * kMaxCtasPerSm).partials_off;
+        wl.total += counts_end - wl.partials_off + (size_t)lp.grid * 16;
+        wl.partials_off = counts_end;
+    }
     if (workspace_bytes < wl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
     if (plan && ((reinterpret_cast<uintptr_t>(plan) & 3u) || plan_bytes < (size_t)plan_words(num_seqs, lp.grid) * 4))
         return PA_ERR_INVALID_ARG;
@@ -623,7 +634,7 @@ pa_status decode_shape(int32_t max_blocks_per_seq, int32_t max_seq_len, int32_t 
     const int32_t max_tiles = (max_len + block_size - 1) / block_size;
     *max_len_out = max_len;
     return plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_tiles > 0 ? max_tiles : 1,
-                       partition_tokens > 0, dtype, lp);
+                       partition_tokens / block_size, dtype, lp);
 }
 
 }  // namespace

@@ -70,19 +70,16 @@ __device__ __forceinline__ Plan fp4_plan(const DecodeParams& p, const int32_t* p
 }
 
 // The plan's ranges in 32 bits, where the batch allows (`small`): the same arithmetic as Plan's without
-// skew.  Both kernels do it before anything is requested from HBM (or with the merge at the end of
-// everything), so it is worth keeping short.  Units are the plan's: weighted tiles, or partitions.
+// skew.  It comes before anything is requested from HBM, so it is worth keeping short.  Units are the plan's: weighted tiles, or partitions.
 struct Fp4Ranges {
     const Plan& P;
     bool fixed, small;
     uint32_t U, C, q, r;
-    float c_per_unit;
     // partitions: whether the plan has them; a constant where one is given
     __device__ __forceinline__ Fp4Ranges(const Plan& plan, bool partitions) : P(plan), fixed(partitions) {
         small = P.KS == 0 && P.U < (int64_t)1 << 31;
         U = (uint32_t)P.U, C = (uint32_t)P.C;
         q = U / max(C, 1u), r = U - q * C;
-        c_per_unit = (float)C / (float)U;
     }
     // the first unit of CTA c's range: c U / C = c (U / C) + c (U % C) / C, rounded up, with partitions down
     __device__ __forceinline__ uint32_t start(uint32_t c) const { return c * q + (c * r + (fixed ? 0 : C - 1)) / C; }
@@ -103,24 +100,6 @@ struct Fp4Ranges {
         b = lo, h = (int32_t)hh, j = (int32_t)(fixed ? rem * P.PT : rem <= A ? 0 : (rem - A + K - 1) / K);
     }
     __device__ __forceinline__ int32_t tile(int32_t b, int32_t h, int32_t j) const { return P.Hkv * P.pref[b] + h * P.nblocks(b) + j; }
-    // the CTA whose range holds unit x: the largest c with start(c) <= x
-    __device__ __forceinline__ int cta_of(uint32_t x) const {
-        int c = min((int)(C - 1), (int)((float)x * c_per_unit));  // off by one at most: C <= 2^16, and 24 bits of x
-        while (c + 1 < (int)C && start(c + 1) <= x) ++c;
-        while (c > 0 && start(c) > x) --c;
-        return c;
-    }
-    // the CTAs that hold the first and the last tile of segment (b, h) of nb > 0 tiles
-    __device__ __forceinline__ void segment_ctas(int32_t b, int32_t h, int32_t nb, int32_t& first, int32_t& last) const {
-        const uint32_t H = P.Hkv, K = Plan::K;
-        if (fixed) {
-            const uint32_t n = P.upref[b + 1] - P.upref[b], x = H * P.upref[b] + h * n;
-            first = cta_of(x), last = cta_of(x + n - 1);
-        } else {
-            const uint32_t x = K * (uint32_t)tile(b, h, 0) + (uint32_t)P.A * (H * b + h + 1);
-            first = cta_of(x), last = cta_of(x + K * (nb - 1));
-        }
-    }
 };
 
 // The first tile of part e (0 .. kWarps) of CTA c's range, and in seq a sequence at or before the one that
@@ -217,9 +196,9 @@ struct Fp4Sum {
         for (int e = 0; e < E; ++e) a[e] = 0.f;
     }
     // Adds up to 32 pieces, one to each lane in `set`, in order of the lanes: ml(lane) loads a lane's piece's (m, l)
-    // for this head, at(k) is the address of lane k's piece's elements.  The loads of four pieces go together,
-    // the first four with the (m, l).
-    template <class Ml, class At>
+    // for this head, at(k) is the address of lane k's piece's elements.  The loads of N pieces go together,
+    // the first N with the (m, l).
+    template <int N, class Ml, class At>
     __device__ __forceinline__ void add(uint32_t set, int lane, Ml ml_of, At at) {
         const bool mine = set >> lane & 1;
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -227,10 +206,10 @@ struct Fp4Sum {
         float w = 0.f;
         bool first = true;
         while (set != 0) {
-            int k[4];
-            float x[4][E];
+            int k[N];
+            float x[N][E];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < N; ++i) {
                 k[i] = __ffs(set) - 1;
                 set &= set - 1;  // stays 0
                 if (k[i] >= 0) {
@@ -253,7 +232,7 @@ struct Fp4Sum {
                 w = !mine ? 0.f : ml.x == m ? 1.f : ex2_approx(ml.x - m);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < N; ++i)
                 if (k[i] >= 0) {
                     const float wk = __shfl_sync(0xffffffffu, w, k[i]);
                     l = fmaf(wk, __shfl_sync(0xffffffffu, ml.y, k[i]), l);
@@ -268,6 +247,17 @@ struct Fp4Sum {
         for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(a[e] * r, a[e + 1] * r);
     }
 };
+
+// What a CTA leaves for the merge, behind the partials: the segment of its last run, if that begins in its range and
+// goes on in the next CTA's (kGoesOn; at most one does), and whether a segment that came from the one before ends
+// in its range (kEndsHere).
+enum Fp4RecordFlag { kGoesOn = 1, kEndsHere = 2 };
+struct alignas(16) Fp4Record {
+    int32_t b, h, flags, pad;
+};
+__device__ __forceinline__ Fp4Record* fp4_records(const DecodeParams& p, size_t slot_floats) {
+    return reinterpret_cast<Fp4Record*>(p.partials + (size_t)2 * p.num_ctas * slot_floats);
+}
 
 // The lane that holds set bit number r of `set` (r < popc(set)).
 __device__ __forceinline__ int nth_set_lane(uint32_t set, int r, int lane) {
@@ -477,6 +467,15 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     const uint32_t ending = __ballot_sync(0xffffffffu, lane < 2 * kWarps && (f.kind & 2));
     const uint32_t heads = filled & (0xaaaaaaaau | (filled & (0u - filled)));
     const int items = __popc(heads) * G;
+    if (warp == kWarps - 1) {  // (the warp least likely to have an item)
+        const int head = 31 - __clz(heads | 1u), one = __ffs(heads | 0x80000000u) - 1;  // the last run, the first
+        const uint32_t later = heads & (heads - 1);                                     // the runs after the first
+        const bool starts0 = __shfl_sync(0xffffffffu, f.kind, one) & 1;
+        const bool ends0 = ending & (later ? (later & (0u - later)) - 1 : 0xffffffffu);
+        if (lane == head)
+            fp4_records(p, slot_floats)[c] = Fp4Record{f.b, f.h, (heads != 0 && (f.kind & 1) && ending >> head == 0 ? kGoesOn : 0) |
+                                                                     (heads != 0 && !starts0 && ends0 ? kEndsHere : 0), 0};
+    }
     auto state = [&](int slot) {
         return slot & 1 ? reinterpret_cast<const float*>(smem + (slot >> 1) * L::kRing) : slot0 + (slot >> 1) * slot_floats;
     };
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
         const int starts = __shfl_sync(0xffffffffu, f.kind, head) & 1, ends = (run & ending) ? 2 : 0;
         Fp4Sum<E> sum;
         sum.reset();
-        sum.add(run, lane, [&]() { return *reinterpret_cast<const float2*>(state(lane) + G * D + 2 * hq); },
+        sum.template add<4>(run, lane, [&]() { return *reinterpret_cast<const float2*>(state(lane) + G * D + 2 * hq); },
                 [&](int k) { return state(k) + hq * D + E * lane; });
         if (starts && ends) {
             sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)fb * Hq + (size_t)fh * G + hq) * D + E * lane, p.out_scale);
@@ -503,130 +502,89 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
     }
 }
 
-// How the merge goes about its items (see merge_fp4_kernel): by segment, and a CTA to an item.  By boundary there is
-// an item for each CTA however many segments there are (256 sequences of 32 heads: 8,192 segments, 151 boundaries), by
-// segment an item for each segment however many CTAs hold it (one sequence of 8 heads: 8 against 151).
-__host__ __device__ inline bool fp4_merge_by_segment(int num_seqs, int num_kv_heads, int ctas) {
-    return (int64_t)num_seqs * num_kv_heads <= ctas;
-}
-__host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads, int ctas) {
-    return (int64_t)num_seqs * num_kv_heads * 8 <= ctas;
-}
-
-// The merge of split segments: M = max m_p, out = sum 2^(m_p - M) o_p / sum 2^(m_p - M) l_p over the
-// CTAs that hold a piece of the segment, in their order.  An item is one query head of one segment.  With
-// no more segments than CTAs the items are enumerated by segment, else by the boundary between two
-// CTAs' ranges, the first boundary inside a segment naming it.  A warp takes an item, or, when segments
-// have eight pieces or more, the four warps of a CTA share its pieces.  The kernel works out its
-// first items while the decode kernel's last CTAs still run; then one round of loads brings the states.
+// The merge of split segments: M = max m_p, out = sum 2^(m_p - M) o_p / sum 2^(m_p - M) l_p over the CTAs that hold a
+// piece, in an order of the kernel's own but always the same.  An item is one query head of the segment that a CTA's
+// record names, if it names one.  A warp takes an item, or, where segments have four pieces or more on average, the four warps
+// of a CTA share its pieces.  The decode's CTAs fill their SMs, so this kernel starts when they exit and all it does is
+// latency: the records and the first pieces are fetched together, before the records say how many there are (what slots
+// hold beyond them is dropped).
 constexpr int kMergeWarps = kMergeThreads / 32;
-template <int BS>
-__device__ __noinline__ bool fp4_named_general(const DecodeParams& p, const int32_t* pref, const int32_t* upref,
-                                               bool by_segment, int i, int* b, int* h, int* ca, int* np) {
-    const Plan P = fp4_plan<BS>(p, pref, upref);
-    if (by_segment) {
-        *b = i / P.Hkv;
-        *h = i - *b * P.Hkv;
-    } else {
-        int64_t split;
-        int seq;
-        const int64_t t = P.cta_start(i + 1, &split, &seq);
-        if (t >= P.T) return false;
-        *b = P.find_seq(P.pref, t);
-        const int64_t local = t - (int64_t)P.Hkv * P.pref[*b];
-        *h = (int)(local / P.nblocks(*b));
-        if (local == (int64_t)*h * P.nblocks(*b)) return false;  // the boundary falls between segments
-    }
-    const int nb = P.nblocks(*b);
-    if (nb == 0) return false;
-    const int64_t s0 = P.seg_start(*b, *h);
-    *ca = P.cta_of_seg(s0, *b, *h);
-    if (!by_segment && *ca != i) return false;  // an earlier boundary of this segment names it
-    *np = P.cta_of_seg(s0 + nb - 1, *b, *h) - *ca + 1;
-    return *np > 1;
+constexpr int kMergeAhead = 8;  // pieces that a warp fetches before it has the record, at most
+__host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads, int ctas) {
+    return (int64_t)num_seqs * num_kv_heads * 4 <= ctas;
 }
-template <int D, int BS>
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const __grid_constant__ DecodeParams p) {
-    extern __shared__ __align__(16) int32_t msm[];
     constexpr int E = D / 32;
     __shared__ float part[kMergeWarps][D + 2];
-    const int B = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool fixed = p.partition_tiles > 0;
-    int32_t* pref = msm;
-    int32_t* upref = pref + (B + 1);
-    int32_t* lens_s = upref + (fixed ? B + 1 : 0);
-    int32_t* wsum = lens_s + B;
-    int32_t pw[kPlanPass];
-    if (p.plan != nullptr) plan_words_load<kMergeThreads>(p, 0, pw);  // in bounds: the host checked its size
-    if (fp4_plan_matches(p, BS))
-        load_plan_arrays<kMergeThreads>(p, pw, pref, upref, lens_s);
-    else
-        scan_lengths<BS, kMergeThreads>(p, false, pref, upref, lens_s, wsum);
-    __syncthreads();
-    const Plan P = fp4_plan<BS>(p, pref, upref);
-    const Fp4Ranges R(P, fixed);
+    const int G = p.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool shared = fp4_merge_shared(p.num_seqs, p.num_kv_heads, p.num_ctas);
+    const int W = shared ? kMergeWarps : 1, first = shared ? warp : 0;  // the warp takes pieces first, first + W, ...
+    const int item = shared ? (int)blockIdx.x : (int)blockIdx.x * kMergeWarps + warp;
+    const int ca = item / G, hq = item - ca * G;
     const size_t slot_floats = partial_slot_floats(G, D);
-    const bool by_segment = fp4_merge_by_segment(B, Hkv, p.num_ctas), shared = fp4_merge_shared(B, Hkv, p.num_ctas);
-    const int64_t items = P.T == 0 ? 0 : (int64_t)G * (by_segment ? B * Hkv : P.C - 1);
-    // an item's sequence, KV head, first CTA and pieces; false if its segment is not split, or named elsewhere
-    auto named = [&](int64_t item, int& b, int& h, int& ca, int& np) -> bool {
-        const int i = (int)(item / G);
-        if (!R.small) return fp4_named_general<BS>(p, pref, upref, by_segment, i, &b, &h, &ca, &np);
-        if (by_segment) {
-            b = i / Hkv;
-            h = i - b * Hkv;
-        } else {
-            int32_t j;
-            R.locate(R.start(i + 1), b, h, j);
-            if (j == 0 || j >= P.nblocks(b)) return false;  // the boundary falls between segments
-        }
-        const int nb = P.nblocks(b);
-        if (nb == 0) return false;
-        int last;
-        R.segment_ctas(b, h, nb, ca, last);
-        if (!by_segment && ca != i) return false;  // an earlier boundary of this segment names it
-        np = last - ca + 1;
-        return np > 1;
-    };
-    const int64_t step = shared ? gridDim.x : (int64_t)gridDim.x * kMergeWarps;
-    int64_t item = shared ? blockIdx.x : (int64_t)blockIdx.x * kMergeWarps + warp;
-    int b = 0, h = 0, ca = 0, np = 0;
-    bool have = item < items && named(item, b, h, ca, np);
-    pdl_launch_dependents();  // what follows may start its own prologue; it waits for this grid before it reads or writes
-    pdl_wait_prerequisites();  // the decode grid has finished; its partials are in memory
-    while (item < items) {
-        if (have) {
-            const int hq = (int)(item % G);
-            Fp4Sum<E> sum;
-            sum.reset();
-            for (int base = 0; base < np; base += 32) {  // lane k's piece is number base + k
-                const int n = min(32, np - base);
-                uint32_t set = n == 32 ? 0xffffffffu : (1u << n) - 1;
-                if (shared) set &= 0x11111111u << warp;
-                sum.add(set, lane,
-                        [&]() { return __ldcg(reinterpret_cast<const float2*>(piece_slot(p.partials, slot_floats, ca + base + lane, ca) + G * D) + hq); },
-                        [&](int k) { return piece_slot(p.partials, slot_floats, ca + base + k, ca) + hq * D + E * lane; });
-            }
-            if (shared) {
-                __syncthreads();
+    // as many pieces as a segment has on average, and two
+    const int guess = min(p.num_ctas / (p.num_seqs * p.num_kv_heads) + 2, min(kMergeAhead * W, p.num_ctas - ca));
+    auto slot = [&](int k) { return piece_slot(p.partials, slot_floats, ca + k, ca); };
+    auto ml_of = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(slot(k) + G * D) + hq); };
+    auto at = [&](int k) { return slot(k) + hq * D + E * lane; };
+    pdl_launch_dependents();   // what follows may start its own prologue; it waits for this grid before it reads or writes
+    pdl_wait_prerequisites();  // the decode grid has finished; its records and partials are in memory
+    if (ca >= p.num_ctas) return;  // (whole warps, of the last CTA, and none where warps share)
+    const int4* records = reinterpret_cast<const int4*>(fp4_records(p, slot_floats));
+    const int4 rec = __ldcg(records + min(ca + lane, p.num_ctas - 1));  // of the CTAs from ca on
+    float2 ml[kMergeAhead];
+    float x[kMergeAhead][E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) part[warp][E * lane + e] = sum.a[e];
-                if (lane == 0) part[warp][D] = sum.m, part[warp][D + 1] = sum.l;
-                __syncthreads();
-                if (warp == 0) {
-                    sum.reset();
-                    sum.add((1u << kMergeWarps) - 1, lane, [&]() { return make_float2(part[lane][D], part[lane][D + 1]); },
-                            [&](int k) { return part[k] + E * lane; });
-                }
+    for (int i = 0; i < kMergeAhead; ++i) {
+        if (first + W * i < guess) {
+            ml[i] = ml_of(first + W * i);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(at(first + W * i) + e));
+                x[i][e] = v.x, x[i][e + 1] = v.y;
             }
-            if (!shared || warp == 0)
-                sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)h * G + hq) * D + E * lane,
-                              p.out_scale);
         }
-        item += step;
-        have = item < items && named(item, b, h, ca, np);
     }
+    if (!(__shfl_sync(0xffffffffu, rec.z, 0) & kGoesOn)) return;
+    const int b = __shfl_sync(0xffffffffu, rec.x, 0), h = __shfl_sync(0xffffffffu, rec.y, 0);
+    int np = 0;  // pieces: up to the first CTA after ca in which the segment ends
+    for (int from = ca, flags = lane ? rec.z : 0;;) {
+        const uint32_t ends = __ballot_sync(0xffffffffu, from + lane < p.num_ctas && (flags & kEndsHere));
+        np = ends ? from - ca + __ffs(ends) : p.num_ctas - ca;
+        from += 32;
+        if (ends != 0 || from >= p.num_ctas) break;
+        flags = __ldcg(&records[min(from + lane, p.num_ctas - 1)].z);
+    }
+    Fp4Sum<E> sum;
+    sum.reset();
+#pragma unroll
+    for (int i = 0; i < kMergeAhead; ++i) {
+        if (first + W * i < min(np, guess)) {
+            const float to = fmaxf(sum.m, ml[i].x);
+            const float f = to == sum.m ? 1.f : ex2_approx(sum.m - to), w = to == ml[i].x ? 1.f : ex2_approx(ml[i].x - to);
+            sum.l = fmaf(sum.l, f, w * ml[i].y);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum.a[e] = fmaf(sum.a[e], f, w * x[i][e]);
+            sum.m = to;
+        }
+    }
+    for (int base = guess; base < np; base += 32) {  // lane k's piece is number base + k
+        const uint32_t set = __ballot_sync(0xffffffffu, base + lane < np && (base + lane) % W == first);
+        sum.template add<kMergeAhead>(set, lane, [&]() { return ml_of(base + lane); }, [&](int k) { return at(base + k); });
+    }
+    if (shared) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[warp][E * lane + e] = sum.a[e];
+        if (lane == 0) part[warp][D] = sum.m, part[warp][D + 1] = sum.l;
+        __syncthreads();
+        if (warp != 0) return;
+        sum.reset();
+        sum.template add<kMergeWarps>((1u << kMergeWarps) - 1, lane, [&]() { return make_float2(part[lane][D], part[lane][D + 1]); },
+                                      [&](int k) { return part[k] + E * lane; });
+    }
+    sum.store_out(static_cast<__nv_bfloat16*>(p.out) + ((size_t)b * p.num_q_heads + (size_t)h * G + hq) * D + E * lane,
+                  p.out_scale);
 }
 
 template <int D, int BS, int kWarps>
@@ -634,8 +592,8 @@ struct Fp4Variant {
     using L = Fp4Layout<D, BS, kWarps>;
     template <int G>
     static int smem(int num_seqs, bool fixed) { return L::bytes(G, num_seqs, fixed); }
-    static void launch(const DecodeParams& p, const CUtensorMap&, const CUtensorMap&, int grid, int smem_bytes, int,
-                       int merge_smem, cudaStream_t stream) {
+    static void launch(const DecodeParams& p, const CUtensorMap&, const CUtensorMap&, int grid, int smem_bytes, int, int,
+                       cudaStream_t stream) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -649,21 +607,17 @@ struct Fp4Variant {
         if (cudaLaunchKernelEx(&cfg, decode_fp4_kernel<D, BS, kWarps>, p) != cudaSuccess) return;
         cudaLaunchConfig_t mcfg = cfg;
         if (grid == 1) return;  // one CTA: nothing is split
-        int64_t items = (int64_t)p.group * (fp4_merge_by_segment(p.num_seqs, p.num_kv_heads, grid)
-                                                ? p.num_seqs * p.num_kv_heads
-                                                : grid - 1);
-        if (!fp4_merge_shared(p.num_seqs, p.num_kv_heads, grid)) items = (items + kMergeWarps - 1) / kMergeWarps;
-        const int64_t most = (int64_t)p.wave_ctas * 2;  // (wave_ctas: the SM count)
-        mcfg.gridDim = dim3((unsigned)(items < most ? items : most));
+        const unsigned items = (unsigned)grid * (unsigned)p.group;
+        mcfg.gridDim = dim3(fp4_merge_shared(p.num_seqs, p.num_kv_heads, grid) ? items : (items + kMergeWarps - 1) / kMergeWarps);
         mcfg.blockDim = dim3(kMergeThreads);
-        mcfg.dynamicSmemBytes = merge_smem;
-        cudaLaunchKernelEx(&mcfg, merge_fp4_kernel<D, BS>, p);
+        mcfg.dynamicSmemBytes = 0;
+        cudaLaunchKernelEx(&mcfg, merge_fp4_kernel<D>, p);
     }
     static DecodeVariant get(int group) {
         static constexpr int (*sizes[kMaxGroup])(int, bool) = {&smem<1>, &smem<2>, &smem<3>, &smem<4>,
                                                                &smem<5>, &smem<6>, &smem<7>, &smem<8>};
         const DecodeBuild b{reinterpret_cast<const void*>(&decode_fp4_kernel<D, BS, kWarps>), L::kStages, 32 * kWarps, sizes[group - 1]};
-        return DecodeVariant{b, b, reinterpret_cast<const void*>(&merge_fp4_kernel<D, BS>), false, &launch};
+        return DecodeVariant{b, b, reinterpret_cast<const void*>(&merge_fp4_kernel<D>), false, &launch};
     }
 };
 

@@ -342,6 +342,32 @@ def test_decode_on_another_stream_and_captured():
         assert np.array_equal(to_numpy(out), want)
 
 
+def test_one_workspace_for_decodes_over_both_pool_types():
+    """The bf16 decode counts split pieces in its workspace and leaves the counts at zero; a 4-bit call between two of
+    them, of another grid, must not disturb that."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    c = Case(16, 8, 8, 128, 16, [700, 300, 90, 1200, 33])
+    ws = torch.zeros(pa.pa_decode_workspace_bytes(5, 8, 8, 128), dtype=torch.uint8, device="cuda")
+    pool = [to_torch(synth.normal(synth.stream_seed(17, i), c.nb * 8 * 16 * 128, "bf16").reshape(c.nb, 8, 16, 128)) for i in (1, 2)]
+    q, tab, lens = to_torch(c.q), to_torch(c.tables), to_torch(c.lens)
+
+    def bf16():
+        out = torch.full_like(q, float("nan"))
+        pa.pa_decode_attention(out, q, *pool, tab, lens, 1200, c.scale, ws)
+        return to_numpy(out)
+
+    try:
+        pa.pa_debug_set_merge_mode(1)
+        first, fp4 = bf16(), c.run(ws=ws)
+        assert np.array_equal(bf16(), first) and np.array_equal(c.run(ws=ws), fp4) and np.array_equal(bf16(), first)
+    finally:
+        pa.pa_debug_set_merge_mode(0)
+    c.check(fp4)
+    assert np.all(np.isfinite(widen(first)))
+
+
 def test_copy_and_swap_of_4_bit_blocks():
     import torch
     import paged_kv_cache_280_gb300 as pa
