@@ -123,9 +123,9 @@ pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* src_dst_pair
  * the largest grid the device can take (8 CTAs on every SM), so it suffices
  * for every call with these head shapes whatever pa_decode_set_ctas_per_sm
  * says.  A call refuses (with PA_ERR_WORKSPACE_TOO_SMALL, before launching)
- * only a workspace smaller than what its own grid touches (over 4-bit pools:
- * the counters' place for the largest grid, two partial slots per CTA and 16
- * bytes per CTA that name the segments to merge).  The caller
+ * only a workspace smaller than what its own grid touches (over 4-bit pools
+ * that is the counters' place for the largest grid, two partial slots per CTA
+ * and 16 bytes per CTA that name the segments to merge).  The caller
  * allocates it ONCE, zero-filled (the status word and the merge counters must
  * start at zero), and may reuse it across calls on one stream: the partial
  * slots are written before they are read, the status word only gathers error

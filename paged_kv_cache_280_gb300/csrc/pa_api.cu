@@ -519,14 +519,15 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     s = plan_launch(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_tiles > 0 ? max_tiles : 1,
                     partition_tokens / block_size, dtype, &lp);
     if (s != PA_OK) return s;
-    // the bytes this launch touches: the status head, a merge counter and two partial slots per CTA of its grid; over
-    // a 4-bit pool no counters, but its partials keep clear of those of any grid, and a record per CTA follows them
+    // The bytes this launch touches: the status head, a merge counter and two partial slots per CTA of its grid.  In a
+    // workspace with room for it the partials lie behind the counters of the largest grid, so that no call leaves its
+    // partials where a call of a larger grid expects its counters at zero.  Over a 4-bit pool, whose decode has no
+    // counters and ends with a record per CTA, they always do.
     WorkspaceLayout wl = workspace_layout(num_q_heads, num_kv_heads, head_dim, lp.grid);
-    if (dtype == PA_FP4_E2M1) {
-        const size_t counts_end = workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)lp.sms * kMaxCtasPerSm).partials_off;
-        wl.total += counts_end - wl.partials_off + (size_t)lp.grid * 16;
-        wl.partials_off = counts_end;
-    }
+    const size_t counts_end =
+        workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)lp.sms * kMaxCtasPerSm).partials_off;
+    const size_t clear_total = wl.total + (counts_end - wl.partials_off) + (dtype == PA_FP4_E2M1 ? (size_t)lp.grid * 16 : 0);
+    if (dtype == PA_FP4_E2M1 || workspace_bytes >= clear_total) wl.partials_off = counts_end, wl.total = clear_total;
     if (workspace_bytes < wl.total) return PA_ERR_WORKSPACE_TOO_SMALL;
     if (plan && ((reinterpret_cast<uintptr_t>(plan) & 3u) || plan_bytes < (size_t)plan_words(num_seqs, lp.grid) * 4))
         return PA_ERR_INVALID_ARG;
