@@ -14,11 +14,11 @@
 // the one before becomes the CTA's partial in the workspace, and a second kernel, launched as the
 // programmatic dependent of this one, merges those.
 //
-// Measured (both kernels, device time): 256 sequences of 32 .. 4095 tokens with 32 heads of their own 165 us, 6.0 TB/s
-// (0.89 of the measured copy rate); 4 sequences of 131072 tokens with 64 / 8 heads 100 us (0.89); 64 sequences with
-// 32 / 8 heads 22 us (0.42: 4.7 us pass before the first tile arrives, 4.5 after the last); one sequence of 1031
-// tokens 7.2 us.  With producer and consumer warps and four CTAs per SM, as over FP8 pools, the first three took
-// 299, 142 and 31 us: the hand-over cost a third of the issue slots.
+// Measured (both kernels, device time): 256 sequences of 32 .. 4095 tokens with 32 heads of their own 164.5 us, 6.0 TB/s
+// (0.89 of the measured copy rate); 4 sequences of 131072 tokens with 64 / 8 heads 100.5 us (0.89); 64 sequences with
+// 32 / 8 heads 21.3 us (0.44: 4.9 us pass before a CTA's first tile arrives, 4 from its last tile to the end of the
+// merge); one sequence of 1031 tokens 7.5 us.  With producer and consumer warps and four CTAs per SM, as over FP8
+// pools, the first three took 299, 142 and 31 us: the hand-over cost a third of the issue slots.
 #include "pa_decode.cuh"
 #include "pa_decode_fp4.cuh"
 
@@ -508,6 +508,10 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(co
 // of a CTA share its pieces.  The decode's CTAs fill their SMs, so this kernel starts when they exit and all it does is
 // latency: the records and the first pieces are fetched together, before the records say how many there are (what slots
 // hold beyond them is dropped).
+// Measured: its last store 2.3 us after the decode grid ends on 64 sequences of 32 / 8 heads.  When it worked the
+// ranges out anew from the lengths instead of reading records, the call took 21.9 us instead of 21.3; one CTA of 16
+// warps per record 22.4 us; merging in the decode kernel, with counters, 1.7 us less there but 5 us more on 256
+// sequences of 32 heads, where its registers spilled.
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeAhead = 8;  // pieces that a warp fetches before it has the record, at most
 __host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads, int ctas) {
