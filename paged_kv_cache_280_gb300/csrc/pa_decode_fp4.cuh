@@ -18,6 +18,8 @@
 //    shared-memory banks and those of V over half of them (slot_token below).
 //  - The row sums l come from one more MMA, whose A operand is all ones: they are sums of the rounded
 //    weights that P V uses, and need no reduction over lanes.
+// As built a token row costs 13.9 warp instructions at D = 128; without its copies the loop does one in 2.65 ns
+// per SM, where HBM delivers one in 3.24 ns.
 // Slots past the sequence's end may hold any bits: their scores become -inf, and their V rows get
 // scale 0 (codes are always finite), so neither reaches the output.
 #pragma once

@@ -564,3 +564,22 @@ def test_a_captured_step_whose_inputs_come_from_two_streams():
         ref, bound = kv4.decode_fp4(rq, kp, vp, 1.0, 1.0, tables, pos + 1, d ** -0.5, bs)
         assert np.all(np.abs(widen(to_numpy(out)) - ref) <= 2.0 ** -8 * (np.abs(ref) + bound) + bound)
     assert status_word(ws) == 0
+
+
+def test_two_decodes_at_once():
+    """Two streams, a workspace each: neither call's pieces reach the other's."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    cases = [Case(18, 32, 8, 128, 16, [2000, 31, 777, 4000]), Case(19, 8, 8, 64, 32, [3000, 1, 500])]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.zeros_like(c.dev[0]) for _ in range(8)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for c, s, o in zip(cases, streams, outs):
+            q, kp, vp, tab, lens = c.dev
+            pa.pa_decode_attention_fp4(o[i], q, kp, vp, *c.scales, tab, lens, int(c.lens.max()), c.scale, c.ws, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(np.array_equal(to_numpy(x), w) for x in o)
