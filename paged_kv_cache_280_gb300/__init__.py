@@ -146,15 +146,19 @@ def _torch():
     return _torch_module
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return PA_F32
-    if t.dtype == torch.bfloat16:
-        return PA_BF16
-    if t.dtype == torch.uint8 or t.dtype == getattr(torch, "float8_e4m3fn", None):
-        return PA_FP8_E4M3
-    raise PAError(2, f"dtype {t.dtype}")
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3})
+        if hasattr(torch, "float8_e4m3fn"):
+            _dtype_codes[torch.float8_e4m3fn] = PA_FP8_E4M3
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise PAError(2, f"dtype {t.dtype}")
+    return code
 
 
 def _dev_ptr(t, name: str) -> int:
@@ -248,8 +252,8 @@ def _status_ptr(t, dev: int):
 def _device() -> int:
     """The current device, on which the library launches; -2, no tensor's, where there is none."""
     try:
-        return _torch().cuda.current_device()
-    except (RuntimeError, AssertionError):
+        return _torch()._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
         return -2
 
 
@@ -467,10 +471,10 @@ def pa_decode_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tabl
 def _token_rows(t, name: str) -> int:
     """Elements from one token to the next of a [N][H][D] tensor whose heads are contiguous within a token."""
     n, h, d = t.shape
-    stride = t.stride()
-    if (d > 1 and stride[2] != 1) or (h > 1 and stride[1] != d):
+    rows, heads, elems = t.stride()
+    if (elems != 1 and d > 1) or (heads != d and h > 1):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] with contiguous heads")
-    return stride[0] if n > 1 else h * d
+    return rows if n > 1 else h * d
 
 
 def _rows_ptr(t, dtype, shape, dev: int, name: str) -> int:
