@@ -27,7 +27,7 @@ namespace {
 
 // Two stages of 32 tokens a warp (2 x 4.6 KB at D = 128, 147 KB per SM): what one warp lacks in depth the
 // other fifteen have.  Measured on the first two batches above (us), warps x stages: 16 x 2 186 / 114, 14 x 2
-// 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.
+// 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.  At D = 64 four stages gain nothing.
 constexpr int kStageTok = 32;
 constexpr size_t partial_slot_bytes_max(int d) { return (size_t)(kMaxGroup * (d + kSlotExtraFloatsPerHead) + 3) / 4 * 16; }
 
