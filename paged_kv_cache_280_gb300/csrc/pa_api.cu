@@ -281,7 +281,7 @@ pa_status plan_launch(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_head
     // Default CTAs per SM: the bf16 tensor-core path, which spends little time per tile,
     // keeps four (about 128 KB of tiles in flight, enough to cover HBM latency with fewer
     // split points); the CUDA-core path and the FP8 tensor-core path (which widens every
-    // stage first) take as many as fit, as do the large CTAs over 4-bit pools (one or two).
+    // stage first) take as many as fit, as do the large CTAs over 4-bit pools (one).
     int want = g_ctas_per_sm.load();
     if (want <= 0) want = lp->mma && dtype == PA_BF16 ? kDefaultCtasPerSmMma : kMaxCtasPerSm;
     const int64_t tiles_bound = (int64_t)num_seqs * num_kv_heads * max_tiles_per_head;

@@ -73,7 +73,7 @@ __device__ __forceinline__ Plan fp4_plan(const DecodeParams& p, const int32_t* p
 // skew.  It comes before anything is requested from HBM, so it is worth keeping short.  Units are the plan's: weighted tiles, or partitions.
 struct Fp4Ranges {
     const Plan& P;
-    bool fixed, small;
+    bool fixed, small;  // (partitions are counted in 32 bits anyhow)
     uint32_t U, C, q, r;
     // partitions: whether the plan has them; a constant where one is given
     __device__ __forceinline__ Fp4Ranges(const Plan& plan, bool partitions) : P(plan), fixed(partitions) {
@@ -113,17 +113,10 @@ __device__ __noinline__ int32_t fp4_part_start_general(const DecodeParams& p, co
         const Fp4Ranges R(P, true);
         c += e == kWarps;
         if (c == P.C) return (int32_t)P.T;
-        int s0 = 0;
-        if (R.small) {
-            int32_t h, j;
-            R.locate(R.start(c), s0, h, j);
-            *seq = s0;
-            return R.tile(s0, h, j);
-        }
-        int64_t split;
-        const int64_t t = P.cta_start(c, &split, &s0);
-        *seq = s0;
-        return (int32_t)t;
+        int32_t b, h, j;
+        R.locate(R.start(c), b, h, j);
+        *seq = b;
+        return R.tile(b, h, j);
     }
     int s0 = 0;
     int64_t split;
@@ -266,7 +259,7 @@ __device__ __forceinline__ int nth_set_lane(uint32_t set, int r, int lane) {
 }
 
 template <int D, int BS, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 1) decode_fp4_kernel(const __grid_constant__ DecodeParams p) {
     using L = Fp4Layout<D, BS, kWarps>;
     constexpr int TPS = L::TPS, NT = 32 * kWarps, kStages = L::kStages;
     extern __shared__ __align__(16) uint8_t smem[];

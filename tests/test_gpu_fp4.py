@@ -253,6 +253,34 @@ def test_decode_many_sequences(part):
     assert status_word(c.ws) == 0
 
 
+def test_decode_of_ranges_past_32_bits():
+    """One sequence whose tiles, weighted as the ranges weigh them, number more than 2^31.  Its table repeats a few
+    blocks; three tiles, the first and the last among them, hold keys whose scores are 200 above all others, so the
+    output is the mean of their values (the other weights together are below 2^33 e^-200)."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    hkv, d, bs, n = 64, 64, 16, 8_400_004
+    assert 4 * n * hkv > 1 << 31
+    kp, vp = np.zeros((7, hkv, bs * 36), np.uint8), _random_pool(22, 7, hkv, bs, d)
+    codes, scales = bs * d // 2, slice(bs * d // 2, None)
+    kp[4:, :, :codes], kp[4:, :, scales] = 0x22, 0x38  # code 1 of scale 1: with q = 1 a score of 64 before its scale
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[None] % 4
+    where = [0, n // 2 + 1, n - 1]
+    table[0, where] = torch.tensor([4, 5, 6], dtype=torch.int32, device="cuda")
+    q = torch.ones(1, hkv, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    ws = torch.zeros(pa.pa_decode_workspace_bytes(1, hkv, hkv, d), dtype=torch.uint8, device="cuda")
+    lens = torch.tensor([n * bs], dtype=torch.int32, device="cuda")
+    pa.pa_decode_attention_fp4(out, q, to_torch(kp), to_torch(vp), 1.0, 0.5, table, lens, n * bs, 200.0 / 64.0, ws)
+    v = kv4.values(vp[4:], d, bs).astype(np.float64) * 0.5  # [3][hkv][bs][d]
+    want = v.transpose(1, 0, 2, 3).reshape(hkv, 3 * bs, d).mean(1)
+    # weights equal up to the rounding of 2^x (2^-11 in f16 each), 48 sums in fp32, the output's rounding
+    size = np.abs(v).transpose(1, 0, 2, 3).reshape(hkv, 3 * bs, d).mean(1)
+    assert np.all(np.abs(widen(to_numpy(out))[0] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size)
+    assert status_word(ws) == 0
+
+
 def test_decode_one_long_sequence():
     c = Case(5, 8, 1, 128, 16, [20000])
     c.check(c.run())
