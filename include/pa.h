@@ -402,8 +402,8 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
 
 /*
  * 4-bit KV pools (an extrapolation like the FP8 pools: the pages list
- * quantised KV formats only by name).  A quarter of the bytes of bf16, with a
- * scale for every 16 elements.
+ * quantised KV formats only by name).  9 bytes for 16 elements, against 32 in
+ * bf16.
  *
  * Format (PA_FP4_E2M1).  An element is an E2M1 code (sign, 0, 0.5, 1, 1.5, 2,
  * 3, 4 or 6); 16 consecutive elements of a row share one E4M3 scale; a pool

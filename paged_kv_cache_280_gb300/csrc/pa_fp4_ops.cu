@@ -49,11 +49,14 @@ __global__ void __launch_bounds__(256, kAppendCtas) reshape_and_cache_fp4_kernel
 #pragma unroll
     for (int i = 0; i < kAppendAhead; ++i) fetch(base + i * stride, i);
     const Divisor d = is_v ? vd : kd;
+    auto slot_of = [&](uint32_t idx) -> int64_t { return idx < total ? slots[heads.div(idx / U)] : -1; };
+    int64_t next = slot_of(base + lane);  // of the turn to come: fetched a turn ahead
     int turn = 0;
     for (; base < total; base += stride) {
         const uint32_t idx = base + lane, u = idx & (U - 1), row = idx / U;
-        const uint32_t tok = heads.div(row), h = row - tok * heads.d;
-        const int64_t slot = idx < total ? slots[tok] : -1;
+        const uint32_t h = row - heads.div(row) * heads.d;
+        const int64_t slot = next;
+        next = slot_of(idx + stride);
         copies_wait<kAppendAhead - 1>();
         __syncwarp();  // the other lanes' copies too
         float x[16];
