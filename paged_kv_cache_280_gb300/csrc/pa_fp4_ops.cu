@@ -14,10 +14,10 @@ namespace {
 // (blockIdx.y = 0) or of V per turn; a warp's 32 groups are consecutive in the input, and the warp has
 // copied those of its next turns ahead into shared memory: the arithmetic (about 200 instructions a group) costs
 // nearly as much as HBM takes, so neither may wait for the other.
-// Measured, 16383 tokens of 8 heads of 128 in bf16 (86 MB): 18.2 us, 4.7 TB/s.  Steps on the way there: rows loaded
-// when their turn comes 22 us, copied two turns ahead 19.5; four tokens of a head to a warp, which makes whole lines
-// of codes, 27.  Twice the tokens take 33.1 us, fp32 input of 8192 tokens 13.9 us (5.5 TB/s): 3 us of each are
-// a launch's ramp and end.  256 tokens of 32 heads take 2.8 us, all ramp.
+// Measured, 16383 tokens of 8 heads of 128 in bf16 (86 MB): 17.4 us, 4.9 TB/s.  Steps on the way there: rows loaded
+// when their turn comes 22 us, copied two turns ahead 19.5, slots fetched a turn ahead 18.2 -> 17.4; four tokens of a
+// head to a warp, which makes whole lines of codes, 27.  Twice the tokens take 32.1 us, fp32 input of 8192 tokens
+// 13.9 us (5.5 TB/s): 3 us of each are a launch's ramp and end.  256 tokens of 32 heads take 2.8 us, all ramp.
 constexpr int kAppendAhead = 2;
 constexpr int kAppendCtas = 4;  // per SM; with 5 (48 registers) 18.8 us against 18.8, and 256 tokens 3.1 against 2.8; with 6, 21.4
 template <typename T, int D>

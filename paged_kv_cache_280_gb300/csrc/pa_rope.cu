@@ -25,10 +25,11 @@ namespace {
 
 enum RopePool { kPoolSame = 0, kPoolFp8 = 1, kPoolFp4 = 2 };
 
-// Measured: 8191 tokens of 64 + 16 heads of 128, bf16 to bf16 (340 MB): 54.6 us, 6.2 TB/s (0.92 of the measured copy
-// rate); with the loads of a unit issued when its turn comes 70 us.  4096 fp32 tokens of 32 + 16 heads 34.4 us
-// (0.88).  4099 tokens of 32 + 16 heads to 4-bit pools 21.3 us (0.63: two groups' codes cost more than HBM takes).
-// One token: 2.0 us, a launch and one trip to memory.
+// Measured: 8191 tokens of 64 + 16 heads of 128, bf16 to bf16 (340 MB): 50.9 us, 6.7 TB/s (0.99 of the measured copy
+// rate); with the loads of a unit issued when its turn comes 70 us, with only its slot and position fetched then
+// 54.6.  4096 fp32 tokens of 32 + 16 heads 34.0 us (0.88).  4099 tokens of 32 + 16 heads to 4-bit pools 21.3 us (0.63: two
+// groups' codes cost more than HBM takes).  One token: 1.9 us, a launch and one trip to memory.
+// CTAs per SM: 4 (64 registers; with 5 it spills and is slower), 3 for the 4-bit pools (80; with 4 21.8 us).
 constexpr int kRopeAhead = 2;  // turns that a thread copies ahead
 
 struct RopeParams {
@@ -64,7 +65,7 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* x, const Divisor& d) {
 }
 
 template <typename T, int POOL, int D>
-__global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, POOL == kPoolFp4 ? 3 : 4) rope_and_cache_kernel(const RopeParams p) {
     // A decode that follows may start its prologue, which reads nothing written here, but only once what came
     // before this kernel is complete: that may have written the lengths and tables it reads.
     pdl_wait_prerequisites();
@@ -107,6 +108,14 @@ __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams
 #pragma unroll
     for (int i = 0; i < kRopeAhead; ++i) fetch(first + i * stride, i);
     int turn = 0;
+    // the slot and position of the turn to come, fetched a turn ahead
+    int64_t next_slot = -1;
+    int next_pos = 0;
+    auto fetch_place = [&](uint32_t idx) {
+        const uint32_t tok = p.heads.div((idx < total ? idx : 0u) / U);
+        next_slot = p.slots[tok], next_pos = p.positions[tok];  // (the position of a padding token: not looked at)
+    };
+    fetch_place(first);
     // every thread of a warp takes the same number of turns: 4-bit groups meet in shuffles
     for (uint32_t base = first & ~31u; base < total; base += stride) {
         const uint32_t idx = base + (threadIdx.x & 31u);
@@ -115,8 +124,9 @@ __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams
         int h;
         row_of(in_range ? idx : 0u, tok, h);
         const bool is_q = h < p.num_q_heads, is_v = h >= first_v;
-        const int64_t slot = p.slots[tok];
-        const int pos = p.positions[tok];  // (of a padding token: not looked at)
+        const int64_t slot = next_slot;
+        const int pos = next_pos;
+        fetch_place(idx + stride);
         bool ok = in_range && slot >= 0;
         if (ok) {
             const bool bad_slot = slot >= p.pool_slots, bad_pos = pos < 0 || pos >= p.max_position;
