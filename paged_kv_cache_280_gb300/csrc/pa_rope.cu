@@ -29,7 +29,7 @@ enum RopePool { kPoolSame = 0, kPoolFp8 = 1, kPoolFp4 = 2 };
 // rate); with the loads of a unit issued when its turn comes 70 us, with only its slot and position fetched then
 // 54.6.  4096 fp32 tokens of 32 + 16 heads 34.0 us (0.88).  4099 tokens of 32 + 16 heads to 4-bit pools 21.3 us (0.63: two
 // groups' codes cost more than HBM takes).  One token: 1.9 us, a launch and one trip to memory.
-// CTAs per SM: 4 (64 registers; with 5 it spills and is slower), 3 for the 4-bit pools (80; with 4 21.8 us).
+// CTAs per SM: 4 (64 registers); with 5 it spills and is slower, with 3 the 4-bit case takes 23.8 us.
 constexpr int kRopeAhead = 2;  // turns that a thread copies ahead
 
 struct RopeParams {
@@ -65,7 +65,7 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* x, const Divisor& d) {
 }
 
 template <typename T, int POOL, int D>
-__global__ void __launch_bounds__(256, POOL == kPoolFp4 ? 3 : 4) rope_and_cache_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams p) {
     // A decode that follows may start its prologue, which reads nothing written here, but only once what came
     // before this kernel is complete: that may have written the lengths and tables it reads.
     pdl_wait_prerequisites();
@@ -108,14 +108,13 @@ __global__ void __launch_bounds__(256, POOL == kPoolFp4 ? 3 : 4) rope_and_cache_
 #pragma unroll
     for (int i = 0; i < kRopeAhead; ++i) fetch(first + i * stride, i);
     int turn = 0;
-    // the slot and position of the turn to come, fetched a turn ahead
-    int64_t next_slot = -1;
-    int next_pos = 0;
-    auto fetch_place = [&](uint32_t idx) {
-        const uint32_t tok = p.heads.div((idx < total ? idx : 0u) / U);
-        next_slot = p.slots[tok], next_pos = p.positions[tok];  // (the position of a padding token: not looked at)
-    };
-    fetch_place(first);
+    // The slot and position of the turn to come, fetched a turn ahead, but not for the 4-bit pools, whose arithmetic
+    // wants the registers (21.8 us with it on the case above).
+    constexpr bool kPlaceAhead = POOL != kPoolFp4;
+    int64_t slot_ahead = -1;
+    int pos_ahead = 0;
+    auto fetch_place = [&](uint32_t tok) { slot_ahead = p.slots[tok], pos_ahead = p.positions[tok]; };
+    if constexpr (kPlaceAhead) fetch_place(p.heads.div((first < total ? first : 0u) / U));
     // every thread of a warp takes the same number of turns: 4-bit groups meet in shuffles
     for (uint32_t base = first & ~31u; base < total; base += stride) {
         const uint32_t idx = base + (threadIdx.x & 31u);
@@ -124,9 +123,10 @@ __global__ void __launch_bounds__(256, POOL == kPoolFp4 ? 3 : 4) rope_and_cache_
         int h;
         row_of(in_range ? idx : 0u, tok, h);
         const bool is_q = h < p.num_q_heads, is_v = h >= first_v;
-        const int64_t slot = next_slot;
-        const int pos = next_pos;
-        fetch_place(idx + stride);
+        if constexpr (!kPlaceAhead) fetch_place(tok);
+        const int64_t slot = slot_ahead;
+        const int pos = pos_ahead;  // (of a padding token: not looked at)
+        if constexpr (kPlaceAhead) fetch_place(p.heads.div((idx + stride < total ? idx + stride : 0u) / U));
         bool ok = in_range && slot >= 0;
         if (ok) {
             const bool bad_slot = slot >= p.pool_slots, bad_pos = pos < 0 || pos >= p.max_position;
