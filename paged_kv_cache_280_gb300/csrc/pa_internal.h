@@ -15,10 +15,11 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 constexpr int kMaxCtasPerSm = 8;
 constexpr int kDefaultCtasPerSmMma = 4;  // default CTAs per SM on the bf16 tensor-core path
-// Decode workspace: the status head, one merge counter per CTA, then two
-// partial slots per CTA of the launch's grid (pa_decode_workspace_bytes sizes
-// it for kMaxCtasPerSm CTAs on every SM, the largest grid); a slot is [G][D]
-// floats of o plus [G][2] floats of (m, l).
+// Decode workspace: the status head, one merge counter per CTA, then, behind the
+// counters of the largest grid where there is room, two partial slots per CTA of
+// the launch's grid (pa_decode_workspace_bytes sizes it for kMaxCtasPerSm CTAs on
+// every SM, the largest grid), and over 4-bit pools a 16-byte record per CTA; a
+// slot is [G][D] floats of o plus [G][2] floats of (m, l).
 constexpr int kSlotExtraFloatsPerHead = 2;
 // floats of one partial slot, a multiple of 4 so that every slot is 16-byte aligned
 inline __host__ __device__ size_t partial_slot_floats(int G, int D) {
