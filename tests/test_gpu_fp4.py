@@ -611,3 +611,24 @@ def test_two_decodes_at_once():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert all(np.array_equal(to_numpy(x), w) for x in o)
+
+
+def test_two_graphs_of_one_workspace():
+    """Calls of different grids captured with the same workspace and replayed in turn on one stream."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    cases = [Case(23, 8, 8, 128, 16, [40]), Case(24, 8, 8, 128, 32, [1500, 0, 700, 33])]
+    want = [c.run() for c in cases]
+    ws = torch.zeros(pa.pa_decode_workspace_bytes(4, 8, 8, 128), dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.zeros_like(c.dev[0]) for c in cases], []
+    for c, o in zip(cases, outs):
+        q, kp, vp, tab, lens = c.dev
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pa.pa_decode_attention_fp4(o, q, kp, vp, *c.scales, tab, lens, int(c.lens.max()), c.scale, ws)
+    for i in (0, 1, 0, 1, 1, 0):
+        outs[i].fill_(7.0)
+        graphs[i].replay()
+        assert np.array_equal(to_numpy(outs[i]), want[i])
+    assert status_word(ws) == 0
