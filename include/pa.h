@@ -440,7 +440,8 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
  * modes, plan and error reporting; plans are built with dtype PA_FP4_E2M1).
  * code * scale is exact in f16, in which the MMAs run with fp32 sums; a query
  * row is first scaled by a power of two so that its largest element lies in
- * [1, 2), so any bf16 magnitudes are in range.  The call is two kernels, the
+ * [1, 2), so any bf16 magnitudes are in range, and so are scores of any size
+ * that fp32 holds (scale * k_scale * q . K[t], in base 2).  The call is two kernels, the
  * second, which merges split segments, a programmatic dependent (with one
  * CTA there is nothing to merge and one kernel); pa_debug_set_merge_mode does not
  * change that.  num_kv_heads <= 32767; num_seqs is bounded by the lengths' room

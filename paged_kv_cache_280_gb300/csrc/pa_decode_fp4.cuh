@@ -66,8 +66,8 @@ struct Fp4State {
     static constexpr int VW = D / 64;       // words of a lane's part of a V row (D / 8 dims)
     static constexpr int kScalesOff = BS * (D / 2);  // the tile's scale bytes
     uint32_t qb[MT][2];  // B fragments of q^T per k-step, rows scaled by a power of two
-    float sc[2];         // score scale (base 2) of heads 2c and 2c + 1, the power of two undone
-    float m[2];          // reference of the weights of heads 2c, 2c + 1 (base 2), the same in every g
+    float sc[2];         // score scale (base 2, > 0) of heads 2c and 2c + 1, the power of two undone
+    float m[2];          // reference of heads 2c, 2c + 1: a score before its scale, the same in every g
     float l[4];          // running sums: [0], [1] of heads 2c, 2c + 1 (the same in every g; [2], [3] repeat them)
     float o[MT][4];
 
@@ -85,7 +85,8 @@ struct Fp4State {
 
     // f16 holds a bf16 value exactly while it is neither above 65504 nor far below 2^-14, so each row is
     // scaled by the power of two that brings its largest element to [1, 2): a smaller element loses
-    // less than 2^-25 of that one, and any bf16 magnitudes are in range.
+    // less than 2^-25 of that one, and any bf16 magnitudes are in range.  A negative score scale turns the
+    // rows' signs, so that sc is positive; it is kept so (and finite) where it would round to 0.
     // rows: q[b][h * G] in global memory.
     __device__ __forceinline__ void load_q(const __nv_bfloat16* rows, int G, int lane, float scale_log2) {
         const int g = lane >> 2, c = lane & 3;
@@ -105,14 +106,16 @@ struct Fp4State {
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
         const int e = min(max((int)(__float_as_uint(a) >> 23), 1), 253);
-        const float f = __uint_as_float((uint32_t)(254 - e) << 23), inv = __uint_as_float((uint32_t)e << 23);
+        const float f = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), scale_log2);
+        const float inv = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             qb[j][0] = pack_f16x2(x[4 * j] * f, x[4 * j + 1] * f);
             qb[j][1] = pack_f16x2(x[4 * j + 2] * f, x[4 * j + 3] * f);
         }
-        sc[0] = scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c);
-        sc[1] = scale_log2 * __shfl_sync(0xffffffffu, inv, 8 * c + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            sc[i] = fminf(fmaxf(fabsf(scale_log2) * __shfl_sync(0xffffffffu, inv, 8 * c + 4 * i), 0x1p-126f), 0x1.fffffep127f);
     }
 
     // S^T of the 16 tokens from row row0 of the tile at kbase: (slot g, head 2c), (g, 2c + 1),
@@ -184,7 +187,9 @@ struct Fp4State {
     // (1 .. 32) of them exist.  Tile t's K is at kb + t * tile bytes, its V at vb + t * tile bytes.
     static constexpr int kTile = BS * fp4_row_bytes(D), kStep1 = BS == 16 ? kTile : 0, kRow1 = BS == 16 ? 0 : 16;
 
-    // The weights of the stage's tokens as P^T B fragments (step 0: pb[0], pb[1]; step 1: pb[2], pb[3]).
+    // The weights of the stage's tokens as P^T B fragments (step 0: pb[0], pb[1]; step 1: pb[2], pb[3]):
+    // 2^((x - m) sc) of the scores x.  The difference comes before the scale, so the reference's own exponent is 0
+    // however large the scores are (x sc - m sc, the second rounded, is off by half a unit of m sc: 64 at 2^30).
     // m is a reference, not the exact maximum: it moves (and O and l are rescaled) only when a score
     // passes it by more than kRaise, so that most stages need no reduction over lanes.  The weights
     // then stay at most 2^kRaise, within f16, and the final ratio does not depend on the reference.
@@ -200,9 +205,11 @@ struct Fp4State {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[s][i] = fmaf(x[s][i], sc[i & 1], -m[i & 1]);
-                    if (MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid) y[s][i] = -INFINITY;
+                for (int i = 0; i < 4; i += 2) {  // a token's two heads
+                    const float2 d = add_f32x2(make_float2(x[s][i], x[s][i + 1]), make_float2(-m[0], -m[1]));
+                    const float2 e = mul_f32x2(d, make_float2(sc[0], sc[1]));
+                    const bool past = MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid;
+                    y[s][i] = past ? -INFINITY : e.x, y[s][i + 1] = past ? -INFINITY : e.y;
                 }
         };
         exponents();  // +inf while m = -inf: no score has been seen
@@ -216,13 +223,14 @@ struct Fp4State {
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        if (!MASK || slot_token(g) + 8 * r + 16 * s < valid) n[i] = fmaxf(n[i], x[s][2 * r + i] * sc[i]);
+                        if (!MASK || slot_token(g) + 8 * r + 16 * s < valid) n[i] = fmaxf(n[i], x[s][2 * r + i]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) n[i] = fmaxf(n[i], __shfl_xor_sync(0xffffffffu, n[i], off));
                 n[i] = fmaxf(n[i], m[i]);
             }
             // a head whose scores are all -inf so far keeps its state (nothing is weighed yet)
-            const float a0 = n[0] == m[0] ? 1.f : ex2_approx(m[0] - n[0]), a1 = n[1] == m[1] ? 1.f : ex2_approx(m[1] - n[1]);
+            const float a0 = n[0] == m[0] ? 1.f : ex2_approx((m[0] - n[0]) * sc[0]);
+            const float a1 = n[1] == m[1] ? 1.f : ex2_approx((m[1] - n[1]) * sc[1]);
             l[0] *= a0, l[1] *= a1, l[2] *= a0, l[3] *= a1;
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[i][0] *= a0, o[i][1] *= a1, o[i][2] *= a0, o[i][3] *= a1;
@@ -261,7 +269,7 @@ struct Fp4State {
         }
     }
 
-    // Unnormalised partial: slot = [G][D] o, then [G] (m, l).
+    // Unnormalised partial: slot = [G][D] o, then [G] (m, l), m in base 2.
     __device__ __forceinline__ void store_partial(float* slot, int G, int lane) const {
         const int g = lane >> 2, h0 = 2 * (lane & 3);
 #pragma unroll
@@ -272,7 +280,7 @@ struct Fp4State {
                 for (int i = 0; i < MT; i += 2)
                     *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[i][j], o[i][2 + j], o[i + 1][j], o[i + 1][2 + j]);
                 if (g == 0) {
-                    slot[G * D + 2 * (h0 + j)] = m[j];
+                    slot[G * D + 2 * (h0 + j)] = m[j] * sc[j];
                     slot[G * D + 2 * (h0 + j) + 1] = l[j];
                 }
             }
