@@ -235,9 +235,9 @@ struct Fp4Sum {
         }
     }
     __device__ __forceinline__ void store_out(__nv_bfloat16* dst, float oscale) const {
-        const float r = oscale / l;
+        const float r = 1.f / l;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(a[e] * r, a[e + 1] * r);
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(a[e] * r * oscale, a[e + 1] * r * oscale);
     }
 };
 

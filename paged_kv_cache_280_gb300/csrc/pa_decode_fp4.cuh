@@ -252,19 +252,21 @@ struct Fp4State {
     }
 
     // Normalised output rows (o_rows = out[b][h * G]): a lane holds D / 8 consecutive dims of its two heads.
+    // The pool scale comes last: divided by l, which may be 2^40, a small one would leave the normal range.
     __device__ __forceinline__ void store_out(__nv_bfloat16* o_rows, int G, int lane, float oscale) const {
         const int g = lane >> 2, h0 = 2 * (lane & 3);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (h0 + j < G) {
-                const float r = oscale / l[j];
+                const float r = 1.f / l[j];
                 __nv_bfloat16* dst = o_rows + (h0 + j) * D + g * (D / 8);
 #pragma unroll
                 for (int i = 0; i < MT; i += 4)
                     *reinterpret_cast<uint4*>(dst + 2 * i) =
-                        make_uint4(pack_bf16x2(o[i][j] * r, o[i][2 + j] * r), pack_bf16x2(o[i + 1][j] * r, o[i + 1][2 + j] * r),
-                                   pack_bf16x2(o[i + 2][j] * r, o[i + 2][2 + j] * r),
-                                   pack_bf16x2(o[i + 3][j] * r, o[i + 3][2 + j] * r));
+                        make_uint4(pack_bf16x2(o[i][j] * r * oscale, o[i][2 + j] * r * oscale),
+                                   pack_bf16x2(o[i + 1][j] * r * oscale, o[i + 1][2 + j] * r * oscale),
+                                   pack_bf16x2(o[i + 2][j] * r * oscale, o[i + 2][2 + j] * r * oscale),
+                                   pack_bf16x2(o[i + 3][j] * r * oscale, o[i + 3][2 + j] * r * oscale));
             }
         }
     }

@@ -83,3 +83,21 @@ def test_scores_of_any_size(size, d, bs, hkv, part):
             loose = 2 * 600 * 2.0 ** -23 * mag
         err = np.abs(got - ref)
         assert np.all(err <= 2.0 ** -8 * (np.abs(ref) + loose) + loose), (np.isnan(got).sum(), np.nanmax(err))
+
+
+@pytest.mark.parametrize("part", [0, 256])
+def test_the_pool_scale_of_the_values_is_of_any_size(part):
+    """A power of two in the values' pool scale comes out in the outputs, down to where a bf16 output is still normal."""
+    rng = np.random.default_rng(3)
+    d, bs, hkv, lens = 128, 16, 2, np.array([40000, 3, 0, 900], np.int32)
+    kp, vp = (rng.integers(0, 256, (50, hkv, bs * 72)).astype(np.uint8) for _ in range(2))
+    for p in (kp, vp):
+        p[..., bs * 64:] = rng.integers(0x28, 0x39, p[..., bs * 64:].shape)
+    vp[..., : bs * 64] &= 0x77                 # positive values,
+    vp[..., : bs * 64] |= 0x22                 # of at least 1
+    vp[..., bs * 64:] += 0x30                  # times 16 and more
+    tables = rng.integers(0, 50, (4, 2500)).astype(np.int32)
+    q = kv4.to_bf16(rng.standard_normal((4, 8, d)).astype(np.float32))
+    args = [to_torch(x) for x in (q, kp, vp, tables, lens)]
+    one, small = (_decode(*args, 0.09, vs=s, part=part) for s in (1.0, 2.0 ** -125))
+    assert one[lens > 0].min() > 1.0 and np.array_equal(small, one * 2.0 ** -125)
