@@ -438,7 +438,9 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
  * and its planned form over 4-bit pools with bf16 q and out, as
  * pa_decode_attention_fp8 does for FP8 pools (same layouts, workspace, split
  * modes, plan and error reporting; plans are built with dtype PA_FP4_E2M1).
- * code * scale is exact in f16, in which the MMAs run with fp32 sums; a query
+ * code * scale is exact in f16, in which the MMAs run with fp32 sums.  The
+ * softmax weights are f16 too: each is off by at most 2^-11 of itself or, below
+ * 2^-25 of the largest, 2^-36 of that one (they are summed as rounded).  A query
  * row is first scaled by a power of two so that its largest element lies in
  * [1, 2), so any bf16 magnitudes are in range, and so are scores of any size
  * that fp32 holds (scale * k_scale * q . K[t], in base 2).  The call is two kernels, the

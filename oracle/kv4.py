@@ -88,7 +88,7 @@ def values(pool: np.ndarray, d: int, bs: int) -> np.ndarray:
 def decode_fp4(q, k_pool, v_pool, k_scale, v_scale, tables, lens, scale, bs, seqs=None):
     """float64 decode attention [B][Hq][D], and a bound on a kernel's error beside its output rounding.
 
-    The bound is for weights rounded to f16 (relative 2^-11; 2^-25 of the largest below f16's normal range),
+    The bound is for weights rounded to f16 (relative 2^-11; 2^-36 of the largest below 2^-25 of it),
     fp32 dot products of D terms in any order (each term and partial sum off by 2^-22 of the terms'
     magnitudes: twice a rounding, for sums that a tensor core truncates), and 2^-18 for the exponentials
     and the merges' weights and sums.  With every weight off by a factor of at most 1 + e, the ratio of two
@@ -114,8 +114,8 @@ def decode_fp4(q, k_pool, v_pool, k_scale, v_scale, tables, lens, scale, bs, seq
             size = (np.abs(kh) @ np.abs(qf[b, h]) * abs(scale)).max()
             e = 2.0 ** -11 + d * 2.0 ** -22 * size + 2.0 ** -18
             out[b, h] = p @ vh
-            # weights below f16's normal range: an absolute 2^-25 of the largest weight each
-            tiny = 2.0 ** -25 * p.max() * np.abs(vh).sum(0)
+            # weights below 2^-25 of the largest one, which is held as 2^11 at least: an absolute 2^-36 of it each
+            tiny = 2.0 ** -36 * p.max() * np.abs(vh).sum(0)
             bound[b, h] = 2.1 * e * (p @ np.abs(vh)) + 2 * tiny
     return out, bound
 

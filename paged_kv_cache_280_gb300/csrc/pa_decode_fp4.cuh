@@ -18,6 +18,8 @@
 //    shared-memory banks and those of V over half of them (slot_token below).
 //  - The row sums l come from one more MMA, whose A operand is all ones: they are sums of the rounded
 //    weights that P V uses, and need no reduction over lanes.
+//  - The sums are fp32, and a tensor core cuts each product at about 2^-23 of the sum that it joins: n tokens of one
+//    warp's piece are off by at most n 2^-23 of their sum, and O and l alike.
 // As built a token row costs 13.9 warp instructions at D = 128; without its copies the loop does one in 2.65 ns
 // per SM, where HBM delivers one in 3.24 ns.
 // Slots past the sequence's end may hold any bits: their scores become -inf, and their V rows get
@@ -188,13 +190,16 @@ struct Fp4State {
     static constexpr int kTile = BS * fp4_row_bytes(D), kStep1 = BS == 16 ? kTile : 0, kRow1 = BS == 16 ? 0 : 16;
 
     // The weights of the stage's tokens as P^T B fragments (step 0: pb[0], pb[1]; step 1: pb[2], pb[3]):
-    // 2^((x - m) sc) of the scores x.  The difference comes before the scale, so the reference's own exponent is 0
-    // however large the scores are (x sc - m sc, the second rounded, is off by half a unit of m sc: 64 at 2^30).
+    // 2^((x - m) sc + kAbove) of the scores x.  The difference comes before the scale, so the reference's own exponent
+    // is kAbove however large the scores are (x sc - m sc, the second rounded, is off by half a unit of m sc: 64 at 2^30).
     // m is a reference, not the exact maximum: it moves (and O and l are rescaled) only when a score
-    // passes it by more than kRaise, so that most stages need no reduction over lanes.  The weights
+    // passes it by more than 2^(kRaise - kAbove), so that most stages need no reduction over lanes.  The weights
     // then stay at most 2^kRaise, within f16, and the final ratio does not depend on the reference.
     // (The reduction and the rescaling are 9 shuffles and 4 MT + 4 multiplications a stage.)
-    static constexpr float kRaise = 8.f;
+    // kAbove puts the largest weight near the top of f16: a weight keeps its 11 bits down to 2^-25 of the largest one of
+    // its piece, and below is off by at most 2^-36 of it, so that a long tail of small weights is not lost.  A reference
+    // that moves after 2^4 costs no more than one that moves after 2^8 (kAbove 7): the same times on 20 batches.
+    static constexpr float kRaise = 15.f, kAbove = 11.f;
     template <bool MASK>
     __device__ __forceinline__ void weights(uint32_t kb, int valid, int lane, uint32_t (&pb)[4]) {
         const int g = lane >> 2;
@@ -207,7 +212,7 @@ struct Fp4State {
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {  // a token's two heads
                     const float2 d = add_f32x2(make_float2(x[s][i], x[s][i + 1]), make_float2(-m[0], -m[1]));
-                    const float2 e = mul_f32x2(d, make_float2(sc[0], sc[1]));
+                    const float2 e = fma_f32x2(d, make_float2(sc[0], sc[1]), make_float2(kAbove, kAbove));
                     const bool past = MASK && slot_token(g) + 8 * (i >> 1) + 16 * s >= valid;
                     y[s][i] = past ? -INFINITY : e.x, y[s][i + 1] = past ? -INFINITY : e.y;
                 }
@@ -271,7 +276,7 @@ struct Fp4State {
         }
     }
 
-    // Unnormalised partial: slot = [G][D] o, then [G] (m, l), m in base 2.
+    // Unnormalised partial: slot = [G][D] o, then [G] (m, l), m in base 2 (that of weight 1).
     __device__ __forceinline__ void store_partial(float* slot, int G, int lane) const {
         const int g = lane >> 2, h0 = 2 * (lane & 3);
 #pragma unroll
@@ -282,7 +287,7 @@ struct Fp4State {
                 for (int i = 0; i < MT; i += 2)
                     *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[i][j], o[i][2 + j], o[i + 1][j], o[i + 1][2 + j]);
                 if (g == 0) {
-                    slot[G * D + 2 * (h0 + j)] = m[j] * sc[j];
+                    slot[G * D + 2 * (h0 + j)] = fmaf(m[j], sc[j], -kAbove);
                     slot[G * D + 2 * (h0 + j) + 1] = l[j];
                 }
             }

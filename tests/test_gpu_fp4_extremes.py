@@ -101,3 +101,32 @@ def test_the_pool_scale_of_the_values_is_of_any_size(part):
     args = [to_torch(x) for x in (q, kp, vp, tables, lens)]
     one, small = (_decode(*args, 0.09, vs=s, part=part) for s in (1.0, 2.0 ** -125))
     assert one[lens > 0].min() > 1.0 and np.array_equal(small, one * 2.0 ** -125)
+
+
+@pytest.mark.parametrize("n,drop", [(131072, 24.4), (131072, 25.01), (1 << 20, 25.01), (1 << 20, 33.0)])
+def test_a_long_tail_of_small_weights(n, drop):
+    """One key ahead of n - 1 equal ones by `drop` powers of two: their share, (n - 1) 2^-drop of the first's, is not lost.
+    As many segments as there are warps, so that a warp takes a whole one; the tables repeat two blocks."""
+    import torch
+
+    d, bs, hkv = 64, 32, 64
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B = -(-sms * 16 * 5 // 4 // hkv)
+    kp, vp = (np.zeros((2, hkv, bs * 36), np.uint8) for _ in range(2))
+    codes = bs * d // 2
+    kp[0, :, 0], kp[0, :, codes] = 0x02, 0x38                    # the first key: 1 in dim 0; all others 0
+    vp[..., :codes], vp[..., codes:] = 0x22, 0x38                # every value 1 ..
+    vp[0, :, : d // 2] = 0                                       # .. but the first, 0
+    q = torch.zeros(B, hkv, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    tables = torch.ones(B, n // bs, dtype=torch.int32, device="cuda")
+    tables[:, 0] = 0
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    got = _decode(q, to_torch(kp), to_torch(vp), tables, lens, drop * np.log(2.0))
+    tail = (n - 1) * 2.0 ** -drop
+    want = tail / (1.0 + tail)
+    # the output's rounding; f16 weights, 2^-11 each or, below 2^-25 of the largest, 2^-36 of it (twice, for two sums);
+    # and the two sums in fp32 by the tensor cores, which align a step's products with the sum they join and cut each
+    # of them there: n terms, each off by up to 2^-23 of the sum
+    lim = (2.0 ** -8 + 2 * (2.0 ** -11 + n * 2.0 ** -23)) * want + 2 * n * 2.0 ** -36
+    assert np.abs(got - want).max() <= lim, f"{np.abs(got - want).max():.3e} off at {want:.3e}, {lim:.3e} allowed"
