@@ -131,6 +131,9 @@ pa_status pa_copy_blocks(void* k_pool, void* v_pool, const int32_t* src_dst_pair
  * slots are written before they are read, the status word only gathers error
  * bits, and every call leaves the merge counters at zero again (also when a
  * wait timed out: every piece is still stored and counted).
+ * That holds for calls of different head shapes too: a call writes its partial
+ * slots behind the counters of the largest grid or, in a workspace too small for
+ * that, clears their place with a memset behind its kernels.
  */
 pa_status pa_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                     int32_t head_dim, size_t* bytes_out);

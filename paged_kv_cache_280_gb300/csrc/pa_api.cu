@@ -521,8 +521,9 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     if (s != PA_OK) return s;
     // The bytes this launch touches: the status head, a merge counter and two partial slots per CTA of its grid.  In a
     // workspace with room for it the partials lie behind the counters of the largest grid, so that no call leaves its
-    // partials where a call of a larger grid expects its counters at zero.  Over a 4-bit pool, whose decode has no
-    // counters and ends with a record per CTA, they always do.
+    // partials where a call of a larger grid expects its counters at zero; in a smaller one they lie behind this grid's
+    // and that place is cleared after the call.  Over a 4-bit pool, whose decode has no counters and ends with a record
+    // per CTA, they always lie behind the largest grid's.
     WorkspaceLayout wl = workspace_layout(num_q_heads, num_kv_heads, head_dim, lp.grid);
     const size_t counts_end =
         workspace_layout(num_q_heads, num_kv_heads, head_dim, (int64_t)lp.sms * kMaxCtasPerSm).partials_off;
@@ -575,6 +576,10 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     if (clear_status && cudaMemsetAsync(workspace, 0, wl.partials_off, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PA_ERR_CUDA;
     lp.v.launch(p, tk, tv, lp.grid, lp.smem, lp.merge_grid, lp.merge_smem, static_cast<cudaStream_t>(stream));
+    const size_t count_bytes = wl.total < counts_end ? wl.total : counts_end;  // (of the largest grid, that are in the workspace)
+    if (wl.partials_off < count_bytes && !clear_status &&  // clear_status: every call of that workspace clears its own first
+        cudaMemsetAsync(ws + wl.partials_off, 0, count_bytes - wl.partials_off, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
