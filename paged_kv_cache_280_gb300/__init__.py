@@ -150,12 +150,15 @@ _dtype_codes = {}
 
 
 def _dtype_code(t) -> int:
-    if not _dtype_codes:
+    global _dtype_codes
+    codes = _dtype_codes
+    if not codes:
         torch = _torch()
-        _dtype_codes.update({torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3})
+        codes = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3}
         if hasattr(torch, "float8_e4m3fn"):
-            _dtype_codes[torch.float8_e4m3fn] = PA_FP8_E4M3
-    code = _dtype_codes.get(t.dtype)
+            codes[torch.float8_e4m3fn] = PA_FP8_E4M3
+        _dtype_codes = codes  # whole: another thread may be here
+    code = codes.get(t.dtype)
     if code is None:
         raise PAError(2, f"dtype {t.dtype}")
     return code
