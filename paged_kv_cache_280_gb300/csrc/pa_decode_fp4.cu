@@ -513,7 +513,8 @@ __host__ __device__ inline bool fp4_merge_shared(int num_seqs, int num_kv_heads,
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_fp4_kernel(const __grid_constant__ DecodeParams p) {
     constexpr int E = D / 32;
-    __shared__ float part[kMergeWarps][D + 2];
+    __shared__ __align__(16) float part[kMergeWarps][D + 2];  // read two floats at a time
+    static_assert((D + 2) % 2 == 0 && E % 2 == 0, "every row, and a lane's part of it, starts on 8 bytes");
     const int G = p.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool shared = fp4_merge_shared(p.num_seqs, p.num_kv_heads, p.num_ctas);
     const int W = shared ? kMergeWarps : 1, first = shared ? warp : 0;  // the warp takes pieces first, first + W, ...
