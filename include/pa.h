@@ -449,7 +449,9 @@ pa_status pa_decode_attention_fp8(void* out, const void* q, const void* k_pool, 
  * that fp32 holds (scale * k_scale * q . K[t], in base 2).  The call is two kernels, the
  * second, which merges split segments, a programmatic dependent (with one
  * CTA there is nothing to merge and one kernel); pa_debug_set_merge_mode does not
- * change that.  num_kv_heads <= 32767; num_seqs is bounded by the lengths' room
+ * change that.  Of a plan the launch takes the lengths and prefix sums; it searches its
+ * ranges itself, finer than the plan's records have them, and takes as long as
+ * without one.  num_kv_heads <= 32767; num_seqs is bounded by the lengths' room
  * in shared memory (at least 10,000; PA_ERR_UNSUPPORTED past it).
  *
  * The append and the unpacking are launched as programmatic dependents too: they

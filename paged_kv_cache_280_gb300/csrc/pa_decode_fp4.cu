@@ -14,10 +14,10 @@
 // the one before becomes the CTA's partial in the workspace, and a second kernel, launched as the
 // programmatic dependent of this one, merges those.
 //
-// Measured (both kernels, device time): 256 sequences of 32 .. 4095 tokens with 32 heads of their own 164.5 us, 6.0 TB/s
-// (0.89 of the measured copy rate); 4 sequences of 131072 tokens with 64 / 8 heads 100.5 us (0.89); 64 sequences with
-// 32 / 8 heads 21.3 us (0.44: 4.9 us pass before a CTA's first tile arrives, 4 from its last tile to the end of the
-// merge); one sequence of 1031 tokens 7.5 us.  With producer and consumer warps and four CTAs per SM, as over FP8
+// Measured (both kernels, device time): 256 sequences of 32 .. 4095 tokens with 32 heads of their own 165.8 us, 6.0 TB/s
+// (0.89 of the measured copy rate); 4 sequences of 131072 tokens with 64 / 8 heads 100.9 us (0.89); 64 sequences with
+// 32 / 8 heads 21.4 us (0.44: 4.9 us pass before a CTA's first tile arrives, 4 from its last tile to the end of the
+// merge); one sequence of 1031 tokens 7.6 us.  With producer and consumer warps and four CTAs per SM, as over FP8
 // pools, the first three took 299, 142 and 31 us: the hand-over cost a third of the issue slots.
 #include "pa_decode.cuh"
 #include "pa_decode_fp4.cuh"
@@ -26,8 +26,8 @@ namespace pa {
 namespace {
 
 // Two stages of 32 tokens a warp (2 x 4.6 KB at D = 128, 147 KB per SM): what one warp lacks in depth the
-// other fifteen have.  Measured on the first two batches above (us), warps x stages: 16 x 2 186 / 114, 14 x 2
-// 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.  At D = 64 four stages gain nothing.
+// other fifteen have.  Measured on the first two batches above (us) when it was chosen, warps x stages: 16 x 2 186 / 114,
+// 14 x 2 210 / 129, 12 x 2 189 / 117, 12 x 3 192 / 118, 10 x 3 226 / 139, 8 x 4 237 / 146.  At D = 64 four stages gain nothing.
 constexpr int kStageTok = 32;
 constexpr size_t partial_slot_bytes_max(int d) { return (size_t)(kMaxGroup * (d + kSlotExtraFloatsPerHead) + 3) / 4 * 16; }
 
@@ -498,12 +498,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_fp4_kernel(const __grid
 // The merge of split segments: M = max m_p, out = sum 2^(m_p - M) o_p / sum 2^(m_p - M) l_p over the CTAs that hold a
 // piece, in an order of the kernel's own but always the same.  An item is one query head of the segment that a CTA's
 // record names, if it names one.  A warp takes an item, or, where segments have four pieces or more on average, the four warps
-// of a CTA share its pieces.  The decode's CTAs fill their SMs, so this kernel starts when they exit and all it does is
+// of a CTA share its pieces (shared / never shared: one sequence of 1031 tokens and 8 KV heads 7.6 / 8.3 us, of 4096 tokens
+// and one 7.9 / 11.4; shared always, 16 sequences of 8 KV heads take 16.1 us instead of 15.1, and from two pieces on, 64 of
+// one 13.5 instead of 12.5).  The decode's CTAs fill their SMs, so this kernel starts when they exit and all it does is
 // latency: the records and the first pieces are fetched together, before the records say how many there are (what slots
 // hold beyond them is dropped).
 // Measured: its last store 2.3 us after the decode grid ends on 64 sequences of 32 / 8 heads.  When it worked the
-// ranges out anew from the lengths instead of reading records, the call took 21.9 us instead of 21.3; one CTA of 16
-// warps per record 22.4 us; merging in the decode kernel, with counters, 1.7 us less there but 5 us more on 256
+// ranges out anew from the lengths instead of reading records, the call took 0.6 us more (21.9 us); with one CTA of 16
+// warps per record 1.1 us more; merging in the decode kernel, with counters, 1.7 us less there but 5 us more on 256
 // sequences of 32 heads, where its registers spilled.
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeAhead = 8;  // pieces that a warp fetches before it has the record, at most

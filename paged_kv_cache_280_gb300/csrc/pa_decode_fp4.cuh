@@ -20,8 +20,8 @@
 //    weights that P V uses, and need no reduction over lanes.
 //  - The sums are fp32, and a tensor core cuts each product at about 2^-23 of the sum that it joins: n tokens of one
 //    warp's piece are off by at most n 2^-23 of their sum, and O and l alike.
-// As built a token row costs 13.9 warp instructions at D = 128; without its copies the loop does one in 2.65 ns
-// per SM, where HBM delivers one in 3.24 ns.
+// As built a token row costs 16.9 warp instructions at D = 128 (70.7 million for 4 sequences of 131,072 tokens and 8 KV
+// heads), of the 25 slots above; on 96 sequences of 32 heads the issue slots are 63 % busy.
 // Slots past the sequence's end may hold any bits: their scores become -inf, and their V rows get
 // scale 0 (codes are always finite), so neither reaches the output.
 #pragma once

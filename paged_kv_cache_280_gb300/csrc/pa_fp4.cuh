@@ -60,8 +60,13 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 }
 
 // ---- correctly rounded quotients of many elements by one divisor ----------------------------------
-// With r the correctly rounded reciprocal of b: q = x r is within an ulp of x / b, its remainder q b - x is
-// exact, and q - remainder * r, rounded, is x / b correctly rounded (Markstein 1990).  This needs no term to
+// With r the correctly rounded reciprocal of b, q = x r is within 1.5 units in the last place of x / b, and
+// q - (q b - x) r, rounded, is x / b correctly rounded (the step is Markstein's, 1990, whose theorem asks for a q
+// within one unit).  Take x and b in [1, 2).  For x >= b, q is within one unit and q b - x is exact; for x < b it
+// may need 25 bits and lose its last one, 2^-47.  With r's error, 2^-25, times the remainder, what is rounded last
+// is within 2^-46 of x / b (2^-47 for x >= b).  So the result could be wrong only where x / b is that near
+// to the middle of two floats: x 2^25 - M b (x 2^24 - M b for x >= b) a multiple of 2^-23 below 8, M odd.  All
+// such pairs, and those with x next to 1, to 2 and to b, have been computed: none is wrong.  This needs no term to
 // leave the normal range: kQuotientMax bounds |x| and b's range (its reciprocal is in range with it).
 // Below, where a quotient or a remainder is tiny, the result may be off by a unit of the smallest number; the
 // callers round what is so small to zero.  A zero keeps its sign.  For b a power of two q is x / b.

@@ -19,7 +19,7 @@ namespace {
 // head to a warp, which makes whole lines of codes, 27.  Twice the tokens take 32.1 us, fp32 input of 8192 tokens
 // 13.9 us (5.5 TB/s): 3 us of each are a launch's ramp and end.  256 tokens of 32 heads take 2.8 us, all ramp.
 constexpr int kAppendAhead = 2;
-constexpr int kAppendCtas = 4;  // per SM; with 5 (48 registers) 18.8 us against 18.8, and 256 tokens 3.1 against 2.8; with 6, 21.4
+constexpr int kAppendCtas = 4;  // per SM; with 3, 4, 5 and 6: 18.2, 17.4, 19.0, 20.3 us; 256 tokens 3.0, 2.8, 3.2, 3.7
 template <typename T, int D>
 __global__ void __launch_bounds__(256, kAppendCtas) reshape_and_cache_fp4_kernel(const T* k_new, const T* v_new, uint8_t* k_pool,
                                                                     uint8_t* v_pool, const int64_t* slots, uint32_t total, const FastDiv heads, int32_t bs_shift,
@@ -101,7 +101,8 @@ __device__ __forceinline__ void store16(float* p, const float* x) {
 // groups are consecutive.  WIDE: the outputs are 32-byte aligned, and a warp's store instruction covers whole lines
 // (with two 16-byte stores it covers half of each, and every line reaches L2 twice).
 // Measured, 8192 blocks of 16 tokens, 8 heads of 128, to bf16 (688 MB): 103 us, 6.7 TB/s (0.98 of the measured copy
-// rate); before the wide stores and pairs of groups 154 us.
+// rate); before the wide stores and pairs of groups 154 us.  To fp32 0.98 as well.  A CTA's 512 places belong to one
+// block: with 2 KV heads of 128 or one in 32-token blocks 0.98, with one in 16-token blocks 0.91, with one of 64 0.68.
 constexpr int kUnpackPer = 2;
 template <typename T, int D, int BS, bool WIDE>
 __global__ void __launch_bounds__(256) unpack_blocks_fp4_kernel(const uint8_t* k_pool, const uint8_t* v_pool,

@@ -36,8 +36,9 @@ constexpr int kMaxSmem = 227 * 1024;
 // about six FP8 tiles: a fit of loop ends against tiles and segments per CTA
 // gave 5.8, and a sweep of the weight was fastest at 24 units on all three
 // unpartitioned workloads.  Over 4-bit pools a segment costs a warp its query fragments, one masked
-// stage and a join: a sweep of the weight at 4, 8, 12, 16, 24, 40 and 64 units took 204, 186, 177, 172,
-// 172, 180 and 193 us on 256 sequences of 32 heads of their own.
+// stage and a join: a sweep of the weight at 4, 8, 12, 16, 18, 20, 24 and 40 units took 202, 183, 173, 168,
+// 166, 166, 168 and 176 us on 256 sequences of 32 heads of their own, 91, 80, 74, 72, 71, 70, 69 and 72 on as
+// many at head_dim 64, and 23.1, 22.1, 21.0, 21.0, 21.4, 21.4, 21.9 and 22.4 on 64 sequences of 32/8 heads.
 constexpr int kTileUnits = 4;
 #ifndef PA_SEG_UNITS_MMA
 #define PA_SEG_UNITS_MMA 4

@@ -242,8 +242,10 @@ PA_HD Plan plan_from_prefix(const int32_t* pref, const int32_t* upref, int B, in
 
 // Ranges that take work in a launch of num_ctas over a 4-bit pool: without partitions a range spans at
 // least kFp4MinRangeTokens tokens (of one KV head), so that a short batch is not cut into pieces whose merge
-// costs more than their computation.  (tiles: of the whole batch.)  Measured on one sequence of 1031
-// tokens and 8 KV heads, least tokens 32, 64, 96, 128, 192: 10.5, 9.75, 9.0, 9.7, 10.1 us.
+// costs more than their computation.  (tiles: of the whole batch.)  Measured with least tokens 32, 64, 96, 128, 192
+// (us): one sequence of 1031 tokens and 8 KV heads 10.1, 9.5, 7.6, 8.1, 7.9; of 4096 tokens and one KV head 12.0, 9.2,
+// 7.9, 7.9, 7.8; of 1031 and 8 at head_dim 64 8.6, 8.3, 6.9, 7.3, 7.3; four of 100 .. 500 and 8 9.6, 9.1, 9.2, 8.6, 8.0;
+// eight of 500 .. 2048 and 2 11.1, 11.1, 11.1, 10.1, 9.8.  Batches of 64 sequences do not depend on it.
 constexpr int kFp4MinRangeTokens = 96;
 PA_HD int32_t fp4_ranges(int64_t tiles, int num_ctas, int partition_tiles, int block_size) {
     if (partition_tiles > 0) return num_ctas;

@@ -27,8 +27,9 @@ enum RopePool { kPoolSame = 0, kPoolFp8 = 1, kPoolFp4 = 2 };
 
 // Measured: 8191 tokens of 64 + 16 heads of 128, bf16 to bf16 (340 MB): 50.9 us, 6.7 TB/s (0.99 of the measured copy
 // rate); with the loads of a unit issued when its turn comes 70 us, with only its slot and position fetched then
-// 54.6.  4096 fp32 tokens of 32 + 16 heads 34.0 us (0.88).  4099 tokens of 32 + 16 heads to 4-bit pools 21.3 us (0.63: two
-// groups' codes cost more than HBM takes).  One token: 1.9 us, a launch and one trip to memory.
+// 54.6.  4096 fp32 tokens of 32 + 16 heads 34.0 us (0.89), bf16 ones to FP8 pools 18.8 (0.75).  4099 tokens of 32 + 16 heads
+// to 4-bit pools 21.4 us (0.63: two groups' codes cost more than HBM takes).  One token: 1.9 us, a launch and one trip
+// to memory.
 // CTAs per SM: 4 (64 registers); with 5 it spills and is slower, with 3 the 4-bit case takes 23.8 us.
 constexpr int kRopeAhead = 2;  // turns that a thread copies ahead
 
