@@ -87,3 +87,67 @@ def test_fp8_codes_beside_their_borders():
         pa.pa_rope_and_cache(None, None, k, to_torch(v), to_torch(pos), table, kp, vp, to_torch(slots), k_scale=1.0, v_scale=float(b))
         want = oracle.e4m3_encode(v / b)
         assert np.array_equal(to_numpy(vp).transpose(0, 2, 1, 3).reshape(nb * bs, hkv, d), want), b
+
+
+def test_nothing_to_append_or_unpack():
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    d, hkv, bs = 64, 2, 16
+    kp, vp = (torch.full((3, hkv, bs * 36), 9, dtype=torch.uint8, device="cuda") for _ in range(2))
+    none = torch.empty(0, hkv, d, device="cuda")
+    slots, ids = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_reshape_and_cache_fp4(none, none, kp, vp, slots, 1.0, 1.0, status=status)
+    pa.pa_rope_and_cache(none, none, none, none, ids, torch.ones(4, d, device="cuda"), kp, vp, slots, status=status)
+    out = torch.empty(0, hkv, bs, d, device="cuda")
+    pa.pa_unpack_blocks_fp4(kp, vp, ids, out, out, 1.0, 1.0, status=status)
+    assert status.item() == 0 and (kp == 9).all() and (vp == 9).all()
+
+
+def test_rows_and_outputs_past_32_bits():
+    """Inputs and outputs of more than 2^32 bytes and 2^31 elements: the last tokens, behind padding, and the last blocks."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    n, heads, d, bs, nb, last = 150_000, 128, 128, 32, 2, 20
+    x = torch.zeros(n, heads, d, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 1 << 31
+    rows = synth.normal(synth.stream_seed(61, 1), last * heads * d, "bf16").reshape(last, heads, d)
+    x[-last:] = to_torch(rows)
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    at = np.arange(last) + 7
+    slots[-last:] = to_torch(at)
+    pools = [torch.zeros(nb, heads, bs * 72, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pa.pa_reshape_and_cache_fp4(x, x, *pools, slots, 0.5, 2.0)
+    kp, vp = (np.zeros((nb, heads, bs * 72), np.uint8) for _ in range(2))
+    kv4.append_fp4(rows, rows, kp, vp, at, bs, 0.5, 2.0)
+    assert np.array_equal(to_numpy(pools[0]), kp) and np.array_equal(to_numpy(pools[1]), vp)
+
+    # queries and keys and values as parts of the same rows
+    hq, hkv = 64, 32
+    table = kv4.cos_sin_table(64, d)
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos[-last:] = 9
+    q_out = torch.zeros(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    pools = [torch.zeros(nb, hkv, bs * 72, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pa.pa_rope_and_cache(q_out, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, to_torch(table), *pools, slots, k_scale=0.5,
+                         v_scale=2.0)
+    kp, vp = (np.zeros((nb, hkv, bs * 72), np.uint8) for _ in range(2))
+    p9 = np.full(last, 9)
+    kv4.append_fp4(kv4.rotate_f32(rows[:, hq:hq + hkv], p9, table, False), kv4.widen32(rows[:, hq + hkv:]), kp, vp, at, bs, 0.5, 2.0)
+    assert np.array_equal(to_numpy(pools[0]), kp) and np.array_equal(to_numpy(pools[1]), vp)
+    assert np.array_equal(to_numpy(q_out[-last:]), kv4.to_bf16(kv4.rotate_f32(rows[:, :hq], p9, table, False)))
+    assert not q_out[:-last].any()
+    del x, q_out
+
+    num, hkv = 5_000, 128
+    pools = [torch.randint(0x20, 0x41, (3, hkv, bs * 72), device="cuda", dtype=torch.uint8) for _ in range(2)]
+    ids = (torch.arange(num, device="cuda", dtype=torch.int32) + 1) % 3
+    out = [torch.empty(num, hkv, bs, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert out[0].numel() > 1 << 31
+    pa.pa_unpack_blocks_fp4(*pools, ids, *out, 1.0, 0.25)
+    for o, p, s in zip(out, pools, (1.0, 0.25)):
+        for i in (0, num // 2, num - 2, num - 1):
+            want = kv4.to_bf16(kv4.values(to_numpy(p)[[int(ids[i])]], d, bs).astype(np.float32) * np.float32(s))
+            assert np.array_equal(to_numpy(o[[i]]), want)
