@@ -524,6 +524,35 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const 
                             int32_t* dev_status, void* stream);
 
 /*
+ * Normed rotating append: pa_rope_and_cache for models that norm every query and
+ * key head before the rotation (the pages name neither step).  For every token i
+ * that pa_rope_and_cache would append, each query and key head x is first
+ *     x' = x / sqrt(mean(x^2) + eps) * w
+ * over its head_dim elements, w = q_weight or k_weight (fp32 [head_dim], read as
+ * they are: a model that stores w - 1 passes w), then turned as there.  In fp32: the
+ * squares are summed in any order, one correctly rounded reciprocal root, two
+ * products.  Values are stored as they are.
+ *     q_out[i] = turned q,  k_out[i] = turned k (unless k_out is NULL),
+ *     K pool at s = turned k,  V pool at s = v[i],
+ * each rounded once, q_out and k_out to in_dtype.  k_out, [num_tokens][num_kv_heads]
+ * [head_dim] contiguous, is what pa_prompt_attention reads after it; it may be k itself
+ * when k is contiguous, and overlaps nothing else.
+ *
+ * q_weight is read when num_q_heads > 0.  eps: finite, >= 0 (a row of zeros under eps 0
+ * is 0 / 0).  A row whose squares' sum leaves fp32 becomes zero; a NaN or infinity in
+ * a query or key head makes that head NaN.  Everything else, padding, bad slots and
+ * positions included, is as for pa_rope_and_cache.
+ */
+pa_status pa_norm_rope_and_cache(void* q_out, void* k_out, const void* q, int64_t q_stride, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, const float* q_weight,
+                                 const float* k_weight, float eps, const int32_t* positions, const float* cos_sin,
+                                 int32_t max_position, int32_t rot_dim, int32_t interleaved, void* k_pool, void* v_pool,
+                                 const int64_t* slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                 pa_dtype in_dtype, pa_dtype pool_dtype, float k_scale, float v_scale,
+                                 int32_t* dev_status, void* stream);
+
+/*
  * Swap a preempted sequence's blocks out to a block store and back
  * (data.6616ai.com "PagedAttention 之外": KV swapped to CPU memory under
  * memory pressure and restored to resume).
@@ -586,6 +615,78 @@ pa_status pa_prefill_attention(void* out, const void* q, const void* k_pool, con
                                const int32_t* cu_q_lens, int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                int32_t num_blocks, float scale, pa_dtype dtype, int32_t* dev_status, void* stream);
+
+/*
+ * Prompt attention: causal attention over whole prompts, packed one behind the
+ * other, reading the keys and values that were just projected instead of a pool (a
+ * prompt needs no cache to attend to itself, and a quantised pool would cost it
+ * precision).  Sequence b is the tokens cu_lens[b] .. cu_lens[b + 1] - 1, its i-th token
+ * sees its tokens 0 .. i:
+ *     out[cu_lens[b] + i][h] = softmax_{j <= i}(scale q_i . k_j) v_j,
+ * query head h reading KV head h / (num_q_heads / num_kv_heads).
+ *
+ * Layouts: q [num_tokens][num_q_heads][head_dim], k and v [num_tokens][num_kv_heads]
+ * [head_dim], bf16, with q_stride, k_stride and v_stride elements from one token to the
+ * next (multiples of 8, at least heads * head_dim), so they may be parts of one fused
+ * projection; out [num_tokens][num_q_heads][head_dim], contiguous, overlapping no input.
+ * cu_lens int32 [num_seqs + 1], non-decreasing; a sequence may be empty.  Rows of no
+ * sequence (before cu_lens[0], behind cu_lens[num_seqs]) are not written.  max_len bounds
+ * every length.  bf16, head_dim 64 or 128, num_q_heads / num_kv_heads <= 8, num_seqs and
+ * num_kv_heads <= 65535.  scale must be finite and > 0.  Keys and values of a sequence's tokens must be finite (a
+ * NaN or infinity there may reach earlier rows of the same sequence too, as in
+ * pa_prefill_attention); what other rows hold reaches nothing.
+ *
+ * Scores and softmax in fp32, weights rounded to bf16 for the product with V.
+ * A sequence outside num_tokens, longer than max_len, or of negative length
+ * sets PA_DEV_BAD_SEQ_LEN in *dev_status (if not NULL) and is not written; a pipeline wait
+ * that gives up sets PA_DEV_WAIT_TIMEOUT.  Asynchronous on `stream`.  Allocates
+ * nothing.
+ */
+pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* cu_lens, int32_t num_seqs,
+                              int32_t num_tokens, int32_t max_len, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, float scale, pa_dtype dtype, int32_t* dev_status, void* stream);
+
+/*
+ * Chunk attention over quantised pools: pa_prefill_attention (same chunks, positions,
+ * tables and layouts) over FP8 or 4-bit pools with bf16 q and out, for later turns of
+ * a conversation whose cache is quantised, and for the check of drafted tokens:
+ *     out = softmax_{t <= p}(scale q . (K codes' values * k_scale)) (V codes' values * v_scale).
+ * FP8 pools: head_dim 128; 4-bit pools: 64 or 128; block_size 16 or 32.  Chunks of one
+ * token work (the decode calls are made for those).  scale, k_scale and v_scale must be finite
+ * and > 0, and so must scale * k_scale in base 2.
+ *
+ * code * scale of a pool is exact in f16, in which the products run with fp32 sums; a query
+ * row is first scaled by a power of two so that its largest element lies in [1, 2), so any
+ * finite bf16 magnitudes are in range (an element 2^-14 or less of its row's largest loses bits
+ * below 2^-24 of that).  The softmax weights are f16: off by at most 2^-11 of themselves or
+ * 2^-32 of the largest.  Slots behind a sequence's end may hold any bytes; a NaN among a
+ * sequence's own values may reach rows of the chunk that do not see it.
+ *
+ * The work is split over the contexts too where there are few rows: every CTA takes an equal
+ * run of (128 keys x one query tile) steps, and the partial results of a tile that several
+ * CTAs share are joined in a fixed order by the last of them to end.
+ * workspace: pa_prefill_workspace_bytes bytes, 16-byte aligned, zero-filled once by the
+ * caller; its first int32 is the status word (bits as for pa_prefill_attention, and
+ * PA_DEV_BAD_SEQ_LEN also where n_b < 0).  It may be used by call after call on one
+ * stream, whatever their shapes, as every call leaves its counters zero; calls that can overlap use different ones
+ * (two captured graphs that may run at once count).  A smaller one is refused with
+ * PA_ERR_WORKSPACE_TOO_SMALL.
+ */
+pa_status pa_prefill_workspace_bytes(int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     size_t* bytes_out);
+pa_status pa_prefill_attention_fp8(void* out, const void* q, const void* k_pool, const void* v_pool, float k_scale,
+                                   float v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* seq_lens, const int32_t* cu_q_lens, int32_t num_seqs,
+                                   int32_t num_q_tokens, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+pa_status pa_prefill_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool, float k_scale,
+                                   float v_scale, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* seq_lens, const int32_t* cu_q_lens, int32_t num_seqs,
+                                   int32_t num_q_tokens, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Host block allocator                                                      */

@@ -90,6 +90,16 @@ _SIGS = {
     "pa_rope_and_cache": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
                                  _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float, _vp,
                                  _vp]),
+    "pa_norm_rope_and_cache": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _i32,
+                                      _i32, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                      ctypes.c_float, ctypes.c_float, _vp, _vp]),
+    "pa_prompt_attention": (_i32, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                   ctypes.c_float, _i32, _vp, _vp]),
+    "pa_prefill_workspace_bytes": (_i32, [_i32, _i32, _i32, _i32, _psz]),
+    "pa_prefill_attention_fp8": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _i32, _vp, _vp, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _sz, _vp]),
+    "pa_prefill_attention_fp4": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, ctypes.c_float, _vp, _i32, _vp, _vp, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _sz, _vp]),
     "pa_prefill_attention": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                     _i32, _i32, ctypes.c_float, _i32, _vp, _vp]),
     "pa_decode_set_ctas_per_sm": (_i32, [_i32]),
@@ -523,6 +533,110 @@ def pa_rope_and_cache(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_m
         k_scale, v_scale, _status_ptr(status, dev), _stream_of(stream, dev))
     if status_code:
         raise PAError(status_code, "pa_rope_and_cache")
+
+
+def pa_norm_rope_and_cache(q_out, k_out, q, k, v, q_weight, k_weight, eps, positions, cos_sin, k_pool, v_pool, slot_mapping,
+                           interleaved=False, k_scale=1.0, v_scale=1.0, status=None, stream=None):
+    """pa_rope_and_cache with every query and key head normed first: x / sqrt(mean(x^2) + eps) * weight.
+
+    q_weight/k_weight fp32 [D]; k_out [N][Hkv][D] (may be k itself, or None) receives the turned keys, which
+    pa_prompt_attention reads; the other arguments are pa_rope_and_cache's (q, q_out and q_weight None: keys and values
+    only)."""
+    torch = _torch()
+    shape, dtype, pdtype, pshape = k.shape, k.dtype, k_pool.dtype, k_pool.shape
+    n, hkv, d = shape
+    if len(pshape) == 3:
+        bs, pool_dtype = _fp4_block_size(k_pool, d, "pa_norm_rope_and_cache"), PA_FP4_E2M1
+        want = (pshape[0], hkv, pshape[2])
+    else:
+        bs, pool_dtype = pshape[2], _dtype_code(k_pool)
+        want = (pshape[0], hkv, bs, d)
+    dev = _device()
+    if q is None or q_out is None or q_weight is None:
+        if q is not None or q_out is not None or q_weight is not None:
+            raise PAError(1, "pa_norm_rope_and_cache: q, q_out and q_weight go together")
+        hq, qo_ptr, q_ptr, q_rows, qw_ptr = 0, None, None, 0, None
+    else:
+        hq = q.shape[1]
+        qo_ptr, q_ptr = _ptr(q_out, dtype, (n, hq, d), dev, "q_out"), _rows_ptr(q, dtype, (n, hq, d), dev, "q")
+        q_rows, qw_ptr = _token_rows(q, "q"), _ptr(q_weight, torch.float32, (d,), dev, "q_weight")
+    max_position, rot_dim = cos_sin.shape
+    status_code = _lib.pa_norm_rope_and_cache(
+        qo_ptr, None if k_out is None else _ptr(k_out, dtype, shape, dev, "k_out"), q_ptr, q_rows,
+        _rows_ptr(k, dtype, shape, dev, "k"), _token_rows(k, "k"), _rows_ptr(v, dtype, shape, dev, "v"), _token_rows(v, "v"),
+        qw_ptr, _ptr(k_weight, torch.float32, (d,), dev, "k_weight"), eps, _ptr(positions, torch.int32, (n,), dev, "positions"),
+        _ptr(cos_sin, torch.float32, (max_position, rot_dim), dev, "cos_sin"), max_position, rot_dim, 1 if interleaved else 0,
+        _ptr(k_pool, pdtype, want, dev, "k_pool"), _ptr(v_pool, pdtype, want, dev, "v_pool"),
+        _ptr(slot_mapping, torch.int64, (n,), dev, "slot_mapping"), n, hq, hkv, d, bs, pshape[0], _dtype_code(k), pool_dtype,
+        k_scale, v_scale, _status_ptr(status, dev), _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_norm_rope_and_cache")
+
+
+def pa_prompt_attention(out, q, k, v, cu_lens, max_len, scale, status=None, stream=None):
+    """Causal attention over whole prompts, packed one behind the other, bf16.
+
+    q [T][Hq][D], k/v [T][Hkv][D], each token's heads contiguous (they may be parts of one fused projection); out
+    [T][Hq][D]; cu_lens int32 [B + 1]: sequence b is the tokens cu_lens[b] .. cu_lens[b + 1] - 1; max_len bounds every
+    length."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    n, hq, d = shape = q.shape
+    kshape = (n, k.shape[1], d)
+    b = cu_lens.shape[0] - 1
+    dev = _device()
+    status_code = _lib.pa_prompt_attention(
+        _ptr(out, bf16, shape, dev, "out"), _rows_ptr(q, bf16, shape, dev, "q"), _token_rows(q, "q"),
+        _rows_ptr(k, bf16, kshape, dev, "k"), _token_rows(k, "k"), _rows_ptr(v, bf16, kshape, dev, "v"), _token_rows(v, "v"),
+        _ptr(cu_lens, torch.int32, (b + 1,), dev, "cu_lens"), b, n, int(max_len), hq, kshape[1], d, scale, PA_BF16,
+        _status_ptr(status, dev), _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, "pa_prompt_attention")
+
+
+def pa_prefill_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim) -> int:
+    """Bytes of the zero-filled workspace of pa_prefill_attention_fp8 / _fp4 calls whose chunks have up to max_q_len tokens."""
+    out = _sz(0)
+    _ok(_lib.pa_prefill_workspace_bytes(int(max_q_len), num_q_heads, num_kv_heads, head_dim, ctypes.byref(out)),
+        "pa_prefill_workspace_bytes")
+    return int(out.value)
+
+
+def _prefill_quant(call, name, out, q, k_pool, v_pool, pshape, bs, k_scale, v_scale, block_tables, seq_lens, cu_q_lens,
+                   max_q_len, scale, workspace, stream):
+    torch = _torch()
+    shape = q.shape
+    t, hq, d = shape
+    b, mb = block_tables.shape
+    dev = _device()
+    status_code = call(
+        _ptr(out, torch.bfloat16, shape, dev, "out"), _ptr(q, torch.bfloat16, shape, dev, "q"),
+        _ptr(k_pool, k_pool.dtype, pshape, dev, "k_pool"), _ptr(v_pool, k_pool.dtype, pshape, dev, "v_pool"), k_scale, v_scale,
+        _ptr(block_tables, torch.int32, (b, mb), dev, "block_tables"), mb, _ptr(seq_lens, torch.int32, (b,), dev, "seq_lens"),
+        _ptr(cu_q_lens, torch.int32, (b + 1,), dev, "cu_q_lens"), b, t, int(max_q_len), hq, pshape[1], d, bs, pshape[0], scale,
+        _ptr(workspace, workspace.dtype, workspace.shape, dev, "workspace"), workspace.nbytes, _stream_of(stream, dev))
+    if status_code:
+        raise PAError(status_code, name)
+
+
+def pa_prefill_attention_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, cu_q_lens, max_q_len, scale,
+                             workspace, stream=None):
+    """pa_prefill_attention over FP8 pools (E4M3 codes [num_blocks][Hkv][bs][128]) with bf16 q/out [T][Hq][128].
+    workspace: a CUDA tensor of pa_prefill_workspace_bytes bytes, zero-filled once; its first int32 is the status word."""
+    nb, hkv, bs, d = pshape = k_pool.shape
+    if _dtype_code(k_pool) != PA_FP8_E4M3 or d != q.shape[2]:
+        raise PAError(1, f"pa_prefill_attention_fp8: pool {k_pool.dtype} {tuple(pshape)} for q {tuple(q.shape)}")
+    _prefill_quant(_lib.pa_prefill_attention_fp8, "pa_prefill_attention_fp8", out, q, k_pool, v_pool, pshape, bs, k_scale,
+                   v_scale, block_tables, seq_lens, cu_q_lens, max_q_len, scale, workspace, stream)
+
+
+def pa_prefill_attention_fp4(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, cu_q_lens, max_q_len, scale,
+                             workspace, stream=None):
+    """pa_prefill_attention over 4-bit pools (uint8 [num_blocks][Hkv][fp4_block_bytes(D, bs)]) with bf16 q/out [T][Hq][D].
+    workspace: as for pa_prefill_attention_fp8."""
+    bs = _fp4_block_size(k_pool, q.shape[2], "pa_prefill_attention_fp4")
+    _prefill_quant(_lib.pa_prefill_attention_fp4, "pa_prefill_attention_fp4", out, q, k_pool, v_pool, k_pool.shape, bs, k_scale,
+                   v_scale, block_tables, seq_lens, cu_q_lens, max_q_len, scale, workspace, stream)
 
 
 def pa_swap_out(k_pool, v_pool, blocks, k_store, v_store, status=None, stream=None):

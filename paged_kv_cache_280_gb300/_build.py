@@ -13,7 +13,7 @@ BUILD = os.path.join(HERE, "_build")
 SOURCES = [
     "pa_api.cu", "pa_cache_ops.cu", "pa_decode_bf16.cu", "pa_decode_bf16_fma.cu", "pa_decode_f32.cu",
     "pa_decode_f32_pow2.cu", "pa_decode_fp8.cu", "pa_decode_fp4.cu", "pa_fp4_ops.cu", "pa_rope.cu", "pa_static_ws.cu",
-    "pa_prefill.cu", "pa_alloc.cpp",
+    "pa_norm_rope.cu", "pa_prefill.cu", "pa_prompt.cu", "pa_prefill_quant.cu", "pa_alloc.cpp",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -26,6 +26,8 @@ inline __host__ __device__ size_t partial_slot_floats(int G, int D) {
     return ((size_t)G * (D + kSlotExtraFloatsPerHead) + 3) & ~(size_t)3;
 }
 constexpr int kMaxSmem = 227 * 1024;
+// Largest distance between tokens of a strided q, k or v, in elements: a tensor map holds strides below 2^40 bytes.
+constexpr int64_t kMaxRowStride = (int64_t)1 << 38;
 
 // Cost weights of the range balance (see DecodeParams): 4 units a tile, and a
 // segment's fixed work in units per compute path.  Measured per-CTA loop ends

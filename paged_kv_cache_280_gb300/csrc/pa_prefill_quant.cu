@@ -1,0 +1,81 @@
+// Chunk attention over FP8 and 4-bit pools: entry points and checks; the kernel in pa_attn.cuh.
+#include <cmath>
+
+#include "pa_attn.cuh"
+
+namespace pa {
+namespace {
+
+pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void* v_pool, float k_scale, float v_scale,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* cu_q_lens, int32_t num_seqs, int32_t num_q_tokens, int32_t max_q_len,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t num_blocks, float scale, void* workspace, size_t workspace_bytes, bool fp4, void* stream) {
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_q_len < 0 ||
+        num_q_tokens < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || !std::isfinite(scale) || !(scale > 0.f) ||
+        !std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
+        return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 8 || (head_dim != 128 && !(fp4 && head_dim == 64)) ||
+        (block_size != 16 && block_size != 32) || num_seqs > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (max_q_len == 0 || num_q_tokens == 0) return PA_OK;
+    if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !cu_q_lens || !workspace) return PA_ERR_INVALID_ARG;
+    if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) ||
+        !aligned_to(workspace, 16) || !aligned_to(block_tables, 4) || !aligned_to(seq_lens, 4) || !aligned_to(cu_q_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+    if (!std::isfinite(scale_log2) || !(scale_log2 > 0.f)) return PA_ERR_INVALID_ARG;
+    size_t need = 0;
+    const pa_status s = pa_prefill_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim, &need);
+    if (s != PA_OK) return s;
+    if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+    AttnParams p = {};
+    p.out = out;
+    p.q = static_cast<const uint16_t*>(q), p.q_stride = (int64_t)num_q_heads * head_dim;
+    p.k_pool = static_cast<const uint8_t*>(k_pool), p.v_pool = static_cast<const uint8_t*>(v_pool);
+    p.block_tables = block_tables, p.seq_lens = seq_lens, p.cu_q_lens = cu_q_lens;
+    p.status = static_cast<int32_t*>(workspace);
+    p.max_blocks_per_seq = max_blocks_per_seq, p.num_seqs = num_seqs, p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads, p.num_blocks = num_blocks, p.num_q_tokens = num_q_tokens;
+    p.max_q_len = max_q_len < num_q_tokens ? max_q_len : num_q_tokens;
+    p.bs_shift = block_size == 16 ? 4 : 5;
+    p.scale_log2 = scale_log2, p.out_scale = v_scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!fp4) return launch_attn<kAttnFp8, 128>(p, st);
+    return head_dim == 128 ? launch_attn<kAttnFp4, 128>(p, st) : launch_attn<kAttnFp4, 64>(p, st);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_prefill_workspace_bytes(int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                                int32_t head_dim, size_t* bytes_out) {
+    if (!bytes_out || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    *bytes_out = pa::kStatusHeadBytes;
+    return PA_OK;
+}
+
+extern "C" pa_status pa_prefill_attention_fp8(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                              float k_scale, float v_scale, const int32_t* block_tables,
+                                              int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                              const int32_t* cu_q_lens, int32_t num_seqs, int32_t num_q_tokens,
+                                              int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    return pa::prefill_quant(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
+                             num_seqs, num_q_tokens, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                             scale, workspace, workspace_bytes, false, stream);
+}
+
+extern "C" pa_status pa_prefill_attention_fp4(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                              float k_scale, float v_scale, const int32_t* block_tables,
+                                              int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                              const int32_t* cu_q_lens, int32_t num_seqs, int32_t num_q_tokens,
+                                              int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                                              void* workspace, size_t workspace_bytes, void* stream) {
+    return pa::prefill_quant(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, max_blocks_per_seq, seq_lens, cu_q_lens,
+                             num_seqs, num_q_tokens, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                             scale, workspace, workspace_bytes, true, stream);
+}

@@ -1,0 +1,37 @@
+// Attention over whole prompts, packed one behind the other: entry point and checks; the kernel in pa_attn.cuh.
+#include <cmath>
+
+#include "pa_attn.cuh"
+
+extern "C" pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* v, int64_t v_stride, const int32_t* cu_lens, int32_t num_seqs,
+                                         int32_t num_tokens, int32_t max_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, float scale, pa_dtype dtype, int32_t* dev_status,
+                                         void* stream) {
+    using namespace pa;
+    if (dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_len < 0 ||
+        num_tokens < 0 || !std::isfinite(scale) || !(scale > 0.f))
+        return PA_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 8 || (head_dim != 64 && head_dim != 128) || num_seqs > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
+    if (q_stride < (int64_t)num_q_heads * head_dim || k_stride < (int64_t)num_kv_heads * head_dim ||
+        v_stride < (int64_t)num_kv_heads * head_dim || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return PA_ERR_INVALID_ARG;
+    if (q_stride > kMaxRowStride || k_stride > kMaxRowStride || v_stride > kMaxRowStride) return PA_ERR_UNSUPPORTED;
+    if (max_len == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !k || !v || !cu_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(cu_lens, 4) ||
+        !aligned_to(dev_status, 4))
+        return PA_ERR_INVALID_ARG;
+    AttnParams p = {};
+    p.out = out;
+    p.q = static_cast<const uint16_t*>(q), p.k = static_cast<const uint16_t*>(k), p.v = static_cast<const uint16_t*>(v);
+    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+    p.cu_q_lens = cu_lens, p.status = dev_status;
+    p.num_seqs = num_seqs, p.num_q_heads = num_q_heads, p.num_kv_heads = num_kv_heads;
+    p.num_q_tokens = num_tokens, p.max_q_len = max_len < num_tokens ? max_len : num_tokens;
+    p.scale_log2 = scale * 1.4426950408889634f, p.out_scale = 1.f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? launch_attn<kAttnPacked, 128>(p, st) : launch_attn<kAttnPacked, 64>(p, st);
+}
