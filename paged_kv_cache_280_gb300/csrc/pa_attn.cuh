@@ -1,9 +1,39 @@
-// Causal attention of several query rows per sequence over packed keys and values or quantised pools: the simple form,
-// one warp per (token, query head), a key at a time with an online softmax in fp32.
+// Causal attention of many query rows per sequence on the fifth-generation tensor cores, over packed keys and values
+// (whole prompts) or quantised pools (chunks of new tokens behind a cached context).
+//
+// Row i of a sequence with n new tokens at the end of len sits at position p = len - n + i and attends to the keys at
+// 0 .. p:  out = softmax(scale q K^T) V,  one pass over the keys with a running maximum and sum per row.
+//
+// Work.  The G query heads of a KV head share its keys: for one (sequence, KV head) a tile is 128 rows, 128 / G tokens
+// of G heads each, one row per TMEM lane.  A unit is two neighbouring tiles, which share every stage of 128 keys; a
+// unit that holds a single tile (few new tokens) lets the tile's two TMEM halves take the even and the odd stages
+// instead, so that either way one half's softmax runs while the tensor core works for the other.
+//   Packed: the units, most keys first, are dealt to the CTAs in snake order (PackedWalk).
+//   Pools:  the units' stages are laid end to end and cut in equal parts (pa_attn_plan.h), so that few rows over a long
+//           context fill the card; the pieces of a cut unit are joined by the last CTA to end (attn_join).
+//
+// Warps.  0 .. 3 and 4 .. 7: the softmax of the two halves, a thread per row.  8: keys and values.  9: the MMAs.  10
+// (and 11 over pools): query rows.  12 .. 15 (pools): widening of the codes.
+//   Packed: K and V stages by TMA, 128-byte swizzle, a ring of slots in shared memory.
+//   Pools:  the blocks' codes by bulk copies into a ring of raw slots; the widening warps turn them into f16 (exact for
+//           E4M3, and for E2M1 codes times their E4M3 scale) in the swizzled layout, with zeros for V rows behind the
+//           sequence's end.  Query rows are scaled by a power of two and rounded to f16 on the way.
+//   S = Q K^T into TMEM (M 128, N 128), O += P V with P read from TMEM, where the softmax wrote it over S.
+//   P is handed over in two halves of 64 keys, so that the product with V begins while the second half's exponentials
+//   are formed.
+// O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since it was last scaled.  Every wait is
+// bounded; one that gives up sets PA_DEV_WAIT_TIMEOUT, every role stops, and the CTA waits for its own copies and MMAs
+// before it frees TMEM.
 #pragma once
 
+#include <cmath>
+#include <type_traits>
+
+#include "pa_attn_plan.h"
+#include "pa_device.cuh"
 #include "pa_fp4.cuh"
 #include "pa_internal.h"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace {
@@ -12,91 +42,1112 @@ enum AttnSource { kAttnPacked = 0, kAttnFp8 = 1, kAttnFp4 = 2 };
 
 struct AttnParams {
     void* out;
-    const uint16_t *q, *k, *v;                // q (and packed k, v): bf16
-    int64_t q_stride, k_stride, v_stride;     // elements from one token to the next
+    const uint16_t* q;             // pools: bf16 [tokens][Hq][D]; packed: through the tensor maps
     const uint8_t *k_pool, *v_pool;
     const int32_t* block_tables;
-    const int32_t* seq_lens;                  // null: packed
+    const int32_t* seq_lens;       // null: packed
     const int32_t* cu_q_lens;
     int32_t* status;
+    int32_t* counts;               // pools: [2 * grid] pieces of a cut tile that have been stored, by the unit's first CTA
+    float2* part_ml;               // pools: [2 * grid slots][tiles][128]: maximum (base 2) and sum of a row's piece
+    float* part_o;                 // pools: [2 * grid slots][tiles][128][D]
+    int32_t part_tiles;            // tiles per slot
     int32_t max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, num_blocks, num_q_tokens, max_q_len, bs_shift;
+    int32_t group, tile_tokens;    // G, 128 / G rounded down
+    int32_t out_align32;           // out is 32-byte aligned: 32-byte stores
     float scale_log2, out_scale;
 };
 
+constexpr int kAtRows = 128;
+constexpr int kAtKvWarp = 8, kAtMmaWarp = 9, kAtQWarp = 10, kAtWidenWarp = 12;
+constexpr uint32_t kAtTmemCols = 512;  // half t: S (P over its first 64 columns) in 256 t + [0, 128), O in 256 t + 128 + [0, D)
+constexpr uint32_t kAtTmemHalf = 256;
+constexpr uint32_t kAtTmemO = 128;
+constexpr float kAtRescaleLog2 = 8.f;
+// f16 weights are held times 2^7: with the lazy rescaling they stay below 2^15, and keep all their bits down to 2^-21 of
+// the largest.
+constexpr float kAtWeightLog2 = 7.f;
+
+template <int I = 0, int N, class F>
+__device__ __forceinline__ void at_static_for_impl(F& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        at_static_for_impl<I + 1, N>(f);
+    }
+}
+template <int N, class F>  // f(integral_constant<int, i>) for i = 0 .. N - 1
+__device__ __forceinline__ void at_static_for(F&& f) {
+    at_static_for_impl<0, N>(f);
+}
+
+// 2^x on the SFU (ex2.approx: 2^-22 relative); 2^-inf = +0.
+__device__ __forceinline__ float at_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int SRC, int D>
-__device__ __forceinline__ void attn_row(const AttnParams& p, bool value, int b, int c0, int t, int g, int lane, float* x) {
-    constexpr int E = D / 32;
-    if constexpr (SRC == kAttnPacked) {
-        const uint16_t* row = (value ? p.v : p.k) + (int64_t)(c0 + t) * (value ? p.v_stride : p.k_stride) + g * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __uint_as_float((uint32_t)row[e] << 16);
-    } else {
-        const int bs = 1 << p.bs_shift, off = t & (bs - 1);
-        int blk = p.block_tables[(int64_t)b * p.max_blocks_per_seq + (t >> p.bs_shift)];
-        if (blk < 0 || blk >= p.num_blocks) {
-            if (lane == 0) flag_status(p.status, PA_DEV_BAD_BLOCK_ID);
-            blk = 0;
+struct AttnLayout {
+    static constexpr bool kPools = SRC != kAttnPacked;
+    static constexpr int kThreads = kPools ? 512 : 384;
+    static constexpr int kPanels = D / 64;
+    static constexpr int kPanelBytes = 128 * 128;           // 128 rows (query rows or keys) of 64 elements
+    static constexpr int kTileBytes = kPanels * kPanelBytes;  // a query tile, or K or V of a stage
+    static constexpr int kSlots = kPools ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
+    static constexpr int kRawBytes = SRC == kAttnFp8 ? 128 * D : 128 * fp4_row_bytes(D);
+    static constexpr int kRaws = !kPools ? 0 : SRC == kAttnFp8 ? 3 : D == 128 ? 5 : 8;
+    static constexpr int kRingOff = 2 * kTileBytes;
+    static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
+    static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors [2 pieces][2 tiles][128] floats
+    static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 * 4 : 0);  // odd half's (m, l) [128]
+    static constexpr int kJoinOff = kMlOff + 128 * 8;                        // join's (m, 1 / l) [2][128]
+    static constexpr int kBarOff = kJoinOff + (kPools ? 2 * 128 * 8 : 0);
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 16;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
+    static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
+    static_assert(kBytes <= kMaxSmem, "shared memory");
+};
+
+template <int SRC, int D>
+struct AttnBars {
+    using L = AttnLayout<SRC, D>;
+    uint32_t base;
+    __device__ uint32_t at(int i) const { return base + 8u * i; }
+    __device__ uint32_t full(int s) const { return at(s); }
+    __device__ uint32_t empty(int s) const { return at(L::kSlots + s); }
+    __device__ uint32_t raw_full(int s) const { return at(2 * L::kSlots + s); }
+    __device__ uint32_t raw_empty(int s) const { return at(2 * L::kSlots + L::kRaws + s); }
+    static constexpr int kRest = 2 * L::kSlots + 2 * L::kRaws;
+    __device__ uint32_t s_full(int t) const { return at(kRest + t); }        // S in TMEM
+    __device__ uint32_t p_first(int t) const { return at(kRest + 2 + t); }   // weights of keys 0 .. 63 in TMEM, O rescaled
+    __device__ uint32_t p_second(int t) const { return at(kRest + 4 + t); }  // the other weights
+    __device__ uint32_t o_final(int t) const { return at(kRest + 6 + t); }   // a piece's last P V
+    __device__ uint32_t q_full() const { return at(kRest + 8); }
+    __device__ uint32_t q_empty() const { return at(kRest + 9); }
+    __device__ uint32_t drain() const { return at(kRest + 10); }
+    __device__ uint32_t tail() const { return at(kRest + 11); }      // packed: a V box with rows behind its sequence's end
+    __device__ uint32_t odd_ml() const { return at(kRest + 12); }    // the odd half's maximum and sum are in shared memory
+    __device__ uint32_t odd_read() const { return at(kRest + 13); }  // the even half's warps have read them, and its O
+    __device__ uint32_t join(int t) const { return at(kRest + 14 + t); }  // the half's four warps have come this far
+};
+
+// Warp-collective bounded wait; gives up once the CTA's abort flag is set.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    bool ok = mbar_wait(bar, parity, kWaitLimitNs, abort_flag);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+        *abort_flag = 1;
+        if ((threadIdx.x & 31) == 0) flag_status(status, PA_DEV_WAIT_TIMEOUT);
+    }
+    return ok;
+}
+// The same for one thread.
+__device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
+    if (*abort_flag) return false;
+    if (mbar_wait(bar, parity, kWaitLimitNs, abort_flag)) return true;
+    *abort_flag = 1;
+    flag_status(status, PA_DEV_WAIT_TIMEOUT);
+    return false;
+}
+
+// ---- work ------------------------------------------------------------------------------------------
+
+// New tokens of sequence b (0: none, or a sequence that breaks the call's bounds), its first row and its length.
+template <int SRC>
+__device__ __forceinline__ int at_sequence(const AttnParams& p, int b, int& c0, int& len, bool* bad = nullptr) {
+    c0 = __ldg(p.cu_q_lens + b);
+    const int end = __ldg(p.cu_q_lens + b + 1), n = end - c0;
+    len = SRC == kAttnPacked ? n : __ldg(p.seq_lens + b);
+    const bool wrong = end < c0 || (n > 0 && (c0 < 0 || end > p.num_q_tokens || n > p.max_q_len || n > len ||
+                                              (SRC != kAttnPacked && (int64_t)len > ((int64_t)p.max_blocks_per_seq << p.bs_shift))));
+    if (bad) *bad = wrong;
+    return wrong ? 0 : n;
+}
+
+// A run of stages of one unit.  Every role walks the same pieces in the same order.
+struct AttnPiece {
+    int b, g, c0, n, len;
+    int i0;         // the unit's first new token
+    bool one;       // a single tile, whose halves take the even and the odd stages
+    int k0, ns;     // stages k0 .. k0 + ns - 1 of the unit
+    int n0;         // two tiles: how many of them the first tile sees
+    bool first, last;  // the unit's first, last stage is among them
+    int64_t at;     // pools: where the unit begins on the line of work
+    int nst;        // the unit's stages
+};
+
+__device__ __forceinline__ void at_fields(const AttnParams& p, int m, AttnPiece& w) {
+    const int T = p.tile_tokens;
+    w.i0 = 2 * m * T;
+    w.one = w.i0 + T >= w.n;
+    const int base = w.len - w.n;
+    w.nst = (base + min(w.n, w.i0 + 2 * T) + kAttnKeys - 1) / kAttnKeys;
+}
+__device__ __forceinline__ void at_stages(const AttnParams& p, int k0, int k1, AttnPiece& w) {
+    w.k0 = k0, w.ns = k1 - k0;
+    const int nst0 = (w.len - w.n + min(w.n, w.i0 + p.tile_tokens) + kAttnKeys - 1) / kAttnKeys;
+    w.n0 = max(0, min(k1, nst0) - k0);
+    w.first = k0 == 0, w.last = k1 == w.nst;
+}
+
+// Packed: the units that exist, by unit index from the last down (the most keys first), then sequence, then KV head; CTA c
+// takes ranks c, 2 C - 1 - c, 2 C + c, ..  Warp-collective.
+struct PackedWalk {
+    int m, chunk, loaded, mine, rank0, wave;
+    uint32_t mask;
+    __device__ PackedWalk(const AttnParams& p, const void*) : chunk(0), loaded(-1), mine(0), rank0(0), wave(0), mask(0) {
+        m = (p.max_q_len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) - 1;
+        look(p);
+    }
+    __device__ __forceinline__ void look(const AttnParams& p) {  // which of the chunk's 32 sequences have a unit m
+        if (loaded != chunk) {
+            const int b = chunk + (threadIdx.x & 31);
+            int c0, len;
+            const int n = b < p.num_seqs ? at_sequence<kAttnPacked>(p, b, c0, len) : 0;
+            mine = (n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+            loaded = chunk;
         }
-        const int64_t head = (int64_t)blk * p.num_kv_heads + g;
-        if constexpr (SRC == kAttnFp8) {
-            const uint8_t* row = (value ? p.v_pool : p.k_pool) + ((head << p.bs_shift) + off) * D + lane * E;
+        mask = __ballot_sync(0xffffffffu, mine > m);
+    }
+    __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
+        const int C = gridDim.x, want = wave * C + ((wave & 1) ? C - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        while (m >= 0) {
+            const int here = __popc(mask) * p.num_kv_heads;
+            if (want < rank0 + here) {
+                const int off = want - rank0, j = off / p.num_kv_heads;
+                w.g = off - j * p.num_kv_heads;
+                w.b = chunk + __fns(mask, 0, j + 1);
+                w.n = at_sequence<kAttnPacked>(p, w.b, w.c0, w.len);
+                at_fields(p, m, w);
+                at_stages(p, 0, w.nst, w);
+                w.at = 0;
+                ++wave;
+                return true;
+            }
+            rank0 += here;
+            chunk += 32;
+            if (chunk >= p.num_seqs) chunk = 0, --m;
+            look(p);
+        }
+        return false;
+    }
+};
+
+// Pools: this CTA's range of the line of work (written by at_plan before the roles start).
+struct AttnRange {
+    int64_t at, end, W;  // the first unit's beginning, the range's end; the whole line
+    int32_t b, g, m, k, C;
+};
+struct RangeWalk {
+    int64_t at, end;
+    int b, g, m, k;
+    bool fresh;
+    int n, len, c0;
+    __device__ RangeWalk(const AttnParams&, const void* range) : fresh(true) {
+        const volatile AttnRange* r = static_cast<const volatile AttnRange*>(range);
+        at = r->at, end = r->end, b = r->b, g = r->g, m = r->m, k = r->k;
+    }
+    __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
+        while (at < end) {
+            if (fresh) {
+                n = at_sequence<kAttnFp8>(p, b, c0, len);
+                fresh = false;
+                if (n == 0) {  // (some later sequence has tokens: the range has not ended)
+                    ++b, fresh = true;
+                    continue;
+                }
+            }
+            w.b = b, w.g = g, w.n = n, w.len = len, w.c0 = c0;
+            at_fields(p, m, w);
+            const int wt = w.one ? kOneTile : kTwoTiles;
+            const int k0 = k, k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt));
+            w.at = at;
+            if (k1 < w.nst) {
+                at = end;
+            } else {
+                at += kUnitWeight + (int64_t)w.nst * wt;
+                k = 0;
+                if (2 * ++m * p.tile_tokens >= n) {
+                    m = 0;
+                    if (++g == p.num_kv_heads) g = 0, ++b, fresh = true;
+                }
+            }
+            if (k0 < k1) {
+                at_stages(p, k0, k1, w);
+                return true;
+            }
+        }
+        return false;
+    }
+};
+template <int SRC>
+using AttnWalk = std::conditional_t<SRC == kAttnPacked, PackedWalk, RangeWalk>;
+
+// One warp: this CTA's range.
+__device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, int lane) {
+    auto line = [&](int b) {
+        int c0, len;
+        const int n = b < p.num_seqs ? at_sequence<kAttnFp8>(p, b, c0, len) : 0;
+        return UnitLine{n, len, p.tile_tokens};
+    };
+    int64_t W = 0, mine = 0;
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        mine = line(b0 + lane).total() * p.num_kv_heads;
+        W += mine;
+    }
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = e4m3_to_float(row[e]);
-        } else {
-            const uint8_t* rec = (value ? p.v_pool : p.k_pool) + head * (int64_t)(fp4_row_bytes(D) << p.bs_shift);
-            const float s = e4m3_to_float(rec[((D / 2) << p.bs_shift) + off * (D / 16) + lane * E / 16]);
+    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    const int64_t C = W > 0 ? ranges(W, gridDim.x) : 0, c = blockIdx.x;
+    if (c >= C) {
+        if (lane == 0) range->at = range->end = 0, range->W = W, range->C = (int)C;
+        return;
+    }
+    const int64_t x = range_begin(c, W, C);
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        if (p.num_seqs > 32) mine = line(b0 + lane).total() * p.num_kv_heads;
+        int64_t incl = mine;
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const __half2 c = __half2(__nv_cvt_fp4x2_to_halfraw2(rec[off * (D / 2) + (lane * E + e) / 2], __NV_E2M1));
-                x[e] = __low2float(c) * s, x[e + 1] = __high2float(c) * s;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int64_t lo = before + incl - mine;
+        if (lo <= x && x < before + incl) {
+            const UnitLine u = line(b0 + lane);
+            const int64_t per_head = u.total();
+            int64_t r = x - lo;
+            const int g = (int)(r / per_head);
+            r -= g * per_head;
+            const int m = u.unit_at(r);
+            r -= u.before(m);
+            range->b = b0 + lane, range->g = g, range->m = m;
+            range->k = (int)min(stage_at(r, u.stage_weight(m)), (int64_t)u.stages(m));
+            range->at = x - r, range->end = range_begin(c + 1, W, C), range->W = W, range->C = (int)C;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// The stages of a piece in the order of their slots: K runs ahead of V by one stage, by two where two halves of one
+// tile take turns.
+struct AttnItems {
+    int k, v, ns, lead;
+    __device__ AttnItems(const AttnPiece& w) : k(0), v(0), ns(w.ns), lead(w.one ? 2 : 1) {}
+    __device__ __forceinline__ bool next(int& stage) {  // true: V
+        if (k < ns && k < v + lead) {
+            stage = k++;
+            return false;
+        }
+        stage = v++;
+        return true;
+    }
+};
+
+// ---- loads -----------------------------------------------------------------------------------------
+
+// Packed: K and V of each stage, a box of 128 tokens per 64-element panel.  The stage that reaches past its sequence
+// holds rows of the next one, or anything: its V rows there are zeroed (a weight of zero times NaN is NaN) before the
+// slot counts as full, so its box lands on a barrier that only this warp waits for.
+template <int D>
+__device__ __forceinline__ void at_load_packed(const AttnParams& p, const CUtensorMap* tk, const CUtensorMap* tv, uint8_t* base,
+                                               uint32_t base_s, const AttnBars<kAttnPacked, D>& bars,
+                                               volatile int32_t* abort_flag, int lane) {
+    using L = AttnLayout<kAttnPacked, D>;
+    if (lane == 0) {
+        prefetch_tensormap(tk);
+        prefetch_tensormap(tv);
+    }
+    PackedWalk walk(p, nullptr);
+    AttnPiece w;
+    int sc = 0, tails = 0;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+        AttnItems items(w);
+        for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
+            int j;
+            const bool is_v = items.next(j);
+            const int s = sc % L::kSlots;
+            if (!at_wait(bars.empty(s), ((sc / L::kSlots) & 1) ^ 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            const int key0 = (w.k0 + j) * kAttnKeys;
+            const uint32_t dst = L::kRingOff + s * L::kTileBytes;
+            const bool tail = is_v && key0 + kAttnKeys > w.len;
+            const uint32_t bar = tail ? bars.tail() : bars.full(s);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, (uint32_t)L::kTileBytes);
+#pragma unroll
+                for (int pn = 0; pn < L::kPanels; ++pn)
+                    tma_load_3d(base_s + dst + pn * L::kPanelBytes, is_v ? tv : tk, pn * 64, w.g, w.c0 + key0, bar);
+            }
+            __syncwarp();
+            if (tail) {
+                if (!at_wait(bar, tails & 1, abort_flag, p.status)) {
+                    mbar_wait(bar, tails & 1);  // (the box must land before the CTA ends)
+                    ok = false;
+                    break;
+                }
+                ++tails;
+                const int z0 = w.len - key0, nz = (kAttnKeys - z0) * 8;  // rows, then 16-byte chunks of a panel
+                for (int e = lane; e < nz * L::kPanels; e += 32) {
+                    const int pn = e >= nz ? 1 : 0, rem = e - pn * nz;
+                    *reinterpret_cast<uint4*>(base + dst + pn * L::kPanelBytes + z0 * 128 + rem * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.full(s));
+            }
+        }
+    }
+    // never leave the CTA with copies still landing in its shared memory
+    for (int kk = sc > L::kSlots ? sc - L::kSlots : 0; kk < sc; ++kk) mbar_wait(bars.full(kk % L::kSlots), (kk / L::kSlots) & 1);
+}
+
+// Packed: a piece's query tiles (3-D boxes of 64 elements x G heads x 128 / G tokens), once the last piece's Q K^T have
+// completed.  A warp of its own, so that keys and values run ahead into the next piece.
+template <int D>
+__device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUtensorMap* tq, uint32_t base_s,
+                                                 const AttnBars<kAttnPacked, D>& bars, volatile int32_t* abort_flag, int lane) {
+    using L = AttnLayout<kAttnPacked, D>;
+    if (lane == 0) prefetch_tensormap(tq);
+    const uint32_t tile_bytes = (uint32_t)(L::kPanels * p.group * p.tile_tokens * 128);
+    PackedWalk walk(p, nullptr);
+    AttnPiece w;
+    int pc = 0;
+    while (walk.next(p, w)) {
+        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) break;
+        if (lane == 0) {
+            const int tiles = w.one ? 1 : 2;
+            mbar_arrive_expect_tx(bars.q_full(), tile_bytes * tiles);
+            for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                for (int pn = 0; pn < L::kPanels; ++pn)
+                    tma_load_3d(base_s + t * L::kTileBytes + pn * L::kPanelBytes, tq, pn * 64, w.g * p.group,
+                                w.c0 + w.i0 + t * p.tile_tokens, bars.q_full());
+        }
+        __syncwarp();
+        ++pc;
+    }
+    if (pc > 0) mbar_wait(bars.q_full(), (pc - 1) & 1);
+}
+
+// Pools: the codes of each stage's blocks, one bulk copy a block (its rows of one KV head are contiguous).  The table
+// entry of the next item is fetched before the wait for a free slot.
+template <int SRC, int D>
+__device__ __forceinline__ void at_load_raw(const AttnParams& p, const void* range, uint32_t base_s, const AttnBars<SRC, D>& bars,
+                                            volatile int32_t* abort_flag, int lane) {
+    using L = AttnLayout<SRC, D>;
+    const int per = kAttnKeys >> p.bs_shift;                       // blocks per stage
+    const uint32_t bytes = (uint32_t)(L::kRawBytes / kAttnKeys) << p.bs_shift;  // of a block and head
+    RangeWalk walk(p, range);
+    AttnPiece w;
+    int sc = 0;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+        const int blocks = (w.len + (1 << p.bs_shift) - 1) >> p.bs_shift;
+        const int32_t* table = p.block_tables + (int64_t)w.b * p.max_blocks_per_seq;
+        AttnItems items(w);
+        int j, j_next = 0;
+        bool is_v, v_next = items.next(j_next);
+        auto entry = [&](int stage) {
+            const int e = (w.k0 + stage) * per + lane;
+            return lane < per && e < blocks ? __ldg(table + e) : 0;
+        };
+        int32_t id_next = entry(j_next);
+        for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
+            j = j_next, is_v = v_next;
+            int32_t id = id_next;
+            if (i + 1 < 2 * w.ns) {
+                v_next = items.next(j_next);
+                id_next = entry(j_next);
+            }
+            const int s = sc % L::kRaws;
+            if (!at_wait(bars.raw_empty(s), ((sc / L::kRaws) & 1) ^ 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+            }
+            const int have = min(per, blocks - (w.k0 + j) * per);
+            if (lane == 0) mbar_arrive_expect_tx(bars.raw_full(s), bytes * have);
+            __syncwarp();
+            if (lane < have) {
+                if (id < 0 || id >= p.num_blocks) {
+                    flag_status(p.status, PA_DEV_BAD_BLOCK_ID);
+                    id = 0;
+                }
+                bulk_load(base_s + L::kRawOff + s * L::kRawBytes + lane * bytes,
+                          (is_v ? p.v_pool : p.k_pool) + ((int64_t)id * p.num_kv_heads + w.g) * bytes, bytes, bars.raw_full(s));
+            }
+            __syncwarp();
+        }
+    }
+    for (int kk = sc > L::kRaws ? sc - L::kRaws : 0; kk < sc; ++kk) mbar_wait(bars.raw_full(kk % L::kRaws), (kk / L::kRaws) & 1);
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Pools: raw codes to f16 in the swizzled layout (128-byte rows of 64 elements, 16-byte chunk c of row r at c ^ (r & 7)).
+// Warp `part` of four takes 32 rows.  In each group of eight lanes the rows and chunks are chosen so that neither the
+// loads nor the stores meet in a bank.
+template <int SRC, int D>
+__device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint32_t base_s, const AttnBars<SRC, D>& bars,
+                                         volatile int32_t* abort_flag, int part, int lane) {
+    using L = AttnLayout<SRC, D>;
+    RangeWalk walk(p, range);
+    AttnPiece w;
+    int sc = 0;
+    const int l8 = lane & 7, l4 = lane >> 3;
+    while (walk.next(p, w)) {
+        AttnItems items(w);
+        for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
+            int j;
+            const bool is_v = items.next(j);
+            const int rs = sc % L::kRaws, fs = sc % L::kSlots;
+            if (!at_wait(bars.raw_full(rs), (sc / L::kRaws) & 1, abort_flag, p.status)) return;
+            if (!at_wait(bars.empty(fs), ((sc / L::kSlots) & 1) ^ 1, abort_flag, p.status)) return;
+            const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes, dst = base_s + L::kRingOff + fs * L::kTileBytes;
+            const int keep = is_v ? w.len - (w.k0 + j) * kAttnKeys : kAttnKeys;  // rows of the sequence
+            if constexpr (SRC == kAttnFp8) {
+                // eight lanes: two rows, four 16-byte chunks of each, the first half of one row and the second of the other
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r = 32 * part + 8 * (it >> 1) + 2 * l4 + (l8 >> 2), c = (((l8 >> 2) ^ (it & 1)) << 2) + (l8 & 3);
+                    const uint4 x = lds16(raw + r * 128 + c * 16);
+                    uint32_t h[8];
+                    e4m3x4_to_f16x2(x.x, h[0], h[1]);
+                    e4m3x4_to_f16x2(x.y, h[2], h[3]);
+                    e4m3x4_to_f16x2(x.z, h[4], h[5]);
+                    e4m3x4_to_f16x2(x.w, h[6], h[7]);
+                    if (r >= keep)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) h[e] = 0u;
+                    const uint32_t row = dst + (c >> 2) * L::kPanelBytes + r * 128, ch = 2 * (c & 3);
+                    sts16(row + ((ch ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    sts16(row + (((ch + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+                }
+            } else {
+                // eight lanes: four rows, two 16-byte chunks (32 codes) of each; at head_dim 128 two rows' first halves and
+                // two rows' second halves
+                constexpr int kIters = D / 32;
+#pragma unroll
+                for (int it = 0; it < kIters; ++it) {
+                    const int rr = l8 >> 1, pn = D == 128 ? (rr >> 1) ^ (it & 1) : 0;
+                    const int r = 32 * part + 16 * (D == 128 ? it >> 1 : it) + 4 * l4 + rr, half = l8 & 1;
+                    const int off = r & ((1 << p.bs_shift) - 1);
+                    const uint32_t rec = raw + (r >> p.bs_shift) * ((uint32_t)fp4_row_bytes(D) << p.bs_shift);
+                    const uint4 x = lds16(rec + off * (D / 2) + pn * 32 + half * 16);
+                    uint16_t sb;
+                    asm volatile("ld.shared.u16 %0, [%1];"
+                                 : "=h"(sb)
+                                 : "r"(rec + ((D / 2) << p.bs_shift) + off * (D / 16) + pn * 4 + half * 2)
+                                 : "memory");
+                    const uint32_t sc2 = e4m3x2_to_f16x2(sb), s0 = f16x2_low_twice(sc2), s1 = f16x2_high_twice(sc2);
+                    const uint32_t row = dst + pn * L::kPanelBytes + r * 128;
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t h[4];
+                        e2m1x8_to_f16x2(xs[e], h);
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) h[f] = r < keep ? mul_f16x2(h[f], e < 2 ? s0 : s1) : 0u;
+                        sts16(row + (((4 * half + e) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bars.raw_empty(rs));
+                mbar_arrive(bars.full(fs));
             }
         }
     }
 }
 
+// Pools: a piece's query rows as f16, each scaled by a power of two so that its largest element lies in [1, 2), and the
+// inverse factors.  Warp `part` of two.  Rows of no token are left as they are: they reach no other row.
 template <int SRC, int D>
-__global__ void __launch_bounds__(256) attn_kernel(const AttnParams p) {
-    constexpr int E = D / 32;
-    const int b = blockIdx.y, i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = p.cu_q_lens[b], n = p.cu_q_lens[b + 1] - c0;
-    const int len = SRC == kAttnPacked ? n : p.seq_lens[b];
-    if (n == 0) return;
-    if (n < 0 || n > len || n > p.max_q_len || c0 < 0 || (int64_t)c0 + n > p.num_q_tokens ||
-        (SRC != kAttnPacked && (int64_t)len > ((int64_t)p.max_blocks_per_seq << p.bs_shift))) {
-        if (i == 0 && threadIdx.x == 0) flag_status(p.status, PA_DEV_BAD_SEQ_LEN);
-        return;
-    }
-    if (i >= n) return;
-    const int G = p.num_q_heads / p.num_kv_heads, pos = len - n + i;
-    for (int h = warp; h < p.num_q_heads; h += 8) {
-        float q[E], o[E], m = -INFINITY, l = 0.f;
-        for (int e = 0; e < E; ++e) {
-            q[e] = __uint_as_float((uint32_t)p.q[(int64_t)(c0 + i) * p.q_stride + h * D + lane * E + e] << 16);
-            o[e] = 0.f;
+__device__ __forceinline__ void at_load_q_pools(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s,
+                                                const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int part, int lane) {
+    using L = AttnLayout<SRC, D>;
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 4;  // lanes per row, rows at a time, loads in flight
+    const int sub = lane / kLanes, c = lane % kLanes;
+    const int G = p.group, T = p.tile_tokens;
+    RangeWalk walk(p, range);
+    AttnPiece w;
+    int pc = 0;
+    while (walk.next(p, w)) {
+        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) return;
+        float* factors = reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256;
+        const int tokens = min(w.n - w.i0, w.one ? T : 2 * T);
+        for (int t = 0; t < 2 && t * T < tokens; ++t) {
+            const int rows = min(T, tokens - t * T) * G;
+            const uint16_t* src = p.q + (int64_t)(w.c0 + w.i0 + t * T) * p.num_q_heads * D;
+            for (int r0 = part * kRowsAt * kBatch; r0 < rows; r0 += 2 * kRowsAt * kBatch) {
+                uint4 x[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = r0 + u * kRowsAt + sub, tok = r / G;
+                    x[u] = r < rows ? *reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.num_q_heads + w.g * G + (r - tok * G)) * D + c * 8)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = r0 + u * kRowsAt + sub;
+                    const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                    uint32_t top = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, xs[e] & 0x7fff7fffu);
+#pragma unroll
+                    for (int o = 1; o < kLanes; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const uint32_t e2 = min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u);  // its exponent
+                    const float inv = __uint_as_float((254u - e2) << 23);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
+                    if (r < rows) {
+                        sts16(base_s + t * L::kTileBytes + (c >> 3) * L::kPanelBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1],
+                              h[2], h[3]);
+                        if (c == 0) factors[t * 128 + r] = __uint_as_float(e2 << 23);
+                    }
+                }
+            }
         }
-        for (int t = 0; t <= pos; ++t) {
-            float x[E], s = 0.f;
-            attn_row<SRC, D>(p, false, b, c0, t, h / G, lane, x);
-            for (int e = 0; e < E; ++e) s += q[e] * x[e];
-            for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            s *= p.scale_log2;
-            const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-            m = mn, l = l * f + w;
-            attn_row<SRC, D>(p, true, b, c0, t, h / G, lane, x);
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * x[e];
-        }
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(c0 + i) * p.num_q_heads + h) * D + lane * E;
-        for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16(o[e] / l * p.out_scale);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.q_full());
+        ++pc;
     }
 }
 
+// ---- MMA -------------------------------------------------------------------------------------------
 template <int SRC, int D>
-pa_status launch_attn(const AttnParams& p, cudaStream_t st) {
-    attn_kernel<SRC, D><<<dim3(p.max_q_len, p.num_seqs), 256, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+__device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, uint32_t base_s, uint32_t tmem,
+                                       const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int lane) {
+    using L = AttnLayout<SRC, D>;
+    constexpr int NS = L::kSlots;
+    constexpr int kBf16 = SRC == kAttnPacked ? 1 : 0;
+    constexpr uint32_t idesc_s = umma_idesc_16(kAtRows, kAttnKeys, 0, 0, kBf16);  // Q (K-major) x K^T (K-major)
+    constexpr uint32_t idesc_o = umma_idesc_16(kAtRows, D, 0, 1, kBf16);          // P (TMEM) x V (MN-major)
+    const uint32_t q_lo = (uint32_t)umma_smem_desc(base_s, 16, 1024);
+    const uint32_t k_lo = (uint32_t)umma_smem_desc(base_s + L::kRingOff, 16, 1024);
+    const uint32_t v_lo = (uint32_t)umma_smem_desc(base_s + L::kRingOff, L::kPanelBytes, 1024);
+    constexpr uint32_t hi = (uint32_t)(umma_smem_desc(0, 0, 1024) >> 32);
+    // S of half t = Q tile `tile` x K^T
+    auto issue_s = [&](int t, int tile, int slot) {
+        const uint32_t qa = q_lo + (uint32_t)(tile * (L::kTileBytes >> 4)), kb = k_lo + (uint32_t)(slot * (L::kTileBytes >> 4));
+        const uint32_t d = tmem + kAtTmemHalf * t;
+        at_static_for<D / 16>([&](auto ks_c) {  // 16 elements: 32 bytes along a 128-byte row, 64-element panels further apart
+            constexpr int ks = decltype(ks_c)::value;
+            constexpr uint32_t o = ((ks >> 2) * L::kPanelBytes + (ks & 3) * 32) >> 4;
+            umma_bf16_lo<o, o>(d, qa, kb, hi, idesc_s, ks > 0 ? 1u : 0u);
+        });
+        umma_commit(bars.s_full(t));
+    };
+    // O of half t += P V over keys 64 h .. 64 h + 63 of the stage
+    auto issue_o = [&](int t, int slot, auto h_c, bool begin) {
+        constexpr int h = decltype(h_c)::value;
+        const uint32_t vb = v_lo + (uint32_t)(slot * (L::kTileBytes >> 4)), d = tmem + kAtTmemHalf * t;
+        const uint32_t acc0 = begin ? 0u : 1u;
+        at_static_for<4>([&](auto kk_c) {
+            constexpr int kk = 4 * h + decltype(kk_c)::value;  // 16 keys: 16 rows of 128 bytes, in units of 16
+            umma_bf16_tmem_a_lo<kk * 128>(d + kAtTmemO, d + kk * 8, vb, hi, idesc_o, kk > 0 ? 1u : acc0);
+        });
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
+    AttnWalk<SRC> walk(p, range);
+    AttnPiece w;
+    int sc = 0, pc = 0, ck0 = 0, ck1 = 0;  // slots, pieces, stages of half 0 and of half 1
+    bool ok = true;
+    while (__shfl_sync(0xffffffffu, (int)ok, 0) && walk.next(p, w)) {
+        if (lane == 0) {
+            auto filled = [&](int c) { return at_wait1(bars.full(c % NS), (c / NS) & 1, abort_flag, p.status); };
+            auto times_v = [&](int t, int slot, bool begin) {
+                int& ck = t ? ck1 : ck0;
+                if (!at_wait1(bars.p_first(t), ck & 1, abort_flag, p.status)) return false;
+                tc_fence_after();
+                issue_o(t, slot, First{}, begin);
+                if (!at_wait1(bars.p_second(t), ck & 1, abort_flag, p.status)) return false;
+                tc_fence_after();
+                issue_o(t, slot, Second{}, begin);
+                ++ck;
+                return true;
+            };
+            ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
+            if (!w.one) {
+                const int a = sc++;
+                ok = ok && filled(a);
+                if (ok) {
+                    tc_fence_after();
+                    if (w.n0 > 0) issue_s(0, 0, a % NS);
+                    issue_s(1, 1, a % NS);
+                    umma_commit(bars.empty(a % NS));
+                    if (w.ns == 1) umma_commit(bars.q_empty());
+                }
+                for (int k = 0; ok && k < w.ns; ++k) {
+                    const int vs = sc++, kn = k + 1 < w.ns ? sc++ : -1;
+                    ok = filled(vs);
+                    bool k_ready = false;
+                    for (int t = 0; ok && t < 2; ++t) {
+                        const int nt = t ? w.ns : w.n0;
+                        if (k >= nt) continue;
+                        ok = times_v(t, vs % NS, k == 0);
+                        if (!ok) break;
+                        if (k + 1 == nt) {
+                            umma_commit(bars.o_final(t));
+                        } else {
+                            if (!k_ready) ok = filled(kn);
+                            k_ready = true;
+                            if (ok) issue_s(t, t, kn % NS);
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit(bars.empty(vs % NS));
+                    if (kn >= 0) {
+                        umma_commit(bars.empty(kn % NS));
+                        if (k + 2 == w.ns) umma_commit(bars.q_empty());  // the piece's last Q K^T were just issued
+                    }
+                }
+            } else {
+                for (int t = 0; ok && t < 2 && t < w.ns; ++t) {
+                    const int a = sc++;
+                    ok = filled(a);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(t, 0, a % NS);
+                    umma_commit(bars.empty(a % NS));
+                }
+                if (ok && w.ns <= 2) umma_commit(bars.q_empty());
+                for (int k = 0; ok && k < w.ns; ++k) {
+                    const int t = k & 1, vs = sc++, kn = k + 2 < w.ns ? sc++ : -1;
+                    ok = filled(vs) && times_v(t, vs % NS, k < 2);
+                    if (!ok) break;
+                    umma_commit(bars.empty(vs % NS));
+                    if (kn < 0) {
+                        umma_commit(bars.o_final(t));
+                    } else {
+                        ok = filled(kn);
+                        if (!ok) break;
+                        issue_s(t, 0, kn % NS);
+                        umma_commit(bars.empty(kn % NS));
+                        if (k + 3 == w.ns) umma_commit(bars.q_empty());
+                    }
+                }
+            }
+            ++pc;
+        }
+        __syncwarp();
+    }
+    // every MMA issued has completed before the CTA may free TMEM or its shared memory
+    if (lane == 0) {
+        umma_commit(bars.drain());
+        mbar_wait(bars.drain(), 0);
+    }
+    __syncwarp();
+}
+
+// ---- softmax ---------------------------------------------------------------------------------------
+
+// 32 fp32 values as 32 bf16 at dst.
+__device__ __forceinline__ void at_store_bf16(uint16_t* dst, const float* x, bool align32) {
+    uint32_t v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+    if (align32) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * e), "r"(v[8 * e]),
+                         "r"(v[8 * e + 1]), "r"(v[8 * e + 2]), "r"(v[8 * e + 3]), "r"(v[8 * e + 4]), "r"(v[8 * e + 5]),
+                         "r"(v[8 * e + 6]), "r"(v[8 * e + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4*>(dst)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+    }
+}
+
+// Pools: the pieces of tile t of a cut unit, stored by CTAs a .. b, joined into out by one half's 128 threads:
+//     out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,   M = max_c m_c,
+// in the CTAs' order, so that the result does not depend on which of them ended last.
+template <int SRC, int D, class Meet>
+__device__ __forceinline__ bool at_join(const AttnParams& p, const AttnPiece& w, int t, int rows, int a, int b, float2* join,
+                                        int thread, Meet meet) {
+    auto slot = [&](int c) { return (int64_t)(2 * c + (c == a ? 1 : 0)) * p.part_tiles + t; };  // (a holds the unit's beginning)
+    if (thread < rows) {
+        float M = -INFINITY, L = 0.f;
+        for (int c = a; c <= b; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot(c) * kAtRows + thread).x);
+        for (int c = a; c <= b; ++c) {
+            const float2 ml = __ldcg(p.part_ml + slot(c) * kAtRows + thread);
+            if (ml.x > -INFINITY) L += ml.y * at_exp2(ml.x - M);
+        }
+        join[thread] = make_float2(M, p.out_scale / L);
+    }
+    if (!meet()) return false;
+    constexpr int kLanes = D / 4, kAt = 128 / kLanes, kBatch = 4;  // lanes per row, rows at a time, rows in flight
+    const int sub = thread / kLanes, e = thread % kLanes * 4;
+    const int64_t first_row = (int64_t)w.c0 + w.i0 + t * p.tile_tokens;
+    for (int r0 = 0; r0 < rows; r0 += kAt * kBatch) {
+        float4 acc[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = a; c <= b; ++c) {
+            const int64_t s = slot(c) * kAtRows;
+            float4 o[kBatch];
+            float m[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int r = min(r0 + u * kAt + sub, rows - 1);
+                m[u] = __ldcg(p.part_ml + s + r).x;
+                o[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (s + r) * D + e));
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const float2 j = join[min(r0 + u * kAt + sub, rows - 1)];
+                const float f = at_exp2(m[u] - j.x) * j.y;
+                if (m[u] > -INFINITY) {  // (a piece that sees none of the row's keys has stored no O)
+                    acc[u].x += f * o[u].x, acc[u].y += f * o[u].y, acc[u].z += f * o[u].z, acc[u].w += f * o[u].w;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kAt + sub;
+            if (r >= rows) continue;
+            const int tok = r / p.group;
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + ((first_row + tok) * p.num_q_heads + (int64_t)w.g * p.group + (r - tok * p.group)) * D;
+            *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(acc[u].x, acc[u].y), pack_bf16x2(acc[u].z, acc[u].w));
+        }
+    }
+    return true;  // (join is written again behind a later piece's meeting)
+}
+
+// Half t: warps 4 t .. 4 t + 3, row r = 32 (warp % 4) + lane = TMEM lane r.
+template <int SRC, int D>
+__device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange* range, int t, uint8_t* base, uint32_t tmem,
+                                           const AttnBars<SRC, D>& bars, volatile int32_t* misc, int warp, int lane) {
+    using L = AttnLayout<SRC, D>;
+    volatile int32_t* abort_flag = misc;
+    const int G = p.group, Hq = p.num_q_heads, T = p.tile_tokens;
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), row_tmem = lanes + kAtTmemHalf * t;
+    float2* odd_ml = reinterpret_cast<float2*>(base + L::kMlOff);
+    float c = p.scale_log2;  // > 0 (checked on the host)
+    int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0, met = 0;  // stages, pieces, final O of each half, odd halves handed over
+    auto meet = [&]() {  // the half's four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.join(t));
+        return at_wait(bars.join(t), met++ & 1, abort_flag, p.status);
+    };
+    AttnWalk<SRC> walk(p, range);
+    AttnPiece w;
+    while (walk.next(p, w)) {
+        const int mine = w.one ? (t ? w.ns / 2 : (w.ns + 1) / 2) : (t ? w.ns : w.n0);
+        const bool other = w.one && w.ns > 1;  // both halves work on the one tile
+        const int tile = w.one ? 0 : t;
+        const int i0 = w.i0 + tile * T, i1 = min(w.n, i0 + T);
+        const int tok = i0 + r / G;
+        const bool valid = r < T * G && tok < i1;
+        const int pos = w.len - w.n + (valid ? tok : i1 - 1);
+        const int kend = w.len - w.n + i1;  // keys that the tile's last row sees
+        float m_raw = -INFINITY, l_run = 0.f;  // maximum of the raw scores, and the weights' sum
+        for (int i = 0; i < mine; ++i, ++ck) {
+            const int k = w.k0 + (w.one ? 2 * i + t : i);
+            if (!at_wait(bars.s_full(t), ck & 1, abort_flag, p.status)) return;
+            tc_fence_after();
+            if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
+                if (i == 0 && valid) c = p.scale_log2 * reinterpret_cast<const volatile float*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
+            }
+            // This S was issued after the last P V of this half and completes after it: O is up to date, and no MMA
+            // touches this half's TMEM until this warp arrives on p_first.
+            const int key0 = k * kAttnKeys;
+            const int nq = min(4, (kend - key0 + 31) >> 5);  // quarters that some row of the tile sees
+            uint32_t sv[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(row_tmem + 32 * q, sv[q]);
+            tmem_wait_ld();
+            if (key0 + kAttnKeys - 1 > pos) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (key0 + 32 * q + e > pos) sv[q][e] = __float_as_uint(-INFINITY);
+            }
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    mx0 = fmax3(mx0, __uint_as_float(sv[q][e]), __uint_as_float(sv[q][e + 1]));
+                    mx1 = fmax3(mx1, __uint_as_float(sv[q][e + 2]), __uint_as_float(sv[q][e + 3]));
+                }
+            const float m_new = fmaxf(m_raw, fmaxf(mx0, mx1));
+            if (i == 0) {
+                m_raw = m_new;
+            } else {
+                const bool need = (m_new - m_raw) * c > kAtRescaleLog2;
+                if (__any_sync(0xffffffffu, need)) {
+                    const float f = need ? at_exp2((m_raw - m_new) * c) : 1.f;
+#pragma unroll
+                    for (int c0o = 0; c0o < D; c0o += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(row_tmem + kAtTmemO + c0o, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                        tmem_st32(row_tmem + kAtTmemO + c0o, ov);
+                    }
+                    if (need) {
+                        l_run *= f;
+                        m_raw = m_new;
+                    }
+                }
+            }
+            // P = 2^(c s - c m) (over pools 2^7 of it) in pairs over the first 64 columns of S, whose scores are in registers.
+            // A row that has seen no key yet weighs all of them 0.
+            const float mc = m_raw > -INFINITY ? m_raw * c : 0.f;
+            const float shift = SRC == kAttnPacked ? -mc : kAtWeightLog2 - mc;
+            const uint64_t c2 = f2_pack(c, c), sh2 = f2_pack(shift, shift);
+            uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q >= nq) {  // past the tile's last position
+                    const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                    tmem_st16(row_tmem + 16 * q, z);
+                } else {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[q][2 * e]), __uint_as_float(sv[q][2 * e + 1])), c2, sh2), x0, x1);
+                        x0 = at_exp2(x0);
+                        x1 = at_exp2(x1);
+                        sum2 = f2_add(sum2, f2_pack(x0, x1));
+                        pw[e] = SRC == kAttnPacked ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                    }
+                    tmem_st16(row_tmem + 16 * q, pw);
+                }
+                if (q == 1 || q == 3) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q == 1 ? bars.p_first(t) : bars.p_second(t));
+                }
+            }
+            float sa, sb;
+            f2_unpack(sum2, sa, sb);
+            l_run += sa + sb;
+        }
+        float m = m_raw > -INFINITY ? m_raw * c : -INFINITY;  // base 2
+        ++pc;
+        if (w.one && t == 1) {
+            if (mine > 0) {
+                odd_ml[r] = make_float2(m, l_run);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.odd_ml());
+                if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
+                ++hand, ++oc1;
+            }
+            continue;
+        }
+        // ---- O / l to out, or O, m and l to the join ----
+        const bool whole = w.first && w.last;
+        float f0 = 1.f, f1 = 0.f;
+        if (mine > 0) {
+            int& oc = t ? oc1 : oc0;
+            if (!at_wait(bars.o_final(t), oc & 1, abort_flag, p.status)) return;
+            ++oc;
+        }
+        if (t == 0 && !w.one) ++oc1;
+        if (other) {
+            if (!at_wait(bars.o_final(1), oc1 & 1, abort_flag, p.status)) return;
+            if (!at_wait(bars.odd_ml(), hand & 1, abort_flag, p.status)) return;
+            ++oc1, ++hand;
+            const float2 o = odd_ml[r];
+            const float top = fmaxf(m, o.x);
+            f0 = m > -INFINITY ? at_exp2(m - top) : 0.f;
+            f1 = o.x > -INFINITY ? at_exp2(o.x - top) : 0.f;
+            l_run = l_run * f0 + o.y * f1;
+            m = top;
+        }
+        tc_fence_after();
+        const int64_t row = ((int64_t)(w.c0 + (valid ? tok : i0)) * Hq + (int64_t)w.g * G + r % G) * D;
+        const int64_t part = SRC == kAttnPacked ? 0 : ((int64_t)(2 * blockIdx.x + (w.first ? 1 : 0)) * p.part_tiles + tile) * kAtRows + r;
+        if (mine > 0) {
+            const float inv = whole ? p.out_scale / l_run : 1.f;
+            f0 *= inv, f1 *= inv;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                uint32_t ov[32];
+                float x[32];
+                tmem_ld32(row_tmem + kAtTmemO + 32 * q, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]) * f0;
+                if (other) {
+                    tmem_ld32(lanes + kAtTmemHalf + kAtTmemO + 32 * q, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] += __uint_as_float(ov[e]) * f1;
+                }
+                if (!valid) continue;
+                if (whole) {
+                    at_store_bf16(static_cast<uint16_t*>(p.out) + row + 32 * q, x, p.out_align32);
+                } else if constexpr (SRC != kAttnPacked) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * q);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+                }
+            }
+        }
+        tc_fence_before();  // the O reads are ordered before this warp's next arrival
+        if (other) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.odd_read());
+        }
+        if constexpr (SRC != kAttnPacked) {
+            if (!whole) {
+                if (valid) __stcg(p.part_ml + part, make_float2(m, l_run));
+                const int wt = w.one ? kOneTile : kTwoTiles;
+                const int a = (int)range_of(w.at, range->W, range->C);
+                const int b = (int)range_of(w.at + stage_begin(w.nst - 1, wt), range->W, range->C);
+                __threadfence();
+                if (!meet()) return;
+                if (r == 0) {
+                    int32_t* count = p.counts + 2 * a + tile;
+                    const bool last = atomicAdd(count, 1) == b - a;
+                    if (last) *count = 0;  // for the next call
+                    misc[4 + t] = last;
+                }
+                if (!meet()) return;
+                if (misc[4 + t]) {
+                    __threadfence();
+                    float2* join = reinterpret_cast<float2*>(base + L::kJoinOff) + t * 128;
+                    if (!at_join<SRC, D>(p, w, tile, (i1 - i0) * G, a, b, join, r, meet)) return;
+                }
+            }
+        }
+    }
+}
+
+// ---- kernel ----------------------------------------------------------------------------------------
+template <int SRC, int D>
+__global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
+    attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v) {
+    using L = AttnLayout<SRC, D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_s - raw_s);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int32_t* misc = reinterpret_cast<volatile int32_t*>(base + L::kMiscOff);  // abort flag; TMEM address; join flags
+    AttnRange* range = reinterpret_cast<AttnRange*>(base + L::kMiscOff + 32);
+    AttnBars<SRC, D> bars{base_s + L::kBarOff};
+    if (tid == 0) {
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(bars.full(s), L::kPools ? 4 : 1);  // each widening warp, or the producer's expect_tx
+            mbar_init(bars.empty(s), 1);                 // tcgen05.commit after the slot's last MMA
+        }
+        for (int s = 0; s < L::kRaws; ++s) {
+            mbar_init(bars.raw_full(s), 1);
+            mbar_init(bars.raw_empty(s), 4);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bars.s_full(t), 1);
+            mbar_init(bars.p_first(t), 4);
+            mbar_init(bars.p_second(t), 4);
+            mbar_init(bars.o_final(t), 1);
+        }
+        mbar_init(bars.q_full(), L::kPools ? 2 : 1);
+        mbar_init(bars.q_empty(), 1);
+        mbar_init(bars.drain(), 1);
+        mbar_init(bars.tail(), 1);
+        mbar_init(bars.odd_ml(), 4);
+        mbar_init(bars.odd_read(), 4);
+        for (int t = 0; t < 2; ++t) mbar_init(bars.join(t), 4);
+        fence_barrier_init();
+        misc[0] = 0;
+    }
+    if (warp == kAtMmaWarp) tmem_alloc(base_s + L::kMiscOff + 8, kAtTmemCols);
+    pdl_wait_prerequisites();
+    if constexpr (L::kPools) {
+        if (warp == kAtKvWarp) at_plan(p, range, lane);
+    }
+    if (blockIdx.x == 0 && warp == kAtQWarp) {
+        for (int b = lane; b < p.num_seqs; b += 32) {
+            int c0, len;
+            bool bad;
+            at_sequence<SRC>(p, b, c0, len, &bad);
+            if (bad) flag_status(p.status, PA_DEV_BAD_SEQ_LEN);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::kMiscOff + 8);
+    // Registers, of the launch's (packed 384 x 168, pools 512 x 128): two softmax warpgroups, loads and MMA, widening:
+    // packed 2 x 224 + 56 = 3 x 168, pools 2 x 192 + 48 + 80 = 4 x 128.
+    if (L::kPools && warp >= kAtWidenWarp) {
+        if constexpr (L::kPools) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+            at_widen<SRC, D>(p, range, base_s, bars, misc, warp - kAtWidenWarp, lane);
+        }
+    } else if (warp >= 8) {
+        if constexpr (L::kPools)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+        if (warp == kAtMmaWarp) {
+            at_mma<SRC, D>(p, range, base_s, tmem, bars, misc, lane);
+        } else if constexpr (L::kPools) {
+            if (warp == kAtKvWarp)
+                at_load_raw<SRC, D>(p, range, base_s, bars, misc, lane);
+            else
+                at_load_q_pools<SRC, D>(p, range, base, base_s, bars, misc, warp - kAtQWarp, lane);
+        } else {
+            if (warp == kAtKvWarp)
+                at_load_packed<D>(p, &tmap_k, &tmap_v, base, base_s, bars, misc, lane);
+            else if (warp == kAtQWarp)
+                at_load_q_packed<D>(p, &tmap_q, base_s, bars, misc, lane);
+        }
+    } else {
+        if constexpr (L::kPools)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+        at_softmax<SRC, D>(p, range, warp >> 2, base, tmem, bars, misc, warp, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kAtMmaWarp) tmem_dealloc(tmem, kAtTmemCols);
 }
 
 bool aligned_to(const void* ptr, unsigned bytes) { return (reinterpret_cast<uintptr_t>(ptr) & (bytes - 1)) == 0; }
+
+// One CTA per SM.
+template <int SRC, int D>
+pa_status launch_attn(const AttnParams& p, int dev, int grid, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                      cudaStream_t st) {
+    using L = AttnLayout<SRC, D>;
+    int occ = 0;
+    if (!kernel_occupancy(dev, reinterpret_cast<const void*>(&attn_kernel<SRC, D>), L::kThreads, L::kBytes, &occ)) return PA_ERR_CUDA;
+    if (occ <= 0) return PA_ERR_UNSUPPORTED;
+    // the roles' register shares (see the kernel) draw on what the launch gives: less would wait for ever
+    static const int regs = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(&attn_kernel<SRC, D>)) == cudaSuccess ? a.numRegs : 0;
+    }();
+    if (regs != (L::kPools ? 128 : 168)) return PA_ERR_INTERNAL;
+    return launch_dependent(&attn_kernel<SRC, D>, dim3(grid), L::kThreads, L::kBytes, st, p, tq, tk, tv) == cudaSuccess ? PA_OK
+                                                                                                                   : PA_ERR_CUDA;
+}
 
 }  // namespace
 }  // namespace pa

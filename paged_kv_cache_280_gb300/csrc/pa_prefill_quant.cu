@@ -1,10 +1,28 @@
 // Chunk attention over FP8 and 4-bit pools: entry points and checks; the kernel in pa_attn.cuh.
 #include <cmath>
+#include <cstring>
 
 #include "pa_attn.cuh"
 
 namespace pa {
 namespace {
+
+// The status head, a count per CTA and tile, then two slots per CTA for pieces of cut units: a maximum and a sum per row,
+// and the rows.
+struct PrefillWorkspace {
+    size_t counts, ml, o, total;
+    int tiles;
+};
+PrefillWorkspace prefill_workspace(int max_q_len, int group, int head_dim, int sms) {
+    PrefillWorkspace w;
+    w.tiles = max_q_len > kAtRows / group ? 2 : 1;
+    w.counts = kStatusHeadBytes;
+    w.ml = w.counts + (((size_t)2 * sms * sizeof(int32_t) + 255) & ~(size_t)255);
+    const size_t rows = (size_t)2 * sms * w.tiles * kAtRows;
+    w.o = w.ml + rows * sizeof(float2);
+    w.total = w.o + rows * head_dim * sizeof(float);
+    return w;
+}
 
 pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void* v_pool, float k_scale, float v_scale,
                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
@@ -25,24 +43,33 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
         return PA_ERR_INVALID_ARG;
     const float scale_log2 = scale * k_scale * 1.4426950408889634f;
     if (!std::isfinite(scale_log2) || !(scale_log2 > 0.f)) return PA_ERR_INVALID_ARG;
-    size_t need = 0;
-    const pa_status s = pa_prefill_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim, &need);
-    if (s != PA_OK) return s;
-    if (workspace_bytes < need) return PA_ERR_WORKSPACE_TOO_SMALL;
+    int dev = 0, sms = 0;
+    if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
+    const int group = num_q_heads / num_kv_heads;
+    const PrefillWorkspace ws = prefill_workspace(max_q_len, group, head_dim, sms);
+    if (workspace_bytes < ws.total) return PA_ERR_WORKSPACE_TOO_SMALL;
     AttnParams p = {};
     p.out = out;
-    p.q = static_cast<const uint16_t*>(q), p.q_stride = (int64_t)num_q_heads * head_dim;
+    p.q = static_cast<const uint16_t*>(q);
     p.k_pool = static_cast<const uint8_t*>(k_pool), p.v_pool = static_cast<const uint8_t*>(v_pool);
     p.block_tables = block_tables, p.seq_lens = seq_lens, p.cu_q_lens = cu_q_lens;
-    p.status = static_cast<int32_t*>(workspace);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    p.status = reinterpret_cast<int32_t*>(base);
+    p.counts = reinterpret_cast<int32_t*>(base + ws.counts);
+    p.part_ml = reinterpret_cast<float2*>(base + ws.ml), p.part_o = reinterpret_cast<float*>(base + ws.o);
+    p.part_tiles = ws.tiles;
     p.max_blocks_per_seq = max_blocks_per_seq, p.num_seqs = num_seqs, p.num_q_heads = num_q_heads;
-    p.num_kv_heads = num_kv_heads, p.num_blocks = num_blocks, p.num_q_tokens = num_q_tokens;
-    p.max_q_len = max_q_len < num_q_tokens ? max_q_len : num_q_tokens;
+    p.num_kv_heads = num_kv_heads, p.num_blocks = num_blocks, p.num_q_tokens = num_q_tokens, p.max_q_len = max_q_len;
     p.bs_shift = block_size == 16 ? 4 : 5;
+    p.group = group, p.tile_tokens = kAtRows / group;
+    p.out_align32 = aligned_to(out, 32) ? 1 : 0;
     p.scale_log2 = scale_log2, p.out_scale = v_scale;
+    CUtensorMap none;  // not read: the codes come by bulk copies
+    memset(&none, 0, sizeof none);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!fp4) return launch_attn<kAttnFp8, 128>(p, st);
-    return head_dim == 128 ? launch_attn<kAttnFp4, 128>(p, st) : launch_attn<kAttnFp4, 64>(p, st);
+    if (!fp4) return launch_attn<kAttnFp8, 128>(p, dev, sms, none, none, none, st);
+    return head_dim == 128 ? launch_attn<kAttnFp4, 128>(p, dev, sms, none, none, none, st)
+                           : launch_attn<kAttnFp4, 64>(p, dev, sms, none, none, none, st);
 }
 
 }  // namespace
@@ -52,7 +79,10 @@ extern "C" pa_status pa_prefill_workspace_bytes(int32_t max_q_len, int32_t num_q
                                                 int32_t head_dim, size_t* bytes_out) {
     if (!bytes_out || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || head_dim <= 0)
         return PA_ERR_INVALID_ARG;
-    *bytes_out = pa::kStatusHeadBytes;
+    if (num_q_heads / num_kv_heads > 8) return PA_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    if (!pa::current_device(&dev, &sms)) return PA_ERR_CUDA;
+    *bytes_out = pa::prefill_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, sms).total;
     return PA_OK;
 }
 

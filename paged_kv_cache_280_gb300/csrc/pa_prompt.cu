@@ -24,14 +24,27 @@ extern "C" pa_status pa_prompt_attention(void* out, const void* q, int64_t q_str
     if (!aligned_to(out, 16) || !aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(cu_lens, 4) ||
         !aligned_to(dev_status, 4))
         return PA_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (!current_device(&dev, &sms)) return PA_ERR_CUDA;
     AttnParams p = {};
     p.out = out;
-    p.q = static_cast<const uint16_t*>(q), p.k = static_cast<const uint16_t*>(k), p.v = static_cast<const uint16_t*>(v);
-    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
     p.cu_q_lens = cu_lens, p.status = dev_status;
     p.num_seqs = num_seqs, p.num_q_heads = num_q_heads, p.num_kv_heads = num_kv_heads;
     p.num_q_tokens = num_tokens, p.max_q_len = max_len < num_tokens ? max_len : num_tokens;
+    p.group = num_q_heads / num_kv_heads, p.tile_tokens = kAtRows / p.group;
+    p.out_align32 = aligned_to(out, 32) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f, p.out_scale = 1.f;
+    if (!std::isfinite(p.scale_log2) || !(p.scale_log2 > 0.f)) return PA_ERR_INVALID_ARG;
+    CUtensorMap tq, tk, tv;
+    if (!rows_map(&tq, q, num_tokens, num_q_heads, head_dim, q_stride, p.group, p.tile_tokens) ||
+        !rows_map(&tk, k, num_tokens, num_kv_heads, head_dim, k_stride, 1, kAttnKeys) ||
+        !rows_map(&tv, v, num_tokens, num_kv_heads, head_dim, v_stride, 1, kAttnKeys))
+        return PA_ERR_CUDA;
+    // a CTA per unit where there are fewer than SMs
+    const int64_t units = (int64_t)((p.max_q_len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens)) * num_seqs * num_kv_heads;
+    if (units >= INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+    const int grid = (int)(units < sms ? units : sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return head_dim == 128 ? launch_attn<kAttnPacked, 128>(p, st) : launch_attn<kAttnPacked, 64>(p, st);
+    return head_dim == 128 ? launch_attn<kAttnPacked, 128>(p, dev, grid, tq, tk, tv, st)
+                           : launch_attn<kAttnPacked, 64>(p, dev, grid, tq, tk, tv, st);
 }

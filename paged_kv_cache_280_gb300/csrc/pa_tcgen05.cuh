@@ -42,6 +42,11 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, int a_mn, i
            | ((uint32_t)(M >> 4) << 24);      // M / 16
 }
 
+// The same for bf16 (bf16 = 1) or f16 (0) operands.
+__host__ __device__ constexpr uint32_t umma_idesc_16(int M, int N, int a_mn, int b_mn, int bf16) {
+    return umma_idesc_bf16(M, N, a_mn, b_mn) & ~(bf16 ? 0u : (1u << 7) | (1u << 10));
+}
+
 // ---- TMEM allocation (warp-collective) ---------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t slot_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols)

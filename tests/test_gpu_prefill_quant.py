@@ -84,7 +84,7 @@ class Case:
         if rows is not None:
             g, want, bound = g[rows], want[rows], bound[rows]
         assert np.all(np.isfinite(g))
-        err, limit = np.abs(g - want), bound + 2.0 ** -8 * (np.abs(want) + bound)
+        err, limit = np.abs(g - want), bound + 2.0 ** -8 * (np.abs(want) + bound) + 1e-30
         worst = np.unravel_index(np.argmax(err / limit), err.shape)
         assert np.all(err <= limit), f"max |err| {err.max():.3e}, {(err / limit).max():.2f} of the bound at {worst}"
 
@@ -108,6 +108,16 @@ def test_chunks_ragged(kind, d, hq, hkv, bs):
                                               ([2500, 2500], [300, 40], 4, 4), ([20000], [17], 4, 1)])
 def test_chunks_split_over_long_contexts(kind, d, lens, news, hq, hkv):
     c = Case(200 + sum(lens) % 97 + d, kind, lens, news, hq, hkv, d, 16)
+    c.check(c.run())
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+def test_many_sequences(kind, d):
+    """More sequences than a warp has lanes, without new tokens here and there, and runs of them."""
+    lens = [1 + 53 * i % 400 for i in range(150)]
+    news = [0 if i % 7 == 0 or 40 <= i < 75 else 1 + (29 * i) % min(n, 70) for i, n in enumerate(lens)]
+    c = Case(250 + d, kind, lens, news, 4, 2, d, 16)
     c.check(c.run())
     assert c.status() == 0
 

@@ -66,6 +66,18 @@ def test_prompts_of_many_stages(hq, hkv, d, lens):
     _check(got, want, bound)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(16, 8, 64), (8, 8, 128)])
+def test_many_short_prompts(hq, hkv, d):
+    """More units than CTAs, most of them a single stage that ends inside its box."""
+    lens = [1 + 37 * i % 150 for i in range(150)]
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    (q, k, v), dev = _inputs(6, int(starts[-1]), hq, hkv, d, True)
+    got, status = _run(*dev, starts, d ** -0.5)
+    want, bound = chunks.prompts(q, k, v, starts, d ** -0.5)
+    assert status == 0
+    _check(got, want, bound)
+
+
 @pytest.mark.parametrize("size,scale", [(1.0, 2.0), (30.0, 0.088), (300.0, 0.088), (1e-20, 1.0), (1.0, 1e-30)])
 def test_prompts_scores_of_any_size(size, scale):
     """One token takes all the weight, or all take the same."""
