@@ -18,7 +18,7 @@
 //   Pools:  the blocks' codes by bulk copies into a ring of raw slots; the widening warps turn them into f16 (exact for
 //           E4M3, and for E2M1 codes times their E4M3 scale) in the swizzled layout, with zeros for V rows behind the
 //           sequence's end.  Query rows are scaled by a power of two and rounded to f16 on the way.
-//   S = Q K^T into TMEM (M 128, N 128), O += P V with P read from TMEM, where the softmax wrote it over S.
+//   S = Q K^T into TMEM (M 128, N 128), O += P V with P read from TMEM, where the softmax wrote it over S's last 64 columns.
 //   P is handed over in two halves of 64 keys, so that the product with V begins while the second half's exponentials
 //   are formed.
 // O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since it was last scaled.  Every wait is
@@ -60,9 +60,9 @@ struct AttnParams {
 
 constexpr int kAtRows = 128;
 constexpr int kAtKvWarp = 8, kAtMmaWarp = 9, kAtQWarp = 10, kAtWidenWarp = 12;
-constexpr uint32_t kAtTmemCols = 512;  // half t: S (P over its first 64 columns) in 256 t + [0, 128), O in 256 t + 128 + [0, D)
+constexpr uint32_t kAtTmemCols = 512;  // half t: S (P over its last 64 columns) in 256 t + [0, 128), O in 256 t + 128 + [0, D)
 constexpr uint32_t kAtTmemHalf = 256;
-constexpr uint32_t kAtTmemO = 128;
+constexpr uint32_t kAtTmemP = 64, kAtTmemO = 128;
 constexpr float kAtRescaleLog2 = 8.f;
 // f16 weights are held times 2^7: with the lazy rescaling they stay below 2^15, and keep all their bits down to 2^-21 of
 // the largest.
@@ -103,7 +103,7 @@ struct AttnLayout {
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 * 4 : 0);  // odd half's (m, l) [128]
     static constexpr int kJoinOff = kMlOff + 128 * 8;                        // join's (m, 1 / l) [2][128]
     static constexpr int kBarOff = kJoinOff + (kPools ? 2 * 128 * 8 : 0);
-    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 16;
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 17;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
     static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
     static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -120,36 +120,37 @@ struct AttnBars {
     __device__ uint32_t raw_empty(int s) const { return at(2 * L::kSlots + L::kRaws + s); }
     static constexpr int kRest = 2 * L::kSlots + 2 * L::kRaws;
     __device__ uint32_t s_full(int t) const { return at(kRest + t); }        // S in TMEM
-    __device__ uint32_t p_first(int t) const { return at(kRest + 2 + t); }   // weights of keys 0 .. 63 in TMEM, O rescaled
+    __device__ uint32_t p_first(int t) const { return at(kRest + 2 + t); }   // weights of keys 64 .. 127 in TMEM, O rescaled
     __device__ uint32_t p_second(int t) const { return at(kRest + 4 + t); }  // the other weights
     __device__ uint32_t o_final(int t) const { return at(kRest + 6 + t); }   // a piece's last P V
     __device__ uint32_t q_full() const { return at(kRest + 8); }
     __device__ uint32_t q_empty() const { return at(kRest + 9); }
-    __device__ uint32_t drain() const { return at(kRest + 10); }
-    __device__ uint32_t tail() const { return at(kRest + 11); }      // packed: a V box with rows behind its sequence's end
-    __device__ uint32_t odd_ml() const { return at(kRest + 12); }    // the odd half's maximum and sum are in shared memory
-    __device__ uint32_t odd_read() const { return at(kRest + 13); }  // the even half's warps have read them, and its O
-    __device__ uint32_t join(int t) const { return at(kRest + 14 + t); }  // the half's four warps have come this far
+    __device__ uint32_t tail() const { return at(kRest + 10); }      // packed: a V box with rows behind its sequence's end
+    __device__ uint32_t odd_ml() const { return at(kRest + 11); }    // the odd half's maximum and sum are in shared memory
+    __device__ uint32_t odd_read() const { return at(kRest + 12); }  // the even half's warps have read them, and its O
+    __device__ uint32_t drain() const { return at(kRest + 15); }
+    __device__ uint32_t join(int t) const { return at(kRest + 13 + t); }  // the half's four warps have come this far
 };
 
-// Warp-collective bounded wait; gives up once the CTA's abort flag is set.
-__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
-    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-    bool ok = mbar_wait(bar, parity, kWaitLimitNs, abort_flag);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {
-        *abort_flag = 1;
-        if ((threadIdx.x & 31) == 0) flag_status(status, PA_DEV_WAIT_TIMEOUT);
-    }
-    return ok;
-}
-// The same for one thread.
+// One thread's bounded wait; gives up once the CTA's abort flag is set.
 __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
-    if (*abort_flag) return false;
-    if (mbar_wait(bar, parity, kWaitLimitNs, abort_flag)) return true;
-    *abort_flag = 1;
-    flag_status(status, PA_DEV_WAIT_TIMEOUT);
-    return false;
+    uint64_t since = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        const uint64_t now = global_timer_ns();
+        if (since == 0) {
+            since = now;
+        } else if (now - since > kWaitLimitNs) {
+            *abort_flag = 1;
+            flag_status(status, PA_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a warp: its lanes go on together.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
+    return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status));
 }
 
 // ---- work ------------------------------------------------------------------------------------------
@@ -346,6 +347,14 @@ struct AttnItems {
     }
 };
 
+// The slots of a piece's stages in that order, from the first slot c on.
+struct AttnSlots {
+    int c, ns, lead;
+    __device__ AttnSlots(const AttnPiece& w, int c) : c(c), ns(w.ns), lead(w.one ? 2 : 1) {}
+    __device__ __forceinline__ int k(int j) const { return c + (lead == 1 ? 2 * j : j < 2 ? j : 2 * j - 1); }
+    __device__ __forceinline__ int v(int j) const { return c + (lead == 1 ? 2 * j + 1 : min(2 * j + 2, ns + j)); }
+};
+
 // ---- loads -----------------------------------------------------------------------------------------
 
 // Packed: K and V of each stage, a box of 128 tokens per 64-element panel.  The stage that reaches past its sequence
@@ -509,23 +518,30 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
             const bool is_v = items.next(j);
             const int rs = sc % L::kRaws, fs = sc % L::kSlots;
             if (!at_wait(bars.raw_full(rs), (sc / L::kRaws) & 1, abort_flag, p.status)) return;
-            if (!at_wait(bars.empty(fs), ((sc / L::kSlots) & 1) ^ 1, abort_flag, p.status)) return;
+            const uint32_t slot_parity = ((sc / L::kSlots) & 1) ^ 1;
+            const bool slot_over = __all_sync(0xffffffffu, mbar_test_wait(bars.empty(fs), slot_parity));
             const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes, dst = base_s + L::kRingOff + fs * L::kTileBytes;
             const int keep = is_v ? w.len - (w.k0 + j) * kAttnKeys : kAttnKeys;  // rows of the sequence
+            // the codes first, all of them, so that one latency serves them all and the raw slot is free again
             if constexpr (SRC == kAttnFp8) {
                 // eight lanes: two rows, four 16-byte chunks of each, the first half of one row and the second of the other
+                auto row_of = [&](int it) { return 32 * part + 8 * (it >> 1) + 2 * l4 + (l8 >> 2); };
+                auto chunk_of = [&](int it) { return (((l8 >> 2) ^ (it & 1)) << 2) + (l8 & 3); };
+                uint4 x[8];
+#pragma unroll
+                for (int it = 0; it < 8; ++it) x[it] = lds16(raw + row_of(it) * 128 + chunk_of(it) * 16);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.raw_empty(rs));
+                if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
 #pragma unroll
                 for (int it = 0; it < 8; ++it) {
-                    const int r = 32 * part + 8 * (it >> 1) + 2 * l4 + (l8 >> 2), c = (((l8 >> 2) ^ (it & 1)) << 2) + (l8 & 3);
-                    const uint4 x = lds16(raw + r * 128 + c * 16);
+                    const int r = row_of(it), c = chunk_of(it);
+                    if (keep < kAttnKeys && r >= keep) x[it] = make_uint4(0u, 0u, 0u, 0u);
                     uint32_t h[8];
-                    e4m3x4_to_f16x2(x.x, h[0], h[1]);
-                    e4m3x4_to_f16x2(x.y, h[2], h[3]);
-                    e4m3x4_to_f16x2(x.z, h[4], h[5]);
-                    e4m3x4_to_f16x2(x.w, h[6], h[7]);
-                    if (r >= keep)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = 0u;
+                    e4m3x4_to_f16x2(x[it].x, h[0], h[1]);
+                    e4m3x4_to_f16x2(x[it].y, h[2], h[3]);
+                    e4m3x4_to_f16x2(x[it].z, h[4], h[5]);
+                    e4m3x4_to_f16x2(x[it].w, h[6], h[7]);
                     const uint32_t row = dst + (c >> 2) * L::kPanelBytes + r * 128, ch = 2 * (c & 3);
                     sts16(row + ((ch ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
                     sts16(row + (((ch + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
@@ -534,37 +550,44 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                 // eight lanes: four rows, two 16-byte chunks (32 codes) of each; at head_dim 128 two rows' first halves and
                 // two rows' second halves
                 constexpr int kIters = D / 32;
+                const int rr = l8 >> 1, half = l8 & 1;
+                auto panel_of = [&](int it) { return D == 128 ? (rr >> 1) ^ (it & 1) : 0; };
+                auto row_of = [&](int it) { return 32 * part + 16 * (D == 128 ? it >> 1 : it) + 4 * l4 + rr; };
+                uint4 x[kIters];
+                uint16_t sb[kIters];
 #pragma unroll
                 for (int it = 0; it < kIters; ++it) {
-                    const int rr = l8 >> 1, pn = D == 128 ? (rr >> 1) ^ (it & 1) : 0;
-                    const int r = 32 * part + 16 * (D == 128 ? it >> 1 : it) + 4 * l4 + rr, half = l8 & 1;
-                    const int off = r & ((1 << p.bs_shift) - 1);
+                    const int r = row_of(it), off = r & ((1 << p.bs_shift) - 1);
                     const uint32_t rec = raw + (r >> p.bs_shift) * ((uint32_t)fp4_row_bytes(D) << p.bs_shift);
-                    const uint4 x = lds16(rec + off * (D / 2) + pn * 32 + half * 16);
-                    uint16_t sb;
+                    x[it] = lds16(rec + off * (D / 2) + panel_of(it) * 32 + half * 16);
                     asm volatile("ld.shared.u16 %0, [%1];"
-                                 : "=h"(sb)
-                                 : "r"(rec + ((D / 2) << p.bs_shift) + off * (D / 16) + pn * 4 + half * 2)
+                                 : "=h"(sb[it])
+                                 : "r"(rec + ((D / 2) << p.bs_shift) + off * (D / 16) + panel_of(it) * 4 + half * 2)
                                  : "memory");
-                    const uint32_t sc2 = e4m3x2_to_f16x2(sb), s0 = f16x2_low_twice(sc2), s1 = f16x2_high_twice(sc2);
-                    const uint32_t row = dst + pn * L::kPanelBytes + r * 128;
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.raw_empty(rs));
+                if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
+#pragma unroll
+                for (int it = 0; it < kIters; ++it) {
+                    const int r = row_of(it);
+                    if (keep < kAttnKeys && r >= keep) x[it] = make_uint4(0u, 0u, 0u, 0u), sb[it] = 0;
+                    const uint32_t sc2 = e4m3x2_to_f16x2(sb[it]), s0 = f16x2_low_twice(sc2), s1 = f16x2_high_twice(sc2);
+                    const uint32_t row = dst + panel_of(it) * L::kPanelBytes + r * 128;
+                    const uint32_t xs[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t h[4];
                         e2m1x8_to_f16x2(xs[e], h);
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) h[f] = r < keep ? mul_f16x2(h[f], e < 2 ? s0 : s1) : 0u;
+                        for (int f = 0; f < 4; ++f) h[f] = mul_f16x2(h[f], e < 2 ? s0 : s1);
                         sts16(row + (((4 * half + e) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
                     }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bars.raw_empty(rs));
-                mbar_arrive(bars.full(fs));
-            }
+            if (lane == 0) mbar_arrive(bars.full(fs));
         }
     }
 }
@@ -626,6 +649,11 @@ __device__ __forceinline__ void at_load_q_pools(const AttnParams& p, const void*
 }
 
 // ---- MMA -------------------------------------------------------------------------------------------
+// One thread issues for both halves in turn (P V of the stage, then S of the next), so that they stay out of step: one
+// half's softmax runs while the tensor core works for the other.  (A warp for each half brings them into step, and both
+// wait for the tensor core at once.)  It issues as fast as the tensor core works, so whatever else it does shows: each
+// turn commits once, to the softmax, which releases the slots in its place; and it asks whether its next waits are over
+// before it issues the matrices in front of them.
 template <int SRC, int D>
 __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, uint32_t base_s, uint32_t tmem,
                                        const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int lane) {
@@ -638,108 +666,78 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
     const uint32_t k_lo = (uint32_t)umma_smem_desc(base_s + L::kRingOff, 16, 1024);
     const uint32_t v_lo = (uint32_t)umma_smem_desc(base_s + L::kRingOff, L::kPanelBytes, 1024);
     constexpr uint32_t hi = (uint32_t)(umma_smem_desc(0, 0, 1024) >> 32);
-    // S of half t = Q tile `tile` x K^T
+    constexpr uint32_t kTile16 = L::kTileBytes >> 4, kPanel16 = L::kPanelBytes >> 4;
+    // S of half t = Q tile `tile` x K^T, 16 elements at a time: 32 bytes along a 128-byte row, 64-element panels further apart
     auto issue_s = [&](int t, int tile, int slot) {
-        const uint32_t qa = q_lo + (uint32_t)(tile * (L::kTileBytes >> 4)), kb = k_lo + (uint32_t)(slot * (L::kTileBytes >> 4));
-        const uint32_t d = tmem + kAtTmemHalf * t;
-        at_static_for<D / 16>([&](auto ks_c) {  // 16 elements: 32 bytes along a 128-byte row, 64-element panels further apart
+        const uint32_t qa = q_lo + tile * kTile16, kb = k_lo + slot * kTile16, d = tmem + kAtTmemHalf * t;
+        at_static_for<D / 16>([&](auto ks_c) {
             constexpr int ks = decltype(ks_c)::value;
-            constexpr uint32_t o = ((ks >> 2) * L::kPanelBytes + (ks & 3) * 32) >> 4;
+            constexpr uint32_t o = (ks >> 2) * kPanel16 + (ks & 3) * 2;
             umma_bf16_lo<o, o>(d, qa, kb, hi, idesc_s, ks > 0 ? 1u : 0u);
         });
         umma_commit(bars.s_full(t));
     };
-    // O of half t += P V over keys 64 h .. 64 h + 63 of the stage
-    auto issue_o = [&](int t, int slot, auto h_c, bool begin) {
+    // O of half t += P V over keys 64 h .. 64 h + 63 of the stage, 16 keys (16 rows of 128 bytes) at a time
+    auto issue_o = [&](int t, int slot, auto h_c, uint32_t acc0) {
         constexpr int h = decltype(h_c)::value;
-        const uint32_t vb = v_lo + (uint32_t)(slot * (L::kTileBytes >> 4)), d = tmem + kAtTmemHalf * t;
-        const uint32_t acc0 = begin ? 0u : 1u;
-        at_static_for<4>([&](auto kk_c) {
-            constexpr int kk = 4 * h + decltype(kk_c)::value;  // 16 keys: 16 rows of 128 bytes, in units of 16
-            umma_bf16_tmem_a_lo<kk * 128>(d + kAtTmemO, d + kk * 8, vb, hi, idesc_o, kk > 0 ? 1u : acc0);
+        const uint32_t d = tmem + kAtTmemHalf * t, vb = v_lo + slot * kTile16;
+        at_static_for<4>([&](auto i_c) {
+            constexpr int i = decltype(i_c)::value, kk = 4 * h + i;
+            umma_bf16_tmem_a_lo<kk * 128>(d + kAtTmemO, d + kAtTmemP + kk * 8, vb, hi, idesc_o, i > 0 ? 1u : acc0);
         });
     };
-    using First = std::integral_constant<int, 0>;
-    using Second = std::integral_constant<int, 1>;
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
     int sc = 0, pc = 0, ck0 = 0, ck1 = 0;  // slots, pieces, stages of half 0 and of half 1
     bool ok = true;
     while (__shfl_sync(0xffffffffu, (int)ok, 0) && walk.next(p, w)) {
         if (lane == 0) {
-            auto filled = [&](int c) { return at_wait1(bars.full(c % NS), (c / NS) & 1, abort_flag, p.status); };
-            auto times_v = [&](int t, int slot, bool begin) {
-                int& ck = t ? ck1 : ck0;
-                if (!at_wait1(bars.p_first(t), ck & 1, abort_flag, p.status)) return false;
-                tc_fence_after();
-                issue_o(t, slot, First{}, begin);
-                if (!at_wait1(bars.p_second(t), ck & 1, abort_flag, p.status)) return false;
-                tc_fence_after();
-                issue_o(t, slot, Second{}, begin);
-                ++ck;
-                return true;
-            };
+            // A turn is P V of stage k of half t, and S of its stage k + lead; of two tiles the halves take turns at every
+            // stage, from S of stage 0 (k = -1) on, of one tile the stages alternate between the halves (k from -2).
+            const AttnSlots at(w, sc);
+            const int lead = at.lead;
+            int k = -lead, t = 0;
+            bool v_over = false, k_over = false, p_over = false;
             ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
-            if (!w.one) {
-                const int a = sc++;
-                ok = ok && filled(a);
-                if (ok) {
+#pragma unroll 1
+            while (ok && k < w.ns) {
+                const int n = w.one ? w.ns : t ? w.ns : w.n0;  // stages of this half
+                const bool product = k >= 0 && k < n, scores = k + lead < n;
+                const int vs = at.v(k), ks = at.k(k + lead), tile = w.one ? 0 : t;
+                const uint32_t parity = (t ? ck1 : ck0) & 1;
+                if (product) {
+                    if (!v_over && !at_wait1(bars.full(vs % NS), (vs / NS) & 1, abort_flag, p.status)) break;
+                    if (!p_over && !at_wait1(bars.p_first(t), parity, abort_flag, p.status)) break;
                     tc_fence_after();
-                    if (w.n0 > 0) issue_s(0, 0, a % NS);
-                    issue_s(1, 1, a % NS);
-                    umma_commit(bars.empty(a % NS));
-                    if (w.ns == 1) umma_commit(bars.q_empty());
-                }
-                for (int k = 0; ok && k < w.ns; ++k) {
-                    const int vs = sc++, kn = k + 1 < w.ns ? sc++ : -1;
-                    ok = filled(vs);
-                    bool k_ready = false;
-                    for (int t = 0; ok && t < 2; ++t) {
-                        const int nt = t ? w.ns : w.n0;
-                        if (k >= nt) continue;
-                        ok = times_v(t, vs % NS, k == 0);
-                        if (!ok) break;
-                        if (k + 1 == nt) {
-                            umma_commit(bars.o_final(t));
-                        } else {
-                            if (!k_ready) ok = filled(kn);
-                            k_ready = true;
-                            if (ok) issue_s(t, t, kn % NS);
-                        }
-                    }
-                    if (!ok) break;
-                    umma_commit(bars.empty(vs % NS));
-                    if (kn >= 0) {
-                        umma_commit(bars.empty(kn % NS));
-                        if (k + 2 == w.ns) umma_commit(bars.q_empty());  // the piece's last Q K^T were just issued
-                    }
-                }
-            } else {
-                for (int t = 0; ok && t < 2 && t < w.ns; ++t) {
-                    const int a = sc++;
-                    ok = filled(a);
-                    if (!ok) break;
+                    p_over = mbar_test_wait(bars.p_second(t), parity);
+                    issue_o(t, vs % NS, std::integral_constant<int, 1>{}, k < lead ? 0u : 1u);
+                    if (!p_over && !at_wait1(bars.p_second(t), parity, abort_flag, p.status)) break;
                     tc_fence_after();
-                    issue_s(t, 0, a % NS);
-                    umma_commit(bars.empty(a % NS));
+                    issue_o(t, vs % NS, std::integral_constant<int, 0>{}, 1u);
+                    if (t)
+                        ++ck1;
+                    else
+                        ++ck0;
                 }
-                if (ok && w.ns <= 2) umma_commit(bars.q_empty());
-                for (int k = 0; ok && k < w.ns; ++k) {
-                    const int t = k & 1, vs = sc++, kn = k + 2 < w.ns ? sc++ : -1;
-                    ok = filled(vs) && times_v(t, vs % NS, k < 2);
-                    if (!ok) break;
-                    umma_commit(bars.empty(vs % NS));
-                    if (kn < 0) {
-                        umma_commit(bars.o_final(t));
-                    } else {
-                        ok = filled(kn);
-                        if (!ok) break;
-                        issue_s(t, 0, kn % NS);
-                        umma_commit(bars.empty(kn % NS));
-                        if (k + 3 == w.ns) umma_commit(bars.q_empty());
-                    }
+                if (scores && !k_over && !at_wait1(bars.full(ks % NS), (ks / NS) & 1, abort_flag, p.status)) break;
+                // the next turn, and whether its waits are over (in vain where it has none)
+                const int t_was = t;
+                const bool last = product && !scores;
+                if (w.one || t) ++k;
+                t ^= 1;
+                const int vn = at.v(max(k, 0)), kn = at.k(k + lead);
+                v_over = mbar_test_wait(bars.full(vn % NS), (vn / NS) & 1);
+                k_over = mbar_test_wait(bars.full(kn % NS), (kn / NS) & 1);
+                p_over = mbar_test_wait(bars.p_first(t), (t ? ck1 : ck0) & 1);
+                if (scores) {
+                    tc_fence_after();
+                    issue_s(t_was, tile, ks % NS);
+                } else if (last) {
+                    umma_commit(bars.o_final(t_was));
                 }
             }
+            ok = k >= w.ns;
+            sc += 2 * w.ns;
             ++pc;
         }
         __syncwarp();
@@ -847,7 +845,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
     };
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
+    int sc = 0;  // slots before the piece
     while (walk.next(p, w)) {
+        // The half whose products are issued last releases a stage's slots: K's when S is complete, V's when what was issued
+        // behind its product is (S of a later stage, or O).
+        const AttnSlots at(w, sc);
+        auto release = [&](int c) { mbar_arrive(bars.empty(c % L::kSlots)); };
+        const bool releases = (warp & 3) == 0 && lane == 0 && (w.one || t == 1);
         const int mine = w.one ? (t ? w.ns / 2 : (w.ns + 1) / 2) : (t ? w.ns : w.n0);
         const bool other = w.one && w.ns > 1;  // both halves work on the one tile
         const int tile = w.one ? 0 : t;
@@ -861,83 +865,127 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             const int k = w.k0 + (w.one ? 2 * i + t : i);
             if (!at_wait(bars.s_full(t), ck & 1, abort_flag, p.status)) return;
             tc_fence_after();
-            if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
-                if (i == 0 && valid) c = p.scale_log2 * reinterpret_cast<const volatile float*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
+            if (releases) {
+                const int j = w.one ? 2 * i + t : i;
+                release(at.k(j));
+                if (i > 0) release(at.v(w.one ? j - 2 : j - 1));
+                if (j + 1 == w.ns) mbar_arrive(bars.q_empty());
             }
+            if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
+                if (i == 0) {
+                    const float f = reinterpret_cast<const volatile float*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
+                    c = valid ? p.scale_log2 * f : p.scale_log2;
+                }
+            }
+            __syncwarp();  // (TMEM instructions want the whole warp, here and wherever lanes part before one)
             // This S was issued after the last P V of this half and completes after it: O is up to date, and no MMA
             // touches this half's TMEM until this warp arrives on p_first.
             const int key0 = k * kAttnKeys;
             const int nq = min(4, (kend - key0 + 31) >> 5);  // quarters that some row of the tile sees
-            uint32_t sv[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(row_tmem + 32 * q, sv[q]);
-            tmem_wait_ld();
-            if (key0 + kAttnKeys - 1 > pos) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+            // Masked scores become -inf: where the stage reaches past the row's position, S is rewritten so first.
+            if (__any_sync(0xffffffffu, key0 + kAttnKeys - 1 > pos)) {
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[32];
+                    tmem_ld32(row_tmem + 32 * q, x);
+                    tmem_wait_ld32(x);
+                    const int seen = pos - key0 - 32 * q;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (key0 + 32 * q + e > pos) sv[q][e] = __float_as_uint(-INFINITY);
-            }
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    mx0 = fmax3(mx0, __uint_as_float(sv[q][e]), __uint_as_float(sv[q][e + 1]));
-                    mx1 = fmax3(mx1, __uint_as_float(sv[q][e + 2]), __uint_as_float(sv[q][e + 3]));
+                        if (e > seen) x[e] = __float_as_uint(-INFINITY);
+                    tmem_st32(row_tmem + 32 * q, x);
                 }
-            const float m_new = fmaxf(m_raw, fmaxf(mx0, mx1));
+                tmem_wait_st();
+            }
+            // The stage's 128 scores of this row pass through twice, for the maximum and for the weights, with the last two
+            // quarters kept and the first two read again (all of them at once would take 128 registers).  Quarter by
+            // quarter from the last to the first, the weights go over S's last 64 columns, behind those still to be read.
+            // (The loops stay rolled for the instruction cache.)
+            uint32_t xa[32], xb[32];
+            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+            auto larger = [&](const uint32_t(&x)[32]) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    mx0 = fmax3(mx0, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    mx1 = fmax3(mx1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                    mx2 = fmax3(mx2, __uint_as_float(x[e + 4]), __uint_as_float(x[e + 5]));
+                    mx3 = fmax3(mx3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
+                }
+            };
+            tmem_ld32(row_tmem, xa);
+            tmem_ld32(row_tmem + 32, xb);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                tmem_wait_ld32(xa);
+                tmem_wait_ld32(xb);
+                larger(xa);
+                if (h == 0) tmem_ld32(row_tmem + 64, xa);
+                larger(xb);
+                if (h == 0) tmem_ld32(row_tmem + 96, xb);
+            }
+            const float m_new = fmaxf(m_raw, fmaxf(fmax3(mx0, mx1, mx2), mx3));
             if (i == 0) {
                 m_raw = m_new;
             } else {
                 const bool need = (m_new - m_raw) * c > kAtRescaleLog2;
                 if (__any_sync(0xffffffffu, need)) {
                     const float f = need ? at_exp2((m_raw - m_new) * c) : 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int c0o = 0; c0o < D; c0o += 32) {
-                        uint32_t ov[32];
-                        tmem_ld32(row_tmem + kAtTmemO + c0o, ov);
-                        tmem_wait_ld();
+                        uint32_t x[32];
+                        tmem_ld32(row_tmem + kAtTmemO + c0o, x);
+                        tmem_wait_ld32(x);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-                        tmem_st32(row_tmem + kAtTmemO + c0o, ov);
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                        tmem_st32(row_tmem + kAtTmemO + c0o, x);
                     }
-                    if (need) {
-                        l_run *= f;
-                        m_raw = m_new;
-                    }
+                    l_run *= f;
+                    m_raw = need ? m_new : m_raw;
                 }
             }
-            // P = 2^(c s - c m) (over pools 2^7 of it) in pairs over the first 64 columns of S, whose scores are in registers.
-            // A row that has seen no key yet weighs all of them 0.
+            // P = 2^(c s - c m) (over pools 2^7 of it).  A row that has seen no key yet weighs all of them 0.
             const float mc = m_raw > -INFINITY ? m_raw * c : 0.f;
             const float shift = SRC == kAttnPacked ? -mc : kAtWeightLog2 - mc;
             const uint64_t c2 = f2_pack(c, c), sh2 = f2_pack(shift, shift);
             uint64_t sum2 = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            auto weigh = [&](int q, const uint32_t(&x)[32]) {
+                uint32_t pw[16];
                 if (q >= nq) {  // past the tile's last position
-                    const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                    tmem_st16(row_tmem + 16 * q, z);
-                } else {
-                    uint32_t pw[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[q][2 * e]), __uint_as_float(sv[q][2 * e + 1])), c2, sh2), x0, x1);
-                        x0 = at_exp2(x0);
-                        x1 = at_exp2(x1);
-                        sum2 = f2_add(sum2, f2_pack(x0, x1));
-                        pw[e] = SRC == kAttnPacked ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                    for (int e = 0; e < 16; ++e) pw[e] = 0u;
+                } else {
+                    // exponents of four pairs ahead of the exponentials of the four before them
+                    uint64_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 20; ++e) {
+                        if (e >= 4) {
+                            float x0, x1;
+                            f2_unpack(y[e & 3], x0, x1);
+                            x0 = at_exp2(x0);
+                            x1 = at_exp2(x1);
+                            sum2 = f2_add(sum2, f2_pack(x0, x1));
+                            pw[e - 4] = SRC == kAttnPacked ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                        }
+                        if (e < 16)
+                            y[e & 3] = f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, sh2);
                     }
-                    tmem_st16(row_tmem + 16 * q, pw);
                 }
-                if (q == 1 || q == 3) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q == 1 ? bars.p_first(t) : bars.p_second(t));
+                tmem_st16(row_tmem + kAtTmemP + 16 * q, pw);
+            };
+#pragma unroll 1
+            for (int h = 1; h >= 0; --h) {
+                weigh(2 * h + 1, xb);
+                if (h) tmem_ld32(row_tmem + 32, xb);
+                weigh(2 * h, xa);
+                if (h) tmem_ld32(row_tmem, xa);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(h ? bars.p_first(t) : bars.p_second(t));
+                __syncwarp();
+                if (h) {
+                    tmem_wait_ld32(xa);
+                    tmem_wait_ld32(xb);
                 }
             }
             float sa, sb;
@@ -946,6 +994,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         }
         float m = m_raw > -INFINITY ? m_raw * c : -INFINITY;  // base 2
         ++pc;
+        const int sc_next = sc + 2 * w.ns;
         if (w.one && t == 1) {
             if (mine > 0) {
                 odd_ml[r] = make_float2(m, l_run);
@@ -954,6 +1003,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                 if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
                 ++hand, ++oc1;
             }
+            sc = sc_next;
             continue;
         }
         // ---- O / l to out, or O, m and l to the join ----
@@ -976,34 +1026,46 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             l_run = l_run * f0 + o.y * f1;
             m = top;
         }
+        if ((warp & 3) == 0 && lane == 0) {  // (of one tile the even half, which waits for both)
+            if (w.one) {
+                release(at.v(w.ns - 1));
+                if (other) release(at.v(w.ns - 2));
+            } else if (t == 1) {
+                release(at.v(w.ns - 1));
+            }
+        }
+        sc = sc_next;
+        __syncwarp();
         tc_fence_after();
         const int64_t row = ((int64_t)(w.c0 + (valid ? tok : i0)) * Hq + (int64_t)w.g * G + r % G) * D;
         const int64_t part = SRC == kAttnPacked ? 0 : ((int64_t)(2 * blockIdx.x + (w.first ? 1 : 0)) * p.part_tiles + tile) * kAtRows + r;
         if (mine > 0) {
             const float inv = whole ? p.out_scale / l_run : 1.f;
             f0 *= inv, f1 *= inv;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t ov[32];
                 float x[32];
                 tmem_ld32(row_tmem + kAtTmemO + 32 * q, ov);
-                tmem_wait_ld();
+                tmem_wait_ld32(ov);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]) * f0;
                 if (other) {
                     tmem_ld32(lanes + kAtTmemHalf + kAtTmemO + 32 * q, ov);
-                    tmem_wait_ld();
+                    tmem_wait_ld32(ov);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] += __uint_as_float(ov[e]) * f1;
                 }
-                if (!valid) continue;
-                if (whole) {
+                if (valid && whole) {
                     at_store_bf16(static_cast<uint16_t*>(p.out) + row + 32 * q, x, p.out_align32);
                 } else if constexpr (SRC != kAttnPacked) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * q);
+                    if (valid) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * q);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+                        for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+                    }
                 }
+                __syncwarp();
             }
         }
         tc_fence_before();  // the O reads are ordered before this warp's next arrival
@@ -1052,7 +1114,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(bars.full(s), L::kPools ? 4 : 1);  // each widening warp, or the producer's expect_tx
-            mbar_init(bars.empty(s), 1);                 // tcgen05.commit after the slot's last MMA
+            mbar_init(bars.empty(s), 1);                 // a softmax warp, once the slot's MMAs have completed
         }
         for (int s = 0; s < L::kRaws; ++s) {
             mbar_init(bars.raw_full(s), 1);
@@ -1092,23 +1154,23 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::kMiscOff + 8);
     // Registers, of the launch's (packed 384 x 168, pools 512 x 128): two softmax warpgroups, loads and MMA, widening:
-    // packed 2 x 224 + 56 = 3 x 168, pools 2 x 192 + 48 + 80 = 4 x 128.
+    // packed 2 x 216 + 72 = 3 x 168, pools 2 x 168 + 80 + 96 = 4 x 128.
     if (L::kPools && warp >= kAtWidenWarp) {
         if constexpr (L::kPools) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" ::: "memory");
             at_widen<SRC, D>(p, range, base_s, bars, misc, warp - kAtWidenWarp, lane);
         }
     } else if (warp >= 8) {
         if constexpr (L::kPools)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
         else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == kAtMmaWarp) {
             at_mma<SRC, D>(p, range, base_s, tmem, bars, misc, lane);
         } else if constexpr (L::kPools) {
             if (warp == kAtKvWarp)
                 at_load_raw<SRC, D>(p, range, base_s, bars, misc, lane);
-            else
+            else if (warp >= kAtQWarp)
                 at_load_q_pools<SRC, D>(p, range, base, base_s, bars, misc, warp - kAtQWarp, lane);
         } else {
             if (warp == kAtKvWarp)
@@ -1118,9 +1180,9 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         }
     } else {
         if constexpr (L::kPools)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
         else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
         at_softmax<SRC, D>(p, range, warp >> 2, base, tmem, bars, misc, warp, lane);
     }
     tc_fence_before();
