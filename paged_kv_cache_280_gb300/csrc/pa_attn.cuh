@@ -667,77 +667,97 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
     const uint32_t v_lo = (uint32_t)umma_smem_desc(base_s + L::kRingOff, L::kPanelBytes, 1024);
     constexpr uint32_t hi = (uint32_t)(umma_smem_desc(0, 0, 1024) >> 32);
     constexpr uint32_t kTile16 = L::kTileBytes >> 4, kPanel16 = L::kPanelBytes >> 4;
-    // S of half t = Q tile `tile` x K^T, 16 elements at a time: 32 bytes along a 128-byte row, 64-element panels further apart
-    auto issue_s = [&](int t, int tile, int slot) {
-        const uint32_t qa = q_lo + tile * kTile16, kb = k_lo + slot * kTile16, d = tmem + kAtTmemHalf * t;
-        at_static_for<D / 16>([&](auto ks_c) {
-            constexpr int ks = decltype(ks_c)::value;
+    // S (at d) = Q K^T over half of the head's elements, 16 at a time: 32 bytes along a 128-byte row, 64-element panels
+    // further apart
+    auto issue_s = [&](uint32_t d, uint32_t qa, uint32_t kb, auto h_c) {
+        at_static_for<D / 32>([&](auto ks_c) {
+            constexpr int ks = D / 32 * decltype(h_c)::value + decltype(ks_c)::value;
             constexpr uint32_t o = (ks >> 2) * kPanel16 + (ks & 3) * 2;
             umma_bf16_lo<o, o>(d, qa, kb, hi, idesc_s, ks > 0 ? 1u : 0u);
         });
-        umma_commit(bars.s_full(t));
     };
-    // O of half t += P V over keys 64 h .. 64 h + 63 of the stage, 16 keys (16 rows of 128 bytes) at a time
-    auto issue_o = [&](int t, int slot, auto h_c, uint32_t acc0) {
+    // O (behind S) += P V over keys 64 h .. 64 h + 63 of the stage, 16 keys (16 rows of 128 bytes) at a time
+    auto issue_o = [&](uint32_t d, uint32_t vb, auto h_c, uint32_t acc0) {
         constexpr int h = decltype(h_c)::value;
-        const uint32_t d = tmem + kAtTmemHalf * t, vb = v_lo + slot * kTile16;
         at_static_for<4>([&](auto i_c) {
             constexpr int i = decltype(i_c)::value, kk = 4 * h + i;
             umma_bf16_tmem_a_lo<kk * 128>(d + kAtTmemO, d + kAtTmemP + kk * 8, vb, hi, idesc_o, i > 0 ? 1u : acc0);
         });
     };
+    struct Ring {  // a slot and the parity of its fill
+        uint32_t slot, parity;
+        __device__ __forceinline__ void ahead(uint32_t by) {  // by < 2 NS
+            slot += by;
+            if (slot >= NS) slot -= NS, parity ^= 1u;
+            if (slot >= NS) slot -= NS, parity ^= 1u;
+        }
+    };
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
-    int sc = 0, pc = 0, ck0 = 0, ck1 = 0;  // slots, pieces, stages of half 0 and of half 1
+    Ring first{0u, 0u};  // the piece's first slot
+    int pc = 0;          // pieces
+    uint32_t ck = 0;     // parity of the halves' stages
     bool ok = true;
     while (__shfl_sync(0xffffffffu, (int)ok, 0) && walk.next(p, w)) {
         if (lane == 0) {
             // A turn is P V of stage k of half t, and S of its stage k + lead; of two tiles the halves take turns at every
-            // stage, from S of stage 0 (k = -1) on, of one tile the stages alternate between the halves (k from -2).
-            const AttnSlots at(w, sc);
+            // stage, from S of stage 0 (k = -1) on, of one tile the stages alternate between the halves (k from -2).  What
+            // the next turn needs is worked out, and asked for, while this one's first MMAs run.
+            const AttnSlots at(w, 0);
             const int lead = at.lead;
-            int k = -lead, t = 0;
-            bool v_over = false, k_over = false, p_over = false;
+            int k = -lead;
+            uint32_t t = 0;
+            Ring kr = first, vr = first;
+            vr.ahead(at.v(0));
+            bool product = false, scores = w.one || w.n0 > 0, v_over = false, k_over = false, p_over = false;
+            using First = std::integral_constant<int, 0>;
+            using Second = std::integral_constant<int, 1>;
+            uint32_t d = tmem, qa = q_lo, vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
+            uint32_t parity = ck & 1u, p_bar = bars.p_first(0);
             ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
 #pragma unroll 1
             while (ok && k < w.ns) {
-                const int n = w.one ? w.ns : t ? w.ns : w.n0;  // stages of this half
-                const bool product = k >= 0 && k < n, scores = k + lead < n;
-                const int vs = at.v(k), ks = at.k(k + lead), tile = w.one ? 0 : t;
-                const uint32_t parity = (t ? ck1 : ck0) & 1;
                 if (product) {
-                    if (!v_over && !at_wait1(bars.full(vs % NS), (vs / NS) & 1, abort_flag, p.status)) break;
-                    if (!p_over && !at_wait1(bars.p_first(t), parity, abort_flag, p.status)) break;
+                    if (!v_over && !at_wait1(bars.full(vr.slot), vr.parity, abort_flag, p.status)) break;
+                    if (!p_over && !at_wait1(p_bar, parity, abort_flag, p.status)) break;
                     tc_fence_after();
-                    p_over = mbar_test_wait(bars.p_second(t), parity);
-                    issue_o(t, vs % NS, std::integral_constant<int, 1>{}, k < lead ? 0u : 1u);
-                    if (!p_over && !at_wait1(bars.p_second(t), parity, abort_flag, p.status)) break;
+                    p_over = mbar_test_wait(p_bar + bars.p_second(0) - bars.p_first(0), parity);
+                    issue_o(d, vb, Second{}, k < lead ? 0u : 1u);
+                    if (!p_over && !at_wait1(p_bar + bars.p_second(0) - bars.p_first(0), parity, abort_flag, p.status)) break;
                     tc_fence_after();
-                    issue_o(t, vs % NS, std::integral_constant<int, 0>{}, 1u);
-                    if (t)
-                        ++ck1;
-                    else
-                        ++ck0;
+                    issue_o(d, vb, First{}, 1u);
+                    ck ^= 1u << t;
                 }
-                if (scores && !k_over && !at_wait1(bars.full(ks % NS), (ks / NS) & 1, abort_flag, p.status)) break;
+                if (scores && !k_over && !at_wait1(bars.full(kr.slot), kr.parity, abort_flag, p.status)) break;
+                const bool do_s = scores, do_o = product && !scores;
+                const uint32_t s_bar = bars.s_full(t), o_bar = bars.o_final(t), d_now = d, qa_now = qa, kb_now = kb;
                 // the next turn, and whether its waits are over (in vain where it has none)
-                const int t_was = t;
-                const bool last = product && !scores;
-                if (w.one || t) ++k;
-                t ^= 1;
-                const int vn = at.v(max(k, 0)), kn = at.k(k + lead);
-                v_over = mbar_test_wait(bars.full(vn % NS), (vn / NS) & 1);
-                k_over = mbar_test_wait(bars.full(kn % NS), (kn / NS) & 1);
-                p_over = mbar_test_wait(bars.p_first(t), (t ? ck1 : ck0) & 1);
-                if (scores) {
+                if (w.one || t) {
+                    if (k >= 0) vr.ahead(at.v(k + 1) - at.v(k));
+                    kr.ahead(at.k(k + lead + 1) - at.k(k + lead));
+                    ++k;
+                }
+                t ^= 1u;
+                const int n = w.one || t ? w.ns : w.n0;
+                product = k >= 0 && k < n, scores = k + lead < n;
+                d = tmem + kAtTmemHalf * t, qa = q_lo + (w.one ? 0u : t * kTile16);
+                vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
+                parity = ck >> t & 1u, p_bar = bars.p_first(t);
+                v_over = mbar_test_wait(bars.full(vr.slot), vr.parity);
+                k_over = mbar_test_wait(bars.full(kr.slot), kr.parity);
+                if (do_s) {
                     tc_fence_after();
-                    issue_s(t_was, tile, ks % NS);
-                } else if (last) {
-                    umma_commit(bars.o_final(t_was));
+                    issue_s(d_now, qa_now, kb_now, First{});
+                    p_over = mbar_test_wait(p_bar, parity);
+                    issue_s(d_now, qa_now, kb_now, Second{});
+                    umma_commit(s_bar);
+                } else {
+                    p_over = mbar_test_wait(p_bar, parity);
+                    if (do_o) umma_commit(o_bar);
                 }
             }
             ok = k >= w.ns;
-            sc += 2 * w.ns;
+            first.ahead((uint32_t)(2 * w.ns) % (2 * NS));
             ++pc;
         }
         __syncwarp();
