@@ -12,8 +12,8 @@
 //   Pools:  the units' stages are laid end to end and cut in equal parts (pa_attn_plan.h), so that few rows over a long
 //           context fill the card; the pieces of a cut unit are joined by the last CTA to end (attn_join).
 //
-// Warps.  0 .. 3 and 4 .. 7: the softmax of the two halves, a thread per row.  8: keys and values.  9: the MMAs.  10
-// (and 11 over pools): query rows.  12 .. 15 (pools): widening of the codes.
+// Warps.  0 .. 3 and 4 .. 7: the softmax of the two halves, a thread per row.  8: keys and values.  9 and 10: the MMAs
+// of the two halves.  11 (packed): query rows.  12 .. 15 (pools): query rows and widening of the codes.
 //   Packed: K and V stages by TMA, 128-byte swizzle, a ring of slots in shared memory.
 //   Pools:  the blocks' codes by bulk copies into a ring of raw slots; the widening warps turn them into f16 (exact for
 //           E4M3, and for E2M1 codes times their E4M3 scale) in the swizzled layout, with zeros for V rows behind the
@@ -59,7 +59,7 @@ struct AttnParams {
 };
 
 constexpr int kAtRows = 128;
-constexpr int kAtKvWarp = 8, kAtMmaWarp = 9, kAtQWarp = 10, kAtWidenWarp = 12;
+constexpr int kAtKvWarp = 8, kAtMmaWarp = 9, kAtQWarp = 11, kAtWidenWarp = 12;
 constexpr uint32_t kAtTmemCols = 512;  // half t: S (P over its last 64 columns) in 256 t + [0, 128), O in 256 t + 128 + [0, D)
 constexpr uint32_t kAtTmemHalf = 256;
 constexpr uint32_t kAtTmemP = 64, kAtTmemO = 128;
@@ -103,7 +103,7 @@ struct AttnLayout {
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 * 4 : 0);  // odd half's (m, l) [128]
     static constexpr int kJoinOff = kMlOff + 128 * 8;                        // join's (m, 1 / l) [2][128]
     static constexpr int kBarOff = kJoinOff + (kPools ? 2 * 128 * 8 : 0);
-    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 17;
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 19;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
     static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
     static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -128,14 +128,17 @@ struct AttnBars {
     __device__ uint32_t tail() const { return at(kRest + 10); }      // packed: a V box with rows behind its sequence's end
     __device__ uint32_t odd_ml() const { return at(kRest + 11); }    // the odd half's maximum and sum are in shared memory
     __device__ uint32_t odd_read() const { return at(kRest + 12); }  // the even half's warps have read them, and its O
-    __device__ uint32_t drain() const { return at(kRest + 15); }
+    __device__ uint32_t drain(int t) const { return at(kRest + 15 + t); }
+    __device__ uint32_t turn(int t) const { return at(kRest + 17 + t); }  // the half's turn at the tensor core
     __device__ uint32_t join(int t) const { return at(kRest + 13 + t); }  // the half's four warps have come this far
 };
 
-// One thread's bounded wait; gives up once the CTA's abort flag is set.
+// One thread's bounded wait; gives up once the CTA's abort flag is set.  (The flag and the clock are looked at now and
+// then only: a thread that is busy with them notices late that its phase has completed.)
 __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
     uint64_t since = 0;
-    while (!mbar_try_wait(bar, parity)) {
+    for (int n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 31) continue;
         if (*abort_flag) return false;
         const uint64_t now = global_timer_ns();
         if (since == 0) {
@@ -500,18 +503,70 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Pools: a piece's query rows as f16, each scaled by a power of two so that its largest element lies in [1, 2), and the
+// inverse factors.  Warp `part` of four.  Rows of no token are left as they are: they reach no other row.  The first rows
+// are on their way while the last piece's Q K^T are still running.
+template <int SRC, int D>
+__device__ __forceinline__ bool at_load_q_pools(const AttnParams& p, const AttnPiece& w, int pc, uint8_t* base, uint32_t base_s,
+                                                const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int part, int lane) {
+    using L = AttnLayout<SRC, D>;
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 8;  // lanes per row, rows at a time, loads in flight
+    const int sub = lane / kLanes, c = lane % kLanes;
+    const int G = p.group, T = p.tile_tokens;
+    float* factors = reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256;
+    const int rows = min(w.n - w.i0, w.one ? T : 2 * T) * G, tile_rows = T * G;  // of the piece, of a tile
+    const uint16_t* src = p.q + ((int64_t)(w.c0 + w.i0) * p.num_q_heads + w.g * G) * D + c * 8;
+    bool free = false;
+#pragma unroll 1
+    for (int r0 = part * kRowsAt * kBatch; r0 < rows || !free; r0 += 4 * kRowsAt * kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kRowsAt + sub, tok = r / G;
+            x[u] = r < rows ? *reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.num_q_heads + (r - tok * G)) * D)
+                            : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (!free && !at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) return false;
+        free = true;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int at = r0 + u * kRowsAt + sub, t = at >= tile_rows ? 1 : 0, r = at - t * tile_rows;
+            const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t top = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, xs[e] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 1; o < kLanes; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t e2 = min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u);  // its exponent
+            const float inv = __uint_as_float((254u - e2) << 23);
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
+            if (at < rows) {
+                sts16(base_s + t * L::kTileBytes + (c >> 3) * L::kPanelBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                if (c == 0) factors[t * 128 + r] = __uint_as_float(e2 << 23);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.q_full());
+    return true;
+}
+
 // Pools: raw codes to f16 in the swizzled layout (128-byte rows of 64 elements, 16-byte chunk c of row r at c ^ (r & 7)).
 // Warp `part` of four takes 32 rows.  In each group of eight lanes the rows and chunks are chosen so that neither the
 // loads nor the stores meet in a bank.
 template <int SRC, int D>
-__device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint32_t base_s, const AttnBars<SRC, D>& bars,
+__device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
                                          volatile int32_t* abort_flag, int part, int lane) {
     using L = AttnLayout<SRC, D>;
     RangeWalk walk(p, range);
     AttnPiece w;
-    int sc = 0;
+    int sc = 0, pc = 0;
     const int l8 = lane & 7, l4 = lane >> 3;
     while (walk.next(p, w)) {
+        if (!at_load_q_pools<SRC, D>(p, w, pc++, base, base_s, bars, abort_flag, part, lane)) return;
         AttnItems items(w);
         for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
             int j;
@@ -522,7 +577,7 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
             const bool slot_over = __all_sync(0xffffffffu, mbar_test_wait(bars.empty(fs), slot_parity));
             const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes, dst = base_s + L::kRingOff + fs * L::kTileBytes;
             const int keep = is_v ? w.len - (w.k0 + j) * kAttnKeys : kAttnKeys;  // rows of the sequence
-            // the codes first, all of them, so that one latency serves them all and the raw slot is free again
+            // the codes first, all of them, so that one latency serves them all
             if constexpr (SRC == kAttnFp8) {
                 // eight lanes: two rows, four 16-byte chunks of each, the first half of one row and the second of the other
                 auto row_of = [&](int it) { return 32 * part + 8 * (it >> 1) + 2 * l4 + (l8 >> 2); };
@@ -530,8 +585,6 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                 uint4 x[8];
 #pragma unroll
                 for (int it = 0; it < 8; ++it) x[it] = lds16(raw + row_of(it) * 128 + chunk_of(it) * 16);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.raw_empty(rs));
                 if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
 #pragma unroll
                 for (int it = 0; it < 8; ++it) {
@@ -565,8 +618,6 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                                  : "r"(rec + ((D / 2) << p.bs_shift) + off * (D / 16) + panel_of(it) * 4 + half * 2)
                                  : "memory");
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.raw_empty(rs));
                 if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
 #pragma unroll
                 for (int it = 0; it < kIters; ++it) {
@@ -587,75 +638,23 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.full(fs));
-        }
-    }
-}
-
-// Pools: a piece's query rows as f16, each scaled by a power of two so that its largest element lies in [1, 2), and the
-// inverse factors.  Warp `part` of two.  Rows of no token are left as they are: they reach no other row.
-template <int SRC, int D>
-__device__ __forceinline__ void at_load_q_pools(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s,
-                                                const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int part, int lane) {
-    using L = AttnLayout<SRC, D>;
-    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 4;  // lanes per row, rows at a time, loads in flight
-    const int sub = lane / kLanes, c = lane % kLanes;
-    const int G = p.group, T = p.tile_tokens;
-    RangeWalk walk(p, range);
-    AttnPiece w;
-    int pc = 0;
-    while (walk.next(p, w)) {
-        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) return;
-        float* factors = reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256;
-        const int tokens = min(w.n - w.i0, w.one ? T : 2 * T);
-        for (int t = 0; t < 2 && t * T < tokens; ++t) {
-            const int rows = min(T, tokens - t * T) * G;
-            const uint16_t* src = p.q + (int64_t)(w.c0 + w.i0 + t * T) * p.num_q_heads * D;
-            for (int r0 = part * kRowsAt * kBatch; r0 < rows; r0 += 2 * kRowsAt * kBatch) {
-                uint4 x[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int r = r0 + u * kRowsAt + sub, tok = r / G;
-                    x[u] = r < rows ? *reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.num_q_heads + w.g * G + (r - tok * G)) * D + c * 8)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int r = r0 + u * kRowsAt + sub;
-                    const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                    uint32_t top = 0;  // largest magnitude, as bf16 bits
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, xs[e] & 0x7fff7fffu);
-#pragma unroll
-                    for (int o = 1; o < kLanes; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const uint32_t e2 = min(max(max(top & 0xffffu, top >> 16) >> 7, 1u), 253u);  // its exponent
-                    const float inv = __uint_as_float((254u - e2) << 23);
-                    uint32_t h[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
-                    if (r < rows) {
-                        sts16(base_s + t * L::kTileBytes + (c >> 3) * L::kPanelBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1],
-                              h[2], h[3]);
-                        if (c == 0) factors[t * 128 + r] = __uint_as_float(e2 << 23);
-                    }
-                }
+            if (lane == 0) {
+                // Only now is the raw slot free: its codes were in registers long ago, but nothing orders a shared-memory
+                // load that has not returned before the next copy into the slot, only the use of what it loaded does.
+                mbar_arrive(bars.raw_empty(rs));
+                mbar_arrive(bars.full(fs));
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.q_full());
-        ++pc;
     }
 }
 
 // ---- MMA -------------------------------------------------------------------------------------------
-// One thread issues for both halves in turn (P V of the stage, then S of the next), so that they stay out of step: one
-// half's softmax runs while the tensor core works for the other.  (A warp for each half brings them into step, and both
-// wait for the tensor core at once.)  It issues as fast as the tensor core works, so whatever else it does shows: each
-// turn commits once, to the softmax, which releases the slots in its place; and it asks whether its next waits are over
-// before it issues the matrices in front of them.
+// One thread issues each half's MMAs (P V of a stage, then S of its next), and the two take turns: an MMA holds up its
+// issuer until the tensor core takes it, so whatever else that thread does (waits, addresses, fetching code that the
+// softmax has pushed out of the instruction cache: about 600 cycles a turn, beside 1024 of MMAs) must run beside the other
+// thread's MMAs.  Without turns the halves fall into step and wait for the tensor core, and it for them, at once.
 template <int SRC, int D>
-__device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, uint32_t base_s, uint32_t tmem,
+__device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, uint32_t t, uint32_t base_s, uint32_t tmem,
                                        const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int lane) {
     using L = AttnLayout<SRC, D>;
     constexpr int NS = L::kSlots;
@@ -694,69 +693,75 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
     };
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
-    Ring first{0u, 0u};  // the piece's first slot
-    int pc = 0;          // pieces
-    uint32_t ck = 0;     // parity of the halves' stages
+    Ring first{0u, 0u};           // the piece's first slot
+    uint32_t pc = 0, ck = 0, rounds = 0;  // pieces, stages of this half, turns
     bool ok = true;
+    const uint32_t d = tmem + kAtTmemHalf * t;
     while (__shfl_sync(0xffffffffu, (int)ok, 0) && walk.next(p, w)) {
         if (lane == 0) {
-            // A turn is P V of stage k of half t, and S of its stage k + lead; of two tiles the halves take turns at every
-            // stage, from S of stage 0 (k = -1) on, of one tile the stages alternate between the halves (k from -2).  What
-            // the next turn needs is worked out, and asked for, while this one's first MMAs run.
-            const AttnSlots at(w, 0);
-            const int lead = at.lead;
-            int k = -lead;
-            uint32_t t = 0;
-            Ring kr = first, vr = first;
-            vr.ahead(at.v(0));
-            bool product = false, scores = w.one || w.n0 > 0, v_over = false, k_over = false, p_over = false;
             using First = std::integral_constant<int, 0>;
             using Second = std::integral_constant<int, 1>;
-            uint32_t d = tmem, qa = q_lo, vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
-            uint32_t parity = ck & 1u, p_bar = bars.p_first(0);
-            ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
+            // In round r the half has its turn: P V of stage j, S of stage j + lead.  Of two tiles both see every stage, of
+            // one tile half 0 has the even stages and half 1 the odd ones.
+            const AttnSlots at(w, 0);
+            const int lead = at.lead, n = w.one || t ? w.ns : w.n0, last = w.one ? (w.ns - 1) / 2 : w.ns - 1;
+            const uint32_t qa = q_lo + (w.one ? 0u : t * kTile16);
+            int j = (w.one ? (int)t : 0) - lead;
+            Ring kr = first, vr = first;
+            if (w.one && t) kr.ahead(at.k(1));
+            vr.ahead(at.v(j + lead));
+            // A half without a stage does not wait for the queries: it has no say in when they are replaced, so it could find
+            // the barrier two phases on.  (Its turns tell it that they were there.)
+            if (j + lead < n) ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
 #pragma unroll 1
-            while (ok && k < w.ns) {
+            for (int r = -1; ok && r <= last; ++r) {
+                const bool product = j >= 0 && j < n, scores = j + lead < n;
+                const uint32_t vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
+                if (product) ok = at_wait1(bars.full(vr.slot), vr.parity, abort_flag, p.status) &&
+                                  at_wait1(bars.p_first(t), ck & 1, abort_flag, p.status);
+                ok = ok && at_wait1(bars.turn(t), (rounds & 1) ^ (t ^ 1), abort_flag, p.status);
+                if (!ok) break;
+                bool k_over = scores && mbar_test_wait(bars.full(kr.slot), kr.parity);
+                // A slot is released by both halves: a half that is alone with a stage gives the other's vote at once.
+                auto release = [&](uint32_t bar, bool alone) {
+                    if (alone) mbar_arrive(bar);
+                    umma_commit(bar);
+                };
                 if (product) {
-                    if (!v_over && !at_wait1(bars.full(vr.slot), vr.parity, abort_flag, p.status)) break;
-                    if (!p_over && !at_wait1(p_bar, parity, abort_flag, p.status)) break;
                     tc_fence_after();
-                    p_over = mbar_test_wait(p_bar + bars.p_second(0) - bars.p_first(0), parity);
-                    issue_o(d, vb, Second{}, k < lead ? 0u : 1u);
-                    if (!p_over && !at_wait1(p_bar + bars.p_second(0) - bars.p_first(0), parity, abort_flag, p.status)) break;
+                    const bool over = mbar_test_wait(bars.p_second(t), ck & 1);
+                    issue_o(d, vb, Second{}, j < lead ? 0u : 1u);
+                    if (!over && !at_wait1(bars.p_second(t), ck & 1, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
                     issue_o(d, vb, First{}, 1u);
-                    ck ^= 1u << t;
+                    release(bars.empty(vr.slot), w.one || j >= w.n0);
+                    ++ck;
                 }
-                if (scores && !k_over && !at_wait1(bars.full(kr.slot), kr.parity, abort_flag, p.status)) break;
-                const bool do_s = scores, do_o = product && !scores;
-                const uint32_t s_bar = bars.s_full(t), o_bar = bars.o_final(t), d_now = d, qa_now = qa, kb_now = kb;
-                // the next turn, and whether its waits are over (in vain where it has none)
-                if (w.one || t) {
-                    if (k >= 0) vr.ahead(at.v(k + 1) - at.v(k));
-                    kr.ahead(at.k(k + lead + 1) - at.k(k + lead));
-                    ++k;
-                }
-                t ^= 1u;
-                const int n = w.one || t ? w.ns : w.n0;
-                product = k >= 0 && k < n, scores = k + lead < n;
-                d = tmem + kAtTmemHalf * t, qa = q_lo + (w.one ? 0u : t * kTile16);
-                vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
-                parity = ck >> t & 1u, p_bar = bars.p_first(t);
-                v_over = mbar_test_wait(bars.full(vr.slot), vr.parity);
-                k_over = mbar_test_wait(bars.full(kr.slot), kr.parity);
-                if (do_s) {
+                if (scores) {
+                    if (!k_over && !at_wait1(bars.full(kr.slot), kr.parity, abort_flag, p.status)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
-                    issue_s(d_now, qa_now, kb_now, First{});
-                    p_over = mbar_test_wait(p_bar, parity);
-                    issue_s(d_now, qa_now, kb_now, Second{});
-                    umma_commit(s_bar);
-                } else {
-                    p_over = mbar_test_wait(p_bar, parity);
-                    if (do_o) umma_commit(o_bar);
+                    issue_s(d, qa, kb, First{});
                 }
+                mbar_arrive(bars.turn(t ^ 1));  // (the other's first MMA comes behind the rest of these)
+                if (scores) {
+                    issue_s(d, qa, kb, Second{});
+                    umma_commit(bars.s_full(t));
+                    release(bars.empty(kr.slot), w.one || j + lead >= w.n0);
+                    if (j + 2 * lead >= n) release(bars.q_empty(), w.one ? w.ns == 1 : w.n0 == 0);  // the half's last S
+                } else if (product) {
+                    umma_commit(bars.o_final(t));
+                }
+                ++rounds;
+                if (j >= 0) vr.ahead(at.v(j + lead) - at.v(j));
+                kr.ahead(at.k(j + 2 * lead) - at.k(j + lead));
+                j += lead;
             }
-            ok = k >= w.ns;
             first.ahead((uint32_t)(2 * w.ns) % (2 * NS));
             ++pc;
         }
@@ -764,8 +769,8 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
     }
     // every MMA issued has completed before the CTA may free TMEM or its shared memory
     if (lane == 0) {
-        umma_commit(bars.drain());
-        mbar_wait(bars.drain(), 0);
+        umma_commit(bars.drain(t));
+        mbar_wait(bars.drain(t), 0);
     }
     __syncwarp();
 }
@@ -865,13 +870,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
     };
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
-    int sc = 0;  // slots before the piece
     while (walk.next(p, w)) {
-        // The half whose products are issued last releases a stage's slots: K's when S is complete, V's when what was issued
-        // behind its product is (S of a later stage, or O).
-        const AttnSlots at(w, sc);
-        auto release = [&](int c) { mbar_arrive(bars.empty(c % L::kSlots)); };
-        const bool releases = (warp & 3) == 0 && lane == 0 && (w.one || t == 1);
         const int mine = w.one ? (t ? w.ns / 2 : (w.ns + 1) / 2) : (t ? w.ns : w.n0);
         const bool other = w.one && w.ns > 1;  // both halves work on the one tile
         const int tile = w.one ? 0 : t;
@@ -885,12 +884,6 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             const int k = w.k0 + (w.one ? 2 * i + t : i);
             if (!at_wait(bars.s_full(t), ck & 1, abort_flag, p.status)) return;
             tc_fence_after();
-            if (releases) {
-                const int j = w.one ? 2 * i + t : i;
-                release(at.k(j));
-                if (i > 0) release(at.v(w.one ? j - 2 : j - 1));
-                if (j + 1 == w.ns) mbar_arrive(bars.q_empty());
-            }
             if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
                 if (i == 0) {
                     const float f = reinterpret_cast<const volatile float*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
@@ -1014,7 +1007,6 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         }
         float m = m_raw > -INFINITY ? m_raw * c : -INFINITY;  // base 2
         ++pc;
-        const int sc_next = sc + 2 * w.ns;
         if (w.one && t == 1) {
             if (mine > 0) {
                 odd_ml[r] = make_float2(m, l_run);
@@ -1023,7 +1015,6 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                 if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
                 ++hand, ++oc1;
             }
-            sc = sc_next;
             continue;
         }
         // ---- O / l to out, or O, m and l to the join ----
@@ -1046,15 +1037,6 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             l_run = l_run * f0 + o.y * f1;
             m = top;
         }
-        if ((warp & 3) == 0 && lane == 0) {  // (of one tile the even half, which waits for both)
-            if (w.one) {
-                release(at.v(w.ns - 1));
-                if (other) release(at.v(w.ns - 2));
-            } else if (t == 1) {
-                release(at.v(w.ns - 1));
-            }
-        }
-        sc = sc_next;
         __syncwarp();
         tc_fence_after();
         const int64_t row = ((int64_t)(w.c0 + (valid ? tok : i0)) * Hq + (int64_t)w.g * G + r % G) * D;
@@ -1134,7 +1116,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(bars.full(s), L::kPools ? 4 : 1);  // each widening warp, or the producer's expect_tx
-            mbar_init(bars.empty(s), 1);                 // a softmax warp, once the slot's MMAs have completed
+            mbar_init(bars.empty(s), 2);                 // tcgen05.commit after each half's last MMA of the slot
         }
         for (int s = 0; s < L::kRaws; ++s) {
             mbar_init(bars.raw_full(s), 1);
@@ -1146,9 +1128,12 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
             mbar_init(bars.p_second(t), 4);
             mbar_init(bars.o_final(t), 1);
         }
-        mbar_init(bars.q_full(), L::kPools ? 2 : 1);
-        mbar_init(bars.q_empty(), 1);
-        mbar_init(bars.drain(), 1);
+        mbar_init(bars.q_full(), L::kPools ? 4 : 1);
+        mbar_init(bars.q_empty(), 2);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bars.drain(t), 1);
+            mbar_init(bars.turn(t), 1);
+        }
         mbar_init(bars.tail(), 1);
         mbar_init(bars.odd_ml(), 4);
         mbar_init(bars.odd_read(), 4);
@@ -1178,24 +1163,21 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (L::kPools && warp >= kAtWidenWarp) {
         if constexpr (L::kPools) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" ::: "memory");
-            at_widen<SRC, D>(p, range, base_s, bars, misc, warp - kAtWidenWarp, lane);
+            at_widen<SRC, D>(p, range, base, base_s, bars, misc, warp - kAtWidenWarp, lane);
         }
     } else if (warp >= 8) {
         if constexpr (L::kPools)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
-        if (warp == kAtMmaWarp) {
-            at_mma<SRC, D>(p, range, base_s, tmem, bars, misc, lane);
+        if (warp == kAtMmaWarp || warp == kAtMmaWarp + 1) {
+            at_mma<SRC, D>(p, range, warp - kAtMmaWarp, base_s, tmem, bars, misc, lane);
         } else if constexpr (L::kPools) {
-            if (warp == kAtKvWarp)
-                at_load_raw<SRC, D>(p, range, base_s, bars, misc, lane);
-            else if (warp >= kAtQWarp)
-                at_load_q_pools<SRC, D>(p, range, base, base_s, bars, misc, warp - kAtQWarp, lane);
+            if (warp == kAtKvWarp) at_load_raw<SRC, D>(p, range, base_s, bars, misc, lane);
         } else {
             if (warp == kAtKvWarp)
                 at_load_packed<D>(p, &tmap_k, &tmap_v, base, base_s, bars, misc, lane);
-            else if (warp == kAtQWarp)
+            else
                 at_load_q_packed<D>(p, &tmap_q, base_s, bars, misc, lane);
         }
     } else {

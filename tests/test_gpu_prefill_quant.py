@@ -207,6 +207,20 @@ def test_one_workspace_for_calls_of_many_shapes(kind, d):
 
 
 @pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("lens,news,hq,hkv", [([2500, 2500], [300, 40], 4, 4), ([700] * 5, [200] * 5, 4, 4), ([9000, 129], [1, 129], 8, 1)])
+def test_chunks_repeat_bit_for_bit(kind, d, lens, news, hq, hkv):
+    """The same call many times over: whichever CTA ends last, and however the roles of a CTA interleave."""
+    import torch
+
+    c = Case(650 + d, kind, lens, news, hq, hkv, d, 16)
+    want = c.run()
+    c.check(want)
+    out = torch.empty_like(want)
+    for _ in range(100):
+        assert torch.equal(c.run(c.ws, out=out), want)
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
 def test_chunks_on_another_stream_and_captured(kind, d):
     import torch
 
