@@ -266,12 +266,12 @@ struct RangeWalk {
             w.b = b, w.g = g, w.n = n, w.len = len, w.c0 = c0;
             at_fields(p, m, w);
             const int wt = w.one ? kOneTile : kTwoTiles;
-            const int k0 = k, k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt));
+            const int k0 = min(k, w.nst), k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt));
             w.at = at;
             if (k1 < w.nst) {
                 at = end;
             } else {
-                at += kUnitWeight + (int64_t)w.nst * wt;
+                at += kUnitWeight + (int64_t)(len - n + min(n, w.i0 + 2 * p.tile_tokens)) * wt;
                 k = 0;
                 if (2 * ++m * p.tile_tokens >= n) {
                     m = 0;
@@ -328,7 +328,7 @@ __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, i
             const int m = u.unit_at(r);
             r -= u.before(m);
             range->b = b0 + lane, range->g = g, range->m = m;
-            range->k = (int)min(stage_at(r, u.stage_weight(m)), (int64_t)u.stages(m));
+            range->k = (int)min(stage_at(r, u.key_weight(m)), (int64_t)INT32_MAX);
             range->at = x - r, range->end = range_begin(c + 1, W, C), range->W = W, range->C = (int)C;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -914,7 +914,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             // quarters kept and the first two read again (all of them at once would take 128 registers).  Quarter by
             // quarter from the last to the first, the weights go over S's last 64 columns, behind those still to be read.
             // (The loops stay rolled for the instruction cache.)
-            uint32_t xa[32], xb[32];
+            uint32_t xa[32], xb[32], xc[32];
             float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
             auto larger = [&](const uint32_t(&x)[32]) {
 #pragma unroll
@@ -925,17 +925,18 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                     mx3 = fmax3(mx3, __uint_as_float(x[e + 6]), __uint_as_float(x[e + 7]));
                 }
             };
-            tmem_ld32(row_tmem, xa);
-            tmem_ld32(row_tmem + 32, xb);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                tmem_wait_ld32(xa);
-                tmem_wait_ld32(xb);
-                larger(xa);
-                if (h == 0) tmem_ld32(row_tmem + 64, xa);
-                larger(xb);
-                if (h == 0) tmem_ld32(row_tmem + 96, xb);
-            }
+            tmem_ld32(row_tmem, xc);
+            tmem_ld32(row_tmem + 32, xa);
+            tmem_wait_ld32(xc);
+            tmem_wait_ld32(xa);
+            tmem_ld32(row_tmem + 96, xb);
+            larger(xc);
+            tmem_ld32(row_tmem + 64, xc);
+            larger(xa);
+            tmem_wait_ld32(xb);
+            tmem_wait_ld32(xc);
+            larger(xb);
+            larger(xc);
             const float m_new = fmaxf(m_raw, fmaxf(fmax3(mx0, mx1, mx2), mx3));
             if (i == 0) {
                 m_raw = m_new;
@@ -989,16 +990,16 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             for (int h = 1; h >= 0; --h) {
                 weigh(2 * h + 1, xb);
                 if (h) tmem_ld32(row_tmem + 32, xb);
-                weigh(2 * h, xa);
-                if (h) tmem_ld32(row_tmem, xa);
+                weigh(2 * h, xc);
+                if (h) tmem_ld32(row_tmem, xc);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(h ? bars.p_first(t) : bars.p_second(t));
                 __syncwarp();
                 if (h) {
-                    tmem_wait_ld32(xa);
                     tmem_wait_ld32(xb);
+                    tmem_wait_ld32(xc);
                 }
             }
             float sa, sb;
