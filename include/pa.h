@@ -530,8 +530,8 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const 
  *     x' = x / sqrt(mean(x^2) + eps) * w
  * over its head_dim elements, w = q_weight or k_weight (fp32 [head_dim], read as
  * they are: a model that stores w - 1 passes w), then turned as there.  In fp32: the
- * squares are summed in any order, one correctly rounded reciprocal root, two
- * products.  Values are stored as they are.
+ * squares are summed in any order, one correctly rounded reciprocal root, its product
+ * with x, and that with the product of w and cos or sin.  Values are stored as they are.
  *     q_out[i] = turned q,  k_out[i] = turned k (unless k_out is NULL),
  *     K pool at s = turned k,  V pool at s = v[i],
  * each rounded once, q_out and k_out to in_dtype.  k_out, [num_tokens][num_kv_heads]
@@ -539,8 +539,9 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const 
  * when k is contiguous, and overlaps nothing else.
  *
  * q_weight is read when num_q_heads > 0.  eps: finite, >= 0 (a row of zeros under eps 0
- * is 0 / 0).  A row whose squares' sum leaves fp32 becomes zero; a NaN or infinity in
- * a query or key head makes that head NaN.  Everything else, padding, bad slots and
+ * is 0 / 0).  A row whose squares' sum leaves fp32 becomes zero; a NaN in a query or key
+ * head makes that head NaN, an infinity itself and what it is turned with, and the rest
+ * of the head zero.  Everything else, padding, bad slots and
  * positions included, is as for pa_rope_and_cache.
  */
 pa_status pa_norm_rope_and_cache(void* q_out, void* k_out, const void* q, int64_t q_stride, const void* k,

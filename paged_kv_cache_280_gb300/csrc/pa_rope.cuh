@@ -52,6 +52,7 @@ struct RopeParams {
     const float *q_weight, *k_weight;
     void* k_out;
     float eps;
+    FastDiv q_heads, kv_heads;  // of a token: queries; keys and values
 };
 
 // E4M3 codes of fp32(x / scale), nearest even, saturated at 448.
@@ -71,7 +72,45 @@ __device__ __forceinline__ uint2 fp8_codes8(const float* x, const Divisor& d) {
     return make_uint2(w[0], w[1]);
 }
 
-template <typename T, int POOL, int D, bool NORM>
+// A unit's 16 elements, two runs of eight at e0 and e1 of a key or value head, to its row of the pool.  Every thread of a
+// warp comes here: 4-bit groups meet in shuffles.
+template <typename T, int POOL, int D>
+__device__ __forceinline__ void append_unit(const RopeParams& p, bool append, bool is_v, int kvh, int64_t slot, int u, int e0, int e1,
+                                            const float (&a)[8], const float (&b)[8]) {
+    uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    const int64_t head = (slot >> p.bs_shift) * p.num_kv_heads + kvh;  // the (block, KV head) in the pool
+    const uint32_t off = (uint32_t)slot & ((1u << p.bs_shift) - 1);
+    if constexpr (POOL == kPoolFp4) {
+        // a run is half a group of 16, the neighbour's the other half (rot_dim is a multiple of 32)
+        float m0 = 0.f, m1 = 0.f;
+        if (append) m0 = amax_nan<8>(a), m1 = amax_nan<8>(b);
+        const float o0 = __shfl_xor_sync(0xffffffffu, m0, 1), o1 = __shfl_xor_sync(0xffffffffu, m1, 1);
+        if (append) {
+            const Divisor d = is_v ? p.v_scale : p.k_scale;
+            const Fp4Scale f0 = fp4_scale(max_nan(m0, o0), d), f1 = fp4_scale(max_nan(m1, o1), d);
+            uint8_t* rec = pool + head * (int64_t)(fp4_row_bytes(D) << p.bs_shift);
+            uint8_t* codes = rec + off * (D / 2);
+            uint8_t* scales = rec + ((D / 2) << p.bs_shift) + off * (D / kFp4Group);
+            *reinterpret_cast<uint32_t*>(codes + e0 / 2) = fp4_codes8(a, d, f0);
+            *reinterpret_cast<uint32_t*>(codes + e1 / 2) = fp4_codes8(b, d, f1);
+            // of the pair, the even thread writes the first run's scale, the odd one the second's
+            scales[((u & 1) ? e1 : e0) / kFp4Group] = (u & 1) ? f1.byte : f0.byte;
+        }
+    } else if (append) {
+        const int64_t r = (head << p.bs_shift) + off;  // the slot's row in the pool
+        if constexpr (POOL == kPoolFp8) {
+            const Divisor d = is_v ? p.v_scale : p.k_scale;
+            *reinterpret_cast<uint2*>(pool + r * D + e0) = fp8_codes8(a, d);
+            *reinterpret_cast<uint2*>(pool + r * D + e1) = fp8_codes8(b, d);
+        } else {
+            T* dst = reinterpret_cast<T*>(pool) + r * D;
+            store8(dst + e0, a);
+            store8(dst + e1, b);
+        }
+    }
+}
+
+template <typename T, int POOL, int D>
 __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams p) {
     // A decode that follows may start its prologue, which reads nothing written here, but only once what came
     // before this kernel is complete: that may have written the lengths and tables it reads.
@@ -83,12 +122,6 @@ __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams
     constexpr uint32_t kTurn = 2 * kParts * kPart;  // two runs
     __shared__ __align__(16) uint8_t ahead[kRopeAhead * kTurn];
     const uint32_t mine = smem_u32(ahead) + threadIdx.x * 16;
-    __shared__ __align__(16) float weights[NORM ? 2 * D : 4];  // of queries, of keys
-    if constexpr (NORM) {
-        for (int i = threadIdx.x; i < 2 * D; i += 256)
-            weights[i] = i >= D ? p.k_weight[i - D] : p.q_weight ? p.q_weight[i] : 0.f;
-        __syncthreads();
-    }
     const int H = p.num_q_heads + 2 * p.num_kv_heads, first_v = p.num_q_heads + p.num_kv_heads, half = p.rot_dim / 2;
     const uint32_t total = (uint32_t)p.num_tokens * (uint32_t)H * U;  // < 2^30 (checked on the host)
     const int u = (int)(threadIdx.x & (U - 1));
@@ -172,23 +205,6 @@ __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams
         take8<T>(mine + turn * kTurn + kParts * kPart, kPart, b);
         fetch(idx + kRopeAhead * stride, turn);
         if (++turn == kRopeAhead) turn = 0;
-        if constexpr (NORM) {
-            // a row's units are U neighbouring lanes of one warp: the sum of its squares meets in shuffles
-            float sq = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq = __fmaf_rn(b[j], b[j], __fmaf_rn(a[j], a[j], sq));
-#pragma unroll
-            for (int o = 1; o < U; o *= 2) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            if (!is_v) {
-                const float r = __frsqrt_rn(sq * (1.f / D) + p.eps);
-                const float* w = weights + (is_q ? 0 : D);
-                float wa[8], wb[8];
-                load8(w + e0, wa);
-                load8(w + e1, wb);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = a[j] * r * wa[j], b[j] = b[j] * r * wb[j];
-            }
-        }
         if (turned) {
             if (p.interleaved) {
 #pragma unroll
@@ -213,64 +229,36 @@ __global__ void __launch_bounds__(256, 4) rope_and_cache_kernel(const RopeParams
             store8(dst + e0, a);
             store8(dst + e1, b);
         }
-        if constexpr (NORM) {
-            if (ok && !is_q && !is_v && p.k_out) {
-                T* dst = static_cast<T*>(p.k_out) + ((int64_t)tok * p.num_kv_heads + (h - p.num_q_heads)) * D;
-                store8(dst + e0, a);
-                store8(dst + e1, b);
-            }
-        }
         const bool append = ok && !is_q;
-        const int kvh = is_v ? h - first_v : h - p.num_q_heads;
-        uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-        const int64_t head = (slot >> p.bs_shift) * p.num_kv_heads + kvh;  // the (block, KV head) in the pool
-        const uint32_t off = (uint32_t)slot & ((1u << p.bs_shift) - 1);
-        if constexpr (POOL == kPoolFp4) {
-            // a run is half a group of 16, the neighbour's the other half (rot_dim is a multiple of 32)
-            float m0 = 0.f, m1 = 0.f;
-            if (append) m0 = amax_nan<8>(a), m1 = amax_nan<8>(b);
-            const float o0 = __shfl_xor_sync(0xffffffffu, m0, 1), o1 = __shfl_xor_sync(0xffffffffu, m1, 1);
-            if (append) {
-                const Divisor d = is_v ? p.v_scale : p.k_scale;
-                const Fp4Scale f0 = fp4_scale(max_nan(m0, o0), d), f1 = fp4_scale(max_nan(m1, o1), d);
-                uint8_t* rec = pool + head * (int64_t)(fp4_row_bytes(D) << p.bs_shift);
-                uint8_t* codes = rec + off * (D / 2);
-                uint8_t* scales = rec + ((D / 2) << p.bs_shift) + off * (D / kFp4Group);
-                *reinterpret_cast<uint32_t*>(codes + e0 / 2) = fp4_codes8(a, d, f0);
-                *reinterpret_cast<uint32_t*>(codes + e1 / 2) = fp4_codes8(b, d, f1);
-                // of the pair, the even thread writes the first run's scale, the odd one the second's
-                scales[((u & 1) ? e1 : e0) / kFp4Group] = (u & 1) ? f1.byte : f0.byte;
-            }
-        } else if (append) {
-            const int64_t r = (head << p.bs_shift) + off;  // the slot's row in the pool
-            if constexpr (POOL == kPoolFp8) {
-                const Divisor d = is_v ? p.v_scale : p.k_scale;
-                *reinterpret_cast<uint2*>(pool + r * D + e0) = fp8_codes8(a, d);
-                *reinterpret_cast<uint2*>(pool + r * D + e1) = fp8_codes8(b, d);
-            } else {
-                T* dst = reinterpret_cast<T*>(pool) + r * D;
-                store8(dst + e0, a);
-                store8(dst + e1, b);
-            }
-        }
+        append_unit<T, POOL, D>(p, append, is_v, is_v ? h - first_v : h - p.num_q_heads, slot, u, e0, e1, a, b);
     }
 }
 
-template <typename T, int POOL, int D, bool NORM>
-bool launch_pool(const RopeParams& p, int dev, int sms, cudaStream_t st) {
-    auto* kernel = &rope_and_cache_kernel<T, POOL, D, NORM>;
+// How a form is launched: its kernel, and its units (of a thread and turn) to a grid.
+struct PlainRope {
+    template <typename T, int POOL, int D>
+    static auto kernel() { return &rope_and_cache_kernel<T, POOL, D>; }
+    static constexpr int kThreads = 256;
+    static unsigned grid(RopeParams&, int64_t units, int resident) {
+        const int64_t want = (units + 255) / 256;
+        return (unsigned)(want < resident ? want : resident);
+    }
+};
+
+template <typename FORM, typename T, int POOL, int D>
+bool launch_pool(RopeParams p, int dev, int sms, cudaStream_t st) {
+    auto* kernel = FORM::template kernel<T, POOL, D>();
     int occ = 0;
-    if (!kernel_occupancy(dev, reinterpret_cast<const void*>(kernel), 256, 0, &occ) || occ <= 0) return false;
-    const int64_t units = (int64_t)p.num_tokens * p.heads.d * (D / 16), want = (units + 255) / 256;
-    const unsigned grid = (unsigned)(want < (int64_t)sms * occ ? want : (int64_t)sms * occ);
-    return launch_dependent(kernel, dim3(grid), 256, 0, st, p) == cudaSuccess;
+    if (!kernel_occupancy(dev, reinterpret_cast<const void*>(kernel), FORM::kThreads, 0, &occ) || occ <= 0) return false;
+    const unsigned grid = FORM::grid(p, (int64_t)p.num_tokens * p.heads.d * (D / 16), sms * occ);
+    return launch_dependent(kernel, dim3(grid), FORM::kThreads, 0, st, p) == cudaSuccess;
 }
 
-template <typename T, int D, bool NORM>
+template <typename FORM, typename T, int D>
 bool launch_rope(const RopeParams& p, pa_dtype pool, int dev, int sms, cudaStream_t st) {
-    return pool == PA_FP4_E2M1   ? launch_pool<T, kPoolFp4, D, NORM>(p, dev, sms, st)
-           : pool == PA_FP8_E4M3 ? launch_pool<T, kPoolFp8, D, NORM>(p, dev, sms, st)
-                                 : launch_pool<T, kPoolSame, D, NORM>(p, dev, sms, st);
+    return pool == PA_FP4_E2M1   ? launch_pool<FORM, T, kPoolFp4, D>(p, dev, sms, st)
+           : pool == PA_FP8_E4M3 ? launch_pool<FORM, T, kPoolFp8, D>(p, dev, sms, st)
+                                 : launch_pool<FORM, T, kPoolSame, D>(p, dev, sms, st);
 }
 
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
@@ -300,7 +288,7 @@ struct RopeCall {
     float eps;
 };
 
-template <bool NORM>
+template <typename FORM>
 pa_status rope_call(const RopeCall& c) {
     if (c.num_tokens < 0 || c.num_q_heads < 0 || c.num_kv_heads <= 0 || c.num_blocks <= 0 || c.max_position <= 0 || c.rot_dim <= 0 ||
         (c.interleaved != 0 && c.interleaved != 1))
@@ -349,11 +337,11 @@ pa_status rope_call(const RopeCall& c) {
     cudaStream_t st = static_cast<cudaStream_t>(c.stream);
     bool ok;
     if (c.in_dtype == PA_BF16)
-        ok = c.head_dim == 128 ? launch_rope<__nv_bfloat16, 128, NORM>(p, c.pool_dtype, dev, sms, st)
-                             : launch_rope<__nv_bfloat16, 64, NORM>(p, c.pool_dtype, dev, sms, st);
+        ok = c.head_dim == 128 ? launch_rope<FORM, __nv_bfloat16, 128>(p, c.pool_dtype, dev, sms, st)
+                             : launch_rope<FORM, __nv_bfloat16, 64>(p, c.pool_dtype, dev, sms, st);
     else
-        ok = c.head_dim == 128 ? launch_rope<float, 128, NORM>(p, c.pool_dtype, dev, sms, st)
-                             : launch_rope<float, 64, NORM>(p, c.pool_dtype, dev, sms, st);
+        ok = c.head_dim == 128 ? launch_rope<FORM, float, 128>(p, c.pool_dtype, dev, sms, st)
+                             : launch_rope<FORM, float, 64>(p, c.pool_dtype, dev, sms, st);
     if (!ok) return PA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
