@@ -54,6 +54,7 @@ struct AttnParams {
     int32_t part_tiles;            // tiles per slot
     int32_t max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, num_blocks, num_q_tokens, max_q_len, bs_shift;
     int32_t group, tile_tokens;    // G, 128 / G rounded down
+    uint32_t group_inverse;        // 2^16 / G rounded up: rows below 256 divided by G
     int32_t out_align32;           // out is 32-byte aligned: 32-byte stores
     float scale_log2, out_scale;
 };
@@ -101,9 +102,8 @@ struct AttnLayout {
     static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
     static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors [2 pieces][2 tiles][128] floats
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 * 4 : 0);  // odd half's (m, l) [128]
-    static constexpr int kJoinOff = kMlOff + 128 * 8;                        // join's (m, 1 / l) [2][128]
-    static constexpr int kBarOff = kJoinOff + (kPools ? 2 * 128 * 8 : 0);
-    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 19;
+    static constexpr int kBarOff = kMlOff + 128 * 8;
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
     static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
     static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -129,6 +129,7 @@ struct AttnBars {
     __device__ uint32_t odd_ml() const { return at(kRest + 11); }    // the odd half's maximum and sum are in shared memory
     __device__ uint32_t odd_read() const { return at(kRest + 12); }  // the even half's warps have read them, and its O
     __device__ uint32_t drain(int t) const { return at(kRest + 15 + t); }
+    __device__ uint32_t verdict(int i) const { return at(kRest + 19 + i); }  // whether this CTA joins the i-th cut unit of one tile
     __device__ uint32_t turn(int t) const { return at(kRest + 17 + t); }  // the half's turn at the tensor core
     __device__ uint32_t join(int t) const { return at(kRest + 13 + t); }  // the half's four warps have come this far
 };
@@ -155,6 +156,8 @@ __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
     return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status));
 }
+
+__device__ __forceinline__ int at_token(const AttnParams& p, int row) { return (int)((uint32_t)row * p.group_inverse >> 16); }
 
 // ---- work ------------------------------------------------------------------------------------------
 
@@ -242,16 +245,17 @@ struct PackedWalk {
 // Pools: this CTA's range of the line of work (written by at_plan before the roles start).
 struct AttnRange {
     int64_t at, end, W;  // the first unit's beginning, the range's end; the whole line
-    int32_t b, g, m, k, C;
+    int32_t b, g, m, k, C, U;
+    int32_t n, len, c0;  // of sequence b
 };
 struct RangeWalk {
     int64_t at, end;
-    int b, g, m, k;
+    int b, g, m, k, U;
     bool fresh;
     int n, len, c0;
-    __device__ RangeWalk(const AttnParams&, const void* range) : fresh(true) {
+    __device__ RangeWalk(const AttnParams&, const void* range) : fresh(false) {
         const volatile AttnRange* r = static_cast<const volatile AttnRange*>(range);
-        at = r->at, end = r->end, b = r->b, g = r->g, m = r->m, k = r->k;
+        at = r->at, end = r->end, b = r->b, g = r->g, m = r->m, k = r->k, n = r->n, len = r->len, c0 = r->c0, U = r->U;
     }
     __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
         while (at < end) {
@@ -266,12 +270,12 @@ struct RangeWalk {
             w.b = b, w.g = g, w.n = n, w.len = len, w.c0 = c0;
             at_fields(p, m, w);
             const int wt = w.one ? kOneTile : kTwoTiles;
-            const int k0 = min(k, w.nst), k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt));
+            const int k0 = min(k, w.nst), k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt, U));
             w.at = at;
             if (k1 < w.nst) {
                 at = end;
             } else {
-                at += kUnitWeight + (int64_t)(len - n + min(n, w.i0 + 2 * p.tile_tokens)) * wt;
+                at += (w.one ? U / 2 : U) + (int64_t)(len - n + min(n, w.i0 + 2 * p.tile_tokens)) * wt;
                 k = 0;
                 if (2 * ++m * p.tile_tokens >= n) {
                     m = 0;
@@ -291,19 +295,26 @@ using AttnWalk = std::conditional_t<SRC == kAttnPacked, PackedWalk, RangeWalk>;
 
 // One warp: this CTA's range.
 __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, int lane) {
+    int c0_mine = 0, U = 0;
     auto line = [&](int b) {
-        int c0, len;
+        int c0 = 0, len = 0;
         const int n = b < p.num_seqs ? at_sequence<kAttnFp8>(p, b, c0, len) : 0;
-        return UnitLine{n, len, p.tile_tokens};
+        c0_mine = c0;
+        return UnitLine{n, len, p.tile_tokens, U};
     };
-    int64_t W = 0, mine = 0;
+    int64_t W = 0, W1 = 0;  // with U = 0, and with 2, which takes it twice for a unit of two tiles and once for one of one
+    UnitLine mine_line{};
     for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        mine = line(b0 + lane).total() * p.num_kv_heads;
-        W += mine;
+        mine_line = line(b0 + lane);
+        W += mine_line.total() * p.num_kv_heads;
+        mine_line.U = 2;
+        W1 += mine_line.total() * p.num_kv_heads;
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-    const int64_t C = W > 0 ? ranges(W, gridDim.x) : 0, c = blockIdx.x;
+    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o), W1 += __shfl_xor_sync(0xffffffffu, W1, o);
+    U = unit_weight(W, gridDim.x);
+    W += (W1 - W) * (U / 2);
+    const int64_t C = W > 0 ? ranges(W, gridDim.x, U) : 0, c = blockIdx.x;
     if (c >= C) {
         if (lane == 0) range->at = range->end = 0, range->W = W, range->C = (int)C;
         return;
@@ -311,7 +322,9 @@ __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, i
     const int64_t x = range_begin(c, W, C);
     int64_t before = 0;
     for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        if (p.num_seqs > 32) mine = line(b0 + lane).total() * p.num_kv_heads;
+        if (p.num_seqs > 32) mine_line = line(b0 + lane);
+        mine_line.U = U;
+        const int64_t mine = mine_line.total() * p.num_kv_heads;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -320,15 +333,15 @@ __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, i
         }
         const int64_t lo = before + incl - mine;
         if (lo <= x && x < before + incl) {
-            const UnitLine u = line(b0 + lane);
+            const UnitLine u = mine_line;
             const int64_t per_head = u.total();
             int64_t r = x - lo;
             const int g = (int)(r / per_head);
             r -= g * per_head;
             const int m = u.unit_at(r);
             r -= u.before(m);
-            range->b = b0 + lane, range->g = g, range->m = m;
-            range->k = (int)min(stage_at(r, u.key_weight(m)), (int64_t)INT32_MAX);
+            range->b = b0 + lane, range->g = g, range->m = m, range->n = u.n, range->len = u.len, range->c0 = c0_mine;
+            range->k = (int)min(stage_at(r, u.key_weight(m), U), (int64_t)INT32_MAX), range->U = U;
             range->at = x - r, range->end = range_begin(c + 1, W, C), range->W = W, range->C = (int)C;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -504,34 +517,42 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
 }
 
 // Pools: a piece's query rows as f16, each scaled by a power of two so that its largest element lies in [1, 2), and the
-// inverse factors.  Warp `part` of four.  Rows of no token are left as they are: they reach no other row.  The first rows
-// are on their way while the last piece's Q K^T are still running.
+// inverse factors.  Warp `part` of four takes every fourth group of rows.  The rows are copied to where they belong as
+// they are, all at once, and then rewritten there, each chunk by the lane that copied it.  Rows of no token stay as they
+// are: they reach no other row.
 template <int SRC, int D>
-__device__ __forceinline__ bool at_load_q_pools(const AttnParams& p, const AttnPiece& w, int pc, uint8_t* base, uint32_t base_s,
-                                                const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int part, int lane) {
+struct AttnQueries {
     using L = AttnLayout<SRC, D>;
-    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes, kBatch = 8;  // lanes per row, rows at a time, loads in flight
-    const int sub = lane / kLanes, c = lane % kLanes;
-    const int G = p.group, T = p.tile_tokens;
-    float* factors = reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256;
-    const int rows = min(w.n - w.i0, w.one ? T : 2 * T) * G, tile_rows = T * G;  // of the piece, of a tile
-    const uint16_t* src = p.q + ((int64_t)(w.c0 + w.i0) * p.num_q_heads + w.g * G) * D + c * 8;
-    bool free = false;
-#pragma unroll 1
-    for (int r0 = part * kRowsAt * kBatch; r0 < rows || !free; r0 += 4 * kRowsAt * kBatch) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u * kRowsAt + sub, tok = r / G;
-            x[u] = r < rows ? *reinterpret_cast<const uint4*>(src + ((int64_t)tok * p.num_q_heads + (r - tok * G)) * D)
-                            : make_uint4(0u, 0u, 0u, 0u);
+    static constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;  // lanes per row, rows at a time
+    int rows, tile_rows, r0, c;
+    uint32_t base_s;
+    const uint16_t* src;
+    __device__ AttnQueries(const AttnParams& p, const AttnPiece& w, uint32_t base_s, int part, int lane) : base_s(base_s) {
+        c = lane % kLanes, r0 = part * kRowsAt + lane / kLanes;
+        tile_rows = p.tile_tokens * p.group;
+        rows = min(w.n - w.i0, w.one ? p.tile_tokens : 2 * p.tile_tokens) * p.group;
+        src = p.q + ((int64_t)(w.c0 + w.i0) * p.num_q_heads + w.g * p.group) * D + c * 8;
+    }
+    __device__ __forceinline__ uint32_t chunk(int at) const {
+        const int t = at >= tile_rows ? 1 : 0, r = at - t * tile_rows;
+        return base_s + t * L::kTileBytes + (c >> 3) * L::kPanelBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    }
+    __device__ __forceinline__ void copy(const AttnParams& p) const {
+#pragma unroll 2
+        for (int at = r0; at < rows; at += 4 * kRowsAt) {
+            const int tok = at_token(p, at);
+            copy_ahead16(chunk(at), src + ((int64_t)tok * p.num_q_heads + (at - tok * p.group)) * D);
         }
-        if (!free && !at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) return false;
-        free = true;
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int at = r0 + u * kRowsAt + sub, t = at >= tile_rows ? 1 : 0, r = at - t * tile_rows;
-            const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        copies_commit();
+    }
+    __device__ __forceinline__ void widen(float* factors) const {
+        copies_wait<0>();
+#pragma unroll 2
+        for (int at0 = r0 - r0 % kRowsAt; at0 < rows; at0 += 4 * kRowsAt) {  // (the same turns for every lane: rows meet in shuffles)
+            const int at = at0 + r0 % kRowsAt;
+            const uint32_t here = chunk(min(at, rows - 1));
+            const uint4 x = lds16(here);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
             uint32_t top = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = __vmaxu2(top, xs[e] & 0x7fff7fffu);
@@ -543,16 +564,14 @@ __device__ __forceinline__ bool at_load_q_pools(const AttnParams& p, const AttnP
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
             if (at < rows) {
-                sts16(base_s + t * L::kTileBytes + (c >> 3) * L::kPanelBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-                if (c == 0) factors[t * 128 + r] = __uint_as_float(e2 << 23);
+                sts16(here, h[0], h[1], h[2], h[3]);
+                if (c == 0) factors[at >= tile_rows ? 128 + at - tile_rows : at] = __uint_as_float(e2 << 23);
             }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars.q_full());
-    return true;
-}
+};
 
 // Pools: raw codes to f16 in the swizzled layout (128-byte rows of 64 elements, 16-byte chunk c of row r at c ^ (r & 7)).
 // Warp `part` of four takes 32 rows.  In each group of eight lanes the rows and chunks are chosen so that neither the
@@ -566,9 +585,22 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
     int sc = 0, pc = 0;
     const int l8 = lane & 7, l4 = lane >> 3;
     while (walk.next(p, w)) {
-        if (!at_load_q_pools<SRC, D>(p, w, pc++, base, base_s, bars, abort_flag, part, lane)) return;
+        // The query rows first if their place is free already; else the first keys are widened before it is.
+        const AttnQueries<SRC, D> queries(p, w, base_s, part, lane);
+        const uint32_t q_parity = (pc & 1) ^ 1;
+        const bool q_free = __all_sync(0xffffffffu, mbar_test_wait(bars.q_empty(), q_parity));
+        auto load_queries = [&]() {
+            queries.copy(p);
+            queries.widen(reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256);
+            if (lane == 0) mbar_arrive(bars.q_full());
+        };
+        if (q_free) load_queries();
         AttnItems items(w);
         for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
+            if (i == 1 && !q_free) {
+                if (!at_wait(bars.q_empty(), q_parity, abort_flag, p.status)) return;
+                load_queries();
+            }
             int j;
             const bool is_v = items.next(j);
             const int rs = sc % L::kRaws, fs = sc % L::kSlots;
@@ -645,6 +677,7 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                 mbar_arrive(bars.full(fs));
             }
         }
+        ++pc;
     }
 }
 
@@ -796,59 +829,103 @@ __device__ __forceinline__ void at_store_bf16(uint16_t* dst, const float* x, boo
     }
 }
 
-// Pools: the pieces of tile t of a cut unit, stored by CTAs a .. b, joined into out by one half's 128 threads:
+// Pools: the pieces of tile t of a cut unit, stored by CTAs a .. b, joined into out by one half's four warps, or both halves':
 //     out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,   M = max_c m_c,
-// in the CTAs' order, so that the result does not depend on which of them ended last.
-template <int SRC, int D, class Meet>
-__device__ __forceinline__ bool at_join(const AttnParams& p, const AttnPiece& w, int t, int rows, int a, int b, float2* join,
-                                        int thread, Meet meet) {
-    auto slot = [&](int c) { return (int64_t)(2 * c + (c == a ? 1 : 0)) * p.part_tiles + t; };  // (a holds the unit's beginning)
-    if (thread < rows) {
-        float M = -INFINITY, L = 0.f;
-        for (int c = a; c <= b; ++c) M = fmaxf(M, __ldcg(p.part_ml + slot(c) * kAtRows + thread).x);
-        for (int c = a; c <= b; ++c) {
-            const float2 ml = __ldcg(p.part_ml + slot(c) * kAtRows + thread);
-            if (ml.x > -INFINITY) L += ml.y * at_exp2(ml.x - M);
-        }
-        join[thread] = make_float2(M, p.out_scale / L);
-    }
-    if (!meet()) return false;
-    constexpr int kLanes = D / 4, kAt = 128 / kLanes, kBatch = 4;  // lanes per row, rows at a time, rows in flight
-    const int sub = thread / kLanes, e = thread % kLanes * 4;
+// in the CTAs' order, so that the result does not depend on which of them ended last.  A warp takes four rows at a time:
+// a lane per piece for the factors, then a lane per D / 32 elements.  Trips to L2 are what it costs, so four rows' next
+// pieces (four, or eight) are on their way at once.
+template <int SRC, int D>
+__device__ __forceinline__ void at_join(const AttnParams& p, const AttnPiece& w, int t, int rows, int a, int b, int warp, int warps,
+                                        int lane) {
+    constexpr int E = D / 32, kRows = 4, kAhead = 16 / E;
+    struct alignas(4 * E) Part {
+        float x[E];
+    };
+    auto slot = [&](int c) { return ((int64_t)(2 * c + (c == a ? 1 : 0)) * p.part_tiles + t) * kAtRows; };  // (a holds the unit's beginning)
     const int64_t first_row = (int64_t)w.c0 + w.i0 + t * p.tile_tokens;
-    for (int r0 = 0; r0 < rows; r0 += kAt * kBatch) {
-        float4 acc[kBatch];
+#pragma unroll 1
+    for (int r0 = warp; r0 < rows; r0 += warps * kRows) {
+        auto row = [&](int u) { return min(r0 + warps * u, rows - 1); };
+        float M[kRows], L[kRows], acc[kRows][E];
+        // (a piece that sees none of a row's keys has stored no O: its factor is 0 and what is read there unused)
+        float m_at[kRows];
+        Part o[kRows][kAhead];
+        auto fetch = [&](int c0) {
+            const int mine = min(c0 + (lane & (kAhead - 1)), b);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = a; c <= b; ++c) {
-            const int64_t s = slot(c) * kAtRows;
-            float4 o[kBatch];
-            float m[kBatch];
+            for (int u = 0; u < kRows; ++u) {
+                m_at[u] = __ldcg(p.part_ml + slot(mine) + row(u)).x;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int r = min(r0 + u * kAt + sub, rows - 1);
-                m[u] = __ldcg(p.part_ml + s + r).x;
-                o[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (s + r) * D + e));
+                for (int i = 0; i < kAhead; ++i) {
+                    const float* src = p.part_o + (slot(min(c0 + i, b)) + row(u)) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                        o[u][i] = Part{v.x, v.y, v.z, v.w};
+                    } else {
+                        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                        o[u][i] = Part{v.x, v.y};
+                    }
+                }
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) M[u] = -INFINITY, L[u] = 0.f;
+#pragma unroll 1
+        for (int c = a + lane; c - lane <= b; c += 32) {
+            float2 ml[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) ml[u] = __ldcg(p.part_ml + slot(min(c, b)) + row(u));
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                if (c > b) ml[u].x = -INFINITY;
+                const float m = fmaxf(M[u], ml[u].x);
+                if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + ml[u].y * at_exp2(ml[u].x - m);
+                M[u] = m;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const float m2 = __shfl_xor_sync(0xffffffffu, M[u], o), l2 = __shfl_xor_sync(0xffffffffu, L[u], o);
+                const float m = fmaxf(M[u], m2);
+                if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + l2 * at_exp2(m2 - m);
+                M[u] = m;
             }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const float2 j = join[min(r0 + u * kAt + sub, rows - 1)];
-                const float f = at_exp2(m[u] - j.x) * j.y;
-                if (m[u] > -INFINITY) {  // (a piece that sees none of the row's keys has stored no O)
-                    acc[u].x += f * o[u].x, acc[u].y += f * o[u].y, acc[u].z += f * o[u].z, acc[u].w += f * o[u].w;
+        for (int u = 0; u < kRows; ++u) {
+            L[u] = p.out_scale / L[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
+        }
+#pragma unroll 1
+        for (int c0 = a; c0 <= b; c0 += kAhead) {
+            fetch(c0);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const float f = m_at[u] > -INFINITY && c0 + (lane & (kAhead - 1)) <= b ? at_exp2(m_at[u] - M[u]) * L[u] : 0.f;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float g = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[u][e] = g != 0.f ? acc[u][e] + g * o[u][i].x[e] : acc[u][e];
                 }
             }
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u * kAt + sub;
-            if (r >= rows) continue;
-            const int tok = r / p.group;
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + ((first_row + tok) * p.num_q_heads + (int64_t)w.g * p.group + (r - tok * p.group)) * D;
-            *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(acc[u].x, acc[u].y), pack_bf16x2(acc[u].z, acc[u].w));
+        for (int u = 0; u < kRows; ++u) {
+            const int r = r0 + warps * u;
+            if (r < rows) {
+                const int tok = at_token(p, r);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ((first_row + tok) * p.num_q_heads +
+                                (int64_t)w.g * p.group + (r - tok * p.group)) * D + lane * E);
+                if constexpr (E == 4)
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[u][0], acc[u][1]), pack_bf16x2(acc[u][2], acc[u][3]));
+                else
+                    *dst = pack_bf16x2(acc[u][0], acc[u][1]);
+            }
         }
     }
-    return true;  // (join is written again behind a later piece's meeting)
 }
 
 // Half t: warps 4 t .. 4 t + 3, row r = 32 (warp % 4) + lane = TMEM lane r.
@@ -863,6 +940,11 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
     float2* odd_ml = reinterpret_cast<float2*>(base + L::kMlOff);
     float c = p.scale_log2;  // > 0 (checked on the host)
     int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0, met = 0;  // stages, pieces, final O of each half, odd halves handed over
+    int cuts = 0;  // pieces of cut units: a range has at most two, its first and its last
+    auto first_of = [&](const AttnPiece& w) { return (int)range_of(w.at, range->W, range->C); };
+    auto last_of = [&](const AttnPiece& w) {
+        return (int)range_of(w.at + stage_begin(w.nst - 1, w.one ? kOneTile : kTwoTiles, range->U), range->W, range->C);
+    };
     auto meet = [&]() {  // the half's four warps
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.join(t));
@@ -875,7 +957,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         const bool other = w.one && w.ns > 1;  // both halves work on the one tile
         const int tile = w.one ? 0 : t;
         const int i0 = w.i0 + tile * T, i1 = min(w.n, i0 + T);
-        const int tok = i0 + r / G;
+        const int tok = i0 + at_token(p, r);
         const bool valid = r < T * G && tok < i1;
         const int pos = w.len - w.n + (valid ? tok : i1 - 1);
         const int kend = w.len - w.n + i1;  // keys that the tile's last row sees
@@ -1016,6 +1098,15 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                 if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
                 ++hand, ++oc1;
             }
+            if constexpr (SRC != kAttnPacked) {  // one tile's pieces are joined by both halves
+                if (!(w.first && w.last)) {
+                    if (!at_wait(bars.verdict(cuts), 0, abort_flag, p.status)) return;
+                    if (misc[4 + 2 * cuts++]) {
+                        __threadfence();
+                        at_join<SRC, D>(p, w, 0, (i1 - i0) * G, first_of(w), last_of(w), warp, 8, lane);
+                    }
+                }
+            }
             continue;
         }
         // ---- O / l to out, or O, m and l to the join ----
@@ -1040,7 +1131,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         }
         __syncwarp();
         tc_fence_after();
-        const int64_t row = ((int64_t)(w.c0 + (valid ? tok : i0)) * Hq + (int64_t)w.g * G + r % G) * D;
+        const int64_t row = ((int64_t)(w.c0 + (valid ? tok : i0)) * Hq + (int64_t)w.g * G + (r - (tok - i0) * G)) * D;
         const int64_t part = SRC == kAttnPacked ? 0 : ((int64_t)(2 * blockIdx.x + (w.first ? 1 : 0)) * p.part_tiles + tile) * kAtRows + r;
         if (mine > 0) {
             const float inv = whole ? p.out_scale / l_run : 1.f;
@@ -1063,9 +1154,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                     at_store_bf16(static_cast<uint16_t*>(p.out) + row + 32 * q, x, p.out_align32);
                 } else if constexpr (SRC != kAttnPacked) {
                     if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + 32 * q);
+                        const float* dst = p.part_o + part * D + 32 * q;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+                        for (int e = 0; e < 32; e += 8)
+                            asm volatile("st.global.cg.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "f"(x[e]),
+                                         "f"(x[e + 1]), "f"(x[e + 2]), "f"(x[e + 3]), "f"(x[e + 4]), "f"(x[e + 5]), "f"(x[e + 6]),
+                                         "f"(x[e + 7])
+                                         : "memory");
                     }
                 }
                 __syncwarp();
@@ -1079,22 +1174,20 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         if constexpr (SRC != kAttnPacked) {
             if (!whole) {
                 if (valid) __stcg(p.part_ml + part, make_float2(m, l_run));
-                const int wt = w.one ? kOneTile : kTwoTiles;
-                const int a = (int)range_of(w.at, range->W, range->C);
-                const int b = (int)range_of(w.at + stage_begin(w.nst - 1, wt), range->W, range->C);
+                const int a = first_of(w), b = last_of(w);
                 __threadfence();
                 if (!meet()) return;
                 if (r == 0) {
                     int32_t* count = p.counts + 2 * a + tile;
                     const bool last = atomicAdd(count, 1) == b - a;
                     if (last) *count = 0;  // for the next call
-                    misc[4 + t] = last;
+                    misc[4 + 2 * cuts + t] = last;
+                    if (w.one) mbar_arrive(bars.verdict(cuts));
                 }
                 if (!meet()) return;
-                if (misc[4 + t]) {
+                if (misc[4 + 2 * cuts++ + t]) {
                     __threadfence();
-                    float2* join = reinterpret_cast<float2*>(base + L::kJoinOff) + t * 128;
-                    if (!at_join<SRC, D>(p, w, tile, (i1 - i0) * G, a, b, join, r, meet)) return;
+                    at_join<SRC, D>(p, w, tile, (i1 - i0) * G, a, b, warp & 3, w.one ? 8 : 4, lane);
                 }
             }
         }
@@ -1133,6 +1226,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         mbar_init(bars.q_empty(), 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(bars.drain(t), 1);
+            mbar_init(bars.verdict(t), 1);
             mbar_init(bars.turn(t), 1);
         }
         mbar_init(bars.tail(), 1);

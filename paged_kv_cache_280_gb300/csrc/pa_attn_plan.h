@@ -2,9 +2,10 @@
 //
 // A unit is two 128-row query tiles of one (sequence, KV head), or one; its work is the keys that its last row sees.
 // Units are numbered sequence by sequence, KV head by KV head, from the first tokens to the last, and laid end to end on a
-// line: a unit of `keys` keys takes kUnitWeight + keys * (kTwoTiles or kOneTile) of it, which adds up in closed form.
+// line: a unit of `keys` keys takes U + keys * kTwoTiles of it, or U / 2 + keys * kOneTile, which adds up in closed form.
+// U, a piece's fixed work, is the same for a whole call (unit_weight).
 // CTA c of C takes the stages of 128 keys that begin in [c W / C, (c + 1) W / C).  Stage 0 begins with its unit, stage s > 0
-// behind the unit's fixed part.  A range is never shorter than kMinRange, which is at least the distance of two stages'
+// behind the unit's fixed part.  A range is never shorter than U + 2 * 128, which is the longest distance of two stages'
 // beginnings, so every CTA between the first and the last of a unit has a piece of it.
 #pragma once
 
@@ -19,23 +20,26 @@
 namespace pa {
 
 constexpr int kAttnKeys = 128;   // keys per stage
-constexpr int kTwoTiles = 3;     // weight of a key that two query tiles share
-constexpr int kOneTile = 2;      // of one that a single tile uses
-constexpr int kUnitWeight = 512;  // a piece's fixed work: query rows, epilogue
-constexpr int kMinRange = 1536;
-static_assert(kMinRange >= kUnitWeight + kTwoTiles * kAttnKeys, "every CTA of a split unit has a piece");
+constexpr int kTwoTiles = 2;     // weight of a key that two query tiles share
+constexpr int kOneTile = 1;      // of one that a single tile uses
+// U: query rows, epilogue and join take about as long as eight stages of one tile (16 x 8 + 1031 tokens over 32 KV heads of
+// 128, FP8: 194 us with 1024, 198 with 512; 64 sequences of 8 tokens over 8 heads: 128 with either).  Where all CTAs get
+// fewer than kFewKeys keys' weight, latency counts and not balance: then more CTAs, of shorter ranges, take part (5 mixed
+// sequences over 4-bit pools: 44 us with 128, 32.5 with 2; one short chunk 30 and 20).
+constexpr int kUnitWeight = 1024, kUnitWeightFew = 2, kFewKeys = 2048;
+PA_HD int unit_weight(int64_t keys_weight, int64_t grid) { return keys_weight < kFewKeys * grid ? kUnitWeightFew : kUnitWeight; }
 
 // The units of one (sequence, KV head): n new tokens at the end of len, T tokens per tile.
 struct UnitLine {
-    int n, len, T;
+    int n, len, T, U;
     PA_HD int units() const { return (n + 2 * T - 1) / (2 * T); }
     PA_HD int two(int m) const { return 2 * m * T + T < n; }  // the unit's second tile has tokens
     PA_HD int keys(int m) const { return len - n + (2 * T * (m + 1) < n ? 2 * T * (m + 1) : n); }
     PA_HD int key_weight(int m) const { return two(m) ? kTwoTiles : kOneTile; }
-    PA_HD int64_t weight(int m) const { return kUnitWeight + (int64_t)keys(m) * key_weight(m); }
+    PA_HD int64_t weight(int m) const { return (two(m) ? U : U / 2) + (int64_t)keys(m) * key_weight(m); }
     // weight of the units before m (m < units(): all but the last unit have two tiles, and all their tokens)
     PA_HD int64_t before(int m) const {
-        return (int64_t)m * (kUnitWeight + kTwoTiles * ((int64_t)(len - n) + (int64_t)T * (m + 1)));
+        return (int64_t)m * (U + kTwoTiles * ((int64_t)(len - n) + (int64_t)T * (m + 1)));
     }
     PA_HD int64_t total() const {
         const int last = units() - 1;
@@ -56,18 +60,19 @@ struct UnitLine {
 };
 
 // The first stage that begins at or behind r of its unit.
-PA_HD int64_t stage_at(int64_t r, int key_weight) {
+PA_HD int64_t stage_at(int64_t r, int key_weight, int U) {
     if (r <= 0) return 0;
-    if (r <= kUnitWeight + key_weight * kAttnKeys) return 1;
-    const int64_t k = r - kUnitWeight + key_weight * kAttnKeys - 1;
+    if (key_weight == kOneTile) U /= 2;
+    if (r <= U + key_weight * kAttnKeys) return 1;
+    const int64_t k = r - U + key_weight * kAttnKeys - 1;
     return (key_weight == kTwoTiles ? k / kTwoTiles : k / kOneTile) / kAttnKeys;
 }
-PA_HD int64_t stage_begin(int64_t s, int key_weight) { return s == 0 ? 0 : kUnitWeight + s * key_weight * kAttnKeys; }
+PA_HD int64_t stage_begin(int64_t s, int key_weight, int U) { return s == 0 ? 0 : (key_weight == kOneTile ? U / 2 : U) + s * key_weight * kAttnKeys; }
 
 PA_HD int64_t range_begin(int64_t c, int64_t W, int64_t C) { return c * W / C; }
 PA_HD int64_t range_of(int64_t at, int64_t W, int64_t C) { return ((at + 1) * C - 1) / W; }
-PA_HD int64_t ranges(int64_t W, int64_t grid) {
-    const int64_t most = W / kMinRange;
+PA_HD int64_t ranges(int64_t W, int64_t grid, int U) {
+    const int64_t most = W / (U + kTwoTiles * kAttnKeys);
     return most < 1 ? 1 : most < grid ? most : grid;
 }
 

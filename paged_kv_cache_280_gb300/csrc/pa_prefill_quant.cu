@@ -7,8 +7,8 @@
 namespace pa {
 namespace {
 
-// The status head, a count per CTA and tile, then two slots per CTA for pieces of cut units: a maximum and a sum per row,
-// and the rows.
+// The status head, then, from the next 256-byte boundary on, a count per CTA and tile and two slots per CTA for pieces of
+// cut units: a maximum and a sum per row, and the rows.
 struct PrefillWorkspace {
     size_t counts, ml, o, total;
     int tiles;
@@ -16,11 +16,11 @@ struct PrefillWorkspace {
 PrefillWorkspace prefill_workspace(int max_q_len, int group, int head_dim, int sms) {
     PrefillWorkspace w;
     w.tiles = max_q_len > kAtRows / group ? 2 : 1;
-    w.counts = kStatusHeadBytes;
+    w.counts = 0;
     w.ml = w.counts + (((size_t)2 * sms * sizeof(int32_t) + 255) & ~(size_t)255);
     const size_t rows = (size_t)2 * sms * w.tiles * kAtRows;
     w.o = w.ml + rows * sizeof(float2);
-    w.total = w.o + rows * head_dim * sizeof(float);
+    w.total = 2 * kStatusHeadBytes + w.o + rows * head_dim * sizeof(float);
     return w;
 }
 
@@ -53,8 +53,8 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.q = static_cast<const uint16_t*>(q);
     p.k_pool = static_cast<const uint8_t*>(k_pool), p.v_pool = static_cast<const uint8_t*>(v_pool);
     p.block_tables = block_tables, p.seq_lens = seq_lens, p.cu_q_lens = cu_q_lens;
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    p.status = reinterpret_cast<int32_t*>(base);
+    p.status = static_cast<int32_t*>(workspace);
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + kStatusHeadBytes + 255) & ~(uintptr_t)255);
     p.counts = reinterpret_cast<int32_t*>(base + ws.counts);
     p.part_ml = reinterpret_cast<float2*>(base + ws.ml), p.part_o = reinterpret_cast<float*>(base + ws.o);
     p.part_tiles = ws.tiles;
@@ -62,6 +62,7 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.num_kv_heads = num_kv_heads, p.num_blocks = num_blocks, p.num_q_tokens = num_q_tokens, p.max_q_len = max_q_len;
     p.bs_shift = block_size == 16 ? 4 : 5;
     p.group = group, p.tile_tokens = kAtRows / group;
+    p.group_inverse = (65536u + p.group - 1) / p.group;
     p.out_align32 = aligned_to(out, 32) ? 1 : 0;
     p.scale_log2 = scale_log2, p.out_scale = v_scale;
     CUtensorMap none;  // not read: the codes come by bulk copies
