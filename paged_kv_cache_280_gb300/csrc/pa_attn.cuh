@@ -97,11 +97,12 @@ struct AttnLayout {
     static constexpr int kTileBytes = kPanels * kPanelBytes;  // a query tile, or K or V of a stage
     static constexpr int kSlots = kPools ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
     static constexpr int kRawBytes = SRC == kAttnFp8 ? 128 * D : 128 * fp4_row_bytes(D);
-    static constexpr int kRaws = !kPools ? 0 : SRC == kAttnFp8 ? 3 : D == 128 ? 5 : 8;
+    static constexpr int kRaws = !kPools ? 0 : SRC == kAttnFp8 ? 4 : D == 128 ? 6 : 8;  // even: a slot always serves the same widening warps
+    static constexpr int kWideners = 2;  // warps that widen an item
     static constexpr int kRingOff = 2 * kTileBytes;
     static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
-    static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors [2 pieces][2 tiles][128] floats
-    static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 * 4 : 0);  // odd half's (m, l) [128]
+    static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors' exponents [2 pieces][2 tiles][128] bytes
+    static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's (m, l) [128]
     static constexpr int kBarOff = kMlOff + 128 * 8;
     static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
@@ -545,7 +546,7 @@ struct AttnQueries {
         }
         copies_commit();
     }
-    __device__ __forceinline__ void widen(float* factors) const {
+    __device__ __forceinline__ void widen(uint8_t* factors) const {
         copies_wait<0>();
 #pragma unroll 2
         for (int at0 = r0 - r0 % kRowsAt; at0 < rows; at0 += 4 * kRowsAt) {  // (the same turns for every lane: rows meet in shuffles)
@@ -565,7 +566,7 @@ struct AttnQueries {
             for (int e = 0; e < 4; ++e) h[e] = pack_f16x2(bf16_lo(xs[e]) * inv, bf16_hi(xs[e]) * inv);
             if (at < rows) {
                 sts16(here, h[0], h[1], h[2], h[3]);
-                if (c == 0) factors[at >= tile_rows ? 128 + at - tile_rows : at] = __uint_as_float(e2 << 23);
+                if (c == 0) factors[at >= tile_rows ? 128 + at - tile_rows : at] = (uint8_t)e2;
             }
         }
         fence_proxy_async_smem();
@@ -574,16 +575,41 @@ struct AttnQueries {
 };
 
 // Pools: raw codes to f16 in the swizzled layout (128-byte rows of 64 elements, 16-byte chunk c of row r at c ^ (r & 7)).
-// Warp `part` of four takes 32 rows.  In each group of eight lanes the rows and chunks are chosen so that neither the
-// loads nor the stores meet in a bank.
+// Two of the four warps (numbers `part`) take an item (K or V of a stage), the other two the next, a warp 64 rows.  In each
+// group of eight lanes the rows and chunks are chosen so that neither the loads nor the stores meet in a bank:
+//   FP8: two rows, four 16-byte chunks (16 codes) of each, the first half of one row and the second of the other;
+//   4-bit: four rows, two 16-byte chunks (32 codes, two scales) of each; at head_dim 128 two rows' first halves and two
+//   rows' second halves.
+// How far the loop is unrolled weighs its latencies against the instruction cache, which all roles share (32 sequences of 5
+// tokens, FP8, and 2 of 9 over 131072 4-bit keys: 2 turns 118 and 164 us, 4: 118 and 159, all: 125 and 149).  With all four
+// warps on each item every wait's latency counts on every item: 127 and 156.
 template <int SRC, int D>
 __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
                                          volatile int32_t* abort_flag, int part, int lane) {
     using L = AttnLayout<SRC, D>;
+    constexpr int kRows = kAttnKeys / L::kWideners;  // of a warp and item
+    constexpr int kPerRow = D == 128 ? 2 : 1;        // turns per row: the other half of the row
+    constexpr int kStep = SRC == kAttnFp8 ? 8 : 16;  // rows a turn (of two)
+    constexpr int kTurns = kRows / kStep * kPerRow;
     RangeWalk walk(p, range);
     AttnPiece w;
     int sc = 0, pc = 0;
     const int l8 = lane & 7, l4 = lane >> 3;
+    const int r_first = kRows * (part % L::kWideners) + (SRC == kAttnFp8 ? 2 * l4 + (l8 >> 2) : 4 * l4 + (l8 >> 1));
+    const uint32_t panel_first = D == 128 ? l8 >> 2 : 0;
+    const uint32_t r7 = (uint32_t)r_first & 7u;
+    // where the thread's first codes and scales are in a raw slot; 4-bit: from 16 rows to the next 16, and on to those behind
+    // them (a block's record: its rows' codes, then their scales)
+    const uint32_t rec = (uint32_t)(L::kRawBytes / kAttnKeys) << p.bs_shift, off = (uint32_t)r_first & ((1u << p.bs_shift) - 1u);
+    const uint32_t codes_at = SRC == kAttnFp8 ? r_first * 128 + (l8 & 3) * 16
+                                              : ((uint32_t)r_first >> p.bs_shift) * rec + off * (D / 2) + (l8 & 1) * 16;
+    const uint32_t scales_at = ((uint32_t)r_first >> p.bs_shift) * rec + ((D / 2) << p.bs_shift) + off * (D / 16) + (l8 & 1) * 2;
+    const uint32_t codes_16 = p.bs_shift == 4 ? rec : 16 * (D / 2), scales_16 = p.bs_shift == 4 ? rec : 16 * (D / 16);
+    const uint32_t codes_32 = p.bs_shift == 4 ? 2 * rec : rec;
+    struct Codes {
+        uint4 c;
+        uint16_t scales;
+    };
     while (walk.next(p, w)) {
         // The query rows first if their place is free already; else the first keys are widened before it is.
         const AttnQueries<SRC, D> queries(p, w, base_s, part, lane);
@@ -591,7 +617,7 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
         const bool q_free = __all_sync(0xffffffffu, mbar_test_wait(bars.q_empty(), q_parity));
         auto load_queries = [&]() {
             queries.copy(p);
-            queries.widen(reinterpret_cast<float*>(base + L::kRowOff) + (pc & 1) * 256);
+            queries.widen(base + L::kRowOff + (pc & 1) * 256);
             if (lane == 0) mbar_arrive(bars.q_full());
         };
         if (q_free) load_queries();
@@ -603,68 +629,53 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
             }
             int j;
             const bool is_v = items.next(j);
+            if (sc % (4 / L::kWideners) != part / L::kWideners) continue;
             const int rs = sc % L::kRaws, fs = sc % L::kSlots;
             if (!at_wait(bars.raw_full(rs), (sc / L::kRaws) & 1, abort_flag, p.status)) return;
-            const uint32_t slot_parity = ((sc / L::kSlots) & 1) ^ 1;
-            const bool slot_over = __all_sync(0xffffffffu, mbar_test_wait(bars.empty(fs), slot_parity));
-            const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes, dst = base_s + L::kRingOff + fs * L::kTileBytes;
+            const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes;
+            auto load = [&](int turn) {
+                const uint32_t step = turn / kPerRow, panel = panel_first ^ (turn & (kPerRow - 1));
+                Codes x;
+                if constexpr (SRC == kAttnFp8) {
+                    x.c = lds16(raw + codes_at + step * (kStep * 128) + panel * 64);
+                    x.scales = 0;
+                } else {
+                    const uint32_t there = raw + (step >> 1) * codes_32;
+                    x.c = lds16(there + codes_at + (step & 1) * codes_16 + panel * 32);
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x.scales) : "r"(there + scales_at + (step & 1) * scales_16 + panel * 4) : "memory");
+                }
+                return x;
+            };
+            Codes next = load(0);
+            const uint32_t dst = base_s + L::kRingOff + fs * L::kTileBytes;
             const int keep = is_v ? w.len - (w.k0 + j) * kAttnKeys : kAttnKeys;  // rows of the sequence
-            // the codes first, all of them, so that one latency serves them all
-            if constexpr (SRC == kAttnFp8) {
-                // eight lanes: two rows, four 16-byte chunks of each, the first half of one row and the second of the other
-                auto row_of = [&](int it) { return 32 * part + 8 * (it >> 1) + 2 * l4 + (l8 >> 2); };
-                auto chunk_of = [&](int it) { return (((l8 >> 2) ^ (it & 1)) << 2) + (l8 & 3); };
-                uint4 x[8];
-#pragma unroll
-                for (int it = 0; it < 8; ++it) x[it] = lds16(raw + row_of(it) * 128 + chunk_of(it) * 16);
-                if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
-#pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int r = row_of(it), c = chunk_of(it);
-                    if (keep < kAttnKeys && r >= keep) x[it] = make_uint4(0u, 0u, 0u, 0u);
+            if (!at_wait(bars.empty(fs), ((sc / L::kSlots) & 1) ^ 1, abort_flag, p.status)) return;
+#pragma unroll(SRC == kAttnFp8 ? 2 : kTurns)
+            for (int turn = 0; turn < kTurns; ++turn) {
+                Codes x = next;
+                if (turn + 1 < kTurns) next = load(turn + 1);
+                const int r = r_first + turn / kPerRow * kStep;
+                const uint32_t row = dst + (panel_first ^ (turn & (kPerRow - 1))) * L::kPanelBytes + r * 128;
+                if (r >= keep) x.c = make_uint4(0u, 0u, 0u, 0u), x.scales = 0;
+                if constexpr (SRC == kAttnFp8) {
+                    const uint32_t ch = 2 * (l8 & 3);
                     uint32_t h[8];
-                    e4m3x4_to_f16x2(x[it].x, h[0], h[1]);
-                    e4m3x4_to_f16x2(x[it].y, h[2], h[3]);
-                    e4m3x4_to_f16x2(x[it].z, h[4], h[5]);
-                    e4m3x4_to_f16x2(x[it].w, h[6], h[7]);
-                    const uint32_t row = dst + (c >> 2) * L::kPanelBytes + r * 128, ch = 2 * (c & 3);
-                    sts16(row + ((ch ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-                    sts16(row + (((ch + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-                }
-            } else {
-                // eight lanes: four rows, two 16-byte chunks (32 codes) of each; at head_dim 128 two rows' first halves and
-                // two rows' second halves
-                constexpr int kIters = D / 32;
-                const int rr = l8 >> 1, half = l8 & 1;
-                auto panel_of = [&](int it) { return D == 128 ? (rr >> 1) ^ (it & 1) : 0; };
-                auto row_of = [&](int it) { return 32 * part + 16 * (D == 128 ? it >> 1 : it) + 4 * l4 + rr; };
-                uint4 x[kIters];
-                uint16_t sb[kIters];
-#pragma unroll
-                for (int it = 0; it < kIters; ++it) {
-                    const int r = row_of(it), off = r & ((1 << p.bs_shift) - 1);
-                    const uint32_t rec = raw + (r >> p.bs_shift) * ((uint32_t)fp4_row_bytes(D) << p.bs_shift);
-                    x[it] = lds16(rec + off * (D / 2) + panel_of(it) * 32 + half * 16);
-                    asm volatile("ld.shared.u16 %0, [%1];"
-                                 : "=h"(sb[it])
-                                 : "r"(rec + ((D / 2) << p.bs_shift) + off * (D / 16) + panel_of(it) * 4 + half * 2)
-                                 : "memory");
-                }
-                if (!slot_over && !at_wait(bars.empty(fs), slot_parity, abort_flag, p.status)) return;
-#pragma unroll
-                for (int it = 0; it < kIters; ++it) {
-                    const int r = row_of(it);
-                    if (keep < kAttnKeys && r >= keep) x[it] = make_uint4(0u, 0u, 0u, 0u), sb[it] = 0;
-                    const uint32_t sc2 = e4m3x2_to_f16x2(sb[it]), s0 = f16x2_low_twice(sc2), s1 = f16x2_high_twice(sc2);
-                    const uint32_t row = dst + panel_of(it) * L::kPanelBytes + r * 128;
-                    const uint32_t xs[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+                    e4m3x4_to_f16x2(x.c.x, h[0], h[1]);
+                    e4m3x4_to_f16x2(x.c.y, h[2], h[3]);
+                    e4m3x4_to_f16x2(x.c.z, h[4], h[5]);
+                    e4m3x4_to_f16x2(x.c.w, h[6], h[7]);
+                    sts16(row + ((ch ^ r7) << 4), h[0], h[1], h[2], h[3]);
+                    sts16(row + (((ch + 1) ^ r7) << 4), h[4], h[5], h[6], h[7]);
+                } else {
+                    const uint32_t sc2 = e4m3x2_to_f16x2(x.scales), s0 = f16x2_low_twice(sc2), s1 = f16x2_high_twice(sc2);
+                    const uint32_t xs[4] = {x.c.x, x.c.y, x.c.z, x.c.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t h[4];
                         e2m1x8_to_f16x2(xs[e], h);
 #pragma unroll
                         for (int f = 0; f < 4; ++f) h[f] = mul_f16x2(h[f], e < 2 ? s0 : s1);
-                        sts16(row + (((4 * half + e) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                        sts16(row + (((4 * (l8 & 1) + e) ^ r7) << 4), h[0], h[1], h[2], h[3]);
                     }
                 }
             }
@@ -968,8 +979,8 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             tc_fence_after();
             if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
                 if (i == 0) {
-                    const float f = reinterpret_cast<const volatile float*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
-                    c = valid ? p.scale_log2 * f : p.scale_log2;
+                    const uint32_t e = reinterpret_cast<const volatile uint8_t*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
+                    c = valid ? p.scale_log2 * __uint_as_float(e << 23) : p.scale_log2;
                 }
             }
             __syncwarp();  // (TMEM instructions want the whole warp, here and wherever lanes part before one)
@@ -1209,12 +1220,12 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     AttnBars<SRC, D> bars{base_s + L::kBarOff};
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(bars.full(s), L::kPools ? 4 : 1);  // each widening warp, or the producer's expect_tx
+            mbar_init(bars.full(s), L::kPools ? L::kWideners : 1);  // each warp that widens it, or the producer's expect_tx
             mbar_init(bars.empty(s), 2);                 // tcgen05.commit after each half's last MMA of the slot
         }
         for (int s = 0; s < L::kRaws; ++s) {
             mbar_init(bars.raw_full(s), 1);
-            mbar_init(bars.raw_empty(s), 4);
+            mbar_init(bars.raw_empty(s), L::kWideners);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bars.s_full(t), 1);
