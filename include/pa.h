@@ -665,12 +665,12 @@ pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const 
  * sequence's own values may reach rows of the chunk that do not see it.
  *
  * The work is split over the contexts too where there are few rows: every CTA takes an equal
- * run of (128 keys x one query tile) steps, and the partial results of a tile that several
- * CTAs share are joined in a fixed order by the last of them to end.
- * workspace: pa_prefill_workspace_bytes bytes, 16-byte aligned, zero-filled once by the
- * caller; its first int32 is the status word (bits as for pa_prefill_attention, and
- * PA_DEV_BAD_SEQ_LEN also where n_b < 0).  It may be used by call after call on one
- * stream, whatever their shapes, as every call leaves its counters zero; calls that can overlap use different ones
+ * run of (128 keys x one query tile) steps, and a second kernel joins the partial results
+ * of a tile that several CTAs share, in a fixed order: equal calls give equal bits.
+ * workspace: pa_prefill_workspace_bytes bytes, 16-byte aligned; its first int32 is the
+ * status word (bits as for pa_prefill_attention, and PA_DEV_BAD_SEQ_LEN also where
+ * n_b < 0), zeroed by the caller; the rest may hold anything.  It may be used by call after
+ * call on one stream, whatever their shapes; calls that can overlap use different ones
  * (two captured graphs that may run at once count).  A smaller one is refused with
  * PA_ERR_WORKSPACE_TOO_SMALL.
  */

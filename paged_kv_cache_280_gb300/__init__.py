@@ -595,7 +595,7 @@ def pa_prompt_attention(out, q, k, v, cu_lens, max_len, scale, status=None, stre
 
 
 def pa_prefill_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim) -> int:
-    """Bytes of the zero-filled workspace of pa_prefill_attention_fp8 / _fp4 calls whose chunks have up to max_q_len tokens."""
+    """Bytes of the workspace of pa_prefill_attention_fp8 / _fp4 calls whose chunks have up to max_q_len tokens."""
     out = _sz(0)
     _ok(_lib.pa_prefill_workspace_bytes(int(max_q_len), num_q_heads, num_kv_heads, head_dim, ctypes.byref(out)),
         "pa_prefill_workspace_bytes")
@@ -622,7 +622,7 @@ def _prefill_quant(call, name, out, q, k_pool, v_pool, pshape, bs, k_scale, v_sc
 def pa_prefill_attention_fp8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, cu_q_lens, max_q_len, scale,
                              workspace, stream=None):
     """pa_prefill_attention over FP8 pools (E4M3 codes [num_blocks][Hkv][bs][128]) with bf16 q/out [T][Hq][128].
-    workspace: a CUDA tensor of pa_prefill_workspace_bytes bytes, zero-filled once; its first int32 is the status word."""
+    workspace: a CUDA tensor of pa_prefill_workspace_bytes bytes, whose first int32 is the status word, zeroed by the caller."""
     nb, hkv, bs, d = pshape = k_pool.shape
     if _dtype_code(k_pool) != PA_FP8_E4M3 or d != q.shape[2]:
         raise PAError(1, f"pa_prefill_attention_fp8: pool {k_pool.dtype} {tuple(pshape)} for q {tuple(q.shape)}")

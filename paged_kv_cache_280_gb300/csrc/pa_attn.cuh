@@ -10,7 +10,7 @@
 // instead, so that either way one half's softmax runs while the tensor core works for the other.
 //   Packed: the units, most keys first, are dealt to the CTAs in snake order (PackedWalk).
 //   Pools:  the units' stages are laid end to end and cut in equal parts (pa_attn_plan.h), so that few rows over a long
-//           context fill the card; the pieces of a cut unit are joined by the last CTA to end (attn_join).
+//           context fill the card; the pieces of cut units are joined by a second kernel (attn_join_kernel).
 //
 // Warps.  0 .. 3 and 4 .. 7: the softmax of the two halves, a thread per row.  8: keys and values.  9 and 10: the MMAs
 // of the two halves.  11 (packed): query rows.  12 .. 15 (pools): query rows and widening of the codes.
@@ -48,7 +48,7 @@ struct AttnParams {
     const int32_t* seq_lens;       // null: packed
     const int32_t* cu_q_lens;
     int32_t* status;
-    int32_t* counts;               // pools: [2 * grid] pieces of a cut tile that have been stored, by the unit's first CTA
+    int4* cuts;                    // pools: [grid] the cut unit that begins in a CTA: first row of q, tokens, KV head, last CTA (-1: none)
     float2* part_ml;               // pools: [2 * grid slots][tiles][128]: maximum (base 2) and sum of a row's piece
     float* part_o;                 // pools: [2 * grid slots][tiles][128][D]
     int32_t part_tiles;            // tiles per slot
@@ -104,7 +104,7 @@ struct AttnLayout {
     static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors' exponents [2 pieces][2 tiles][128] bytes
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's (m, l) [128]
     static constexpr int kBarOff = kMlOff + 128 * 8;
-    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 17;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
     static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
     static_assert(kBytes <= kMaxSmem, "shared memory");
@@ -129,10 +129,8 @@ struct AttnBars {
     __device__ uint32_t tail() const { return at(kRest + 10); }      // packed: a V box with rows behind its sequence's end
     __device__ uint32_t odd_ml() const { return at(kRest + 11); }    // the odd half's maximum and sum are in shared memory
     __device__ uint32_t odd_read() const { return at(kRest + 12); }  // the even half's warps have read them, and its O
-    __device__ uint32_t drain(int t) const { return at(kRest + 15 + t); }
-    __device__ uint32_t verdict(int i) const { return at(kRest + 19 + i); }  // whether this CTA joins the i-th cut unit of one tile
-    __device__ uint32_t turn(int t) const { return at(kRest + 17 + t); }  // the half's turn at the tensor core
-    __device__ uint32_t join(int t) const { return at(kRest + 13 + t); }  // the half's four warps have come this far
+    __device__ uint32_t drain(int t) const { return at(kRest + 13 + t); }
+    __device__ uint32_t turn(int t) const { return at(kRest + 15 + t); }  // the half's turn at the tensor core
 };
 
 // One thread's bounded wait; gives up once the CTA's abort flag is set.  (The flag and the clock are looked at now and
@@ -840,105 +838,6 @@ __device__ __forceinline__ void at_store_bf16(uint16_t* dst, const float* x, boo
     }
 }
 
-// Pools: the pieces of tile t of a cut unit, stored by CTAs a .. b, joined into out by one half's four warps, or both halves':
-//     out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,   M = max_c m_c,
-// in the CTAs' order, so that the result does not depend on which of them ended last.  A warp takes four rows at a time:
-// a lane per piece for the factors, then a lane per D / 32 elements.  Trips to L2 are what it costs, so four rows' next
-// pieces (four, or eight) are on their way at once.
-template <int SRC, int D>
-__device__ __forceinline__ void at_join(const AttnParams& p, const AttnPiece& w, int t, int rows, int a, int b, int warp, int warps,
-                                        int lane) {
-    constexpr int E = D / 32, kRows = 4, kAhead = 16 / E;
-    struct alignas(4 * E) Part {
-        float x[E];
-    };
-    auto slot = [&](int c) { return ((int64_t)(2 * c + (c == a ? 1 : 0)) * p.part_tiles + t) * kAtRows; };  // (a holds the unit's beginning)
-    const int64_t first_row = (int64_t)w.c0 + w.i0 + t * p.tile_tokens;
-#pragma unroll 1
-    for (int r0 = warp; r0 < rows; r0 += warps * kRows) {
-        auto row = [&](int u) { return min(r0 + warps * u, rows - 1); };
-        float M[kRows], L[kRows], acc[kRows][E];
-        // (a piece that sees none of a row's keys has stored no O: its factor is 0 and what is read there unused)
-        float m_at[kRows];
-        Part o[kRows][kAhead];
-        auto fetch = [&](int c0) {
-            const int mine = min(c0 + (lane & (kAhead - 1)), b);
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                m_at[u] = __ldcg(p.part_ml + slot(mine) + row(u)).x;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const float* src = p.part_o + (slot(min(c0 + i, b)) + row(u)) * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                        o[u][i] = Part{v.x, v.y, v.z, v.w};
-                    } else {
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                        o[u][i] = Part{v.x, v.y};
-                    }
-                }
-            }
-        };
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) M[u] = -INFINITY, L[u] = 0.f;
-#pragma unroll 1
-        for (int c = a + lane; c - lane <= b; c += 32) {
-            float2 ml[kRows];
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) ml[u] = __ldcg(p.part_ml + slot(min(c, b)) + row(u));
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                if (c > b) ml[u].x = -INFINITY;
-                const float m = fmaxf(M[u], ml[u].x);
-                if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + ml[u].y * at_exp2(ml[u].x - m);
-                M[u] = m;
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, M[u], o), l2 = __shfl_xor_sync(0xffffffffu, L[u], o);
-                const float m = fmaxf(M[u], m2);
-                if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + l2 * at_exp2(m2 - m);
-                M[u] = m;
-            }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            L[u] = p.out_scale / L[u];
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
-        }
-#pragma unroll 1
-        for (int c0 = a; c0 <= b; c0 += kAhead) {
-            fetch(c0);
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const float f = m_at[u] > -INFINITY && c0 + (lane & (kAhead - 1)) <= b ? at_exp2(m_at[u] - M[u]) * L[u] : 0.f;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const float g = __shfl_sync(0xffffffffu, f, i);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[u][e] = g != 0.f ? acc[u][e] + g * o[u][i].x[e] : acc[u][e];
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int r = r0 + warps * u;
-            if (r < rows) {
-                const int tok = at_token(p, r);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ((first_row + tok) * p.num_q_heads +
-                                (int64_t)w.g * p.group + (r - tok * p.group)) * D + lane * E);
-                if constexpr (E == 4)
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[u][0], acc[u][1]), pack_bf16x2(acc[u][2], acc[u][3]));
-                else
-                    *dst = pack_bf16x2(acc[u][0], acc[u][1]);
-            }
-        }
-    }
-}
-
 // Half t: warps 4 t .. 4 t + 3, row r = 32 (warp % 4) + lane = TMEM lane r.
 template <int SRC, int D>
 __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange* range, int t, uint8_t* base, uint32_t tmem,
@@ -950,17 +849,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), row_tmem = lanes + kAtTmemHalf * t;
     float2* odd_ml = reinterpret_cast<float2*>(base + L::kMlOff);
     float c = p.scale_log2;  // > 0 (checked on the host)
-    int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0, met = 0;  // stages, pieces, final O of each half, odd halves handed over
-    int cuts = 0;  // pieces of cut units: a range has at most two, its first and its last
-    auto first_of = [&](const AttnPiece& w) { return (int)range_of(w.at, range->W, range->C); };
-    auto last_of = [&](const AttnPiece& w) {
-        return (int)range_of(w.at + stage_begin(w.nst - 1, w.one ? kOneTile : kTwoTiles, range->U), range->W, range->C);
-    };
-    auto meet = [&]() {  // the half's four warps
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.join(t));
-        return at_wait(bars.join(t), met++ & 1, abort_flag, p.status);
-    };
+    int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0;  // stages, pieces, final O of each half, odd halves handed over
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
     while (walk.next(p, w)) {
@@ -1109,15 +998,6 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
                 if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
                 ++hand, ++oc1;
             }
-            if constexpr (SRC != kAttnPacked) {  // one tile's pieces are joined by both halves
-                if (!(w.first && w.last)) {
-                    if (!at_wait(bars.verdict(cuts), 0, abort_flag, p.status)) return;
-                    if (misc[4 + 2 * cuts++]) {
-                        __threadfence();
-                        at_join<SRC, D>(p, w, 0, (i1 - i0) * G, first_of(w), last_of(w), warp, 8, lane);
-                    }
-                }
-            }
             continue;
         }
         // ---- O / l to out, or O, m and l to the join ----
@@ -1183,23 +1063,10 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             if (lane == 0) mbar_arrive(bars.odd_read());
         }
         if constexpr (SRC != kAttnPacked) {
-            if (!whole) {
-                if (valid) __stcg(p.part_ml + part, make_float2(m, l_run));
-                const int a = first_of(w), b = last_of(w);
-                __threadfence();
-                if (!meet()) return;
-                if (r == 0) {
-                    int32_t* count = p.counts + 2 * a + tile;
-                    const bool last = atomicAdd(count, 1) == b - a;
-                    if (last) *count = 0;  // for the next call
-                    misc[4 + 2 * cuts + t] = last;
-                    if (w.one) mbar_arrive(bars.verdict(cuts));
-                }
-                if (!meet()) return;
-                if (misc[4 + 2 * cuts++ + t]) {
-                    __threadfence();
-                    at_join<SRC, D>(p, w, tile, (i1 - i0) * G, a, b, warp & 3, w.one ? 8 : 4, lane);
-                }
+            if (!whole && valid) __stcg(p.part_ml + part, make_float2(m, l_run));
+            if (w.first && !w.last && t == 0 && r == 0) {
+                const int64_t last = w.at + stage_begin(w.nst - 1, w.one ? kOneTile : kTwoTiles, range->U);
+                p.cuts[blockIdx.x] = make_int4(w.c0 + i0, min(w.n - i0, w.one ? T : 2 * T), w.g, (int)range_of(last, range->W, range->C));
             }
         }
     }
@@ -1237,13 +1104,11 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         mbar_init(bars.q_empty(), 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(bars.drain(t), 1);
-            mbar_init(bars.verdict(t), 1);
             mbar_init(bars.turn(t), 1);
         }
         mbar_init(bars.tail(), 1);
         mbar_init(bars.odd_ml(), 4);
         mbar_init(bars.odd_read(), 4);
-        for (int t = 0; t < 2; ++t) mbar_init(bars.join(t), 4);
         fence_barrier_init();
         misc[0] = 0;
     }
@@ -1251,6 +1116,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     pdl_wait_prerequisites();
     if constexpr (L::kPools) {
         if (warp == kAtKvWarp) at_plan(p, range, lane);
+        if (tid == 0) p.cuts[blockIdx.x].w = -1;
     }
     if (blockIdx.x == 0 && warp == kAtQWarp) {
         for (int b = lane; b < p.num_seqs; b += 32) {
@@ -1299,6 +1165,123 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (warp == kAtMmaWarp) tmem_dealloc(tmem, kAtTmemCols);
 }
 
+// Pools: the pieces of the unit that begins in CTA a = blockIdx.x and ends in CTA b, joined into out:
+//     out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c,   M = max_c m_c,  in the CTAs' order.
+// A warp takes kJoinRows rows, a lane per piece for the factors, then a lane per D / 32 elements; the factors' and the first
+// pieces' loads are under way at once, for trips to L2 are what it costs.  A kernel of its own, on all SMs at once: the last
+// CTA of a unit to end took 19 us for a join of 256 rows (4 sequences' turns over 32 KV heads, FP8: 179 us in all, 163 with
+// this kernel; a mixed batch over 4-bit pools 33 and 23).  It is not let in before attn_kernel has ended: its blocks would
+// wait beside the last CTAs (166).
+constexpr int kJoinRows = 2, kJoinAhead = 4, kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps, 3) attn_join_kernel(const AttnParams p) {
+    constexpr int E = D / 32;
+    struct alignas(4 * E) Part {
+        float x[E];
+    };
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    const int4 cut = __ldcg(p.cuts + blockIdx.x);
+    const int a = blockIdx.x, b = cut.w, lane = threadIdx.x & 31, rows = cut.y * p.group, tile_rows = p.tile_tokens * p.group;
+    const int r0 = (blockIdx.y * kJoinWarps + threadIdx.x / 32) * kJoinRows;
+    if (b < 0 || r0 >= rows) return;
+    int64_t at[kJoinRows];  // the row's place in a slot's tiles
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u) {
+        const int r = min(r0 + u, rows - 1);
+        at[u] = r >= tile_rows ? kAtRows + r - tile_rows : r;
+    }
+    auto slot = [&](int c) { return (int64_t)(2 * c + (c == a ? 1 : 0)) * p.part_tiles * kAtRows; };  // (a holds the unit's beginning)
+    float m_at[kJoinRows];
+    Part o[kJoinRows][kJoinAhead];
+    // (a piece that sees none of a row's keys has stored no O: its factor is 0 and what is read there unused)
+    auto fetch = [&](int c0) {
+        const int mine = min(c0 + (lane & (kJoinAhead - 1)), b);
+#pragma unroll
+        for (int u = 0; u < kJoinRows; ++u) {
+            m_at[u] = __ldcg(p.part_ml + slot(mine) + at[u]).x;
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                if (c0 + i > b) continue;
+                const float* src = p.part_o + (slot(c0 + i) + at[u]) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                    o[u][i] = Part{v.x, v.y, v.z, v.w};
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                    o[u][i] = Part{v.x, v.y};
+                }
+            }
+        }
+    };
+    float2 ml[kJoinRows];
+    auto fetch_ml = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < kJoinRows; ++u) ml[u] = __ldcg(p.part_ml + slot(min(c, b)) + at[u]);
+    };
+    fetch_ml(a + lane);
+    fetch(a);
+    float M[kJoinRows], L[kJoinRows], acc[kJoinRows][E];
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u) M[u] = -INFINITY, L[u] = 0.f;
+#pragma unroll 1
+    for (int c = a + lane;; c += 32) {
+#pragma unroll
+        for (int u = 0; u < kJoinRows; ++u) {
+            if (c > b) ml[u].x = -INFINITY;
+            const float m = fmaxf(M[u], ml[u].x);
+            if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + ml[u].y * at_exp2(ml[u].x - m);
+            M[u] = m;
+        }
+        if (c - lane + 32 > b) break;
+        fetch_ml(c + 32);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+#pragma unroll
+        for (int u = 0; u < kJoinRows; ++u) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, M[u], x), l2 = __shfl_xor_sync(0xffffffffu, L[u], x);
+            const float m = fmaxf(M[u], m2);
+            if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + l2 * at_exp2(m2 - m);
+            M[u] = m;
+        }
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u) {
+        L[u] = p.out_scale / L[u];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
+    }
+#pragma unroll 1
+    for (int c0 = a;;) {
+#pragma unroll
+        for (int u = 0; u < kJoinRows; ++u) {
+            const float f = m_at[u] > -INFINITY && c0 + (lane & (kJoinAhead - 1)) <= b ? at_exp2(m_at[u] - M[u]) * L[u] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[u][e] = g != 0.f ? acc[u][e] + g * o[u][i].x[e] : acc[u][e];
+            }
+        }
+        c0 += kJoinAhead;
+        if (c0 > b) break;
+        fetch(c0);
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinRows; ++u) {
+        const int r = r0 + u;
+        if (r < rows) {
+            const int tok = at_token(p, r);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) +
+                                                        (((int64_t)cut.x + tok) * p.num_q_heads + (int64_t)cut.z * p.group + (r - tok * p.group)) * D + lane * E);
+            if constexpr (E == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[u][0], acc[u][1]), pack_bf16x2(acc[u][2], acc[u][3]));
+            else
+                *dst = pack_bf16x2(acc[u][0], acc[u][1]);
+        }
+    }
+}
+
 bool aligned_to(const void* ptr, unsigned bytes) { return (reinterpret_cast<uintptr_t>(ptr) & (bytes - 1)) == 0; }
 
 // One CTA per SM.
@@ -1315,8 +1298,12 @@ pa_status launch_attn(const AttnParams& p, int dev, int grid, const CUtensorMap&
         return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(&attn_kernel<SRC, D>)) == cudaSuccess ? a.numRegs : 0;
     }();
     if (regs != (L::kPools ? 128 : 168)) return PA_ERR_INTERNAL;
-    return launch_dependent(&attn_kernel<SRC, D>, dim3(grid), L::kThreads, L::kBytes, st, p, tq, tk, tv) == cudaSuccess ? PA_OK
-                                                                                                                   : PA_ERR_CUDA;
+    if (launch_dependent(&attn_kernel<SRC, D>, dim3(grid), L::kThreads, L::kBytes, st, p, tq, tk, tv) != cudaSuccess) return PA_ERR_CUDA;
+    if constexpr (L::kPools) {
+        const dim3 join(grid, p.part_tiles * kAtRows / (kJoinRows * kJoinWarps));
+        if (launch_dependent(&attn_join_kernel<D>, join, 32 * kJoinWarps, 0, st, p) != cudaSuccess) return PA_ERR_CUDA;
+    }
+    return PA_OK;
 }
 
 }  // namespace

@@ -7,17 +7,16 @@
 namespace pa {
 namespace {
 
-// The status head, then, from the next 256-byte boundary on, a count per CTA and tile and two slots per CTA for pieces of
-// cut units: a maximum and a sum per row, and the rows.
+// The status head, then, from the next 256-byte boundary on, the cut unit that begins in each CTA and two slots per CTA for
+// pieces of cut units: a maximum and a sum per row, and the rows.
 struct PrefillWorkspace {
-    size_t counts, ml, o, total;
+    size_t ml, o, total;
     int tiles;
 };
 PrefillWorkspace prefill_workspace(int max_q_len, int group, int head_dim, int sms) {
     PrefillWorkspace w;
     w.tiles = max_q_len > kAtRows / group ? 2 : 1;
-    w.counts = 0;
-    w.ml = w.counts + (((size_t)2 * sms * sizeof(int32_t) + 255) & ~(size_t)255);
+    w.ml = ((size_t)sms * sizeof(int4) + 255) & ~(size_t)255;
     const size_t rows = (size_t)2 * sms * w.tiles * kAtRows;
     w.o = w.ml + rows * sizeof(float2);
     w.total = 2 * kStatusHeadBytes + w.o + rows * head_dim * sizeof(float);
@@ -55,7 +54,7 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.block_tables = block_tables, p.seq_lens = seq_lens, p.cu_q_lens = cu_q_lens;
     p.status = static_cast<int32_t*>(workspace);
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + kStatusHeadBytes + 255) & ~(uintptr_t)255);
-    p.counts = reinterpret_cast<int32_t*>(base + ws.counts);
+    p.cuts = reinterpret_cast<int4*>(base);
     p.part_ml = reinterpret_cast<float2*>(base + ws.ml), p.part_o = reinterpret_cast<float*>(base + ws.o);
     p.part_tiles = ws.tiles;
     p.max_blocks_per_seq = max_blocks_per_seq, p.num_seqs = num_seqs, p.num_q_heads = num_q_heads;

@@ -207,6 +207,19 @@ def test_one_workspace_for_calls_of_many_shapes(kind, d):
 
 
 @pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("byte", [0xFF, 0x7F])
+def test_a_workspace_may_hold_anything_behind_its_status_word(kind, d, byte):
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    for c in (Case(610, kind, [4000, 700], [3, 500], 8, 2, d, 16), Case(611, kind, [40], [1], 1, 1, d, 32)):
+        want = c.run().clone()
+        ws = torch.full((pa.pa_prefill_workspace_bytes(int(c.news.max()), c.hq, c.hkv, d),), byte, dtype=torch.uint8, device="cuda")
+        ws[:4] = 0
+        assert torch.equal(c.run(ws), want) and c.status() == 0
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
 @pytest.mark.parametrize("lens,news,hq,hkv", [([2500, 2500], [300, 40], 4, 4), ([700] * 5, [200] * 5, 4, 4), ([9000, 129], [1, 129], 8, 1)])
 def test_chunks_repeat_bit_for_bit(kind, d, lens, news, hq, hkv):
     """The same call many times over: whichever CTA ends last, and however the roles of a CTA interleave."""
