@@ -97,8 +97,7 @@ struct AttnLayout {
     static constexpr int kTileBytes = kPanels * kPanelBytes;  // a query tile, or K or V of a stage
     static constexpr int kSlots = kPools ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
     static constexpr int kRawBytes = SRC == kAttnFp8 ? 128 * D : 128 * fp4_row_bytes(D);
-    static constexpr int kRaws = !kPools ? 0 : SRC == kAttnFp8 ? 4 : D == 128 ? 6 : 8;  // even: a slot always serves the same widening warps
-    static constexpr int kWideners = 2;  // warps that widen an item
+    static constexpr int kRaws = !kPools ? 0 : SRC == kAttnFp8 ? 4 : D == 128 ? 6 : 8;  // even: a slot always serves the same pair of widening warps
     static constexpr int kRingOff = 2 * kTileBytes;
     static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
     static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors' exponents [2 pieces][2 tiles][128] bytes
@@ -362,12 +361,29 @@ struct AttnItems {
     }
 };
 
+// The stage of a piece's item i in that order (keys are zeroed behind the sequence's end like values: nothing reads them).
+__device__ __forceinline__ int at_item_stage(const AttnPiece& w, int i) {
+    if (!w.one) return i >> 1;
+    const int first = min(2, w.ns), m = i - first;  // the keys ahead, then a stage's values and the keys two on
+    return m < 0 ? i : m < 2 * (w.ns - first) ? (m >> 1) + ((m & 1) << 1) : i - w.ns;
+}
+
 // The slots of a piece's stages in that order, from the first slot c on.
 struct AttnSlots {
     int c, ns, lead;
     __device__ AttnSlots(const AttnPiece& w, int c) : c(c), ns(w.ns), lead(w.one ? 2 : 1) {}
     __device__ __forceinline__ int k(int j) const { return c + (lead == 1 ? 2 * j : j < 2 ? j : 2 * j - 1); }
     __device__ __forceinline__ int v(int j) const { return c + (lead == 1 ? 2 * j + 1 : min(2 * j + 2, ns + j)); }
+};
+
+template <int NS>
+struct AttnRing {  // a slot of NS and the parity of its fill
+    uint32_t slot, parity;
+    __device__ __forceinline__ void ahead(uint32_t by) {  // by < 2 NS
+        slot += by;
+        if (slot >= NS) slot -= NS, parity ^= 1u;
+        if (slot >= NS) slot -= NS, parity ^= 1u;
+    }
 };
 
 // ---- loads -----------------------------------------------------------------------------------------
@@ -579,21 +595,24 @@ struct AttnQueries {
 //   4-bit: four rows, two 16-byte chunks (32 codes, two scales) of each; at head_dim 128 two rows' first halves and two
 //   rows' second halves.
 // How far the loop is unrolled weighs its latencies against the instruction cache, which all roles share (32 sequences of 5
-// tokens, FP8, and 2 of 9 over 131072 4-bit keys: 2 turns 118 and 164 us, 4: 118 and 159, all: 125 and 149).  With all four
-// warps on each item every wait's latency counts on every item: 127 and 156.
+// tokens, FP8, and 2 of 9 over 131072 4-bit keys: 2 turns 113 and 164 us, 4: 112 and 139, all: 125 and 142).  All four warps
+// on each item wait for each item's barriers: 127 and 156.
 template <int SRC, int D>
 __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
                                          volatile int32_t* abort_flag, int part, int lane) {
     using L = AttnLayout<SRC, D>;
-    constexpr int kRows = kAttnKeys / L::kWideners;  // of a warp and item
+    constexpr int kRows = kAttnKeys / 2;  // of a warp and item
     constexpr int kPerRow = D == 128 ? 2 : 1;        // turns per row: the other half of the row
     constexpr int kStep = SRC == kAttnFp8 ? 8 : 16;  // rows a turn (of two)
     constexpr int kTurns = kRows / kStep * kPerRow;
     RangeWalk walk(p, range);
     AttnPiece w;
-    int sc = 0, pc = 0;
+    int pc = 0;
+    // the pair's first raw slot and slot
+    AttnRing<L::kRaws> raws{(uint32_t)part >> 1, 0u};
+    AttnRing<L::kSlots> slots{(uint32_t)part >> 1, 0u};
     const int l8 = lane & 7, l4 = lane >> 3;
-    const int r_first = kRows * (part % L::kWideners) + (SRC == kAttnFp8 ? 2 * l4 + (l8 >> 2) : 4 * l4 + (l8 >> 1));
+    const int r_first = kRows * (part & 1) + (SRC == kAttnFp8 ? 2 * l4 + (l8 >> 2) : 4 * l4 + (l8 >> 1));
     const uint32_t panel_first = D == 128 ? l8 >> 2 : 0;
     const uint32_t r7 = (uint32_t)r_first & 7u;
     // where the thread's first codes and scales are in a raw slot; 4-bit: from 16 rows to the next 16, and on to those behind
@@ -619,18 +638,15 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
             if (lane == 0) mbar_arrive(bars.q_full());
         };
         if (q_free) load_queries();
-        AttnItems items(w);
-        for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
-            if (i == 1 && !q_free) {
+        bool q_due = !q_free;
+        for (int i = part >> 1; i < 2 * w.ns; i += 2) {  // (a piece's items are even in number)
+            if (q_due && i > 0) {
+                q_due = false;
                 if (!at_wait(bars.q_empty(), q_parity, abort_flag, p.status)) return;
                 load_queries();
             }
-            int j;
-            const bool is_v = items.next(j);
-            if (sc % (4 / L::kWideners) != part / L::kWideners) continue;
-            const int rs = sc % L::kRaws, fs = sc % L::kSlots;
-            if (!at_wait(bars.raw_full(rs), (sc / L::kRaws) & 1, abort_flag, p.status)) return;
-            const uint32_t raw = base_s + L::kRawOff + rs * L::kRawBytes;
+            if (!at_wait(bars.raw_full(raws.slot), raws.parity, abort_flag, p.status)) return;
+            const uint32_t raw = base_s + L::kRawOff + raws.slot * L::kRawBytes;
             auto load = [&](int turn) {
                 const uint32_t step = turn / kPerRow, panel = panel_first ^ (turn & (kPerRow - 1));
                 Codes x;
@@ -645,16 +661,15 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                 return x;
             };
             Codes next = load(0);
-            const uint32_t dst = base_s + L::kRingOff + fs * L::kTileBytes;
-            const int keep = is_v ? w.len - (w.k0 + j) * kAttnKeys : kAttnKeys;  // rows of the sequence
-            if (!at_wait(bars.empty(fs), ((sc / L::kSlots) & 1) ^ 1, abort_flag, p.status)) return;
-#pragma unroll(SRC == kAttnFp8 ? 2 : kTurns)
+            const uint32_t dst = base_s + L::kRingOff + slots.slot * L::kTileBytes;
+            const int keep = min(kAttnKeys, w.len - (w.k0 + at_item_stage(w, i)) * kAttnKeys);  // rows of the sequence
+            if (!at_wait(bars.empty(slots.slot), slots.parity ^ 1u, abort_flag, p.status)) return;
+#pragma unroll 4
             for (int turn = 0; turn < kTurns; ++turn) {
                 Codes x = next;
                 if (turn + 1 < kTurns) next = load(turn + 1);
                 const int r = r_first + turn / kPerRow * kStep;
                 const uint32_t row = dst + (panel_first ^ (turn & (kPerRow - 1))) * L::kPanelBytes + r * 128;
-                if (r >= keep) x.c = make_uint4(0u, 0u, 0u, 0u), x.scales = 0;
                 if constexpr (SRC == kAttnFp8) {
                     const uint32_t ch = 2 * (l8 & 3);
                     uint32_t h[8];
@@ -677,14 +692,30 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
                     }
                 }
             }
+            if (keep < kAttnKeys) {  // (the whole warp) rows behind the sequence's end: whatever is there may be NaN
+#pragma unroll 1
+                for (int turn = 0; turn < kTurns; ++turn) {
+                    const int r = r_first + turn / kPerRow * kStep;
+                    const uint32_t row = dst + (panel_first ^ (turn & (kPerRow - 1))) * L::kPanelBytes + r * 128;
+                    const int first = SRC == kAttnFp8 ? 2 * (l8 & 3) : 4 * (l8 & 1);
+                    if (r < keep) continue;
+#pragma unroll 1
+                    for (int e = first; e < first + (SRC == kAttnFp8 ? 2 : 4); ++e) sts16(row + ((e ^ r7) << 4), 0u, 0u, 0u, 0u);
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 // Only now is the raw slot free: its codes were in registers long ago, but nothing orders a shared-memory
                 // load that has not returned before the next copy into the slot, only the use of what it loaded does.
-                mbar_arrive(bars.raw_empty(rs));
-                mbar_arrive(bars.full(fs));
+                mbar_arrive(bars.raw_empty(raws.slot));
+                mbar_arrive(bars.full(slots.slot));
             }
+            raws.ahead(2), slots.ahead(2);
+        }
+        if (q_due) {
+            if (!at_wait(bars.q_empty(), q_parity, abort_flag, p.status)) return;
+            load_queries();
         }
         ++pc;
     }
@@ -725,14 +756,7 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
             umma_bf16_tmem_a_lo<kk * 128>(d + kAtTmemO, d + kAtTmemP + kk * 8, vb, hi, idesc_o, i > 0 ? 1u : acc0);
         });
     };
-    struct Ring {  // a slot and the parity of its fill
-        uint32_t slot, parity;
-        __device__ __forceinline__ void ahead(uint32_t by) {  // by < 2 NS
-            slot += by;
-            if (slot >= NS) slot -= NS, parity ^= 1u;
-            if (slot >= NS) slot -= NS, parity ^= 1u;
-        }
-    };
+    using Ring = AttnRing<NS>;
     AttnWalk<SRC> walk(p, range);
     AttnPiece w;
     Ring first{0u, 0u};           // the piece's first slot
@@ -1087,12 +1111,12 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     AttnBars<SRC, D> bars{base_s + L::kBarOff};
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
-            mbar_init(bars.full(s), L::kPools ? L::kWideners : 1);  // each warp that widens it, or the producer's expect_tx
+            mbar_init(bars.full(s), L::kPools ? 2 : 1);  // each warp that widens it, or the producer's expect_tx
             mbar_init(bars.empty(s), 2);                 // tcgen05.commit after each half's last MMA of the slot
         }
         for (int s = 0; s < L::kRaws; ++s) {
             mbar_init(bars.raw_full(s), 1);
-            mbar_init(bars.raw_empty(s), L::kWideners);
+            mbar_init(bars.raw_empty(s), 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bars.s_full(t), 1);
