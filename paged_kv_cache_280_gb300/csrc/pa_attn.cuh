@@ -103,9 +103,11 @@ struct AttnLayout {
     static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors' exponents [2 pieces][2 tiles][128] bytes
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's (m, l) [128]
     static constexpr int kBarOff = kMlOff + 128 * 8;
-    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 17;
-    static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // abort flag, TMEM address, join flags, work range
-    static constexpr int kBytes = kMiscOff + 128 + 1024;     // +1 KB to align the base
+    static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
+    static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // abort flag, TMEM address; work range at + 16
+    static constexpr int kPieceOff = kMiscOff + 80;                           // two pieces of kPieceBytes
+    static constexpr int kPieceBytes = 48;
+    static constexpr int kBytes = kPieceOff + 2 * kPieceBytes + 1024;  // +1 KB to align the base
     static_assert(kBytes <= kMaxSmem, "shared memory");
 };
 
@@ -129,6 +131,8 @@ struct AttnBars {
     __device__ uint32_t odd_ml() const { return at(kRest + 11); }    // the odd half's maximum and sum are in shared memory
     __device__ uint32_t odd_read() const { return at(kRest + 12); }  // the even half's warps have read them, and its O
     __device__ uint32_t drain(int t) const { return at(kRest + 13 + t); }
+    __device__ uint32_t piece_full(int i) const { return at(kRest + 17 + i); }   // a piece's entry is written
+    __device__ uint32_t piece_empty(int i) const { return at(kRest + 19 + i); }  // every warp of a role has read it
     __device__ uint32_t turn(int t) const { return at(kRest + 15 + t); }  // the half's turn at the tensor core
 };
 
@@ -171,7 +175,7 @@ __device__ __forceinline__ int at_sequence(const AttnParams& p, int b, int& c0, 
     return wrong ? 0 : n;
 }
 
-// A run of stages of one unit.  Every role walks the same pieces in the same order.
+// A run of stages of one unit.  All roles take the same pieces in the same order.
 struct AttnPiece {
     int b, g, c0, n, len;
     int i0;         // the unit's first new token
@@ -179,8 +183,8 @@ struct AttnPiece {
     int k0, ns;     // stages k0 .. k0 + ns - 1 of the unit
     int n0;         // two tiles: how many of them the first tile sees
     bool first, last;  // the unit's first, last stage is among them
-    int64_t at;     // pools: where the unit begins on the line of work
-    int nst;        // the unit's stages
+    int cut_end;    // pools: the last CTA of a cut unit that begins here, else -1
+    int nst;        // the unit's stages (of the walks)
 };
 
 __device__ __forceinline__ void at_fields(const AttnParams& p, int m, AttnPiece& w) {
@@ -227,7 +231,7 @@ struct PackedWalk {
                 w.n = at_sequence<kAttnPacked>(p, w.b, w.c0, w.len);
                 at_fields(p, m, w);
                 at_stages(p, 0, w.nst, w);
-                w.at = 0;
+                w.cut_end = -1;
                 ++wave;
                 return true;
             }
@@ -247,13 +251,14 @@ struct AttnRange {
     int32_t n, len, c0;  // of sequence b
 };
 struct RangeWalk {
-    int64_t at, end;
-    int b, g, m, k, U;
+    int64_t at, end, W;
+    int b, g, m, k, U, C;
     bool fresh;
     int n, len, c0;
     __device__ RangeWalk(const AttnParams&, const void* range) : fresh(false) {
         const volatile AttnRange* r = static_cast<const volatile AttnRange*>(range);
         at = r->at, end = r->end, b = r->b, g = r->g, m = r->m, k = r->k, n = r->n, len = r->len, c0 = r->c0, U = r->U;
+        W = r->W, C = r->C;
     }
     __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
         while (at < end) {
@@ -269,7 +274,7 @@ struct RangeWalk {
             at_fields(p, m, w);
             const int wt = w.one ? kOneTile : kTwoTiles;
             const int k0 = min(k, w.nst), k1 = (int)min((int64_t)w.nst, stage_at(end - at, wt, U));
-            w.at = at;
+            w.cut_end = k0 == 0 && k1 < w.nst ? (int)range_of(at + stage_begin(w.nst - 1, wt, U), W, C) : -1;
             if (k1 < w.nst) {
                 at = end;
             } else {
@@ -288,8 +293,6 @@ struct RangeWalk {
         return false;
     }
 };
-template <int SRC>
-using AttnWalk = std::conditional_t<SRC == kAttnPacked, PackedWalk, RangeWalk>;
 
 // One warp: this CTA's range.
 __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, int lane) {
@@ -346,6 +349,61 @@ __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, i
     }
 }
 
+// Sequences that break the call's bounds are flagged by one warp of the first CTA, when it has nothing else to do.
+template <int SRC>
+__device__ __forceinline__ void at_flag_sequences(const AttnParams& p, int lane) {
+    if (blockIdx.x) return;
+    for (int b = lane; b < p.num_seqs; b += 32) {
+        int c0, len;
+        bool bad;
+        at_sequence<SRC>(p, b, c0, len, &bad);
+        if (bad) flag_status(p.status, PA_DEV_BAD_SEQ_LEN);
+    }
+}
+
+// The pieces in shared memory: one warp walks and writes them two ahead, the other roles read them.  (Walked by every role
+// for itself, the MMA and softmax warps' walk, about 2000 cycles, lay between a piece's last stage and the next one's first.)
+template <int SRC, int D>
+struct AttnPieces {
+    using L = AttnLayout<SRC, D>;
+    uint8_t* base;
+    AttnBars<SRC, D> bars;
+    int i;
+    __device__ AttnPieces(uint8_t* base, const AttnBars<SRC, D>& bars) : base(base), bars(bars), i(0) {}
+    __device__ __forceinline__ void get(int n, AttnPiece& w) const {
+        const uint32_t at = bars.base - L::kBarOff + L::kPieceOff + (n & 1) * L::kPieceBytes;
+        const uint4 a = lds16(at), b = lds16(at + 16), c = lds16(at + 32);
+        const int4 x = {(int)a.x, (int)a.y, (int)a.z, (int)a.w}, y = {(int)b.x, (int)b.y, (int)b.z, (int)b.w}, z = {(int)c.x, (int)c.y, (int)c.z, 0};
+        w.b = x.x, w.g = x.y, w.c0 = x.z, w.n = x.w;
+        w.len = y.x, w.i0 = y.y, w.k0 = y.z, w.ns = y.w;
+        w.n0 = z.x, w.one = z.y & 1, w.first = z.y & 2, w.last = z.y & 4, w.cut_end = z.z, w.nst = 0;
+    }
+    // A whole warp: the next piece; false behind the last one, or when a wait has been given up.
+    __device__ __forceinline__ bool next(AttnPiece& w, volatile int32_t* abort_flag, int32_t* status, int lane) {
+        if (!at_wait(bars.piece_full(i & 1), (i >> 1) & 1, abort_flag, status)) return false;
+        get(i, w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.piece_empty(i & 1));
+        ++i;
+        __syncwarp();
+        return w.ns > 0;
+    }
+    // The walking warp: piece i (have: false behind the last one).
+    __device__ __forceinline__ bool put(const AttnPiece& w, bool have, volatile int32_t* abort_flag, int32_t* status, int lane) {
+        if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status)) return false;
+        if (lane == 0) {
+            int4* e = reinterpret_cast<int4*>(base + L::kPieceOff + (i & 1) * L::kPieceBytes);
+            e[0] = make_int4(w.b, w.g, w.c0, w.n);
+            e[1] = make_int4(w.len, w.i0, w.k0, have ? w.ns : 0);
+            e[2] = make_int4(w.n0, (w.one ? 1 : 0) | (w.first ? 2 : 0) | (w.last ? 4 : 0), w.cut_end, 0);
+            mbar_arrive(bars.piece_full(i & 1));
+        }
+        ++i;
+        __syncwarp();
+        return true;
+    }
+};
+
 // The stages of a piece in the order of their slots: K runs ahead of V by one stage, by two where two halves of one
 // tile take turns.
 struct AttnItems {
@@ -400,11 +458,11 @@ __device__ __forceinline__ void at_load_packed(const AttnParams& p, const CUtens
         prefetch_tensormap(tk);
         prefetch_tensormap(tv);
     }
-    PackedWalk walk(p, nullptr);
+    AttnPieces<kAttnPacked, D> pieces(base, bars);
     AttnPiece w;
     int sc = 0, tails = 0;
     bool ok = true;
-    while (ok && walk.next(p, w)) {
+    while (ok && pieces.next(w, abort_flag, p.status, lane)) {
         AttnItems items(w);
         for (int i = 0; i < 2 * w.ns; ++i, ++sc) {
             int j;
@@ -448,17 +506,28 @@ __device__ __forceinline__ void at_load_packed(const AttnParams& p, const CUtens
 }
 
 // Packed: a piece's query tiles (3-D boxes of 64 elements x G heads x 128 / G tokens), once the last piece's Q K^T have
-// completed.  A warp of its own, so that keys and values run ahead into the next piece.
+// completed.  A warp of its own, so that keys and values run ahead into the next piece; it also walks.
 template <int D>
-__device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUtensorMap* tq, uint32_t base_s,
+__device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUtensorMap* tq, uint8_t* base, uint32_t base_s,
                                                  const AttnBars<kAttnPacked, D>& bars, volatile int32_t* abort_flag, int lane) {
     using L = AttnLayout<kAttnPacked, D>;
     if (lane == 0) prefetch_tensormap(tq);
     const uint32_t tile_bytes = (uint32_t)(L::kPanels * p.group * p.tile_tokens * 128);
     PackedWalk walk(p, nullptr);
-    AttnPiece w;
+    AttnPieces<kAttnPacked, D> pieces(base, bars);
+    AttnPiece ahead, w;
     int pc = 0;
-    while (walk.next(p, w)) {
+    bool more = true;  // pieces to put
+    auto put = [&]() {
+        const bool have = walk.next(p, ahead);
+        more = pieces.put(ahead, have, abort_flag, p.status, lane) && have;
+    };
+    put();
+    if (more) put();
+    for (;;) {
+        if (pc == pieces.i) break;  // (a wait was given up)
+        pieces.get(pc, w);
+        if (w.ns == 0) break;
         if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) break;
         if (lane == 0) {
             const int tiles = w.one ? 1 : 2;
@@ -471,23 +540,45 @@ __device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUte
         }
         __syncwarp();
         ++pc;
+        if (more) put();
     }
     if (pc > 0) mbar_wait(bars.q_full(), (pc - 1) & 1);
+    __syncwarp();
+    at_flag_sequences<kAttnPacked>(p, lane);
+    __syncwarp();
+}
+
+// Pools: the walk, a warp of its own.
+template <int SRC, int D>
+__device__ __forceinline__ void at_walk(const AttnParams& p, AttnRange* range, uint8_t* base, const AttnBars<SRC, D>& bars,
+                                        volatile int32_t* abort_flag, int lane) {
+    at_plan(p, range, lane);
+    __syncwarp();
+    RangeWalk walk(p, range);
+    AttnPieces<SRC, D> pieces(base, bars);
+    AttnPiece w;
+    for (bool more = true; more;) {
+        const bool have = walk.next(p, w);
+        more = pieces.put(w, have, abort_flag, p.status, lane) && have;
+    }
+    __syncwarp();
+    at_flag_sequences<SRC>(p, lane);
+    __syncwarp();
 }
 
 // Pools: the codes of each stage's blocks, one bulk copy a block (its rows of one KV head are contiguous).  The table
 // entry of the next item is fetched before the wait for a free slot.
 template <int SRC, int D>
-__device__ __forceinline__ void at_load_raw(const AttnParams& p, const void* range, uint32_t base_s, const AttnBars<SRC, D>& bars,
+__device__ __forceinline__ void at_load_raw(const AttnParams& p, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
                                             volatile int32_t* abort_flag, int lane) {
     using L = AttnLayout<SRC, D>;
     const int per = kAttnKeys >> p.bs_shift;                       // blocks per stage
     const uint32_t bytes = (uint32_t)(L::kRawBytes / kAttnKeys) << p.bs_shift;  // of a block and head
-    RangeWalk walk(p, range);
+    AttnPieces<SRC, D> pieces(base, bars);
     AttnPiece w;
     int sc = 0;
     bool ok = true;
-    while (ok && walk.next(p, w)) {
+    while (ok && pieces.next(w, abort_flag, p.status, lane)) {
         const int blocks = (w.len + (1 << p.bs_shift) - 1) >> p.bs_shift;
         const int32_t* table = p.block_tables + (int64_t)w.b * p.max_blocks_per_seq;
         AttnItems items(w);
@@ -598,14 +689,14 @@ struct AttnQueries {
 // tokens, FP8, and 2 of 9 over 131072 4-bit keys: 2 turns 113 and 164 us, 4: 112 and 139, all: 125 and 142).  All four warps
 // on each item wait for each item's barriers: 127 and 156.
 template <int SRC, int D>
-__device__ __forceinline__ void at_widen(const AttnParams& p, const void* range, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
+__device__ __forceinline__ void at_widen(const AttnParams& p, uint8_t* base, uint32_t base_s, const AttnBars<SRC, D>& bars,
                                          volatile int32_t* abort_flag, int part, int lane) {
     using L = AttnLayout<SRC, D>;
     constexpr int kRows = kAttnKeys / 2;  // of a warp and item
     constexpr int kPerRow = D == 128 ? 2 : 1;        // turns per row: the other half of the row
     constexpr int kStep = SRC == kAttnFp8 ? 8 : 16;  // rows a turn (of two)
     constexpr int kTurns = kRows / kStep * kPerRow;
-    RangeWalk walk(p, range);
+    AttnPieces<SRC, D> pieces(base, bars);
     AttnPiece w;
     int pc = 0;
     // the pair's first raw slot and slot
@@ -627,7 +718,7 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
         uint4 c;
         uint16_t scales;
     };
-    while (walk.next(p, w)) {
+    while (pieces.next(w, abort_flag, p.status, lane)) {
         // The query rows first if their place is free already; else the first keys are widened before it is.
         const AttnQueries<SRC, D> queries(p, w, base_s, part, lane);
         const uint32_t q_parity = (pc & 1) ^ 1;
@@ -727,7 +818,7 @@ __device__ __forceinline__ void at_widen(const AttnParams& p, const void* range,
 // softmax has pushed out of the instruction cache: about 600 cycles a turn, beside 1024 of MMAs) must run beside the other
 // thread's MMAs.  Without turns the halves fall into step and wait for the tensor core, and it for them, at once.
 template <int SRC, int D>
-__device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, uint32_t t, uint32_t base_s, uint32_t tmem,
+__device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t* base, uint32_t base_s, uint32_t tmem,
                                        const AttnBars<SRC, D>& bars, volatile int32_t* abort_flag, int lane) {
     using L = AttnLayout<SRC, D>;
     constexpr int NS = L::kSlots;
@@ -757,13 +848,13 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, const void* range, u
         });
     };
     using Ring = AttnRing<NS>;
-    AttnWalk<SRC> walk(p, range);
+    AttnPieces<SRC, D> pieces(base, bars);
     AttnPiece w;
     Ring first{0u, 0u};           // the piece's first slot
     uint32_t pc = 0, ck = 0, rounds = 0;  // pieces, stages of this half, turns
     bool ok = true;
     const uint32_t d = tmem + kAtTmemHalf * t;
-    while (__shfl_sync(0xffffffffu, (int)ok, 0) && walk.next(p, w)) {
+    while (__shfl_sync(0xffffffffu, (int)ok, 0) && pieces.next(w, abort_flag, p.status, lane)) {
         if (lane == 0) {
             using First = std::integral_constant<int, 0>;
             using Second = std::integral_constant<int, 1>;
@@ -864,7 +955,7 @@ __device__ __forceinline__ void at_store_bf16(uint16_t* dst, const float* x, boo
 
 // Half t: warps 4 t .. 4 t + 3, row r = 32 (warp % 4) + lane = TMEM lane r.
 template <int SRC, int D>
-__device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange* range, int t, uint8_t* base, uint32_t tmem,
+__device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* base, uint32_t tmem,
                                            const AttnBars<SRC, D>& bars, volatile int32_t* misc, int warp, int lane) {
     using L = AttnLayout<SRC, D>;
     volatile int32_t* abort_flag = misc;
@@ -874,9 +965,9 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
     float2* odd_ml = reinterpret_cast<float2*>(base + L::kMlOff);
     float c = p.scale_log2;  // > 0 (checked on the host)
     int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0;  // stages, pieces, final O of each half, odd halves handed over
-    AttnWalk<SRC> walk(p, range);
+    AttnPieces<SRC, D> pieces(base, bars);
     AttnPiece w;
-    while (walk.next(p, w)) {
+    while (pieces.next(w, abort_flag, p.status, lane)) {
         const int mine = w.one ? (t ? w.ns / 2 : (w.ns + 1) / 2) : (t ? w.ns : w.n0);
         const bool other = w.one && w.ns > 1;  // both halves work on the one tile
         const int tile = w.one ? 0 : t;
@@ -884,7 +975,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         const int tok = i0 + at_token(p, r);
         const bool valid = r < T * G && tok < i1;
         const int pos = w.len - w.n + (valid ? tok : i1 - 1);
-        const int kend = w.len - w.n + i1;  // keys that the tile's last row sees
+        const int pos_low = __shfl_sync(0xffffffffu, pos, 0), pos_high = __shfl_sync(0xffffffffu, pos, 31);  // (they do not fall)
         float m_raw = -INFINITY, l_run = 0.f;  // maximum of the raw scores, and the weights' sum
         for (int i = 0; i < mine; ++i, ++ck) {
             const int k = w.k0 + (w.one ? 2 * i + t : i);
@@ -900,18 +991,24 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             // This S was issued after the last P V of this half and completes after it: O is up to date, and no MMA
             // touches this half's TMEM until this warp arrives on p_first.
             const int key0 = k * kAttnKeys;
-            const int nq = min(4, (kend - key0 + 31) >> 5);  // quarters that some row of the tile sees
-            // Masked scores become -inf: where the stage reaches past the row's position, S is rewritten so first.
-            if (__any_sync(0xffffffffu, key0 + kAttnKeys - 1 > pos)) {
+            const int nq = min(4, (pos_high - key0 + 32) >> 5);  // quarters that some row of the warp sees
+            // Masked scores become -inf: the quarters that reach past the position of some of the warp's rows are rewritten so
+            // first (those past all of them without being read).
+            if (key0 + kAttnKeys - 1 > pos_low) {
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = max(0, pos_low + 1 - key0) >> 5; q < 4; ++q) {
                     uint32_t x[32];
-                    tmem_ld32(row_tmem + 32 * q, x);
-                    tmem_wait_ld32(x);
                     const int seen = pos - key0 - 32 * q;
+                    if (q < nq) {
+                        tmem_ld32(row_tmem + 32 * q, x);
+                        tmem_wait_ld32(x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e > seen) x[e] = __float_as_uint(-INFINITY);
+                        for (int e = 0; e < 32; ++e)
+                            if (e > seen) x[e] = __float_as_uint(-INFINITY);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(-INFINITY);
+                    }
                     tmem_st32(row_tmem + 32 * q, x);
                 }
                 tmem_wait_st();
@@ -970,7 +1067,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
             uint64_t sum2 = f2_pack(0.f, 0.f);
             auto weigh = [&](int q, const uint32_t(&x)[32]) {
                 uint32_t pw[16];
-                if (q >= nq) {  // past the tile's last position
+                if (q >= nq) {  // past the warp's last position
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pw[e] = 0u;
                 } else {
@@ -1088,10 +1185,8 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, const AttnRange*
         }
         if constexpr (SRC != kAttnPacked) {
             if (!whole && valid) __stcg(p.part_ml + part, make_float2(m, l_run));
-            if (w.first && !w.last && t == 0 && r == 0) {
-                const int64_t last = w.at + stage_begin(w.nst - 1, w.one ? kOneTile : kTwoTiles, range->U);
-                p.cuts[blockIdx.x] = make_int4(w.c0 + i0, min(w.n - i0, w.one ? T : 2 * T), w.g, (int)range_of(last, range->W, range->C));
-            }
+            if (w.cut_end >= 0 && t == 0 && r == 0)
+                p.cuts[blockIdx.x] = make_int4(w.c0 + i0, min(w.n - i0, w.one ? T : 2 * T), w.g, w.cut_end);
         }
     }
 }
@@ -1106,8 +1201,8 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_s - raw_s);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int32_t* misc = reinterpret_cast<volatile int32_t*>(base + L::kMiscOff);  // abort flag; TMEM address; join flags
-    AttnRange* range = reinterpret_cast<AttnRange*>(base + L::kMiscOff + 32);
+    volatile int32_t* misc = reinterpret_cast<volatile int32_t*>(base + L::kMiscOff);  // abort flag; TMEM address
+    AttnRange* range = reinterpret_cast<AttnRange*>(base + L::kMiscOff + 16);
     AttnBars<SRC, D> bars{base_s + L::kBarOff};
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
@@ -1129,6 +1224,8 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(bars.drain(t), 1);
             mbar_init(bars.turn(t), 1);
+            mbar_init(bars.piece_full(t), 1);
+            mbar_init(bars.piece_empty(t), L::kPools ? 15 : 11);  // softmax 8, MMA 2, keys and values 1, widening 4
         }
         mbar_init(bars.tail(), 1);
         mbar_init(bars.odd_ml(), 4);
@@ -1139,16 +1236,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (warp == kAtMmaWarp) tmem_alloc(base_s + L::kMiscOff + 8, kAtTmemCols);
     pdl_wait_prerequisites();
     if constexpr (L::kPools) {
-        if (warp == kAtKvWarp) at_plan(p, range, lane);
         if (tid == 0) p.cuts[blockIdx.x].w = -1;
-    }
-    if (blockIdx.x == 0 && warp == kAtQWarp) {
-        for (int b = lane; b < p.num_seqs; b += 32) {
-            int c0, len;
-            bool bad;
-            at_sequence<SRC>(p, b, c0, len, &bad);
-            if (bad) flag_status(p.status, PA_DEV_BAD_SEQ_LEN);
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1159,7 +1247,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     if (L::kPools && warp >= kAtWidenWarp) {
         if constexpr (L::kPools) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" ::: "memory");
-            at_widen<SRC, D>(p, range, base, base_s, bars, misc, warp - kAtWidenWarp, lane);
+            at_widen<SRC, D>(p, base, base_s, bars, misc, warp - kAtWidenWarp, lane);
         }
     } else if (warp >= 8) {
         if constexpr (L::kPools)
@@ -1167,21 +1255,24 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
         if (warp == kAtMmaWarp || warp == kAtMmaWarp + 1) {
-            at_mma<SRC, D>(p, range, warp - kAtMmaWarp, base_s, tmem, bars, misc, lane);
+            at_mma<SRC, D>(p, warp - kAtMmaWarp, base, base_s, tmem, bars, misc, lane);
         } else if constexpr (L::kPools) {
-            if (warp == kAtKvWarp) at_load_raw<SRC, D>(p, range, base_s, bars, misc, lane);
+            if (warp == kAtKvWarp)
+                at_load_raw<SRC, D>(p, base, base_s, bars, misc, lane);
+            else
+                at_walk<SRC, D>(p, range, base, bars, misc, lane);
         } else {
             if (warp == kAtKvWarp)
                 at_load_packed<D>(p, &tmap_k, &tmap_v, base, base_s, bars, misc, lane);
             else
-                at_load_q_packed<D>(p, &tmap_q, base_s, bars, misc, lane);
+                at_load_q_packed<D>(p, &tmap_q, base, base_s, bars, misc, lane);
         }
     } else {
         if constexpr (L::kPools)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
-        at_softmax<SRC, D>(p, range, warp >> 2, base, tmem, bars, misc, warp, lane);
+        at_softmax<SRC, D>(p, warp >> 2, base, tmem, bars, misc, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
