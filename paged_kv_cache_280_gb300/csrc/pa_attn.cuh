@@ -388,6 +388,14 @@ struct AttnPieces {
         __syncwarp();
         return w.ns > 0;
     }
+    // The same for one thread that reads alone for its warp.
+    __device__ __forceinline__ bool next1(AttnPiece& w, volatile int32_t* abort_flag, int32_t* status) {
+        if (!at_wait1(bars.piece_full(i & 1), (i >> 1) & 1, abort_flag, status)) return false;
+        get(i, w);
+        mbar_arrive(bars.piece_empty(i & 1));
+        ++i;
+        return w.ns > 0;
+    }
     // The walking warp: piece i (have: false behind the last one).
     __device__ __forceinline__ bool put(const AttnPiece& w, bool have, volatile int32_t* abort_flag, int32_t* status, int lane) {
         if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status)) return false;
@@ -852,10 +860,13 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t*
     AttnPiece w;
     Ring first{0u, 0u};           // the piece's first slot
     uint32_t pc = 0, ck = 0, rounds = 0;  // pieces, stages of this half, turns
-    bool ok = true;
     const uint32_t d = tmem + kAtTmemHalf * t;
-    while (__shfl_sync(0xffffffffu, (int)ok, 0) && pieces.next(w, abort_flag, p.status, lane)) {
-        if (lane == 0) {
+    // One lane all the way, and the next piece's entry read ahead: what it does between a piece's last MMA and the next
+    // one's first is what the tensor core waits for (with the warp meeting at each piece 3000 cycles).
+    if (lane == 0) {
+        AttnPiece ahead;
+        bool ok = true, more = pieces.next1(w, abort_flag, p.status), given = false;  // given: the piece's first S is issued
+        while (ok && more) {
             using First = std::integral_constant<int, 0>;
             using Second = std::integral_constant<int, 1>;
             // In round r the half has its turn: P V of stage j, S of stage j + lead.  Of two tiles both see every stage, of
@@ -869,16 +880,33 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t*
             vr.ahead(at.v(j + lead));
             // A half without a stage does not wait for the queries: it has no say in when they are replaced, so it could find
             // the barrier two phases on.  (Its turns tell it that they were there.)
-            if (j + lead < n) ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
+            if (!given && j + lead < n) ok = at_wait1(bars.q_full(), pc & 1, abort_flag, p.status);
+            bool early = false;
 #pragma unroll 1
             for (int r = -1; ok && r <= last; ++r) {
-                const bool product = j >= 0 && j < n, scores = j + lead < n;
-                const uint32_t vb = v_lo + vr.slot * kTile16, kb = k_lo + kr.slot * kTile16;
+                if (r == last) more = pieces.next1(ahead, abort_flag, p.status);
+                const bool product = j >= 0 && j < n;
+                bool scores = j + lead < n && !(given && r < 0);
+                Ring ks = kr;
+                bool k_alone = w.one || j + lead >= w.n0, q_vote = j + 2 * lead >= n, q_alone = w.one ? w.ns == 1 : w.n0 == 0;
+                // Packed: the first half's last turn is empty where its tile does not see the unit's last stage.  Then the next
+                // piece's first S takes it, as soon as its queries are there (for which the other half has done its part: its
+                // last S of this piece has been issued), and runs beside the other half's last softmax (16 prompts of 1031
+                // tokens: 158 us, without it 165).  Over pools, where the queries come later, the turn is better passed on
+                // (162 us against 157 on the FP8 turns).
+                if (SRC == kAttnPacked && r == last && !product && t == 0 && more && (ahead.one || ahead.n0 > 0)) {
+                    early = scores = true;
+                    ks = first;
+                    ks.ahead((uint32_t)(2 * w.ns) % (2 * NS));
+                    k_alone = ahead.one, q_vote = ahead.one ? ahead.ns <= 2 : ahead.n0 == 1, q_alone = ahead.one && ahead.ns == 1;
+                }
+                const uint32_t vb = v_lo + vr.slot * kTile16, kb = k_lo + ks.slot * kTile16;
                 if (product) ok = at_wait1(bars.full(vr.slot), vr.parity, abort_flag, p.status) &&
                                   at_wait1(bars.p_first(t), ck & 1, abort_flag, p.status);
                 ok = ok && at_wait1(bars.turn(t), (rounds & 1) ^ (t ^ 1), abort_flag, p.status);
+                if (ok && early && r == last) ok = at_wait1(bars.q_full(), (pc + 1) & 1, abort_flag, p.status);
                 if (!ok) break;
-                bool k_over = scores && mbar_test_wait(bars.full(kr.slot), kr.parity);
+                const bool k_over = scores && mbar_test_wait(bars.full(ks.slot), ks.parity);
                 // A slot is released by both halves: a half that is alone with a stage gives the other's vote at once.
                 auto release = [&](uint32_t bar, bool alone) {
                     if (alone) mbar_arrive(bar);
@@ -898,7 +926,7 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t*
                     ++ck;
                 }
                 if (scores) {
-                    if (!k_over && !at_wait1(bars.full(kr.slot), kr.parity, abort_flag, p.status)) {
+                    if (!k_over && !at_wait1(bars.full(ks.slot), ks.parity, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -909,8 +937,8 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t*
                 if (scores) {
                     issue_s(d, qa, kb, Second{});
                     umma_commit(bars.s_full(t));
-                    release(bars.empty(kr.slot), w.one || j + lead >= w.n0);
-                    if (j + 2 * lead >= n) release(bars.q_empty(), w.one ? w.ns == 1 : w.n0 == 0);  // the half's last S
+                    release(bars.empty(ks.slot), k_alone);
+                    if (q_vote) release(bars.q_empty(), q_alone);  // the half's last S
                 } else if (product) {
                     umma_commit(bars.o_final(t));
                 }
@@ -921,9 +949,10 @@ __device__ __forceinline__ void at_mma(const AttnParams& p, uint32_t t, uint8_t*
             }
             first.ahead((uint32_t)(2 * w.ns) % (2 * NS));
             ++pc;
+            w = ahead, given = early;
         }
-        __syncwarp();
     }
+    __syncwarp();
     // every MMA issued has completed before the CTA may free TMEM or its shared memory
     if (lane == 0) {
         umma_commit(bars.drain(t));
