@@ -313,9 +313,10 @@ __device__ __forceinline__ void at_plan(const AttnParams& p, AttnRange* range, i
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o), W1 += __shfl_xor_sync(0xffffffffu, W1, o);
-    U = unit_weight(W, gridDim.x);
-    W += (W1 - W) * (U / 2);
-    const int64_t C = W > 0 ? ranges(W, gridDim.x, U) : 0, c = blockIdx.x;
+    const int64_t units = W1 - W;
+    U = unit_weight(W, units, gridDim.x, p.part_tiles == 1);
+    W += units * (U / 2);
+    const int64_t C = W > 0 ? ranges(W, gridDim.x, U, p.part_tiles == 1) : 0, c = blockIdx.x;
     if (c >= C) {
         if (lane == 0) range->at = range->end = 0, range->W = W, range->C = (int)C;
         return;

@@ -5,8 +5,9 @@
 // line: a unit of `keys` keys takes U + keys * kTwoTiles of it, or U / 2 + keys * kOneTile, which adds up in closed form.
 // U, a piece's fixed work, is the same for a whole call (unit_weight).
 // CTA c of C takes the stages of 128 keys that begin in [c W / C, (c + 1) W / C).  Stage 0 begins with its unit, stage s > 0
-// behind the unit's fixed part.  A range is never shorter than U + 2 * 128, which is the longest distance of two stages'
-// beginnings, so every CTA between the first and the last of a unit has a piece of it.
+// behind the unit's fixed part.  A range is never shorter than U + 2 * 128 (U / 2 + 128 in a call without units of two tiles),
+// which is the longest distance of two stages' beginnings, so every CTA between the first and the last of a unit has a piece
+// of it.
 #pragma once
 
 #include <stdint.h>
@@ -22,12 +23,21 @@ namespace pa {
 constexpr int kAttnKeys = 128;   // keys per stage
 constexpr int kTwoTiles = 2;     // weight of a key that two query tiles share
 constexpr int kOneTile = 1;      // of one that a single tile uses
-// U: query rows, epilogue and join take about as long as eight stages of one tile (16 x 8 + 1031 tokens over 32 KV heads of
-// 128, FP8: 194 us with 1024, 198 with 512; 64 sequences of 8 tokens over 8 heads: 128 with either).  Where all CTAs get
-// fewer than kFewKeys keys' weight, latency counts and not balance: then more CTAs, of shorter ranges, take part (5 mixed
-// sequences over 4-bit pools: 44 us with 128, 32.5 with 2; one short chunk 30 and 20).
-constexpr int kUnitWeight = 1024, kUnitWeightFew = 2, kFewKeys = 2048;
-PA_HD int unit_weight(int64_t keys_weight, int64_t grid) { return keys_weight < kFewKeys * grid ? kUnitWeightFew : kUnitWeight; }
+// U: a piece's query rows and epilogue take about as long as eight stages of one tile (4 sequences of 129 to 517 tokens over
+// 32 KV heads of 128, FP8: 157 us with 1024, 163 with 512; 32 of 5 tokens over 8 heads: 111 and 114).  But the shortest range
+// grows with U, so in a call of little work it is well below the largest with which every CTA still has a range (one short
+// chunk: 22 us with 64, 17 with 2, which it gets; a mixed batch over 4-bit pools: 25 with that largest, 23 with an eighth of
+// it), unless the units are so short that more of U makes more ranges (20 sequences of one token and up to 25 keys over 4
+// heads: 63 us with 2, 17 with 1024).
+constexpr int kUnitWeight = 1024;
+// units: 1 for each of one tile, 2 for each of two
+PA_HD int unit_weight(int64_t keys_weight, int64_t units, int64_t grid, bool one_tile) {
+    if (keys_weight <= kAttnKeys * units) return kUnitWeight;
+    // (keys_weight + units U / 2) / (U / 2 + 128 or twice that) >= grid
+    const int64_t per = one_tile ? kOneTile : kTwoTiles, spare = keys_weight - per * kAttnKeys * grid, each = per * grid - units;
+    if (each <= 0 || spare >= each * (kUnitWeight / 2)) return kUnitWeight;
+    return spare < 8 * each ? 2 : 2 * (int)(spare / (8 * each));
+}
 
 // The units of one (sequence, KV head): n new tokens at the end of len, T tokens per tile.
 struct UnitLine {
@@ -71,8 +81,8 @@ PA_HD int64_t stage_begin(int64_t s, int key_weight, int U) { return s == 0 ? 0 
 
 PA_HD int64_t range_begin(int64_t c, int64_t W, int64_t C) { return c * W / C; }
 PA_HD int64_t range_of(int64_t at, int64_t W, int64_t C) { return ((at + 1) * C - 1) / W; }
-PA_HD int64_t ranges(int64_t W, int64_t grid, int U) {
-    const int64_t most = W / (U + kTwoTiles * kAttnKeys);
+PA_HD int64_t ranges(int64_t W, int64_t grid, int U, bool one_tile) {
+    const int64_t most = W / (one_tile ? U / 2 + kOneTile * kAttnKeys : U + kTwoTiles * kAttnKeys);
     return most < 1 ? 1 : most < grid ? most : grid;
 }
 
