@@ -13,10 +13,11 @@
 //           context fill the card; the pieces of cut units are joined by a second kernel (attn_join_kernel).
 //
 // Warps.  0 .. 3 and 4 .. 7: the softmax of the two halves, a thread per row.  8: keys and values.  9 and 10: the MMAs
-// of the two halves.  11 (packed): query rows.  12 .. 15 (pools): query rows and widening of the codes.
+// of the two halves.  11: the walk over the work (AttnPieces), and query rows (packed).  12 .. 15 (pools): query rows and
+// widening of the codes.
 //   Packed: K and V stages by TMA, 128-byte swizzle, a ring of slots in shared memory.
 //   Pools:  the blocks' codes by bulk copies into a ring of raw slots; the widening warps turn them into f16 (exact for
-//           E4M3, and for E2M1 codes times their E4M3 scale) in the swizzled layout, with zeros for V rows behind the
+//           E4M3, and for E2M1 codes times their E4M3 scale) in the swizzled layout, with zeros for rows behind the
 //           sequence's end.  Query rows are scaled by a power of two and rounded to f16 on the way.
 //   S = Q K^T into TMEM (M 128, N 128), O += P V with P read from TMEM, where the softmax wrote it over S's last 64 columns.
 //   P is handed over in two halves of 64 keys, so that the product with V begins while the second half's exponentials
@@ -24,6 +25,18 @@
 // O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since it was last scaled.  Every wait is
 // bounded; one that gives up sets PA_DEV_WAIT_TIMEOUT, every role stops, and the CTA waits for its own copies and MMAs
 // before it frees TMEM.
+//
+// Bound and measured.  Two 128 x 128 x 128 products a stage and tile are 1024 cycles of the tensor core; Q and K of an S, both
+// from shared memory, take all its 128 bytes a clock meanwhile.  The softmax of a stage is some 1900 cycles of a half's warps
+// (64 exponentials a thread and SFU, TMEM both ways), which the other half's products cover but for its hand-overs, so a stage of
+// two tiles takes about 3500 (the products' 2050).  A unit's end and the next one's start cost some 3000 more.
+//   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 787 us, 1.40 PFLOP/s (0.73 of the measured bf16 rate; tensor pipe busy
+//   60 %); 32 / 8 heads: 16 prompts of 1031 tokens 158 us (0.46: half of the stages are a unit's masked last ones or its first).
+//   Pools: the widening beside it (4 warps, about 1100 cycles of conversions and stores for K or V of a stage, which share the
+//   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens behind 30720: 840 us (0.67); 2 x 9
+//   tokens over 131072 keys, 64 / 8 heads: 133 us (tiles of 72 rows and less are padded to 128, so the tensor core's 44 % busy
+//   cycles and the widening bound it, not HBM's 45 us); FP8, 32 / 32 heads, 129 to 517 tokens over up to 16383 keys: 157 us (HBM
+//   57; a tile is one head's, so every key is widened for 256 rows at most).
 #pragma once
 
 #include <cmath>
@@ -138,7 +151,8 @@ struct AttnBars {
 
 // One thread's bounded wait; gives up once the CTA's abort flag is set.  (The flag and the clock are looked at now and
 // then only: a thread that is busy with them notices late that its phase has completed.)
-__device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
+__device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status,
+                                         uint64_t limit_ns = kWaitLimitNs) {
     uint64_t since = 0;
     for (int n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n & 31) continue;
@@ -146,7 +160,7 @@ __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile
         const uint64_t now = global_timer_ns();
         if (since == 0) {
             since = now;
-        } else if (now - since > kWaitLimitNs) {
+        } else if (now - since > limit_ns) {
             *abort_flag = 1;
             flag_status(status, PA_DEV_WAIT_TIMEOUT);
             return false;
@@ -155,9 +169,13 @@ __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 // The same for a warp: its lanes go on together.
-__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
-    return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status));
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status,
+                                        uint64_t limit_ns = kWaitLimitNs) {
+    return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status, limit_ns));
 }
+// For the waits that last as long as a piece: one of the longest context that fits into memory takes some 20 s.  (Where a
+// copy or an MMA is lost, the other roles notice within kWaitLimitNs.)
+constexpr uint64_t kPieceLimitNs = 32 * kWaitLimitNs;
 
 __device__ __forceinline__ int at_token(const AttnParams& p, int row) { return (int)((uint32_t)row * p.group_inverse >> 16); }
 
@@ -399,7 +417,7 @@ struct AttnPieces {
     }
     // The walking warp: piece i (have: false behind the last one).
     __device__ __forceinline__ bool put(const AttnPiece& w, bool have, volatile int32_t* abort_flag, int32_t* status, int lane) {
-        if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status)) return false;
+        if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status, kPieceLimitNs)) return false;
         if (lane == 0) {
             int4* e = reinterpret_cast<int4*>(base + L::kPieceOff + (i & 1) * L::kPieceBytes);
             e[0] = make_int4(w.b, w.g, w.c0, w.n);
@@ -537,7 +555,7 @@ __device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUte
         if (pc == pieces.i) break;  // (a wait was given up)
         pieces.get(pc, w);
         if (w.ns == 0) break;
-        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status)) break;
+        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status, kPieceLimitNs)) break;
         if (lane == 0) {
             const int tiles = w.one ? 1 : 2;
             mbar_arrive_expect_tx(bars.q_full(), tile_bytes * tiles);

@@ -224,3 +224,11 @@ def test_norm_rope_on_another_stream_and_captured():
     call(a)
     graph.replay()
     assert torch.equal(a[0], c[0])
+
+
+@pytest.mark.parametrize("case", [(3000, 24, 8, 128, 16, "bf16", "fp8", 128, False, True),
+                                  (4000, 40, 16, 64, 32, "f32", "fp4", 32, True, False),
+                                  (5003, 15, 5, 128, 16, "bf16", "bf16", 64, False, True)])
+def test_norm_rope_rows_behind_one_another(case):
+    """Several rows to a thread, across tokens and from keys to values, with padding among them."""
+    test_norm_rope(*case)

@@ -291,3 +291,39 @@ def test_small_workspace_is_refused():
     need = pa.pa_prefill_workspace_bytes(4, 4, 2, 128)
     with pytest.raises(pa.PAError, match="WORKSPACE_TOO_SMALL"):
         c.run(torch.zeros(need - 16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("lens,news,hkv,max_q", [([9 + 5 * i % 17 for i in range(20)], [1] * 20, 4, None),
+                                                 ([1 + 7 * i % 90 for i in range(48)], [1] * 48, 8, 500),
+                                                 ([30 + 41 * i % 900 for i in range(32)], [1 + i % 3 for i in range(32)], 8, None)])
+def test_many_short_units(kind, d, lens, news, hkv, max_q):
+    """More units than CTAs or nearly so, each a stage or a few; in slots of two tiles too."""
+    c = Case(700 + d + len(lens), kind, lens, news, hkv, hkv, d, 32)
+    c.check(c.run(max_q=max_q))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+def test_two_graphs_at_once_and_an_output_aligned_to_16_bytes(kind, d):
+    """Captured calls on workspaces of their own, replayed on two streams at once, again and again."""
+    import torch
+
+    cases = [Case(800, kind, [5000, 70], [6, 70], 8, 2, d, 16).device(), Case(801, kind, [900, 2100], [300, 40], 4, 4, d, 32).device()]
+    want = [c.run().clone() for c in cases]
+    outs = [torch.zeros(w.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(w.shape) for w in want]
+    graphs, streams = [], [torch.cuda.Stream() for _ in cases]
+    for c, out, s in zip(cases, outs, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.run(c.ws, out=out)
+        graphs.append(g)
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, out, w in zip(cases, outs, want):
+        assert out.data_ptr() % 32 == 16 and torch.equal(out, w) and c.status() == 0
+        c.check(out)

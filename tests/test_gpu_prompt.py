@@ -201,3 +201,41 @@ def test_prompts_on_another_stream_captured_and_repeated():
     a, _ = _run(q, k, v, starts, 0.1)
     graph.replay()
     assert torch.equal(a, out)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(6, 2, 64), (8, 2, 128)])
+def test_prompts_odd_strides_and_alignment(hq, hkv, d):
+    """Token strides that are multiples of 16 bytes only, an output that is 16-byte aligned only, a loose bound on the lengths."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    lens = [130, 1, 77, 300]
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    n = int(starts[-1])
+    host, dev = _inputs(77 + d, n, hq, hkv, d, False)
+    spread = []
+    for x, extra in zip(dev, (8, 24, 40)):
+        wide = torch.full((n, x.shape[1] * d + extra), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, : x.shape[1] * d] = x.flatten(1)
+        spread.append(wide.as_strided(x.shape, (wide.shape[1], d, 1)))
+    out = torch.full((n * hq * d + 8,), 7.0, dtype=torch.bfloat16, device="cuda")[8:].view(n, hq, d)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_prompt_attention(out, *spread, to_torch(starts), 1 << 30, d ** -0.5, status=status)
+    assert status.item() == 0 and out.data_ptr() % 32 == 16
+    _check(out, *chunks.prompts(*host, starts, d ** -0.5))
+
+
+@pytest.mark.parametrize("hq,hkv,d,lens", [(16, 8, 128, [300] * 40), (16, 8, 64, [129, 300, 61, 500] * 12), (8, 8, 128, [270, 140] * 30)])
+def test_prompts_many_units_to_a_cta(hq, hkv, d, lens):
+    """Units of two tiles and of one behind one another in every CTA, tiles that see a stage less than their neighbour; equal
+    calls give equal bits."""
+    import torch
+
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    host, dev = _inputs(900 + d + hq, int(starts[-1]), hq, hkv, d, True)
+    got, status = _run(*dev, starts, d ** -0.5)
+    assert status == 0
+    _check(got, *chunks.prompts(*host, starts, d ** -0.5))
+    for _ in range(20):
+        again, status = _run(*dev, starts, d ** -0.5)
+        assert status == 0 and torch.equal(again, got)
