@@ -33,7 +33,7 @@
 //   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 787 us, 1.40 PFLOP/s (0.73 of the measured bf16 rate; tensor pipe busy
 //   60 %); 32 / 8 heads: 16 prompts of 1031 tokens 158 us (0.46: half of the stages are a unit's masked last ones or its first).
 //   Pools: the widening beside it (4 warps, about 1100 cycles of conversions and stores for K or V of a stage, which share the
-//   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens behind 30720: 840 us (0.67); 2 x 9
+//   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens at the end of 32767: 840 us (0.67); 2 x 9
 //   tokens over 131072 keys, 64 / 8 heads: 133 us (tiles of 72 rows and less are padded to 128, so the tensor core's 44 % busy
 //   cycles and the widening bound it, not HBM's 45 us); FP8, 32 / 32 heads, 129 to 517 tokens over up to 16383 keys: 157 us (HBM
 //   57; a tile is one head's, so every key is widened for 256 rows at most).
@@ -1041,13 +1041,16 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             const int key0 = k * kAttnKeys;
             const int nq = min(4, (pos_high - key0 + 32) >> 5);  // quarters that some row of the warp sees
             // Masked scores become -inf: the quarters that reach past the position of some of the warp's rows are rewritten so
-            // first (those past all of them without being read).
+            // first.  Those past all of them (from nq on) are left out of the maximum (packed: 16 prompts of 1031 tokens 156 us,
+            // 158 with them), or filled without being read (pools: the branches below cost every stage more, 143 us against 133
+            // over 131072 keys).
+            constexpr bool kLeaveOut = SRC == kAttnPacked;
             if (key0 + kAttnKeys - 1 > pos_low) {
 #pragma unroll 1
-                for (int q = max(0, pos_low + 1 - key0) >> 5; q < 4; ++q) {
+                for (int q = max(0, pos_low + 1 - key0) >> 5; q < (kLeaveOut ? nq : 4); ++q) {
                     uint32_t x[32];
                     const int seen = pos - key0 - 32 * q;
-                    if (q < nq) {
+                    if (kLeaveOut || q < nq) {
                         tmem_ld32(row_tmem + 32 * q, x);
                         tmem_wait_ld32(x);
 #pragma unroll
@@ -1081,13 +1084,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             tmem_wait_ld32(xc);
             tmem_wait_ld32(xa);
             tmem_ld32(row_tmem + 96, xb);
-            larger(xc);
+            if (!kLeaveOut || nq > 0) larger(xc);
             tmem_ld32(row_tmem + 64, xc);
-            larger(xa);
+            if (!kLeaveOut || nq > 1) larger(xa);
             tmem_wait_ld32(xb);
             tmem_wait_ld32(xc);
-            larger(xb);
-            larger(xc);
+            if (!kLeaveOut || nq > 3) larger(xb);
+            if (!kLeaveOut || nq > 2) larger(xc);
             const float m_new = fmaxf(m_raw, fmaxf(fmax3(mx0, mx1, mx2), mx3));
             if (i == 0) {
                 m_raw = m_new;
