@@ -28,10 +28,10 @@
 //
 // Bound and measured.  Two 128 x 128 x 128 products a stage and tile are 1024 cycles of the tensor core; Q and K of an S, both
 // from shared memory, take all its 128 bytes a clock meanwhile.  The softmax of a stage is some 1900 cycles of a half's warps
-// (64 exponentials a thread and SFU, TMEM both ways), which the other half's products cover but for its hand-overs, so a stage of
+// (128 exponentials a thread, TMEM both ways), which the other half's products cover but for its hand-overs, so a stage of
 // two tiles takes about 3500 (the products' 2050).  A unit's end and the next one's start cost some 3000 more.
-//   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 787 us, 1.40 PFLOP/s (0.73 of the measured bf16 rate; tensor pipe busy
-//   60 %); 32 / 8 heads: 16 prompts of 1031 tokens 158 us (0.46: half of the stages are a unit's masked last ones or its first).
+//   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 795 us, 1.38 PFLOP/s (0.73 of the measured bf16 rate; tensor pipe busy
+//   60 %); 32 / 8 heads: 16 prompts of 1031 tokens 158 us (0.46: a unit has five stages on average, the last one masked).
 //   Pools: the widening beside it (4 warps, about 1100 cycles of conversions and stores for K or V of a stage, which share the
 //   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens at the end of 32767: 840 us (0.67); 2 x 9
 //   tokens over 131072 keys, 64 / 8 heads: 133 us (tiles of 72 rows and less are padded to 128, so the tensor core's 44 % busy
@@ -219,28 +219,40 @@ __device__ __forceinline__ void at_stages(const AttnParams& p, int k0, int k1, A
     w.first = k0 == 0, w.last = k1 == w.nst;
 }
 
-// Packed: the units that exist, by unit index from the last down (the most keys first), then sequence, then KV head; CTA c
-// takes ranks c, 2 C - 1 - c, 2 C + c, ..  Warp-collective.
+// Packed: the units that exist, 256 sequences at a time, in them by unit index from the last down (the most keys first), then
+// sequence, then KV head; CTA c takes ranks c, 2 C - 1 - c, 2 C + c, ..  Every unit index looked at has units among the 256
+// sequences, so that the walk is no longer than eight steps a unit, however loose the bound on the lengths is.
+// Warp-collective.
 struct PackedWalk {
-    int m, chunk, loaded, mine, rank0, wave;
+    static constexpr int kTogether = 256;
+    int first, m, chunk, loaded, mine, rank0, wave;
     uint32_t mask;
-    __device__ PackedWalk(const AttnParams& p, const void*) : chunk(0), loaded(-1), mine(0), rank0(0), wave(0), mask(0) {
-        m = (p.max_q_len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) - 1;
-        look(p);
+    __device__ PackedWalk() : first(-kTogether), m(-1), chunk(0), loaded(-1), mine(0), rank0(0), wave(0), mask(0) {}
+    __device__ __forceinline__ void load(const AttnParams& p) {  // how many units the chunk's 32 sequences have
+        if (loaded == chunk) return;
+        const int b = chunk + (threadIdx.x & 31);
+        int c0, len;
+        const int n = b < p.num_seqs ? at_sequence<kAttnPacked>(p, b, c0, len) : 0;
+        mine = (n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+        loaded = chunk;
     }
-    __device__ __forceinline__ void look(const AttnParams& p) {  // which of the chunk's 32 sequences have a unit m
-        if (loaded != chunk) {
-            const int b = chunk + (threadIdx.x & 31);
-            int c0, len;
-            const int n = b < p.num_seqs ? at_sequence<kAttnPacked>(p, b, c0, len) : 0;
-            mine = (n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-            loaded = chunk;
-        }
+    __device__ __forceinline__ int end(const AttnParams& p) const { return min(first + kTogether, p.num_seqs); }
+    __device__ __forceinline__ void begin(const AttnParams& p) {  // at the 256 sequences from `first` on
+        int most = 0;
+        for (chunk = first; chunk < end(p); chunk += 32) load(p), most = max(most, mine);
+        m = (int)__reduce_max_sync(0xffffffffu, (unsigned)most) - 1;
+        chunk = first;
+        load(p);
         mask = __ballot_sync(0xffffffffu, mine > m);
     }
     __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
         const int C = gridDim.x, want = wave * C + ((wave & 1) ? C - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        while (m >= 0) {
+        while (first < p.num_seqs) {
+            if (m < 0) {
+                first += kTogether;
+                begin(p);
+                continue;
+            }
             const int here = __popc(mask) * p.num_kv_heads;
             if (want < rank0 + here) {
                 const int off = want - rank0, j = off / p.num_kv_heads;
@@ -255,8 +267,9 @@ struct PackedWalk {
             }
             rank0 += here;
             chunk += 32;
-            if (chunk >= p.num_seqs) chunk = 0, --m;
-            look(p);
+            if (chunk >= end(p)) chunk = first, --m;
+            load(p);
+            mask = __ballot_sync(0xffffffffu, mine > m);
         }
         return false;
     }
@@ -540,7 +553,7 @@ __device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUte
     using L = AttnLayout<kAttnPacked, D>;
     if (lane == 0) prefetch_tensormap(tq);
     const uint32_t tile_bytes = (uint32_t)(L::kPanels * p.group * p.tile_tokens * 128);
-    PackedWalk walk(p, nullptr);
+    PackedWalk walk;
     AttnPieces<kAttnPacked, D> pieces(base, bars);
     AttnPiece ahead, w;
     int pc = 0;

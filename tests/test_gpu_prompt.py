@@ -239,3 +239,14 @@ def test_prompts_many_units_to_a_cta(hq, hkv, d, lens):
     for _ in range(20):
         again, status = _run(*dev, starts, d ** -0.5)
         assert status == 0 and torch.equal(again, got)
+
+
+@pytest.mark.parametrize("where", [0, 300, 599])
+def test_hundreds_of_prompts_with_a_long_one_and_a_loose_bound(where):
+    lens = [(7 * i) % 40 for i in range(600)]
+    lens[where] = 2500
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    host, dev = _inputs(1234 + where, int(starts[-1]), 2, 1, 64, False)
+    got, status = _run(*dev, starts, 0.125, max_len=1 << 30)
+    assert status == 0
+    _check(got, *chunks.prompts(*host, starts, 0.125))
