@@ -662,7 +662,8 @@ pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const 
  * finite bf16 magnitudes are in range (an element 2^-14 or less of its row's largest loses bits
  * below 2^-24 of that).  The softmax weights are f16: off by at most 2^-11 of themselves or
  * 2^-32 of the largest.  Slots behind a sequence's end may hold any bytes; a NaN among a
- * sequence's own values may reach rows of the chunk that do not see it.
+ * sequence's own values may reach rows of the chunk that do not see it.  A sequence of more
+ * than 2^31 - 256 tokens is a bad one.
  *
  * The work is split over the contexts too where there are few rows: every CTA takes an equal
  * run of (128 keys x one query tile) steps, and a second kernel joins the partial results

@@ -69,6 +69,7 @@ struct AttnParams {
     int32_t group, tile_tokens;    // G, 128 / G rounded down
     uint32_t group_inverse;        // 2^16 / G rounded up: rows below 256 divided by G
     int32_t out_align32;           // out is 32-byte aligned: 32-byte stores
+    int32_t max_len;               // pools: the longest context that a table holds (kAttnMaxLen at most)
     float scale_log2, out_scale;
 };
 
@@ -188,7 +189,7 @@ __device__ __forceinline__ int at_sequence(const AttnParams& p, int b, int& c0, 
     const int end = __ldg(p.cu_q_lens + b + 1), n = end - c0;
     len = SRC == kAttnPacked ? n : __ldg(p.seq_lens + b);
     const bool wrong = end < c0 || (n > 0 && (c0 < 0 || end > p.num_q_tokens || n > p.max_q_len || n > len ||
-                                              (SRC != kAttnPacked && (int64_t)len > ((int64_t)p.max_blocks_per_seq << p.bs_shift))));
+                                              (SRC != kAttnPacked && len > p.max_len)));
     if (bad) *bad = wrong;
     return wrong ? 0 : n;
 }

@@ -21,6 +21,7 @@
 namespace pa {
 
 constexpr int kAttnKeys = 128;   // keys per stage
+constexpr int kAttnMaxLen = INT32_MAX - 255;  // longest sequence: a stage's keys, or two tiles' tokens, beyond it are still an int
 constexpr int kTwoTiles = 2;     // weight of a key that two query tiles share
 constexpr int kOneTile = 1;      // of one that a single tile uses
 // U: a piece's query rows and epilogue take about as long as eight stages of one tile (4 sequences of 129 to 517 tokens over

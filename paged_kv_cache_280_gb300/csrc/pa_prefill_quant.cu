@@ -60,6 +60,8 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.max_blocks_per_seq = max_blocks_per_seq, p.num_seqs = num_seqs, p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads, p.num_blocks = num_blocks, p.num_q_tokens = num_q_tokens, p.max_q_len = max_q_len;
     p.bs_shift = block_size == 16 ? 4 : 5;
+    const int64_t held = (int64_t)max_blocks_per_seq * block_size;
+    p.max_len = (int32_t)(held < kAttnMaxLen ? held : kAttnMaxLen);
     p.group = group, p.tile_tokens = kAtRows / group;
     p.group_inverse = (65536u + p.group - 1) / p.group;
     p.out_align32 = aligned_to(out, 32) ? 1 : 0;

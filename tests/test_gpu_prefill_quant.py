@@ -327,3 +327,20 @@ def test_two_graphs_at_once_and_an_output_aligned_to_16_bytes(kind, d):
     for c, out, w in zip(cases, outs, want):
         assert out.data_ptr() % 32 == 16 and torch.equal(out, w) and c.status() == 0
         c.check(out)
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+def test_the_longest_sequences_are_refused(kind, d):
+    """Lengths whose last stage would pass 31 bits, over a table that is wide enough: flagged, their rows not written."""
+    import torch
+    import paged_kv_cache_280_gb300 as pa
+
+    c = Case(820, kind, [40, 33], [1, 2], 1, 1, d, 16).device()
+    want = c.run().clone()
+    table = torch.zeros((2, 1 << 27), dtype=torch.int32, device="cuda")
+    table[:, : c.tables.shape[1]] = c.dev[2]
+    for length in (2 ** 31 - 1, 2 ** 31 - 255):
+        c.dev[2], c.dev[3] = table, torch.tensor([length, 33], dtype=torch.int32, device="cuda")
+        got = c.run()
+        assert c.status() == pa.PA_DEV_BAD_SEQ_LEN
+        assert (got[0] == 7.0).all() and torch.equal(got[1:], want[1:])
