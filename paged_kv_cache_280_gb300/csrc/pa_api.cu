@@ -155,19 +155,6 @@ bool prefill_q_map(CUtensorMap* map, int dev, const void* q, int64_t tokens, int
     return true;
 }
 
-bool rows_map(CUtensorMap* map, const void* rows, int64_t tokens, int heads, int head_dim, int64_t stride, int box_heads,
-              int box_tokens) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
-    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Dynamic shared memory opted into, and the occupancy found, per (device,
 // kernel, shared-memory size): set and queried once instead of every call.
 struct KernelEntry {

@@ -26,8 +26,6 @@ inline __host__ __device__ size_t partial_slot_floats(int G, int D) {
     return ((size_t)G * (D + kSlotExtraFloatsPerHead) + 3) & ~(size_t)3;
 }
 constexpr int kMaxSmem = 227 * 1024;
-// Largest distance between tokens of a strided q, k or v, in elements: a tensor map holds strides below 2^40 bytes.
-constexpr int64_t kMaxRowStride = (int64_t)1 << 38;
 
 // Cost weights of the range balance (see DecodeParams): 4 units a tile, and a
 // segment's fixed work in units per compute path.  Measured per-CTA loop ends
@@ -168,10 +166,6 @@ bool pool_map(CUtensorMap* map, int dev, const void* pool, int64_t rows, int hea
 // the 128-byte swizzle; cached per (device, q, shape).
 bool prefill_q_map(CUtensorMap* map, int dev, const void* q, int64_t tokens, int heads, int head_dim, int box_heads,
                    int box_tokens);
-// The TMA map of bf16 rows [tokens][heads][head_dim] with `stride` elements from one token to the next, viewed as
-// (head_dim, heads, tokens): one box = 64 elements x box_heads x box_tokens with the 128-byte swizzle.
-bool rows_map(CUtensorMap* map, const void* rows, int64_t tokens, int heads, int head_dim, int64_t stride, int box_heads,
-              int box_tokens);
 // Opts the kernel into `smem` bytes of dynamic shared memory and returns its
 // CTAs per SM; cached per (device, kernel, smem).
 bool kernel_occupancy(int dev, const void* kernel, int threads, int smem, int* occ);

@@ -1,7 +1,42 @@
 // Attention over whole prompts, packed one behind the other: entry point and checks; the kernel in pa_attn.cuh.
 #include <cmath>
+#include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "pa_attn.cuh"
+
+namespace pa {
+namespace {
+
+// Largest distance between tokens of a strided q, k or v, in elements: a tensor map holds strides below 2^40 bytes.
+constexpr int64_t kMaxRowStride = (int64_t)1 << 38;
+
+// The TMA map of bf16 rows [tokens][heads][head_dim] with `stride` elements from one token to the next, viewed as
+// (head_dim, heads, tokens): one box = 64 elements x box_heads x box_tokens with the 128-byte swizzle.
+bool rows_map(CUtensorMap* map, const void* rows, int64_t tokens, int heads, int head_dim, int64_t stride, int box_heads,
+              int box_tokens) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!encode) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace pa
 
 extern "C" pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                          const void* v, int64_t v_stride, const int32_t* cu_lens, int32_t num_seqs,
