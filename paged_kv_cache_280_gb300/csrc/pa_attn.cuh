@@ -186,12 +186,13 @@ __device__ __forceinline__ int at_token(const AttnParams& p, int row) { return (
 template <int SRC>
 __device__ __forceinline__ int at_sequence(const AttnParams& p, int b, int& c0, int& len, bool* bad = nullptr) {
     c0 = __ldg(p.cu_q_lens + b);
-    const int end = __ldg(p.cu_q_lens + b + 1), n = end - c0;
-    len = SRC == kAttnPacked ? n : __ldg(p.seq_lens + b);
-    const bool wrong = end < c0 || (n > 0 && (c0 < 0 || end > p.num_q_tokens || n > p.max_q_len || n > len ||
-                                              (SRC != kAttnPacked && len > p.max_len)));
+    len = SRC == kAttnPacked ? INT32_MAX : __ldg(p.seq_lens + b);
+    bool wrong;
+    const int n = sequence_tokens(c0, __ldg(p.cu_q_lens + b + 1), len, p.num_q_tokens, p.max_q_len,
+                                  SRC == kAttnPacked ? INT32_MAX : p.max_len, wrong);
+    if (SRC == kAttnPacked) len = n;
     if (bad) *bad = wrong;
-    return wrong ? 0 : n;
+    return n;
 }
 
 // A run of stages of one unit.  All roles take the same pieces in the same order.

@@ -22,6 +22,17 @@ namespace pa {
 
 constexpr int kAttnKeys = 128;   // keys per stage
 constexpr int kAttnMaxLen = INT32_MAX - 255;  // longest sequence: a stage's keys, or two tiles' tokens, beyond it are still an int
+
+// How many new tokens a sequence has whose rows are c0 .. end - 1 and which is len tokens long; none (and wrong) where it
+// breaks the call's bounds.  The rows are compared with those before they are subtracted: a difference of two offsets that
+// are anything may leave 32 bits.  (INT32_MAX for len: its new tokens are all there is.)
+PA_HD int sequence_tokens(int c0, int end, int len, int num_tokens, int max_new, int max_len, bool& wrong) {
+    wrong = end < c0 || (end > c0 && (c0 < 0 || end > num_tokens));
+    const int n = wrong ? 0 : end - c0;
+    if (n > 0) wrong = n > max_new || n > len || len > max_len;
+    return wrong ? 0 : n;
+}
+
 constexpr int kTwoTiles = 2;     // weight of a key that two query tiles share
 constexpr int kOneTile = 1;      // of one that a single tile uses
 // U: a piece's query rows and epilogue take about as long as eight stages of one tile (4 sequences of 129 to 517 tokens over
