@@ -223,13 +223,15 @@ __device__ __forceinline__ void at_stages(const AttnParams& p, int k0, int k1, A
 
 // Packed: the units that exist, 256 sequences at a time, in them by unit index from the last down (the most keys first), then
 // sequence, then KV head; CTA c takes ranks c, 2 C - 1 - c, 2 C + c, ..  Every unit index looked at has units among the 256
-// sequences, so that the walk is no longer than eight steps a unit, however loose the bound on the lengths is.
-// Warp-collective.
+// sequences, so that the walk is no longer than eight steps a unit and eight for each 256 sequences, however loose the bound on
+// the lengths is.  The walk counts from step to step (`off`), so that no number of units leaves 32 bits.  Warp-collective.
 struct PackedWalk {
     static constexpr int kTogether = 256;
-    int first, m, chunk, loaded, mine, rank0, wave;
+    int first, m, chunk, loaded, mine;
+    int off;  // from the first unit of this step (unit index, 32 sequences) to the CTA's next
+    bool back;  // the snake goes backwards there
     uint32_t mask;
-    __device__ PackedWalk() : first(-kTogether), m(-1), chunk(0), loaded(-1), mine(0), rank0(0), wave(0), mask(0) {}
+    __device__ PackedWalk() : first(-kTogether), m(-1), chunk(0), loaded(-1), mine(0), off(blockIdx.x), back(false), mask(0) {}
     __device__ __forceinline__ void load(const AttnParams& p) {  // how many units the chunk's 32 sequences have
         if (loaded == chunk) return;
         const int b = chunk + (threadIdx.x & 31);
@@ -248,7 +250,6 @@ struct PackedWalk {
         mask = __ballot_sync(0xffffffffu, mine > m);
     }
     __device__ __forceinline__ bool next(const AttnParams& p, AttnPiece& w) {
-        const int C = gridDim.x, want = wave * C + ((wave & 1) ? C - 1 - (int)blockIdx.x : (int)blockIdx.x);
         while (first < p.num_seqs) {
             if (m < 0) {
                 first += kTogether;
@@ -256,18 +257,19 @@ struct PackedWalk {
                 continue;
             }
             const int here = __popc(mask) * p.num_kv_heads;
-            if (want < rank0 + here) {
-                const int off = want - rank0, j = off / p.num_kv_heads;
+            if (off < here) {
+                const int j = off / p.num_kv_heads;
                 w.g = off - j * p.num_kv_heads;
                 w.b = chunk + __fns(mask, 0, j + 1);
                 w.n = at_sequence<kAttnPacked>(p, w.b, w.c0, w.len);
                 at_fields(p, m, w);
                 at_stages(p, 0, w.nst, w);
                 w.cut_end = -1;
-                ++wave;
+                off += 2 * (back ? (int)blockIdx.x : (int)(gridDim.x - 1 - blockIdx.x)) + 1;
+                back = !back;
                 return true;
             }
-            rank0 += here;
+            off -= here;
             chunk += 32;
             if (chunk >= end(p)) chunk = first, --m;
             load(p);

@@ -33,6 +33,14 @@ PA_HD int sequence_tokens(int c0, int end, int len, int num_tokens, int max_new,
     return wrong ? 0 : n;
 }
 
+// The most units of up to two tiles of T tokens that packed sequences can have, whatever their lengths within max_len and
+// num_tokens in all: each one's full units, and one more where it has tokens.  (max_len alone, however loose, is no measure.)
+PA_HD int64_t most_packed_units(int64_t num_seqs, int64_t num_tokens, int64_t max_len, int64_t kv_heads, int T) {
+    const int64_t by_length = (max_len + 2 * T - 1) / (2 * T) * num_seqs;
+    const int64_t by_tokens = num_tokens / (2 * T) + (num_seqs < num_tokens ? num_seqs : num_tokens);
+    return (by_length < by_tokens ? by_length : by_tokens) * kv_heads;
+}
+
 constexpr int kTwoTiles = 2;     // weight of a key that two query tiles share
 constexpr int kOneTile = 1;      // of one that a single tile uses
 // U: a piece's query rows and epilogue take about as long as eight stages of one tile (4 sequences of 129 to 517 tokens over

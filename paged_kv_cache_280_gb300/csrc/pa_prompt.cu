@@ -77,8 +77,7 @@ extern "C" pa_status pa_prompt_attention(void* out, const void* q, int64_t q_str
         !rows_map(&tv, v, num_tokens, num_kv_heads, head_dim, v_stride, 1, kAttnKeys))
         return PA_ERR_CUDA;
     // a CTA per unit where there are fewer than SMs
-    const int64_t units = (int64_t)((p.max_q_len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens)) * num_seqs * num_kv_heads;
-    if (units >= INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+    const int64_t units = most_packed_units(num_seqs, num_tokens, p.max_q_len, num_kv_heads, p.tile_tokens);
     const int grid = (int)(units < sms ? units : sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return head_dim == 128 ? launch_attn<kAttnPacked, 128>(p, dev, grid, tq, tk, tv, st)

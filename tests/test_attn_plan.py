@@ -21,6 +21,9 @@ int t_sequence(int c0, int end, int len, int num_tokens, int max_new, int max_le
     *wrong = w;
     return n;
 }
+long long t_most_packed_units(int seqs, int tokens, int max_len, int kv_heads, int T) {
+    return most_packed_units(seqs, tokens, max_len, kv_heads, T);
+}
 }
 """
 
@@ -35,7 +38,9 @@ def plan(tmp_path_factory):
     src.write_text(SHIM)
     # signed overflow ends the process instead of wrapping unseen
     subprocess.check_call([cxx, "-std=c++17", "-O1", "-ftrapv", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)])
-    return ctypes.CDLL(str(lib))
+    lib = ctypes.CDLL(str(lib))
+    lib.t_most_packed_units.restype = ctypes.c_longlong
+    return lib
 
 
 def test_tokens_of_sequences_whatever_the_offsets(plan):
@@ -52,3 +57,20 @@ def test_tokens_of_sequences_whatever_the_offsets(plan):
         bad = n < 0 or (n > 0 and (c0 < 0 or end > tokens or n > new or n > length or length > longest))
         got = plan.t_sequence(c0, end, length, tokens, new, longest, ctypes.byref(wrong))
         assert (got, bool(wrong.value)) == (0 if bad else n, bad), (c0, end, length, tokens, new, longest)
+
+
+def test_most_units_of_packed_sequences(plan):
+    """Never below the units that there are, and no more than their tokens allow where the bound on the lengths is loose."""
+    rng = random.Random(2)
+    for _ in range(3000):
+        T, heads = 128 // rng.randint(1, 8), rng.randint(1, 70)
+        top = rng.choice([1, 3, 40, 300, 5000])
+        lens = [rng.choice([0, 1, top, rng.randint(0, top)]) for _ in range(rng.randint(1, 60))]
+        tokens = sum(lens) + rng.randint(0, 9)
+        loose = rng.choice([max(lens), tokens, max(lens) + rng.randint(0, 100)])
+        there = sum(-(-n // (2 * T)) for n in lens) * heads
+        most = plan.t_most_packed_units(len(lens), tokens, loose, heads, T)
+        assert there <= most <= (tokens // (2 * T) + len(lens)) * heads
+    assert plan.t_most_packed_units(65535, 66000, 66000, 8, 16) == 8 * (66000 // 32 + 65535)
+    assert plan.t_most_packed_units(65535, INT_MAX, INT_MAX, 65535, 16) < 2 ** 43
+    assert plan.t_most_packed_units(7, 4096, 33, 3, 16) == 7 * 2 * 3

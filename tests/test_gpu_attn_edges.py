@@ -33,3 +33,26 @@ def test_chunks_of_offsets_past_32_bits_are_flagged(kind, d):
         got = c.run()
         assert c.status() == pa.PA_DEV_BAD_SEQ_LEN
         _check(got, want, bound)
+
+
+def test_tens_of_thousands_of_prompts_and_a_bound_of_all_tokens():
+    """As many prompts as a call takes, nearly all of one token (whose output is its value, exactly), a bound on the lengths that
+    only the sum of them keeps, and longer prompts at the ends and between."""
+    import torch
+
+    hq, hkv, d, n = 64, 8, 64, 65535
+    lens = np.ones(n, np.int64)
+    lens[[0, 31000, n - 1]] = 150, 61, 200
+    lens[[5, 6, 40000]] = 0
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    total = int(starts[-1])
+    x = torch.randn(total, hq + 2 * hkv, d, device="cuda", generator=torch.Generator("cuda").manual_seed(3)).to(torch.bfloat16)
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    got, status = _run(q, k, v, starts, 0.125, max_len=1 << 30)
+    assert status == 0
+    single = torch.tensor(np.repeat(lens == 1, lens), device="cuda")
+    assert torch.equal(got[single], v[single].repeat_interleave(hq // hkv, 1))
+    for b in (0, 31000, n - 1):
+        rows = slice(int(starts[b]), int(starts[b + 1]))
+        host = [t[rows].contiguous().view(torch.int16).cpu().numpy().view(np.uint16) for t in (q, k, v)]
+        _check(got[rows], *chunks.prompts(*host, [0, int(lens[b])], 0.125))
