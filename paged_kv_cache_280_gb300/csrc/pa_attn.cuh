@@ -70,7 +70,8 @@ struct AttnParams {
     uint32_t group_inverse;        // 2^16 / G rounded up: rows below 256 divided by G
     int32_t out_align32;           // out is 32-byte aligned: 32-byte stores
     int32_t max_len;               // pools: the longest context that a table holds (kAttnMaxLen at most)
-    float scale_log2, out_scale;
+    float scale_log2, out_scale;   // pools: scale_log2 in [1, 2], times 2^scale_exp
+    int32_t scale_exp;
 };
 
 constexpr int kAtRows = 128;
@@ -1028,7 +1029,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
     const int r = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), row_tmem = lanes + kAtTmemHalf * t;
     float2* odd_ml = reinterpret_cast<float2*>(base + L::kMlOff);
-    float c = p.scale_log2;  // > 0 (checked on the host)
+    float c = p.scale_log2;  // > 0 (checked on the host); pools: the row's, below
     int ck = 0, pc = 0, oc0 = 0, oc1 = 0, hand = 0;  // stages, pieces, final O of each half, odd halves handed over
     AttnPieces<SRC, D> pieces(base, bars);
     AttnPiece w;
@@ -1048,8 +1049,11 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             tc_fence_after();
             if constexpr (SRC != kAttnPacked) {  // (the factors were written before the MMAs of this S were issued)
                 if (i == 0) {
-                    const uint32_t e = reinterpret_cast<const volatile uint8_t*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
-                    c = valid ? p.scale_log2 * __uint_as_float(e << 23) : p.scale_log2;
+                    // The row's factor goes through c's exponent, held inside fp32's: a c of 0 or infinity would make NaN of a
+                    // masked or a zero score.  Where it is held, nothing changes: S is below 2^21, so at 2^-126 all the row's
+                    // weights are 1, and unequal scores differ by 2^-34 and more, so at 2^126 all but the largest's are 0.
+                    const int e = reinterpret_cast<const volatile uint8_t*>(base + L::kRowOff)[(pc & 1) * 256 + tile * 128 + r];
+                    c = p.scale_log2 * __uint_as_float((uint32_t)min(max((valid ? e : 127) + p.scale_exp, 1), 253) << 23);
                 }
             }
             __syncwarp();  // (TMEM instructions want the whole warp, here and wherever lanes part before one)

@@ -65,7 +65,12 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.group = group, p.tile_tokens = kAtRows / group;
     p.group_inverse = (65536u + p.group - 1) / p.group;
     p.out_align32 = aligned_to(out, 32) ? 1 : 0;
-    p.scale_log2 = scale_log2, p.out_scale = v_scale;
+    // the same product as a number in [1, 2] and its power of two (its factors may lie near fp32's ends, and so may the rows')
+    int e_scale, e_pool, e_product;
+    const float product = std::frexp(scale, &e_scale) * std::frexp(k_scale, &e_pool) * 1.4426950408889634f;
+    p.scale_log2 = 2.f * std::frexp(product, &e_product);
+    p.scale_exp = e_scale + e_pool + e_product - 1;
+    p.out_scale = v_scale;
     CUtensorMap none;  // not read: the codes come by bulk copies
     memset(&none, 0, sizeof none);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -56,3 +56,29 @@ def test_tens_of_thousands_of_prompts_and_a_bound_of_all_tokens():
         rows = slice(int(starts[b]), int(starts[b + 1]))
         host = [t[rows].contiguous().view(torch.int16).cpu().numpy().view(np.uint16) for t in (q, k, v)]
         _check(got[rows], *chunks.prompts(*host, [0, int(lens[b])], 0.125))
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("lens,news,hq,hkv", [([300, 140], [60, 140], 4, 2), ([5001, 77], [5, 77], 8, 1)])
+@pytest.mark.parametrize("scale", [2e-8, 2e-25, 2e-36])
+def test_chunks_zero_rows_under_the_smallest_scales(kind, d, lens, news, hq, hkv, scale):
+    """A row of zeros weighs all the keys that it sees the same, whatever the scales, in units that are cut and that are not."""
+    c = Case(830 + d, kind, lens, news, hq, hkv, d, 16, scale=scale)
+    c.q[[0, 3, len(c.q) - 1]] = 0
+    c.q[2, 1] = 0
+    c.q[4, 0] = 0x8000  # negative zeros
+    c.check(c.run())
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("scale", [1.0, 8.0, 1e30])
+def test_chunks_largest_rows_over_keys_of_zeros(kind, d, scale):
+    """Query rows at bf16's end, whose factor times the scale leaves fp32: scores of 0 all the same."""
+    c = Case(840 + d, kind, [300, 140], [60, 140], 4, 2, d, 16, size=5e37, scale=scale)
+    if kind == "fp8":
+        c.kp[c.kp != 0x7F] &= 0x80
+    else:
+        c.kp[:, :, : 16 * d // 2] &= 0x88
+    c.check(c.run())
+    assert c.status() == 0
