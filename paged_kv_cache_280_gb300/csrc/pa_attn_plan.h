@@ -27,9 +27,8 @@ constexpr int kAttnMaxLen = INT32_MAX - 255;  // longest sequence: a stage's key
 // breaks the call's bounds.  The rows are compared with those before they are subtracted: a difference of two offsets that
 // are anything may leave 32 bits.  (INT32_MAX for len: its new tokens are all there is.)
 PA_HD int sequence_tokens(int c0, int end, int len, int num_tokens, int max_new, int max_len, bool& wrong) {
-    wrong = end < c0 || (end > c0 && (c0 < 0 || end > num_tokens));
-    const int n = wrong ? 0 : end - c0;
-    if (n > 0) wrong = n > max_new || n > len || len > max_len;
+    const int n = (int)((uint32_t)end - (uint32_t)c0);
+    wrong = end < c0 || (end > c0 && (c0 < 0 || end > num_tokens || n > max_new || n > len || len > max_len));
     return wrong ? 0 : n;
 }
 
