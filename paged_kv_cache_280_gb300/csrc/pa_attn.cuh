@@ -62,7 +62,7 @@ struct AttnParams {
     const int32_t* cu_q_lens;
     int32_t* status;
     int4* cuts;                    // pools: [grid] the cut unit that begins in a CTA: first row of q, tokens, KV head, last CTA (-1: none)
-    float2* part_ml;               // pools: [2 * grid slots][tiles][128]: maximum (base 2) and sum of a row's piece
+    float2* part_ml;               // pools: [2 * grid slots][tiles][128]: reference (base 2, times kAtRefUnit) and sum of a row's piece
     float* part_o;                 // pools: [2 * grid slots][tiles][128][D]
     int32_t part_tiles;            // tiles per slot
     int32_t max_blocks_per_seq, num_seqs, num_q_heads, num_kv_heads, num_blocks, num_q_tokens, max_q_len, bs_shift;
@@ -83,6 +83,12 @@ constexpr float kAtRescaleLog2 = 8.f;
 // f16 weights are held times 2^7: with the lazy rescaling they stay below 2^15, and keep all their bits down to 2^-21 of
 // the largest.
 constexpr float kAtWeightLog2 = 7.f;
+// A weight is 2^(c s + shift), one fma, with shift = 7 - c m (packed: -c m) rounded to fp32, the same for all keys that share
+// m; what rescales and joins takes differences of such shifts, so their rounding cancels.  It is 1 / 2 at most, and the f16
+// weights stay in range, while |c m| is below this; a piece with larger scores goes to at_softmax_large.
+constexpr float kAtLargeLog2 = 4194304.f;
+// A piece's reference (minus its shift) is handed on times this: finite however large c m is.
+constexpr float kAtRefUnit = 1.f / 4294967296.f;
 
 template <int I = 0, int N, class F>
 __device__ __forceinline__ void at_static_for_impl(F& f) {
@@ -103,6 +109,9 @@ __device__ __forceinline__ float at_exp2(float x) {
     return y;
 }
 
+// 2^x, x a difference of references.
+__device__ __forceinline__ float at_ref_exp2(float x) { return at_exp2(x * (1.f / kAtRefUnit)); }
+
 template <int SRC, int D>
 struct AttnLayout {
     static constexpr bool kPools = SRC != kAttnPacked;
@@ -116,7 +125,7 @@ struct AttnLayout {
     static constexpr int kRingOff = 2 * kTileBytes;
     static constexpr int kRawOff = kRingOff + kSlots * kTileBytes;
     static constexpr int kRowOff = kRawOff + kRaws * kRawBytes;  // pools: row factors' exponents [2 pieces][2 tiles][128] bytes
-    static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's (m, l) [128]
+    static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's maximum and sum (below 0: a large piece's) [128]
     static constexpr int kBarOff = kMlOff + 128 * 8;
     static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
     static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // abort flag, TMEM address; work range at + 16
@@ -1019,11 +1028,92 @@ __device__ __forceinline__ void at_store_bf16(uint16_t* dst, const float* x, boo
     }
 }
 
+// The rest of a piece, from stage i on (whose scores have arrived), for a warp some of whose rows have scores past
+// kAtLargeLog2: their maximum is taken off the scores before c scales them, P = 2^(c (s - m)) (pools: 2^7 of it), at any size.
+// Apart from the loop below, whose registers and code it leaves alone (with a branch for such rows in it, all others took 2 to
+// 10 % longer): each stage's scores pass through twice, quarter by quarter.
+template <int SRC, int D>
+__device__ __forceinline__ bool at_softmax_large(const AttnBars<SRC, D>& bars, int t, volatile int32_t* abort_flag, int32_t* status,
+                                                 uint32_t row_tmem, float c, const AttnPiece& w, int pos, int pos_high, int lane,
+                                                 int i, int mine, int& ck, float& m_raw, float& l_run) {
+    constexpr float kTop = SRC == kAttnPacked ? 0.f : kAtWeightLog2;
+    // what the loop before has summed is relative to its rounded shift
+    const float old_shift = kTop - m_raw * c;
+    const int i0 = i;
+#pragma unroll 1
+    for (; i < mine; ++i, ++ck) {
+        if (i > i0 && !at_wait(bars.s_full(t), ck & 1, abort_flag, status)) return false;
+        tc_fence_after();
+        __syncwarp();
+        const int key0 = (w.k0 + (w.one ? 2 * i + t : i)) * kAttnKeys;
+        const int nq = max(0, min(4, (pos_high - key0 + 32) >> 5));
+        uint32_t x[32];
+        auto load = [&](int q) {
+            const int seen = pos - key0 - 32 * q;
+            tmem_ld32(row_tmem + 32 * q, x);
+            tmem_wait_ld32(x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (e > seen) x[e] = __float_as_uint(-INFINITY);
+        };
+        float m_new = m_raw;
+#pragma unroll 1
+        for (int q = 0; q < nq; ++q) {
+            load(q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) m_new = fmaxf(m_new, __uint_as_float(x[e]));
+        }
+        if (i > 0) {
+            const float f = m_raw == -INFINITY ? 0.f
+                            : i == i0          ? at_exp2(kTop - fmaf(m_new, c, old_shift))
+                                               : at_exp2((m_raw - m_new) * c);
+            if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                for (int c0o = 0; c0o < D; c0o += 32) {
+                    tmem_ld32(row_tmem + kAtTmemO + c0o, x);
+                    tmem_wait_ld32(x);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                    tmem_st32(row_tmem + kAtTmemO + c0o, x);
+                }
+                l_run *= f;
+            }
+        }
+        m_raw = m_new;
+        const float less = m_raw > -INFINITY ? m_raw : 0.f;
+#pragma unroll 1
+        for (int q = 3; q >= 0; --q) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pw[e] = 0u;
+            if (q < nq) {
+                load(q);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float x0 = at_exp2(fmaf(__uint_as_float(x[e]) - less, c, kTop));
+                    const float x1 = at_exp2(fmaf(__uint_as_float(x[e + 1]) - less, c, kTop));
+                    l_run += x0 + x1;
+                    pw[e / 2] = SRC == kAttnPacked ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+                }
+            }
+            tmem_st16(row_tmem + kAtTmemP + 16 * q, pw);
+            if (q & 1) continue;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q ? bars.p_first(t) : bars.p_second(t));
+            __syncwarp();
+        }
+    }
+    return true;
+}
+
 // Half t: warps 4 t .. 4 t + 3, row r = 32 (warp % 4) + lane = TMEM lane r.
 template <int SRC, int D>
 __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* base, uint32_t tmem,
                                            const AttnBars<SRC, D>& bars, volatile int32_t* misc, int warp, int lane) {
     using L = AttnLayout<SRC, D>;
+    constexpr float kTop = SRC == kAttnPacked ? 0.f : kAtWeightLog2;
     volatile int32_t* abort_flag = misc;
     const int G = p.group, Hq = p.num_q_heads, T = p.tile_tokens;
     const int r = 32 * (warp & 3) + lane;
@@ -1043,7 +1133,11 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
         const int pos = w.len - w.n + (valid ? tok : i1 - 1);
         const int pos_low = __shfl_sync(0xffffffffu, pos, 0), pos_high = __shfl_sync(0xffffffffu, pos, 31);  // (they do not fall)
         float m_raw = -INFINITY, l_run = 0.f;  // maximum of the raw scores, and the weights' sum
-        for (int i = 0; i < mine; ++i, ++ck) {
+        auto shift_of = [&](float m) { return kTop - m * c; };
+        // (of the warp's rows; those of no token hold anything and have no say)
+        auto is_large = [&](float m) { return __any_sync(0xffffffffu, valid && m > -INFINITY && fabsf(m) * c > kAtLargeLog2) != 0; };
+        int i = 0;
+        for (; i < mine; ++i, ++ck) {
             const int k = w.k0 + (w.one ? 2 * i + t : i);
             if (!at_wait(bars.s_full(t), ck & 1, abort_flag, p.status)) return;
             tc_fence_after();
@@ -1114,11 +1208,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             if (!kLeaveOut || nq > 2) larger(xc);
             const float m_new = fmaxf(m_raw, fmaxf(fmax3(mx0, mx1, mx2), mx3));
             if (i == 0) {
+                if (is_large(m_new)) break;
                 m_raw = m_new;
             } else {
                 const bool need = (m_new - m_raw) * c > kAtRescaleLog2;
                 if (__any_sync(0xffffffffu, need)) {
-                    const float f = need ? at_exp2((m_raw - m_new) * c) : 1.f;
+                    if (is_large(m_new)) break;
+                    const float f = need ? at_exp2(shift_of(m_new) - shift_of(m_raw)) : 1.f;
 #pragma unroll 1
                     for (int c0o = 0; c0o < D; c0o += 32) {
                         uint32_t x[32];
@@ -1133,8 +1229,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
                 }
             }
             // P = 2^(c s - c m) (over pools 2^7 of it).  A row that has seen no key yet weighs all of them 0.
-            const float mc = m_raw > -INFINITY ? m_raw * c : 0.f;
-            const float shift = SRC == kAttnPacked ? -mc : kAtWeightLog2 - mc;
+            const float shift = shift_of(m_raw > -INFINITY ? m_raw : 0.f);
             const uint64_t c2 = f2_pack(c, c), sh2 = f2_pack(shift, shift);
             uint64_t sum2 = f2_pack(0.f, 0.f);
             auto weigh = [&](int q, const uint32_t(&x)[32]) {
@@ -1181,11 +1276,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             f2_unpack(sum2, sa, sb);
             l_run += sa + sb;
         }
-        float m = m_raw > -INFINITY ? m_raw * c : -INFINITY;  // base 2
+        bool large = i < mine;  // of the warp's rows: O and l_run are relative to 2^(c m - kTop), not to 2^-shift
+        if (large && !at_softmax_large<SRC, D>(bars, t, abort_flag, p.status, row_tmem, c, w, pos, pos_high, lane, i, mine, ck, m_raw, l_run))
+            return;
         ++pc;
         if (w.one && t == 1) {
             if (mine > 0) {
-                odd_ml[r] = make_float2(m, l_run);
+                odd_ml[r] = make_float2(m_raw, large ? -l_run : l_run);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.odd_ml());
                 if (!at_wait(bars.odd_read(), hand & 1, abort_flag, p.status)) return;
@@ -1207,11 +1304,15 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             if (!at_wait(bars.odd_ml(), hand & 1, abort_flag, p.status)) return;
             ++oc1, ++hand;
             const float2 o = odd_ml[r];
-            const float top = fmaxf(m, o.x);
-            f0 = m > -INFINITY ? at_exp2(m - top) : 0.f;
-            f1 = o.x > -INFINITY ? at_exp2(o.x - top) : 0.f;
-            l_run = l_run * f0 + o.y * f1;
-            m = top;
+            const float top = fmaxf(m_raw, o.x);
+            const bool odd_large = o.y < 0.f, any_large = large || odd_large;
+            auto factor = [&](float m, bool was_large) {  // from a half's reference to both halves'
+                const float x = !any_large ? shift_of(top) - shift_of(m) : was_large ? (m - top) * c : kTop - fmaf(top, c, shift_of(m));
+                return m > -INFINITY ? at_exp2(x) : 0.f;
+            };
+            f0 = factor(m_raw, large), f1 = factor(o.x, odd_large);
+            l_run = l_run * f0 + fabsf(o.y) * f1;
+            m_raw = top, large = any_large;
         }
         __syncwarp();
         tc_fence_after();
@@ -1256,7 +1357,10 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             if (lane == 0) mbar_arrive(bars.odd_read());
         }
         if constexpr (SRC != kAttnPacked) {
-            if (!whole && valid) __stcg(p.part_ml + part, make_float2(m, l_run));
+            if (!whole && valid) {
+                const float ref = large ? m_raw * (c * kAtRefUnit) - kTop * kAtRefUnit : -shift_of(m_raw) * kAtRefUnit;
+                __stcg(p.part_ml + part, make_float2(m_raw > -INFINITY ? ref : -INFINITY, l_run));
+            }
             if (w.cut_end >= 0 && t == 0 && r == 0)
                 p.cuts[blockIdx.x] = make_int4(w.c0 + i0, min(w.n - i0, w.one ? T : 2 * T), w.g, w.cut_end);
         }
@@ -1417,7 +1521,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) attn_join_kernel(const Att
         for (int u = 0; u < kJoinRows; ++u) {
             if (c > b) ml[u].x = -INFINITY;
             const float m = fmaxf(M[u], ml[u].x);
-            if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + ml[u].y * at_exp2(ml[u].x - m);
+            if (m > -INFINITY) L[u] = L[u] * at_ref_exp2(M[u] - m) + ml[u].y * at_ref_exp2(ml[u].x - m);
             M[u] = m;
         }
         if (c - lane + 32 > b) break;
@@ -1429,7 +1533,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) attn_join_kernel(const Att
         for (int u = 0; u < kJoinRows; ++u) {
             const float m2 = __shfl_xor_sync(0xffffffffu, M[u], x), l2 = __shfl_xor_sync(0xffffffffu, L[u], x);
             const float m = fmaxf(M[u], m2);
-            if (m > -INFINITY) L[u] = L[u] * at_exp2(M[u] - m) + l2 * at_exp2(m2 - m);
+            if (m > -INFINITY) L[u] = L[u] * at_ref_exp2(M[u] - m) + l2 * at_ref_exp2(m2 - m);
             M[u] = m;
         }
 #pragma unroll
@@ -1442,7 +1546,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 3) attn_join_kernel(const Att
     for (int c0 = a;;) {
 #pragma unroll
         for (int u = 0; u < kJoinRows; ++u) {
-            const float f = m_at[u] > -INFINITY && c0 + (lane & (kJoinAhead - 1)) <= b ? at_exp2(m_at[u] - M[u]) * L[u] : 0.f;
+            const float f = m_at[u] > -INFINITY && c0 + (lane & (kJoinAhead - 1)) <= b ? at_ref_exp2(m_at[u] - M[u]) * L[u] : 0.f;
 #pragma unroll
             for (int i = 0; i < kJoinAhead; ++i) {
                 const float g = __shfl_sync(0xffffffffu, f, i);

@@ -3,7 +3,8 @@ in float64."""
 import numpy as np
 import pytest
 
-from oracle import chunks
+from gpu_cases import to_numpy, to_torch, widen
+from oracle import chunks, kv4
 from test_gpu_prefill_quant import KINDS, Case
 from test_gpu_prompt import _check, _inputs, _run
 
@@ -82,3 +83,65 @@ def test_chunks_largest_rows_over_keys_of_zeros(kind, d, scale):
         c.kp[:, :, : 16 * d // 2] &= 0x88
     c.check(c.run())
     assert c.status() == 0
+
+
+def _near(got, want, v_top, weight_eps, where=""):
+    """Where the scores are exact: weights rounded (relative weight_eps) in the product with V, their exponents' fp32 rounding and
+    the sums' (2^-16 together), and the output's."""
+    g = widen(to_numpy(got))
+    assert np.all(np.isfinite(g)), where
+    err, limit = np.abs(g - want), (weight_eps + 2.0 ** -16) * v_top * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+    assert np.all(err <= limit), f"{where}: max |err| {err.max():.3e}, {np.max(err / limit):.2f} of the bound"
+
+
+def _one_element_rows(shape, size, seed):
+    """Query rows with one element that is not 0, +-size: their products with keys are exact in fp32, whatever the size."""
+    rng = np.random.default_rng(seed)
+    q = np.zeros(shape, np.float32)
+    at = rng.integers(0, shape[2], shape[:2])
+    np.put_along_axis(q, at[..., None], rng.choice([-size, size], shape[:2])[..., None], 2)
+    return kv4.to_bf16(q)
+
+
+LARGE = [(2.0 ** 10, 1.0), (2.0 ** 17, 1.0), (2.0 ** 26, 1.0), (2.0 ** 33, 2.0), (2.0 ** 70, 1.0), (2.0 ** 124, 1.0), (2.0 ** 124, 2.0 ** 20),
+         (1.0, 2.0 ** 40), (2.0 ** 100, 2.0 ** 100)]
+
+
+@pytest.mark.parametrize("size,scale", LARGE)
+@pytest.mark.parametrize("hq,hkv,d,lens", [(8, 2, 128, [300, 1, 700]), (4, 4, 64, [129, 520])])
+def test_prompts_of_exact_scores_however_large(hq, hkv, d, lens, size, scale):
+    """Scores past every power of two that fp32 and the weights have: the largest take all, in equal parts where they are equal."""
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    (q, k, v), (_, dk, dv) = _inputs(31 + d, int(starts[-1]), hq, hkv, d, False)
+    k = kv4.to_bf16(np.round(widen(k) * 2) / 2)  # few values, so that many keys share the largest score
+    q = _one_element_rows(q.shape, size, 5)
+    got, status = _run(to_torch(q), to_torch(k), dv, starts, scale)
+    assert status == 0
+    _near(got, chunks.prompts(q, k, v, starts, np.float64(scale))[0], np.abs(widen(v)).max(), chunks.EPS_BF16)
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+@pytest.mark.parametrize("size,scale", LARGE)
+@pytest.mark.parametrize("lens,news,hq,hkv", [([300, 140], [60, 140], 4, 2), ([5001, 77, 900], [5, 77, 200], 8, 1)])
+def test_chunks_of_exact_scores_however_large(kind, d, lens, news, hq, hkv, size, scale):
+    """The same over pools, in whole and in cut units, of one tile and of two."""
+    c = Case(850 + d, kind, lens, news, hq, hkv, d, 16, scale=scale)
+    c.q = _one_element_rows(c.q.shape, size, 6)
+    got = c.run()
+    assert c.status() == 0
+    top = np.nanmax(np.abs(chunks.pool_values(c.vp, kind, d, 16))) * c.vs
+    _near(got, c.want()[0], top, chunks.EPS_F16)
+
+
+@pytest.mark.parametrize("common", [2.0 ** 12, 2.0 ** 16, 2.0 ** 19])
+def test_prompts_of_large_scores_that_differ_little(common):
+    """scale q k is a large number that all keys share plus one of 0 .. 4: only the small one counts."""
+    starts = np.array([0, 700, 1000], np.int32)
+    (q, k, v), (_, _, dv) = _inputs(33, 1000, 4, 2, 128, False)
+    q, k = np.zeros(q.shape, np.float32), np.zeros(k.shape, np.float32)
+    q[..., 0], q[..., 1] = common, 1
+    k[..., 0], k[..., 1] = 1, np.random.default_rng(7).integers(0, 5, k.shape[:2])
+    q, k = kv4.to_bf16(q), kv4.to_bf16(k)
+    got, status = _run(to_torch(q), to_torch(k), dv, starts, 1.0)
+    assert status == 0
+    _near(got, chunks.prompts(q, k, v, starts, 1.0)[0], np.abs(widen(v)).max(), chunks.EPS_BF16)
