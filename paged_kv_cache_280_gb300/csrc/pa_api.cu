@@ -1,7 +1,5 @@
 // Host side of pa_decode_attention: argument checks, the workspace layout,
 // grid sizing, the TMA descriptors of the two pools, and the launch.
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -41,8 +39,6 @@ bool current_device(int* dev, int* sms) {
     return true;
 }
 
-namespace {
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -56,6 +52,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     });
     return fn;
 }
+
+namespace {
 
 // 2-D view of a pool: rows = num_blocks * Hkv * BS, columns = head_dim; one
 // box = BS rows x 128 bytes, loaded with the 128-byte swizzle.

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -157,6 +158,8 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
 // Host launch helpers shared by the entry points (pa_api.cu).
 // The current device and its SM count, which is asked for once.
 bool current_device(int* dev, int* sms);
+// The driver's encoder of tensor maps, looked up once; null where it is missing.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // The TMA map of a pool viewed as [num_blocks * Hkv * block_size][head_dim]
 // rows, one box = block_size rows x 128 bytes with the 128-byte swizzle;
 // cached per (device, pool, shape).

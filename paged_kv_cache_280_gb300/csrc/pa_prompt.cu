@@ -1,8 +1,5 @@
 // Attention over whole prompts, packed one behind the other: entry point and checks; the kernel in pa_attn.cuh.
 #include <cmath>
-#include <mutex>
-
-#include <cudaTypedefs.h>
 
 #include "pa_attn.cuh"
 
@@ -16,15 +13,7 @@ constexpr int64_t kMaxRowStride = (int64_t)1 << 38;
 // (head_dim, heads, tokens): one box = 64 elements x box_heads x box_tokens with the 128-byte swizzle.
 bool rows_map(CUtensorMap* map, const void* rows, int64_t tokens, int heads, int head_dim, int64_t stride, int box_heads,
               int box_tokens) {
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
+    const auto encode = tensor_map_encoder();
     if (!encode) return false;
     cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
