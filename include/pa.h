@@ -310,14 +310,17 @@ pa_status pa_decode_set_ctas_per_sm(int32_t ctas);
 /*
  * Testing aid for failure detection (no counterpart on the pages): the time
  * limit, in nanoseconds, of the decode kernel's waits for its query rows and
- * KV tiles (consumer side).  Every on-chip wait of the kernels is bounded; one
- * that runs out sets PA_DEV_WAIT_TIMEOUT in the status word, the CTA stops
- * issuing and consuming, waits (with the full limit) for the copies it has
- * already issued, and exits, so the context stays usable and the output of
- * that call is not valid.  A limit far below a DRAM round trip makes the waits
- * run out on purpose.  0 restores the default (2 s); values above it return
- * PA_ERR_INVALID_ARG.  Process-wide; affects later pa_decode_attention,
- * pa_decode_attention_fp8, _fp4 and pa_decode_attention_static calls.
+ * KV tiles (consumer side), and of all waits of pa_prompt_attention,
+ * pa_prefill_attention_fp8 and _fp4, where those that last as long as a piece of
+ * the work have 32 times as much and the clock is looked at now and then only.
+ * Every on-chip wait of the kernels is bounded; one that runs out sets
+ * PA_DEV_WAIT_TIMEOUT in the status word, the CTA stops issuing and consuming,
+ * waits (with the full limit) for the copies it has already issued, and exits, so
+ * the context stays usable and the output of that call is not valid.  A limit far
+ * below a DRAM round trip makes the waits run out on purpose.  0 restores the
+ * default (2 s); values above it return PA_ERR_INVALID_ARG.  Process-wide; affects
+ * later calls of the decode (pa_decode_attention, _fp8, _fp4, _static) and of the
+ * three attentions named.
  */
 pa_status pa_debug_set_wait_limit_ns(uint64_t ns);
 

@@ -678,7 +678,7 @@ def pa_decode_set_ctas_per_sm(ctas: int) -> None:
 
 
 def pa_debug_set_wait_limit_ns(ns: int) -> None:
-    """Testing aid: time limit of the decode consumer's waits (0 restores the 2 s default)."""
+    """Testing aid: time limit of the waits of the decode's consumer and of prompt and chunk attention (0 restores the 2 s default)."""
     _ok(_lib.pa_debug_set_wait_limit_ns(int(ns)), "pa_debug_set_wait_limit_ns")
 
 

@@ -27,6 +27,11 @@ std::mutex g_mu;
 
 }  // namespace
 
+uint64_t wait_limit_ns() {
+    const uint64_t ns = g_wait_limit_ns.load();
+    return ns ? ns : kWaitLimitNs;
+}
+
 bool current_device(int* dev, int* sms) {
     if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return false;
     std::lock_guard<std::mutex> lk(g_mu);
@@ -565,8 +570,7 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
     p.wave_skew = lp.wave_skew;
     p.scale_log2 = scale * 1.4426950408889634f * k_scale;
     p.out_scale = v_scale;
-    const uint64_t lim = g_wait_limit_ns.load();
-    p.wait_limit_ns = lim ? lim : kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns();
     p.merge_in_kernel = lp.merge_in_kernel ? 1 : 0;
     p.plan = static_cast<const int32_t*>(plan);
     p.k_pool = static_cast<const uint8_t*>(k_pool);

@@ -72,7 +72,9 @@ struct AttnParams {
     int32_t max_len;               // pools: the longest context that a table holds (kAttnMaxLen at most)
     float scale_log2, out_scale;   // pools: scale_log2 in [1, 2], times 2^scale_exp
     int32_t scale_exp;
+    int32_t wait_limit_ns;         // kWaitLimitNs, or less in tests
 };
+static_assert(kWaitLimitNs <= INT32_MAX, "a wait's limit is handed to the kernel in 32 bits");
 
 constexpr int kAtRows = 128;
 constexpr int kAtKvWarp = 8, kAtMmaWarp = 9, kAtQWarp = 11, kAtWidenWarp = 12;
@@ -128,7 +130,7 @@ struct AttnLayout {
     static constexpr int kMlOff = kRowOff + (kPools ? 2 * 2 * 128 : 0);  // odd half's maximum and sum (below 0: a large piece's) [128]
     static constexpr int kBarOff = kMlOff + 128 * 8;
     static constexpr int kNumBars = 2 * kSlots + 2 * kRaws + 21;
-    static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // abort flag, TMEM address; work range at + 16
+    static constexpr int kMiscOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // abort flag, limit, TMEM address; work range at + 16
     static constexpr int kPieceOff = kMiscOff + 80;                           // two pieces of kPieceBytes
     static constexpr int kPieceBytes = 48;
     static constexpr int kBytes = kPieceOff + 2 * kPieceBytes + 1024;  // +1 KB to align the base
@@ -160,10 +162,10 @@ struct AttnBars {
     __device__ uint32_t turn(int t) const { return at(kRest + 15 + t); }  // the half's turn at the tensor core
 };
 
-// One thread's bounded wait; gives up once the CTA's abort flag is set.  (The flag and the clock are looked at now and
+// One thread's wait, for `limits` times the launch's limit (behind the abort flag) at most; gives up once that flag is set.  (The flag and the clock are looked at now and
 // then only: a thread that is busy with them notices late that its phase has completed.)
 __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status,
-                                         uint64_t limit_ns = kWaitLimitNs) {
+                                         uint32_t limits = 1) {
     uint64_t since = 0;
     for (int n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n & 31) continue;
@@ -171,7 +173,7 @@ __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile
         const uint64_t now = global_timer_ns();
         if (since == 0) {
             since = now;
-        } else if (now - since > limit_ns) {
+        } else if (now - since > (uint64_t)(uint32_t)abort_flag[1] * limits) {
             *abort_flag = 1;
             flag_status(status, PA_DEV_WAIT_TIMEOUT);
             return false;
@@ -181,12 +183,12 @@ __device__ __forceinline__ bool at_wait1(uint32_t bar, uint32_t parity, volatile
 }
 // The same for a warp: its lanes go on together.
 __device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status,
-                                        uint64_t limit_ns = kWaitLimitNs) {
-    return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status, limit_ns));
+                                        uint32_t limits = 1) {
+    return __all_sync(0xffffffffu, at_wait1(bar, parity, abort_flag, status, limits));
 }
 // For the waits that last as long as a piece: one of the longest context that fits into memory takes some 20 s.  (Where a
-// copy or an MMA is lost, the other roles notice within kWaitLimitNs.)
-constexpr uint64_t kPieceLimitNs = 32 * kWaitLimitNs;
+// copy or an MMA is lost, the other roles notice within one limit.)
+constexpr uint32_t kPieceLimits = 32;
 
 __device__ __forceinline__ int at_token(const AttnParams& p, int row) { return (int)((uint32_t)row * p.group_inverse >> 16); }
 
@@ -444,7 +446,7 @@ struct AttnPieces {
     }
     // The walking warp: piece i (have: false behind the last one).
     __device__ __forceinline__ bool put(const AttnPiece& w, bool have, volatile int32_t* abort_flag, int32_t* status, int lane) {
-        if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status, kPieceLimitNs)) return false;
+        if (!at_wait(bars.piece_empty(i & 1), ((i >> 1) & 1) ^ 1, abort_flag, status, kPieceLimits)) return false;
         if (lane == 0) {
             int4* e = reinterpret_cast<int4*>(base + L::kPieceOff + (i & 1) * L::kPieceBytes);
             e[0] = make_int4(w.b, w.g, w.c0, w.n);
@@ -582,7 +584,7 @@ __device__ __forceinline__ void at_load_q_packed(const AttnParams& p, const CUte
         if (pc == pieces.i) break;  // (a wait was given up)
         pieces.get(pc, w);
         if (w.ns == 0) break;
-        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status, kPieceLimitNs)) break;
+        if (!at_wait(bars.q_empty(), (pc & 1) ^ 1, abort_flag, p.status, kPieceLimits)) break;
         if (lane == 0) {
             const int tiles = w.one ? 1 : 2;
             mbar_arrive_expect_tx(bars.q_full(), tile_bytes * tiles);
@@ -1377,7 +1379,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     const uint32_t raw_s = smem_u32(smem_raw), base_s = (raw_s + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_s - raw_s);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    volatile int32_t* misc = reinterpret_cast<volatile int32_t*>(base + L::kMiscOff);  // abort flag; TMEM address
+    volatile int32_t* misc = reinterpret_cast<volatile int32_t*>(base + L::kMiscOff);  // abort flag; the waits' limit; TMEM address
     AttnRange* range = reinterpret_cast<AttnRange*>(base + L::kMiscOff + 16);
     AttnBars<SRC, D> bars{base_s + L::kBarOff};
     if (tid == 0) {
@@ -1407,7 +1409,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
         mbar_init(bars.odd_ml(), 4);
         mbar_init(bars.odd_read(), 4);
         fence_barrier_init();
-        misc[0] = 0;
+        misc[0] = 0, misc[1] = p.wait_limit_ns;
     }
     if (warp == kAtMmaWarp) tmem_alloc(base_s + L::kMiscOff + 8, kAtTmemCols);
     pdl_wait_prerequisites();

@@ -158,6 +158,8 @@ pa_status decode_common(void* out, const void* q, const void* k_pool, const void
 // Host launch helpers shared by the entry points (pa_api.cu).
 // The current device and its SM count, which is asked for once.
 bool current_device(int* dev, int* sms);
+// What pa_debug_set_wait_limit_ns has set, or kWaitLimitNs.
+uint64_t wait_limit_ns();
 // The driver's encoder of tensor maps, looked up once; null where it is missing.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // The TMA map of a pool viewed as [num_blocks * Hkv * block_size][head_dim]

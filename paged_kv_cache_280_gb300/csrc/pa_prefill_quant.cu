@@ -64,6 +64,7 @@ pa_status prefill_quant(void* out, const void* q, const void* k_pool, const void
     p.max_len = (int32_t)(held < kAttnMaxLen ? held : kAttnMaxLen);
     p.group = group, p.tile_tokens = kAtRows / group;
     p.group_inverse = (65536u + p.group - 1) / p.group;
+    p.wait_limit_ns = (int32_t)wait_limit_ns();
     p.out_align32 = aligned_to(out, 32) ? 1 : 0;
     // the same product as a number in [1, 2] and its power of two (its factors may lie near fp32's ends, and so may the rows')
     int e_scale, e_pool, e_product;

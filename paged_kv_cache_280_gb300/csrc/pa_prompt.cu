@@ -57,6 +57,7 @@ extern "C" pa_status pa_prompt_attention(void* out, const void* q, int64_t q_str
     p.num_q_tokens = num_tokens, p.max_q_len = max_len < num_tokens ? max_len : num_tokens;
     p.group = num_q_heads / num_kv_heads, p.tile_tokens = kAtRows / p.group;
     p.group_inverse = (65536u + p.group - 1) / p.group;
+    p.wait_limit_ns = (int32_t)wait_limit_ns();
     p.out_align32 = aligned_to(out, 32) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f, p.out_scale = 1.f;
     if (!std::isfinite(p.scale_log2) || !(p.scale_log2 > 0.f)) return PA_ERR_INVALID_ARG;
