@@ -39,6 +39,7 @@
 //   57; a tile is one head's, so every key is widened for 256 rows at most).
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -118,6 +119,11 @@ template <int SRC, int D>
 struct AttnLayout {
     static constexpr bool kPools = SRC != kAttnPacked;
     static constexpr int kThreads = kPools ? 512 : 384;
+    // Registers a thread: at launch (all that a CTA alone on its SM can have), and the warpgroups' shares of those: two of
+    // softmax, loads and MMA, widening.
+    static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = kPools ? 168 : 216, kLoadRegs = kPools ? 80 : 72, kWidenRegs = kPools ? 96 : 0;
+    static_assert(2 * kSoftmaxRegs + kLoadRegs + kWidenRegs <= kThreads / 128 * kRegs, "more registers than the launch has: a wait for ever");
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = 128 * 128;           // 128 rows (query rows or keys) of 64 elements
     static constexpr int kTileBytes = kPanels * kPanelBytes;  // a query tile, or K or V of a stage
@@ -1420,18 +1426,13 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + L::kMiscOff + 8);
-    // Registers, of the launch's (packed 384 x 168, pools 512 x 128): two softmax warpgroups, loads and MMA, widening:
-    // packed 2 x 216 + 72 = 3 x 168, pools 2 x 168 + 80 + 96 = 4 x 128.
     if (L::kPools && warp >= kAtWidenWarp) {
         if constexpr (L::kPools) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;" ::: "memory");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kWidenRegs) : "memory");
             at_widen<SRC, D>(p, base, base_s, bars, misc, warp - kAtWidenWarp, lane);
         }
     } else if (warp >= 8) {
-        if constexpr (L::kPools)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kLoadRegs) : "memory");
         if (warp == kAtMmaWarp || warp == kAtMmaWarp + 1) {
             at_mma<SRC, D>(p, warp - kAtMmaWarp, base, base_s, tmem, bars, misc, lane);
         } else if constexpr (L::kPools) {
@@ -1446,10 +1447,7 @@ __global__ void __launch_bounds__(AttnLayout<SRC, D>::kThreads, 1)
                 at_load_q_packed<D>(p, &tmap_q, base, base_s, bars, misc, lane);
         }
     } else {
-        if constexpr (L::kPools)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;" ::: "memory");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs) : "memory");
         at_softmax<SRC, D>(p, warp >> 2, base, tmem, bars, misc, warp, lane);
     }
     tc_fence_before();
@@ -1585,12 +1583,15 @@ pa_status launch_attn(const AttnParams& p, int dev, int grid, const CUtensorMap&
     int occ = 0;
     if (!kernel_occupancy(dev, reinterpret_cast<const void*>(&attn_kernel<SRC, D>), L::kThreads, L::kBytes, &occ)) return PA_ERR_CUDA;
     if (occ <= 0) return PA_ERR_UNSUPPORTED;
-    // the roles' register shares (see the kernel) draw on what the launch gives: less would wait for ever
-    static const int regs = [] {
+    // The shares draw on what the launch gives, and with less the last one would be waited for for ever.  ptxas gives a kernel with
+    // shares all that its launch bounds allow; a build where it did not is refused here.  (Shares that fit are enough.)
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(&attn_kernel<SRC, D>)) == cudaSuccess ? a.numRegs : 0;
-    }();
-    if (regs != (L::kPools ? 128 : 168)) return PA_ERR_INTERNAL;
+        if (cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(&attn_kernel<SRC, D>)) != cudaSuccess) return PA_ERR_CUDA;
+        regs.store(a.numRegs);
+    }
+    if (regs.load() * (L::kThreads / 128) < 2 * L::kSoftmaxRegs + L::kLoadRegs + L::kWidenRegs) return PA_ERR_INTERNAL;
     if (launch_dependent(&attn_kernel<SRC, D>, dim3(grid), L::kThreads, L::kBytes, st, p, tq, tk, tv) != cudaSuccess) return PA_ERR_CUDA;
     if constexpr (L::kPools) {
         const dim3 join(grid, p.part_tiles * kAtRows / (kJoinRows * kJoinWarps));
