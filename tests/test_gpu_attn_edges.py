@@ -145,3 +145,43 @@ def test_prompts_of_large_scores_that_differ_little(common):
     got, status = _run(to_torch(q), to_torch(k), dv, starts, 1.0)
     assert status == 0
     _near(got, chunks.prompts(q, k, v, starts, 1.0)[0], np.abs(widen(v)).max(), chunks.EPS_BF16)
+
+
+@pytest.mark.parametrize("kind,d", KINDS)
+def test_chunks_leave_rows_behind_the_last_sequence(kind, d):
+    """Rows of the batch past the last chunk are left as they were, and what their queries hold reaches nothing."""
+    c = Case(860 + d, kind, [300, 90, 1500], [130, 1, 40], 6, 2, d, 16)
+    want, bound = c.want()
+    n = len(c.q)
+    c.q = np.concatenate([c.q, np.full((9, *c.q.shape[1:]), 0x7FC0, np.uint16)])  # NaN
+    got = c.run()
+    assert c.status() == 0 and (got[n:] == 7).all()
+    _check(got[:n], want, bound)
+
+
+@pytest.mark.parametrize("kind,d", [("fp8", 128), ("fp4", 64)])
+def test_chunks_of_as_many_sequences_as_a_call_takes(kind, d):
+    """65535 sequences, over a hundred blocks that they share: most of one token, whose output is its value; some with no new token,
+    some longer, at the ends and between."""
+    import torch
+
+    b, hq, hkv, bs, shared = 65535, 8, 2, 16, 100
+    c = Case(870 + d, kind, [16] * shared, [1] * shared, hq, hkv, d, bs, poison=False)
+    rng = np.random.default_rng(8)
+    c.lens, c.news = np.ones(b, np.int32), np.ones(b, np.int32)
+    longer = [0, 1, 40000, b - 1]
+    c.lens[longer], c.news[longer] = [300, 40, 513, 77], [20, 1, 130, 33]
+    c.news[[2, 3, 50000, b - 2]] = 0
+    c.starts = np.concatenate([[0], np.cumsum(c.news)]).astype(np.int32)
+    c.tables = rng.integers(0, shared, (b, 33)).astype(np.int32)
+    c.q = kv4.to_bf16(rng.standard_normal((int(c.starts[-1]), hq, d)).astype(np.float32))
+    got = c.run()
+    assert c.status() == 0
+    want, bound = c.want(longer)
+    for s in longer:
+        rows = slice(int(c.starts[s]), int(c.starts[s + 1]))
+        _check(got[rows], want[rows], bound[rows])
+    single = np.flatnonzero((c.lens == 1) & (c.news == 1))
+    v = chunks.pool_values(c.vp, kind, d, bs)[c.tables[single, 0], :, 0] * np.float64(np.float32(c.vs))
+    rows = torch.as_tensor(c.starts[single], dtype=torch.int64, device="cuda")
+    _near(got[rows], np.repeat(v, hq // hkv, 1), np.abs(v).max(), 0.0)
