@@ -1164,16 +1164,15 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             const int key0 = k * kAttnKeys;
             const int nq = min(4, (pos_high - key0 + 32) >> 5);  // quarters that some row of the warp sees
             // Masked scores become -inf: the quarters that reach past the position of some of the warp's rows are rewritten so
-            // first.  Those past all of them (from nq on) are left out of the maximum (packed: 16 prompts of 1031 tokens 156 us,
-            // 158 with them), or filled without being read (pools: the branches below cost every stage more, 143 us against 133
-            // over 131072 keys).
-            constexpr bool kLeaveOut = SRC == kAttnPacked;
+            // first, those past all of them (from nq on) without being read.  (With those left out of the maximum instead, the
+            // branches cost every stage more: one prompt of 8191 tokens 838 us against 827, 2 x 9 tokens over 131072 keys 143
+            // against 133.)
             if (key0 + kAttnKeys - 1 > pos_low) {
 #pragma unroll 1
-                for (int q = max(0, pos_low + 1 - key0) >> 5; q < (kLeaveOut ? nq : 4); ++q) {
+                for (int q = max(0, pos_low + 1 - key0) >> 5; q < 4; ++q) {
                     uint32_t x[32];
                     const int seen = pos - key0 - 32 * q;
-                    if (kLeaveOut || q < nq) {
+                    if (q < nq) {
                         tmem_ld32(row_tmem + 32 * q, x);
                         tmem_wait_ld32(x);
 #pragma unroll
@@ -1207,13 +1206,13 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
             tmem_wait_ld32(xc);
             tmem_wait_ld32(xa);
             tmem_ld32(row_tmem + 96, xb);
-            if (!kLeaveOut || nq > 0) larger(xc);
+            larger(xc);
             tmem_ld32(row_tmem + 64, xc);
-            if (!kLeaveOut || nq > 1) larger(xa);
+            larger(xa);
             tmem_wait_ld32(xb);
             tmem_wait_ld32(xc);
-            if (!kLeaveOut || nq > 3) larger(xb);
-            if (!kLeaveOut || nq > 2) larger(xc);
+            larger(xb);
+            larger(xc);
             const float m_new = fmaxf(m_raw, fmaxf(fmax3(mx0, mx1, mx2), mx3));
             if (i == 0) {
                 if (is_large(m_new)) break;
