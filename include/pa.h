@@ -541,8 +541,9 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, int64_t q_stride, const 
  * [head_dim] contiguous, is what pa_prompt_attention reads after it; it may be k itself
  * when k is contiguous, and overlaps nothing else.
  *
- * q_weight is read when num_q_heads > 0.  eps: finite, >= 0 (a row of zeros under eps 0
- * is 0 / 0).  A row whose squares' sum leaves fp32 becomes zero; a NaN in a query or key
+ * q_weight is read when num_q_heads > 0.  eps: finite, >= 0 (under eps 0 a row of zeros
+ * is 0 / 0, and one whose squares fall below fp32, elements of about 2^-63 and less, loses
+ * bits or becomes infinite).  A row whose squares' sum leaves fp32 becomes zero; a NaN in a query or key
  * head makes that head NaN, an infinity itself and what it is turned with, and the rest
  * of the head zero.  Everything else, padding, bad slots and
  * positions included, is as for pa_rope_and_cache.
@@ -635,12 +636,13 @@ pa_status pa_prefill_attention(void* out, const void* q, const void* k_pool, con
  * projection; out [num_tokens][num_q_heads][head_dim], contiguous, overlapping no input.
  * cu_lens int32 [num_seqs + 1], non-decreasing; a sequence may be empty.  Rows of no
  * sequence (before cu_lens[0], behind cu_lens[num_seqs]) are not written.  max_len bounds
- * every length.  bf16, head_dim 64 or 128, num_q_heads / num_kv_heads <= 8, num_seqs and
+ * every length (num_tokens does where nothing closer is known).  bf16, head_dim 64 or 128, num_q_heads / num_kv_heads <= 8, num_seqs and
  * num_kv_heads <= 65535.  scale must be finite and > 0.  Keys and values of a sequence's tokens must be finite (a
  * NaN or infinity there may reach earlier rows of the same sequence too, as in
  * pa_prefill_attention); what other rows hold reaches nothing.
  *
- * Scores and softmax in fp32, weights rounded to bf16 for the product with V.
+ * Scores and softmax in fp32, weights rounded to bf16 for the product with V; scores of any
+ * size that fp32 holds.
  * A sequence outside num_tokens, longer than max_len, or of negative length
  * sets PA_DEV_BAD_SEQ_LEN in *dev_status (if not NULL) and is not written; a pipeline wait
  * that gives up sets PA_DEV_WAIT_TIMEOUT.  Asynchronous on `stream`.  Allocates
@@ -662,7 +664,7 @@ pa_status pa_prompt_attention(void* out, const void* q, int64_t q_stride, const 
  *
  * code * scale of a pool is exact in f16, in which the products run with fp32 sums; a query
  * row is first scaled by a power of two so that its largest element lies in [1, 2), so any
- * finite bf16 magnitudes are in range (an element 2^-14 or less of its row's largest loses bits
+ * finite bf16 magnitudes are in range, rows of zeros and scores of any size among them (an element 2^-14 or less of its row's largest loses bits
  * below 2^-24 of that).  The softmax weights are f16: off by at most 2^-11 of themselves or
  * 2^-32 of the largest.  Slots behind a sequence's end may hold any bytes; a NaN among a
  * sequence's own values may reach rows of the chunk that do not see it.  A sequence of more

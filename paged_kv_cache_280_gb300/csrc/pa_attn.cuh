@@ -22,7 +22,8 @@
 //   S = Q K^T into TMEM (M 128, N 128), O += P V with P read from TMEM, where the softmax wrote it over S's last 64 columns.
 //   P is handed over in two halves of 64 keys, so that the product with V begins while the second half's exponentials
 //   are formed.
-// O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since it was last scaled.  Every wait is
+// O is rescaled in TMEM only when a row's maximum has grown by more than 2^8 since it was last scaled.  Scores too large for a
+// weight's exponent to be one fma leave the loop for one of their own (at_softmax_large).  Every wait is
 // bounded; one that gives up sets PA_DEV_WAIT_TIMEOUT, every role stops, and the CTA waits for its own copies and MMAs
 // before it frees TMEM.
 //
@@ -30,12 +31,13 @@
 // from shared memory, take all its 128 bytes a clock meanwhile.  The softmax of a stage is some 1900 cycles of a half's warps
 // (128 exponentials a thread, TMEM both ways), which the other half's products cover but for its hand-overs, so a stage of
 // two tiles takes about 3500 (the products' 2050).  A unit's end and the next one's start cost some 3000 more.
-//   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 795 us, 1.38 PFLOP/s (0.73 of the measured bf16 rate; tensor pipe busy
-//   60 %); 32 / 8 heads: 16 prompts of 1031 tokens 158 us (0.46: a unit has five stages on average, the last one masked).
+//   Packed, 64 / 8 heads of 128: one prompt of 8191 tokens 792 to 838 us from one card to the next, 1.31 to 1.39 PFLOP/s (0.69 to
+//   0.73 of the measured bf16 rate; tensor pipe busy 59 %); 32 / 8 heads: 16 prompts of 1031 tokens 160 us (0.46: a unit has five
+//   stages on average, the last one masked).
 //   Pools: the widening beside it (4 warps, about 1100 cycles of conversions and stores for K or V of a stage, which share the
-//   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens at the end of 32767: 840 us (0.67); 2 x 9
-//   tokens over 131072 keys, 64 / 8 heads: 133 us (tiles of 72 rows and less are padded to 128, so the tensor core's 44 % busy
-//   cycles and the widening bound it, not HBM's 45 us); FP8, 32 / 32 heads, 129 to 517 tokens over up to 16383 keys: 157 us (HBM
+//   issue slots and shared memory with the rest).  4-bit, 32 / 8 heads of 128, 2047 tokens at the end of 32767: 848 us (0.66); 2 x 9
+//   tokens over 131072 keys, 64 / 8 heads: 134 us (tiles of 72 rows and less are padded to 128, so the tensor core's 44 % busy
+//   cycles and the widening bound it, not HBM's 45 us); FP8, 32 / 32 heads, 129 to 517 tokens over up to 16383 keys: 158 us (HBM
 //   57; a tile is one head's, so every key is widened for 256 rows at most).
 #pragma once
 

@@ -11,8 +11,8 @@
 namespace pa {
 namespace {
 
-// Measured: 8191 tokens of 64 + 16 heads of 128, bf16 into FP8 pools, keys also stored dense (306 MB): 60 us, 5.1 TB/s (0.75
-// of the measured copy rate; DRAM moves 300 MB).  With the weights and cos / sin applied one after the other and read for
+// Measured: 8191 tokens of 64 + 16 heads of 128, bf16 into FP8 pools, keys also stored dense (340 MB): 58.6 us, 5.8 TB/s (0.85
+// of the measured copy rate; DRAM moves 296 MB, the rest is written back later).  With the weights and cos / sin applied one after the other and read for
 // every row, as the plain append reads them, 75: the rows' shared-memory and issue slots bound it then, 302 instructions
 // a warp's turn against 206; now it is memory latency.  Keys and values in the queries' loop: 59.6, but registers spill
 // into the 4-bit pools.  CTAs per SM: 5 (96 registers, none spilled); 4: 62, 6: 66.  One wave of CTAs: 62, 2: 60, 4: 61.
