@@ -89,7 +89,7 @@ constexpr float kAtRescaleLog2 = 8.f;
 // the largest.
 constexpr float kAtWeightLog2 = 7.f;
 // A weight is 2^(c s + shift), one fma, with shift = 7 - c m (packed: -c m) rounded to fp32, the same for all keys that share
-// m; what rescales and joins takes differences of such shifts, so their rounding cancels.  It is 1 / 2 at most, and the f16
+// m; what rescales and joins takes differences of such shifts, so their rounding cancels.  It is 1 / 4 at most, and the f16
 // weights stay in range, while |c m| is below this; a piece with larger scores goes to at_softmax_large.
 constexpr float kAtLargeLog2 = 4194304.f;
 // A piece's reference (minus its shift) is handed on times this: finite however large c m is.
@@ -114,6 +114,11 @@ __device__ __forceinline__ float at_exp2(float x) {
     return y;
 }
 
+// The shift of a row whose maximum is m: rounded once, the same way wherever it is formed.
+template <int SRC>
+__device__ __forceinline__ float at_shift(float m, float c) {
+    return __fmaf_rn(-m, c, SRC == kAttnPacked ? 0.f : kAtWeightLog2);
+}
 // 2^x, x a difference of references.
 __device__ __forceinline__ float at_ref_exp2(float x) { return at_exp2(x * (1.f / kAtRefUnit)); }
 
@@ -1048,7 +1053,7 @@ __device__ __forceinline__ bool at_softmax_large(const AttnBars<SRC, D>& bars, i
                                                  int i, int mine, int& ck, float& m_raw, float& l_run) {
     constexpr float kTop = SRC == kAttnPacked ? 0.f : kAtWeightLog2;
     // what the loop before has summed is relative to its rounded shift
-    const float old_shift = kTop - m_raw * c;
+    const float old_shift = at_shift<SRC>(m_raw, c);
     const int i0 = i;
 #pragma unroll 1
     for (; i < mine; ++i, ++ck) {
@@ -1143,7 +1148,7 @@ __device__ __forceinline__ void at_softmax(const AttnParams& p, int t, uint8_t* 
         const int pos = w.len - w.n + (valid ? tok : i1 - 1);
         const int pos_low = __shfl_sync(0xffffffffu, pos, 0), pos_high = __shfl_sync(0xffffffffu, pos, 31);  // (they do not fall)
         float m_raw = -INFINITY, l_run = 0.f;  // maximum of the raw scores, and the weights' sum
-        auto shift_of = [&](float m) { return kTop - m * c; };
+        auto shift_of = [&](float m) { return at_shift<SRC>(m, c); };
         // (of the warp's rows; those of no token hold anything and have no say)
         auto is_large = [&](float m) { return __any_sync(0xffffffffu, valid && m > -INFINITY && fabsf(m) * c > kAtLargeLog2) != 0; };
         int i = 0;
