@@ -85,8 +85,8 @@ constexpr uint32_t kAtTmemCols = 512;  // half t: S (P over its last 64 columns)
 constexpr uint32_t kAtTmemHalf = 256;
 constexpr uint32_t kAtTmemP = 64, kAtTmemO = 128;
 constexpr float kAtRescaleLog2 = 8.f;
-// f16 weights are held times 2^7: with the lazy rescaling they stay below 2^15, and keep all their bits down to 2^-21 of
-// the largest.
+// f16 weights are held times 2^7: with the lazy rescaling they stay below 2^15 (2^15.25 where their shift is coarse), and keep
+// all their bits down to 2^-21 of the largest.
 constexpr float kAtWeightLog2 = 7.f;
 // A weight is 2^(c s + shift), one fma, with shift = 7 - c m (packed: -c m) rounded to fp32, the same for all keys that share
 // m; what rescales and joins takes differences of such shifts, so their rounding cancels.  It is 1 / 4 at most, and the f16

@@ -24,8 +24,8 @@ constexpr int kAttnKeys = 128;   // keys per stage
 constexpr int kAttnMaxLen = INT32_MAX - 255;  // longest sequence: a stage's keys, or two tiles' tokens, beyond it are still an int
 
 // How many new tokens a sequence has whose rows are c0 .. end - 1 and which is len tokens long; none (and wrong) where it
-// breaks the call's bounds.  The rows are compared with those before they are subtracted: a difference of two offsets that
-// are anything may leave 32 bits.  (INT32_MAX for len: its new tokens are all there is.)
+// breaks the call's bounds.  The offsets may be anything, so that their difference may leave 32 bits: it is taken modulo 2^32
+// and counts only where 0 <= c0 < end.  (INT32_MAX for len: its new tokens are all there is.)
 PA_HD int sequence_tokens(int c0, int end, int len, int num_tokens, int max_new, int max_len, bool& wrong) {
     const int n = (int)((uint32_t)end - (uint32_t)c0);
     wrong = end < c0 || (end > c0 && (c0 < 0 || end > num_tokens || n > max_new || n > len || len > max_len));
